@@ -365,6 +365,129 @@ int qspec_quant_act_fp8(const uint16_t *x_bf16, int M, int K, int ldx, uint8_t *
 int qspec_linear_fp8(const uint8_t *xq, const float *sa, const uint8_t *w8, const float *s8, int M, int N,
                      int K, uint16_t *y_bf16, int ldy, int32_t *dev_status, qspec_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Between the linears of a decoder layer: the norm in front of the Q8 linear,
+ * a 4-bit KV cache, and the attention that reads it or a prompt's own rows.
+ * The pages have no counterpart for these; they are the standard operators of
+ * a decoder layer in the library's own formats.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * Residual addition, root-mean-square norm and per-token E4M3 quantisation in
+ * one pass: what stands in front of qspec_linear_fp8.  Per row m:
+ *   h = bf16(x + res)  (h = x when res is NULL), stored to h_out
+ *   y = h w / sqrt(mean_k h^2 + eps)
+ *   sa = max_k |y| / 448, xq = E4M3(y / sa)   (a row of zeros: sa = 0, codes 0)
+ * Sums, norm and quotient in fp32; y is rounded once, to E4M3 (and to bf16
+ * where y_bf16 is asked for, for a W4A16 linear on the same rows).
+ *
+ *   x_bf16   uint16 [M][ldx]   input rows
+ *   res_bf16 uint16 [M][ldr]   nullable: the residual stream
+ *   w_bf16   uint16 [K]        the norm's weights
+ *   h_bf16   uint16 [M][ldh]   out, required with res_bf16 and NULL without it;
+ *                              may be res_bf16 or x_bf16 itself (same leading dimension)
+ *   xq       uint8  [M][K]     out: E4M3 codes, as qspec_linear_fp8 reads them
+ *   sa       float  [M]        out: scales
+ *   y_bf16   uint16 [M][ldy]   nullable out
+ * K a multiple of 128, at most 32768; eps positive and finite
+ * (QSPEC_ERR_SHAPE).  Leading dimensions are at least K and multiples of 8,
+ * pointers 16-byte aligned (xq 8, sa 4).  Device errors: QSPEC_ERR_NONFINITE
+ * (a NaN or inf among x, res, h, w or y).
+ */
+int qspec_rmsnorm_fp8(const uint16_t *x_bf16, int ldx, const uint16_t *res_bf16, int ldr,
+                      const uint16_t *w_bf16, float eps, int M, int K, uint16_t *h_bf16, int ldh,
+                      uint8_t *xq, float *sa, uint16_t *y_bf16, int ldy, int32_t *dev_status,
+                      qspec_stream_t stream);
+
+/*
+ * The 4-bit KV cache of one layer, in the library's asymmetric INT4 format
+ * with one group per (position, head):
+ *   k_codes, v_codes uint8  [B][H][T][D/2]  byte j = code[2j] | code[2j+1] << 4
+ *   k_sz, v_sz       uint32 [B][H][T]       fp16 bits of s | fp16 bits of z << 16
+ * and stands for x^ = s (code - z), z an integer 0..15.  D is 64 or 128.
+ *
+ * qspec_kv4_append quantises bf16 rows into it.  Per row and head,
+ * lo = min(0, min x), hi = max(0, max x):
+ *   s = fp16((hi - lo) / 15), z = clamp(rint(-lo / s), 0, 15),
+ *   code = clamp(rint(x / s) + z, 0, 15)    (s == 0: code = z = 0)
+ * in fp32 (IEEE quotients, ties to even), so every bit is fixed.
+ * qspec_kv4_load reads rows back as bf16(s (code - z)).
+ *
+ * Rows are packed: rows row_start[b] .. row_start[b + 1] - 1 are positions
+ * base_pos[b], base_pos[b] + 1, ... of sequence b (a prompt, the row of a
+ * draft step, or the gamma + 1 rows of a verify pass, which replace the draft's).
+ *
+ *   k_bf16, v_bf16 uint16 [rows][ld]  head h of row m at m ld + h D
+ *                                     (ldk, ldv >= H D, multiples of 8)
+ *   row_start int32 [B + 1], base_pos int32 [B]   on the device
+ *   rows      rows in k_bf16 / v_bf16; row_start[B] <= rows
+ * k_bf16, v_bf16 and the codes 16-byte aligned.  rows may be 0.  Device
+ * errors: QSPEC_ERR_RANGE when 0 <= row_start[b] <= row_start[b + 1] <= rows,
+ * base_pos[b] >= 0 or base_pos[b] + (its rows) <= T does not hold (that
+ * sequence is left untouched); append: QSPEC_ERR_NONFINITE (a NaN or inf, or
+ * a scale beyond fp16).
+ */
+int qspec_kv4_append(const uint16_t *k_bf16, int ldk, const uint16_t *v_bf16, int ldv,
+                     const int32_t *row_start, const int32_t *base_pos, int rows, int B, int H, int T,
+                     int D, uint8_t *k_codes, uint32_t *k_sz, uint8_t *v_codes, uint32_t *v_sz,
+                     int32_t *dev_status, qspec_stream_t stream);
+int qspec_kv4_load(const uint8_t *k_codes, const uint32_t *k_sz, const uint8_t *v_codes,
+                   const uint32_t *v_sz, const int32_t *row_start, const int32_t *base_pos, int rows,
+                   int B, int H, int T, int D, uint16_t *k_bf16, int ldk, uint16_t *v_bf16, int ldv,
+                   int32_t *dev_status, qspec_stream_t stream);
+
+/* Bytes of workspace qspec_attn_kv4 needs (0 for sizes that it refuses). */
+size_t qspec_attn_kv4_workspace_bytes(int B, int R, int Hq, int H, int D);
+
+/*
+ * Attention of the newest R rows of every sequence over the 4-bit cache: a
+ * draft step (R = 1) or the verify pass (R = gamma + 1), their own K and V
+ * already in the cache (qspec_kv4_append).  Query head j reads KV head
+ * j / (Hq / H).  Row r of sequence b sees positions 0 .. len[b] - R + r (none
+ * when that is negative: its output is 0):
+ *   a_t = scale sum_d q_d k^_td,  o = sum_t softmax(a)_t v^_t
+ * Scores, softmax statistics and sums in fp32; the weights softmax(a)_t s_t are rounded
+ * to bf16 for the tensor cores.
+ *
+ *   q_bf16 uint16 [B R][ldq]   head j of row b R + r at (b R + r) ldq + j D
+ *   len    int32  [B]          cache length of each sequence, its R rows included (0 .. T)
+ *   o_bf16 uint16 [B R][ldo]   out
+ *   workspace, ws_bytes        device scratch of qspec_attn_kv4_workspace_bytes, 16-byte aligned.
+ *                              Its first use needs it zeroed; every call leaves it
+ *                              ready for the next, of any shape that fits.  Calls
+ *                              that may overlap on the GPU need one each.
+ * 1 <= R <= 17, Hq a multiple of H, D 64 or 128; q, o and the codes 16-byte
+ * aligned, ldq, ldo multiples of 8.  Device errors: QSPEC_ERR_RANGE (len[b]
+ * outside [0, T]; that sequence's outputs are left untouched).
+ */
+int qspec_attn_kv4(const uint16_t *q_bf16, int ldq, const uint8_t *k_codes, const uint32_t *k_sz,
+                   const uint8_t *v_codes, const uint32_t *v_sz, const int32_t *len, int B, int R,
+                   int Hq, int H, int T, int D, float scale, uint16_t *o_bf16, int ldo,
+                   void *workspace, size_t ws_bytes, int32_t *dev_status, qspec_stream_t stream);
+
+/*
+ * Causal attention of packed prompts over bf16 rows, grouped heads.  Sequence
+ * b has query rows q_start[b] .. q_start[b + 1] - 1 (Lq of them) and key / value
+ * rows k_start[b] .. k_start[b + 1] - 1 (Lk); its query row i sees key rows
+ * 0 .. i + Lk - Lq of it (Lk > Lq: a prefix before the rows; none when the
+ * bound is negative: the output is 0).  Values at places that a row does not
+ * see never reach it, whatever they are.
+ *
+ *   q_bf16 uint16 [q_rows][ldq], k_bf16, v_bf16 uint16 [k_rows][ldk / ldv],
+ *   o_bf16 uint16 [q_rows][ldo]   head j of row m at m ld + j D
+ *   q_start, k_start int32 [B + 1] on the device
+ * Scores, softmax statistics and sums in fp32; the weights exp(a - max) are rounded to
+ * bf16 for the tensor cores.  Hq a multiple of H, D 64 or 128, pointers 16-byte
+ * aligned, leading dimensions multiples of 8, at least the heads' width.
+ * q_rows or k_rows may be 0.  Device errors: QSPEC_ERR_RANGE when
+ * 0 <= start[b] <= start[b + 1] <= rows does not hold (that sequence is left
+ * untouched), QSPEC_ERR_TIMEOUT (a bounded wait expired).
+ */
+int qspec_attn_prompt(const uint16_t *q_bf16, int ldq, const uint16_t *k_bf16, int ldk,
+                      const uint16_t *v_bf16, int ldv, const int32_t *q_start, const int32_t *k_start,
+                      int q_rows, int k_rows, int B, int Hq, int H, int D, float scale,
+                      uint16_t *o_bf16, int ldo, int32_t *dev_status, qspec_stream_t stream);
+
 /*
  * Diagnostic for tests of the bounded waits; the pages have no counterpart.
  * Runs one of the library's tensor-core linear kernels on the same arguments

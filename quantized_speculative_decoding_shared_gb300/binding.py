@@ -11,6 +11,7 @@ sm_103 part, the calls raise.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -35,7 +36,9 @@ EXPORTED = ["qspec_version", "qspec_status_string", "qspec_last_cuda_error", "qs
             "qspec_verify_workspace_bytes", "qspec_verify_greedy", "qspec_verify_sample",
             "qspec_kv_overwrite", "qspec_verify_sample_noalloc", "qspec_draft_workspace_bytes",
             "qspec_draft_sample", "qspec_debug_linear_bounded", "qspec_quant_weights_fp8",
-            "qspec_quant_act_fp8", "qspec_linear_fp8", "qspec_linear_w4a16_kv"]
+            "qspec_quant_act_fp8", "qspec_linear_fp8", "qspec_linear_w4a16_kv",
+            "qspec_rmsnorm_fp8", "qspec_kv4_append", "qspec_kv4_load", "qspec_attn_kv4_workspace_bytes",
+            "qspec_attn_kv4", "qspec_attn_prompt"]
 KERNEL_W4A16_TC, KERNEL_W4A4_GEMV_TC, KERNEL_W4A4_TC = 0, 1, 2
 NOALLOC_SCRATCH_BYTES = 1 << 20
 
@@ -65,6 +68,7 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
                                "quantized_speculative_decoding_shared_gb300.build.build()" % p)
         lib = ctypes.CDLL(p)
         vp, i32, sz_t, u64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_uint64
+        f32 = ctypes.c_float
         proto = {
             "qspec_version": ([], i32),
             "qspec_kernel_launches": ([], ctypes.c_ulonglong),
@@ -93,6 +97,15 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
             "qspec_linear_fp8": ([vp, vp, vp, vp, i32, i32, i32, vp, i32, vp, vp], i32),
             "qspec_linear_w4a16_kv": ([vp, i32, vp, vp, i32, i32, i32, vp, i32, i32, i32, i32, i32, i32,
                                        vp, vp, vp, vp, vp, vp], i32),
+            "qspec_rmsnorm_fp8": ([vp, i32, vp, i32, vp, f32, i32, i32, vp, i32, vp, vp, vp, i32, vp, vp], i32),
+            "qspec_kv4_append": ([vp, i32, vp, i32, vp, vp, i32, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp],
+                                 i32),
+            "qspec_kv4_load": ([vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, vp, i32, vp, i32, vp, vp], i32),
+            "qspec_attn_kv4_workspace_bytes": ([i32, i32, i32, i32, i32], sz_t),
+            "qspec_attn_kv4": ([vp, i32, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, f32, vp, i32, vp, sz_t,
+                                vp, vp], i32),
+            "qspec_attn_prompt": ([vp, i32, vp, i32, vp, i32, vp, vp, i32, i32, i32, i32, i32, i32, f32, vp, i32,
+                                   vp, vp], i32),
         }
         for name, (args, res) in proto.items():
             f = getattr(lib, name)
@@ -248,6 +261,43 @@ def qspec_linear_fp8(xq, sa, w8, s8, M, N, K, y, ldy, dev_status=None, stream=No
                                            _ptr(dev_status), _stream(stream))
 
 
+def qspec_rmsnorm_fp8(x, ldx, res, ldr, w, eps, M, K, h, ldh, xq, sa, y, ldy, dev_status=None, stream=None):
+    return load_library().qspec_rmsnorm_fp8(_ptr(x), ldx, _ptr(res), ldr, _ptr(w), eps, M, K, _ptr(h), ldh,
+                                            _ptr(xq), _ptr(sa), _ptr(y), ldy, _ptr(dev_status), _stream(stream))
+
+
+def qspec_kv4_append(k, ldk, v, ldv, row_start, base_pos, rows, B, H, T, D, k_codes, k_sz, v_codes, v_sz,
+                     dev_status=None, stream=None):
+    return load_library().qspec_kv4_append(_ptr(k), ldk, _ptr(v), ldv, _ptr(row_start), _ptr(base_pos), rows, B,
+                                           H, T, D, _ptr(k_codes), _ptr(k_sz), _ptr(v_codes), _ptr(v_sz),
+                                           _ptr(dev_status), _stream(stream))
+
+
+def qspec_kv4_load(k_codes, k_sz, v_codes, v_sz, row_start, base_pos, rows, B, H, T, D, k, ldk, v, ldv,
+                   dev_status=None, stream=None):
+    return load_library().qspec_kv4_load(_ptr(k_codes), _ptr(k_sz), _ptr(v_codes), _ptr(v_sz), _ptr(row_start),
+                                         _ptr(base_pos), rows, B, H, T, D, _ptr(k), ldk, _ptr(v), ldv,
+                                         _ptr(dev_status), _stream(stream))
+
+
+def qspec_attn_kv4_workspace_bytes(B, R, Hq, H, D):
+    return int(load_library().qspec_attn_kv4_workspace_bytes(B, R, Hq, H, D))
+
+
+def qspec_attn_kv4(q, ldq, k_codes, k_sz, v_codes, v_sz, length, B, R, Hq, H, T, D, scale, o, ldo, workspace,
+                   ws_bytes, dev_status=None, stream=None):
+    return load_library().qspec_attn_kv4(_ptr(q), ldq, _ptr(k_codes), _ptr(k_sz), _ptr(v_codes), _ptr(v_sz),
+                                         _ptr(length), B, R, Hq, H, T, D, scale, _ptr(o), ldo, _ptr(workspace),
+                                         ws_bytes, _ptr(dev_status), _stream(stream))
+
+
+def qspec_attn_prompt(q, ldq, k, ldk, v, ldv, q_start, k_start, q_rows, k_rows, B, Hq, H, D, scale, o, ldo,
+                      dev_status=None, stream=None):
+    return load_library().qspec_attn_prompt(_ptr(q), ldq, _ptr(k), ldk, _ptr(v), ldv, _ptr(q_start),
+                                            _ptr(k_start), q_rows, k_rows, B, Hq, H, D, scale, _ptr(o), ldo,
+                                            _ptr(dev_status), _stream(stream))
+
+
 # ---------------------------------------------------------------------------
 # allocating conveniences (torch tensors in, torch tensors out)
 # ---------------------------------------------------------------------------
@@ -395,3 +445,138 @@ def linear_fp8(xq, sa, w8, s8, out=None, dev_status=None, stream=None):
     y = out if out is not None else torch.empty((M, N), dtype=torch.bfloat16, device=xq.device)
     _check(qspec_linear_fp8(xq, sa, w8, s8, M, N, K, y, y.stride(0), dev_status, stream), "qspec_linear_fp8")
     return y
+
+
+def _heads(t, name):
+    """A [rows][heads][D] bf16 CUDA tensor whose heads of a row are contiguous
+    (rows may be strided, as columns of a fused projection's output are):
+    (rows, heads, D, leading dimension)."""
+    if t.device.type != "cuda" or t.dtype != torch.bfloat16 or t.dim() != 3:
+        raise ValueError("%s must be a bf16 CUDA tensor [rows][heads][D]" % name)
+    rows, H, D = t.shape
+    if rows and (t.stride(2) != 1 or (H > 1 and t.stride(1) != D)):
+        raise ValueError("%s: the heads of a row must be contiguous" % name)
+    return rows, H, D, (t.stride(0) if rows > 1 else H * D)
+
+
+def rmsnorm_fp8(x, w, eps, residual=None, want_bf16=False, dev_status=None, stream=None):
+    """x bf16 [M][K] (plus residual bf16 [M][K]) -> (xq uint8 [M][K] E4M3, sa fp32 [M], h bf16 [M][K] or
+    None without a residual, y bf16 [M][K] or None without want_bf16)."""
+    _need(w, torch.bfloat16, "w")
+    for t, name in ((x, "x"), (residual, "residual")):
+        if t is not None and (t.device.type != "cuda" or t.dtype != torch.bfloat16 or t.dim() != 2
+                              or t.shape != x.shape or (t.numel() and t.stride(1) != 1)):
+            raise ValueError("%s must be a bf16 CUDA tensor [M][K] with contiguous rows" % name)
+    M, K = x.shape
+    if w.numel() != K:
+        raise ValueError("w must hold %d values" % K)
+    ld = lambda t: t.stride(0) if M > 1 else K      # noqa: E731
+    xq = torch.empty((M, K), dtype=torch.uint8, device=x.device)
+    sa = torch.empty(M, dtype=torch.float32, device=x.device)
+    h = torch.empty((M, K), dtype=torch.bfloat16, device=x.device) if residual is not None else None
+    y = torch.empty((M, K), dtype=torch.bfloat16, device=x.device) if want_bf16 else None
+    _check(qspec_rmsnorm_fp8(x, ld(x), residual, K if residual is None else ld(residual), w, eps, M, K, h, K, xq,
+                             sa, y, K, dev_status, stream), "qspec_rmsnorm_fp8")
+    return xq, sa, h, y
+
+
+def kv4_cache(B, H, T, D, device="cuda"):
+    """A zeroed 4-bit cache of one layer: (k_codes uint8 [B][H][T][D/2], k_sz int32 [B][H][T], v_codes, v_sz)."""
+    codes = lambda: torch.zeros((B, H, T, D // 2), dtype=torch.uint8, device=device)   # noqa: E731
+    words = lambda: torch.zeros((B, H, T), dtype=torch.int32, device=device)           # noqa: E731
+    return codes(), words(), codes(), words()
+
+
+def _cache_shape(cache):
+    k_codes, k_sz, v_codes, v_sz = cache
+    for t, dt, name in ((k_codes, torch.uint8, "k_codes"), (v_codes, torch.uint8, "v_codes"),
+                        (k_sz, torch.int32, "k_sz"), (v_sz, torch.int32, "v_sz")):
+        _need(t, dt, name)
+    B, H, T, D2 = k_codes.shape
+    if v_codes.shape != k_codes.shape or k_sz.shape != (B, H, T) or v_sz.shape != (B, H, T):
+        raise ValueError("codes must be [B][H][T][D/2] and scale words [B][H][T], for K and V alike")
+    return B, H, T, 2 * D2
+
+
+def _starts(t, B, name):
+    _need(t, torch.int32, name)
+    if t.numel() != B:
+        raise ValueError("%s must hold %d values" % (name, B))
+
+
+def kv4_append(cache, k, v, row_start, base_pos, dev_status=None, stream=None):
+    """Quantise packed rows k, v bf16 [rows][H][D] into a cache (as kv4_cache gives it): rows row_start[b] ..
+    row_start[b + 1] - 1 become positions base_pos[b], base_pos[b] + 1, ... of sequence b."""
+    B, H, T, D = _cache_shape(cache)
+    rows, Hk, Dk, ldk = _heads(k, "k")
+    rv, Hv, Dv, ldv = _heads(v, "v")
+    if (Hk, Dk) != (H, D) or (rv, Hv, Dv) != (rows, H, D):
+        raise ValueError("k and v must be [rows][%d][%d]" % (H, D))
+    _starts(row_start, B + 1, "row_start")
+    _starts(base_pos, B, "base_pos")
+    k_codes, k_sz, v_codes, v_sz = cache
+    _check(qspec_kv4_append(k, ldk, v, ldv, row_start, base_pos, rows, B, H, T, D, k_codes, k_sz, v_codes, v_sz,
+                            dev_status, stream), "qspec_kv4_append")
+
+
+def kv4_load(cache, row_start, base_pos, rows, dev_status=None, stream=None):
+    """The rows of kv4_append back from the cache: (k, v) bf16 [rows][H][D].  Rows of no sequence are zeros."""
+    B, H, T, D = _cache_shape(cache)
+    _starts(row_start, B + 1, "row_start")
+    _starts(base_pos, B, "base_pos")
+    k_codes, k_sz, v_codes, v_sz = cache
+    k = torch.zeros((rows, H, D), dtype=torch.bfloat16, device=k_codes.device)
+    v = torch.zeros_like(k)
+    _check(qspec_kv4_load(k_codes, k_sz, v_codes, v_sz, row_start, base_pos, rows, B, H, T, D, k, H * D, v, H * D,
+                          dev_status, stream), "qspec_kv4_load")
+    return k, v
+
+
+def attn_kv4_workspace(B, R, Hq, H, D, device="cuda"):
+    """Workspace of attn_kv4, zeroed as its first use needs it."""
+    n = qspec_attn_kv4_workspace_bytes(B, R, Hq, H, D)
+    if n == 0:
+        raise QspecError(ERR_SHAPE, "qspec_attn_kv4_workspace_bytes")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def attn_kv4(q, cache, length, scale, workspace=None, out=None, dev_status=None, stream=None):
+    """q bf16 [B R][Hq][D], the newest R rows of each sequence, over a 4-bit cache; length int32 [B] counts them.
+    Returns o bf16 [B R][Hq][D]."""
+    B, H, T, D = _cache_shape(cache)
+    rows, Hq, Dq, ldq = _heads(q, "q")
+    if Dq != D or rows % B:
+        raise ValueError("q must be [B R][Hq][%d] with B = %d" % (D, B))
+    _starts(length, B, "length")
+    R = rows // B
+    o = out if out is not None else torch.empty((rows, Hq, D), dtype=torch.bfloat16, device=q.device)
+    if _heads(o, "out")[:3] != (rows, Hq, D):
+        raise ValueError("out must be [%d][%d][%d]" % (rows, Hq, D))
+    if workspace is None:
+        with torch.cuda.stream(stream) if isinstance(stream, torch.cuda.Stream) else contextlib.nullcontext():
+            workspace = attn_kv4_workspace(B, R, Hq, H, D, q.device)
+    k_codes, k_sz, v_codes, v_sz = cache
+    _check(qspec_attn_kv4(q, ldq, k_codes, k_sz, v_codes, v_sz, length, B, R, Hq, H, T, D, scale, o,
+                          _heads(o, "out")[3], workspace, workspace.numel(), dev_status, stream), "qspec_attn_kv4")
+    return o
+
+
+def attn_prompt(q, k, v, q_start, k_start=None, scale=None, out=None, dev_status=None, stream=None):
+    """Causal attention over packed prompts: q bf16 [q_rows][Hq][D], k and v bf16 [k_rows][H][D], q_start and
+    k_start int32 [B + 1] (k_start None: the same).  scale None: 1 / sqrt(D).  Returns o bf16 [q_rows][Hq][D]."""
+    q_rows, Hq, D, ldq = _heads(q, "q")
+    k_rows, H, Dk, ldk = _heads(k, "k")
+    rv, Hv, Dv, ldv = _heads(v, "v")
+    if Dk != D or (rv, Hv, Dv) != (k_rows, H, D):
+        raise ValueError("k and v must be [k_rows][H][%d]" % D)
+    k_start = q_start if k_start is None else k_start
+    B = q_start.numel() - 1
+    _starts(q_start, B + 1, "q_start")
+    _starts(k_start, B + 1, "k_start")
+    o = out if out is not None else torch.empty((q_rows, Hq, D), dtype=torch.bfloat16, device=q.device)
+    if _heads(o, "out")[:3] != (q_rows, Hq, D):
+        raise ValueError("out must be [%d][%d][%d]" % (q_rows, Hq, D))
+    _check(qspec_attn_prompt(q, ldq, k, ldk, v, ldv, q_start, k_start, q_rows, k_rows, B, Hq, H, D,
+                             D ** -0.5 if scale is None else scale, o, _heads(o, "out")[3], dev_status, stream),
+           "qspec_attn_prompt")
+    return o

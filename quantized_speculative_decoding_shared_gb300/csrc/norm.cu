@@ -1,0 +1,206 @@
+// norm.cu -- residual addition, root-mean-square norm and per-token E4M3
+// quantisation in one pass over the rows (what stands in front of the Q8
+// linear of fp8.cu).
+//
+// Per row: h = bf16(x + r), y = h w rstd with rstd = 1 / sqrt(mean h^2 + eps),
+// sa = max |y| / 448, xq = E4M3(y / sa).  With a = h w the quotient is
+// a rstd / (max |a| rstd / 448) = a (448 / max |a|): the norm drops out of the
+// codes, so ONE block reduction gives both the sum of squares and max |a|, and
+// the row stays in registers between its single load and its stores.
+// Bound: HBM (2 K read per input, 2 K written for h, K for the codes).
+#include <algorithm>
+#include <cmath>
+#include <cuda_fp8.h>
+
+#include "qspec_device.cuh"
+#include "qspec_host.h"
+
+namespace qspec {
+
+namespace {
+
+namespace nrm {
+
+constexpr int kMaxK = 32768;
+
+__device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+    return (uint32_t)float_to_bf16_bits(a) | ((uint32_t)float_to_bf16_bits(b) << 16);
+}
+// four E4M3 codes, element 0 in the low byte
+__device__ __forceinline__ uint32_t pack_e4m3(float a, float b, float c, float d) {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+    return lo | (hi << 16);
+}
+
+// sum and maximum over the TPR threads of a row (all rows of a CTA take part)
+template <int TPR>
+__device__ __forceinline__ void row_reduce(float &sum, float &mx, float2 *red) {
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) {
+        sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    }
+    if constexpr (TPR > 32) {
+        constexpr int kW = TPR / 32;
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        __syncthreads();                       // red free again (a second pass over the row)
+        if (lane == 0) red[warp] = make_float2(sum, mx);
+        __syncthreads();
+        const float2 v = red[lane % kW];       // every warp folds the kW partials in the same order
+        sum = v.x;
+        mx = v.y;
+#pragma unroll
+        for (int o = kW / 2; o >= 1; o >>= 1) {
+            sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        }
+    }
+}
+
+// TPR threads per row, up to NV 16-byte words of a row per thread
+template <int TPR, int NV>
+__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR)
+    rmsnorm_fp8_kernel(const uint16_t *x, int ldx, const uint16_t *res, int ldr,
+                       const uint16_t *__restrict__ w, float eps, int M, int K, uint16_t *h, int ldh,
+                       uint8_t *__restrict__ xq, float *__restrict__ sa, uint16_t *__restrict__ y, int ldy,
+                       int32_t *st) {
+    constexpr int kRows = TPR < 128 ? 128 / TPR : 1;
+    __shared__ float2 red[32];
+    const int t = threadIdx.x % TPR;
+    const int m = blockIdx.x * kRows + (TPR < 128 ? threadIdx.x / TPR : 0);
+    const int n8 = K / 8;
+    const bool row_ok = m < M;
+    pdl_launch_dependents();
+    pdl_wait();
+    uint4 hv[NV], wv[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int i = t + j * TPR;
+        const bool in = row_ok && i < n8;
+        hv[j] = in ? __ldcs(reinterpret_cast<const uint4 *>(x + (size_t)m * ldx) + i) : make_uint4(0, 0, 0, 0);
+        wv[j] = in ? __ldg(reinterpret_cast<const uint4 *>(w) + i) : make_uint4(0, 0, 0, 0);
+    }
+    if (res != nullptr) {
+        uint4 rv[NV];
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int i = t + j * TPR;
+            rv[j] = row_ok && i < n8 ? __ldcs(reinterpret_cast<const uint4 *>(res + (size_t)m * ldr) + i)
+                                     : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int i = t + j * TPR;
+            uint32_t a[4] = {hv[j].x, hv[j].y, hv[j].z, hv[j].w};
+            const uint32_t b[4] = {rv[j].x, rv[j].y, rv[j].z, rv[j].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) a[e] = pack_bf16(lo_f(a[e]) + lo_f(b[e]), hi_f(a[e]) + hi_f(b[e]));
+            hv[j] = make_uint4(a[0], a[1], a[2], a[3]);
+            if (row_ok && i < n8) reinterpret_cast<uint4 *>(h + (size_t)m * ldh)[i] = hv[j];
+        }
+    }
+    // sum h^2 and max |h w|.  Where the squares or products of finite values
+    // pass fp32 (|h| above 1e19), the row is taken again times 2^-80.
+    float down = 1.0f, ss, amax;
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass) {
+        ss = 0.0f;
+        amax = 0.0f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const uint32_t a[4] = {hv[j].x, hv[j].y, hv[j].z, hv[j].w};
+            const uint32_t b[4] = {wv[j].x, wv[j].y, wv[j].z, wv[j].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float h0 = lo_f(a[e]) * down, h1 = hi_f(a[e]) * down;
+                ss = fmaf(h0, h0, ss);
+                ss = fmaf(h1, h1, ss);
+                const float p0 = fabsf(h0 * lo_f(b[e])), p1 = fabsf(h1 * hi_f(b[e]));
+                amax = fmaxf(amax, fmaxf(p0 < INFINITY ? p0 : INFINITY, p1 < INFINITY ? p1 : INFINITY));   // NaN counts as inf
+            }
+        }
+        row_reduce<TPR>(ss, amax, red);
+        const bool again = pass == 0 && !(ss < INFINITY && amax < INFINITY);
+        if (TPR > 32 ? !again : !__any_sync(0xffffffffu, again)) break;
+        down = again ? 8.271806125530277e-25f : 1.0f;    // 2^-80
+    }
+    if (!row_ok) return;
+    const float rstd = rsqrtf(fmaf(ss, 1.0f / (float)K, eps * down * down));
+    // y = a rstd; codes a (448 / max |a|), where 448 / max |a| would pass fp32
+    // with a brought up first
+    const float up = amax < 1.0e-30f ? 7.9228162514264338e28f : 1.0f;   // 2^96
+    const float inv = amax > 0.0f ? __fdiv_rn(448.0f, amax * up) : 0.0f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int i = t + j * TPR;
+        if (i >= n8) continue;
+        const uint32_t a[4] = {hv[j].x, hv[j].y, hv[j].z, hv[j].w};
+        const uint32_t b[4] = {wv[j].x, wv[j].y, wv[j].z, wv[j].w};
+        float p[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            p[2 * e] = lo_f(a[e]) * down * lo_f(b[e]);
+            p[2 * e + 1] = hi_f(a[e]) * down * hi_f(b[e]);
+        }
+        reinterpret_cast<uint2 *>(xq + (size_t)m * K)[i] =
+            amax > 0.0f ? make_uint2(pack_e4m3(p[0] * up * inv, p[1] * up * inv, p[2] * up * inv, p[3] * up * inv),
+                                     pack_e4m3(p[4] * up * inv, p[5] * up * inv, p[6] * up * inv, p[7] * up * inv))
+                        : make_uint2(0u, 0u);         // no code of -0 in a row of zeros
+        if (y != nullptr)
+            reinterpret_cast<uint4 *>(y + (size_t)m * ldy)[i] =
+                make_uint4(pack_bf16(p[0] * rstd, p[1] * rstd), pack_bf16(p[2] * rstd, p[3] * rstd),
+                           pack_bf16(p[4] * rstd, p[5] * rstd), pack_bf16(p[6] * rstd, p[7] * rstd));
+    }
+    if (t == 0) {
+        const float s = __fdiv_rn(amax * rstd, 448.0f);
+        sa[m] = s;
+        if (!(ss < INFINITY) || !(s < INFINITY)) flag(st, QSPEC_ERR_NONFINITE);
+    }
+}
+
+template <int TPR, int NV>
+int launch(const uint16_t *x, int ldx, const uint16_t *res, int ldr, const uint16_t *w, float eps, int M, int K,
+           uint16_t *h, int ldh, uint8_t *xq, float *sa, uint16_t *y, int ldy, int32_t *st, cudaStream_t stream) {
+    constexpr int kRows = TPR < 128 ? 128 / TPR : 1;
+    return launch_pdl("qspec_rmsnorm_fp8", rmsnorm_fp8_kernel<TPR, NV>, dim3((unsigned)((M + kRows - 1) / kRows)),
+                      dim3(TPR < 128 ? 128 : TPR), 0, stream, x, ldx, res, ldr, w, eps, M, K, h, ldh, xq, sa, y, ldy,
+                      st);
+}
+
+}  // namespace nrm
+
+}  // namespace
+
+}  // namespace qspec
+
+using namespace qspec;
+
+extern "C" int qspec_rmsnorm_fp8(const uint16_t *x_bf16, int ldx, const uint16_t *res_bf16, int ldr,
+                                 const uint16_t *w_bf16, float eps, int M, int K, uint16_t *h_bf16, int ldh,
+                                 uint8_t *xq, float *sa, uint16_t *y_bf16, int ldy, int32_t *dev_status,
+                                 qspec_stream_t stream) {
+    if (!x_bf16 || !w_bf16 || !xq || !sa || (res_bf16 != nullptr) != (h_bf16 != nullptr)) return QSPEC_ERR_NULL;
+    if (M < 1 || K < kGroup || K % kGroup || K > nrm::kMaxK || !(eps > 0.0f) || !std::isfinite(eps) || ldx < K ||
+        (res_bf16 && (ldr < K || ldh < K)) || (y_bf16 && ldy < K))
+        return QSPEC_ERR_SHAPE;
+    if (!aligned(x_bf16, 16) || !aligned(w_bf16, 16) || !aligned(xq, 8) || !aligned(sa, 4) || ldx % 8 ||
+        (res_bf16 && (!aligned(res_bf16, 16) || !aligned(h_bf16, 16) || ldr % 8 || ldh % 8)) ||
+        (y_bf16 && (!aligned(y_bf16, 16) || ldy % 8)))
+        return QSPEC_ERR_ALIGN;
+    int rc = check_device();
+    if (rc) return rc;
+    cudaStream_t s = as_cuda(stream);
+    auto go = [&](auto launcher) {
+        return launcher(x_bf16, ldx, res_bf16, ldr, w_bf16, eps, M, K, h_bf16, ldh, xq, sa, y_bf16, ldy, dev_status,
+                        s);
+    };
+    const int n8 = K / 8;
+    if (n8 <= 128) return go(nrm::launch<32, 4>);
+    if (n8 <= 512) return go(nrm::launch<256, 2>);
+    if (n8 <= 1024) return go(nrm::launch<512, 2>);
+    if (n8 <= 2048) return go(nrm::launch<1024, 2>);
+    return go(nrm::launch<1024, 4>);
+}
