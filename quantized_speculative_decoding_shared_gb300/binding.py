@@ -59,6 +59,8 @@ _lib = None
 def load_library(path: str | None = None) -> ctypes.CDLL:
     """Load libqspec.so and declare its prototypes.  Raises if it is missing."""
     global _lib
+    if _lib is not None and path is None:
+        return _lib
     with _lock:
         if _lib is not None and path is None:
             return _lib
@@ -117,15 +119,18 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
 
 
 def _ptr(t):
-    if t is None:
-        return None
-    return ctypes.c_void_p(t.data_ptr())
+    # a plain int: the declared argument types make it a pointer, and a
+    # c_void_p object per argument costs as much as the rest of a small call
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream):
     if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+        # the handle alone (building a torch.cuda.Stream object takes 3 us)
+        if not torch.cuda.is_initialized():
+            torch.cuda.init()
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _check(rc: int, where: str):
