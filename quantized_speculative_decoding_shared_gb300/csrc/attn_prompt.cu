@@ -1,13 +1,30 @@
-// attn_prompt.cu -- causal attention of packed prompts, grouped heads.
+// attn_prompt.cu -- causal attention of packed prompts, grouped heads, on the
+// Blackwell tensor cores.
 //
 //   a_ij = scale q_i . k_j for j <= i + Lk - Lq,  o_i = sum_j softmax(a_i)_j v_j
 //
-// First form: one CTA per (32 query rows of a sequence, query head), eight
-// rows per warp, key tiles of 32 rows in shared memory, running maximum and sum.
+// The Lq G query rows that read one KV head (row-major position, head of the
+// group minor) form one matrix, cut into tiles of 128 rows whatever G is; a CTA
+// takes two consecutive tiles, so each key tile of 128 rows is read once for 256
+// rows and both tiles end at nearly the same key.  Per key tile and row tile t:
+//   S_t = Q_t K^T (tcgen05, both operands in shared memory, S in tensor memory),
+//   the softmax warps of t read S_t (thread = row), keep a running reference m and
+//   sum l, and write p = 2^(c (s - m)) as bf16 over S_t in tensor memory,
+//   O_t += P_t V (P from tensor memory, V rows as they are: an MN-major operand).
+// The issuing lane interleaves the two tiles, so one tile's softmax runs under
+// the other's products.  m is only moved (and O_t rescaled, by the softmax
+// warps themselves) when a score passes it by more than 2^8: the completed
+// product S_t(i + 1) implies O_t += P_t(i) V has completed, so no other
+// synchronisation is needed for it.
+//
+// Bound: tensor cores (512 clocks per 128 x 128 tile at D = 128) with the exponentials
+// close behind (16384 per tile).
+#include <algorithm>
 #include <cmath>
 
 #include "qspec_device.cuh"
 #include "qspec_host.h"
+#include "umma.cuh"
 
 namespace qspec {
 
@@ -15,97 +32,433 @@ namespace {
 
 namespace apr {
 
-constexpr int kThreads = 128, kTile = 32, kRowsPerWarp = 8;
+constexpr int kTile = 128;                      // query rows per tile, keys per tile
+constexpr int kSoftmax = 256;                   // softmax threads: 128 per row tile
+constexpr int kMmaWarp = kSoftmax / 32, kTmaWarp = kMmaWarp + 1;
+constexpr int kThreads = kSoftmax + 64;
+constexpr uint32_t kCols = 512;                 // tensor memory: S0, S1 (128 columns each), O0, O1 (D each)
+constexpr uint32_t kS = 0, kO = 256;
+constexpr float kRescale = 8.0f;                // log2 of the largest p
 
 template <int D>
-__global__ void __launch_bounds__(kThreads)
-    simple_kernel(const uint16_t *__restrict__ q, int ldq, const uint16_t *__restrict__ k, int ldk,
-                  const uint16_t *__restrict__ v, int ldv, const int32_t *__restrict__ q_start,
-                  const int32_t *__restrict__ k_start, int q_rows, int k_rows, int B, int Hq, int H, float scale,
-                  uint16_t *__restrict__ o, int ldo, int32_t *st) {
+constexpr int tile_bytes() { return kTile * D * 2; }
+template <int D>
+constexpr int ring() { return D == 128 ? 4 : 8; }
+
+struct Ctl {
+    uint64_t full[8], empty[8];                 // K / V tiles: landed, read
+    uint64_t sfull[2], pfull[2], odone[2];      // S_t written, P_t written (and S_t read), O_t complete
+    uint64_t drain;
+    uint32_t tmem;
+    int timeout;
+    int unit[6];                                // b found, q0, lq, k0, lk, first flattened row
+};
+
+template <int D>
+constexpr size_t smem_total() { return 1024 + 2 * (size_t)tile_bytes<D>() + (size_t)ring<D>() * tile_bytes<D>() + sizeof(Ctl); }
+
+struct Args {
+    const uint16_t *q, *k, *v;
+    const int32_t *q_start, *k_start;
+    uint16_t *o;
+    int32_t *st;
+    int ldq, ldk, ldv, ldo, q_rows, k_rows, B, H, G;
+    float scale;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// K-major operand, 128-byte swizzle: 8 rows x 128 bytes per 1024-byte atom, the
+// row groups 1024 bytes apart (rows of 64 bf16; the next 64 one box further)
+__device__ __forceinline__ uint64_t desc_k(uint32_t saddr) {
+    return umma::smem_desc(saddr, 16, 1024) | ((uint64_t)2 << 61);
+}
+// MN-major operand (V as it lies: rows = K dimension), 128-byte swizzle: 64
+// values of the MN dimension per 128-byte row, the next 64 one box (kTile rows)
+// further, groups of 8 rows 1024 bytes apart
+__device__ __forceinline__ uint64_t desc_mn(uint32_t saddr) {
+    return umma::smem_desc(saddr, kTile * 128, 1024) | ((uint64_t)2 << 61);
+}
+
+// One row by a warp in the plain order, seen keys only: for rows whose result
+// is not finite.  A weight of 0 times a NaN or inf of an unseen key (a masked
+// place of the last key tiles) is the case that this mends.
+template <int D>
+__device__ __noinline__ void row_again(const Args &a, int h, const uint16_t *qrow, int k0, int lim, uint16_t *orow) {
     constexpr int E = D / 32;
-    __shared__ float sq[kTile][D], sk[kTile][D + 1];
-    __shared__ uint16_t sv[kTile][D];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, j = blockIdx.y, h = j / (Hq / H);
+    const int lane = threadIdx.x & 31;
+    float qv[E], acc[E], m = -INFINITY, l = 0.0f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        qv[e] = bf16_bits_to_float(qrow[lane * E + e]);
+        acc[e] = 0.0f;
+    }
+    for (int j = 0; j <= lim; ++j) {
+        const uint16_t *kr = a.k + (size_t)(k0 + j) * a.ldk + (size_t)h * D;
+        const uint16_t *vr = a.v + (size_t)(k0 + j) * a.ldv + (size_t)h * D;
+        float s = 0.0f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) s = fmaf(qv[e], bf16_bits_to_float(kr[lane * E + e]), s);
+#pragma unroll
+        for (int x = 16; x >= 1; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
+        s *= a.scale;
+        const float m1 = fmaxf(m, s), ref = m1 > -INFINITY ? m1 : 0.0f, f = expf(m - ref), p = expf(s - ref);
+        m = m1;
+        l = l * f + p;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = fmaf(p, bf16_bits_to_float(vr[lane * E + e]), acc[e] * f);
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) orow[lane * E + e] = float_to_bf16_bits(l == 0.0f ? 0.0f : acc[e] / l);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_prompt_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
+                       const __grid_constant__ Args a,
+                       uint32_t wait_limit) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    constexpr int kT = tile_bytes<D>(), NS = ring<D>();
+    uint8_t *sq = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *skv = sq + 2 * kT;
+    Ctl &sm = *reinterpret_cast<Ctl *>(skv + NS * kT);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int h = blockIdx.x % a.H, G = a.G;
+
+    if (warp == kMmaWarp) umma::tmem_alloc(&sm.tmem, kCols);
+    if (tid == 0) {
+        for (int s = 0; s < NS; ++s) {
+            umma::mbar_init(&sm.full[s], 1);
+            umma::mbar_init(&sm.empty[s], 1);
+        }
+        for (int t = 0; t < 2; ++t) {
+            umma::mbar_init(&sm.sfull[t], 1);
+            umma::mbar_init(&sm.pfull[t], kTile);
+            umma::mbar_init(&sm.odone[t], 1);
+        }
+        umma::mbar_init(&sm.drain, 1);
+        sm.timeout = 0;
+        sm.unit[0] = -1;
+        umma::mbar_fence_init();
+    }
     pdl_launch_dependents();
     pdl_wait();
-    // tile blockIdx.x of the sequences' 32-row tiles in order
-    int left = blockIdx.x, b = 0, q0 = 0, q1 = 0, k0 = 0, k1 = 0;
-    for (; b < B; ++b) {
-        q0 = q_start[b], q1 = q_start[b + 1], k0 = k_start[b], k1 = k_start[b + 1];
-        if (q0 < 0 || q1 < q0 || q1 > q_rows || k0 < 0 || k1 < k0 || k1 > k_rows) {
-            if (threadIdx.x == 0) flag(st, QSPEC_ERR_RANGE);
-            continue;
+    umma::fence_before_sync();
+    __syncthreads();
+    umma::fence_after_sync();
+    // this CTA's unit of 256 flattened rows: the sequences in order, each one's
+    // last (longest) unit first
+    if (warp == kTmaWarp) {
+        int left = blockIdx.x / a.H;
+        for (int b0 = 0; b0 < a.B && left >= 0; b0 += 32) {
+            const int b = b0 + lane;
+            int q0 = 0, lq = 0, k0 = 0, lk = 0;
+            bool bad = false;
+            if (b < a.B) {
+                const int q1 = a.q_start[b + 1], k1 = a.k_start[b + 1];
+                q0 = a.q_start[b];
+                k0 = a.k_start[b];
+                bad = q0 < 0 || q1 < q0 || q1 > a.q_rows || k0 < 0 || k1 < k0 || k1 > a.k_rows;
+                lq = bad ? 0 : q1 - q0;
+                lk = bad ? 0 : k1 - k0;
+            }
+            if (bad) flag(a.st, QSPEC_ERR_RANGE);
+            const int units = (int)(((long long)lq * G + 2 * kTile - 1) / (2 * kTile));
+            int upto = units;
+#pragma unroll
+            for (int x = 1; x < 32; x <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, upto, x);
+                if (lane >= x) upto += y;
+            }
+            if (left >= upto - units && left < upto) {
+                sm.unit[1] = q0;
+                sm.unit[2] = lq;
+                sm.unit[3] = k0;
+                sm.unit[4] = lk;
+                sm.unit[5] = units - 1 - (left - (upto - units));
+                sm.unit[0] = b;
+            }
+            const int total = __shfl_sync(0xffffffffu, upto, 31);
+            left = left < total ? -1 : left - total;
         }
-        const int tiles = (q1 - q0 + kTile - 1) / kTile;
-        if (left < tiles) break;
-        left -= tiles;
+        // the sequences that no CTA walks to are checked by the first one
+        if (blockIdx.x == 0)
+            for (int b = lane; b < a.B; b += 32)
+                if (a.q_start[b] < 0 || a.q_start[b + 1] < a.q_start[b] || a.q_start[b + 1] > a.q_rows ||
+                    a.k_start[b] < 0 || a.k_start[b + 1] < a.k_start[b] || a.k_start[b + 1] > a.k_rows)
+                    flag(a.st, QSPEC_ERR_RANGE);
     }
-    if (blockIdx.x == 0 && j == 0)                 // the sequences after this tile's are checked too
-        for (int c = threadIdx.x; c < B; c += kThreads)
-            if (q_start[c] < 0 || q_start[c + 1] < q_start[c] || q_start[c + 1] > q_rows || k_start[c] < 0 ||
-                k_start[c + 1] < k_start[c] || k_start[c + 1] > k_rows)
-                flag(st, QSPEC_ERR_RANGE);
-    if (b == B) return;
-    const int lq = q1 - q0, lk = k1 - k0, r0 = left * kTile;
-    for (int e = threadIdx.x; e < kTile * D; e += kThreads) {
-        const int i = e / D, d = e - i * D;
-        sq[i][d] = r0 + i < lq ? bf16_bits_to_float(q[(size_t)(q0 + r0 + i) * ldq + (size_t)j * D + d]) : 0.0f;
-    }
-    float m[kRowsPerWarp], l[kRowsPerWarp], acc[kRowsPerWarp][E];
-#pragma unroll
-    for (int i = 0; i < kRowsPerWarp; ++i) {
-        m[i] = -INFINITY;
-        l[i] = 0.0f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[i][e] = 0.0f;
-    }
-    const int end = min(lk, min(r0 + kTile, lq) + lk - lq);          // keys that any row of the tile sees
-    for (int t0 = 0; t0 < end; t0 += kTile) {
-        __syncthreads();
-        for (int e = threadIdx.x; e < kTile * D; e += kThreads) {
-            const int i = e / D, d = e - i * D;
-            const bool in = t0 + i < end;
-            sk[i][d] = in ? bf16_bits_to_float(k[(size_t)(k0 + t0 + i) * ldk + (size_t)h * D + d]) : 0.0f;
-            sv[i][d] = in ? v[(size_t)(k0 + t0 + i) * ldv + (size_t)h * D + d] : (uint16_t)0;
+    __syncthreads();
+    const uint32_t tmem = sm.tmem;
+    const bool work = sm.unit[0] >= 0;
+    const int q0 = sm.unit[1], lq = sm.unit[2], k0 = sm.unit[3], lk = sm.unit[4];
+    const long long row0 = (long long)sm.unit[5] * (2 * kTile), rows = (long long)lq * G;
+    const int off = lk - lq;
+    // key tiles that the unit's last row sees
+    const int p_last = work ? (int)((min(row0 + 2 * kTile, rows) - 1) / G) : 0;
+    const int n = work ? max(0, (p_last + off + kTile) / kTile) : 0;
+    const int nt = work && row0 + kTile < rows ? 2 : 1;     // row tiles with rows
+
+    int loads = 0;
+    bool issued = false;
+    auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
+        if (*reinterpret_cast<volatile int *>(&sm.timeout)) return false;
+        if (umma::mbar_wait(bar, parity, wait_limit)) return true;
+        *reinterpret_cast<volatile int *>(&sm.timeout) = 1;
+        return false;
+    };
+
+    // ---- Q tiles into shared memory (both operands' swizzle); a negative scale
+    // turns the signs, a zero one the values, so that the softmax has c > 0 ----
+    if (work && n > 0 && warp < kMmaWarp) {
+        const int t = warp >> 2, w = tid & (kTile - 1);
+        const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u, keep = a.scale != 0.0f ? 0xFFFFFFFFu : 0u;
+#pragma unroll 4
+        for (int it = 0; it < D / 8; ++it) {
+            const int e = it * kTile + w, r = e / (D / 8), ch = e % (D / 8);
+            const long long idx = row0 + t * kTile + r;
+            uint4 x = make_uint4(0, 0, 0, 0);
+            if (idx < rows) {
+                const int p = (int)(idx / G), g = (int)(idx - (long long)p * G);
+                x = *reinterpret_cast<const uint4 *>(a.q + (size_t)(q0 + p) * a.ldq + (size_t)(h * G + g) * D + ch * 8);
+            }
+            x = make_uint4((x.x ^ flip) & keep, (x.y ^ flip) & keep, (x.z ^ flip) & keep, (x.w ^ flip) & keep);
+            *reinterpret_cast<uint4 *>(sq + t * kT + (ch >> 3) * (kTile * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = x;
         }
-        __syncthreads();
+        umma::fence_proxy_async();
+    }
+    // the first tiles' copies go out before the Q tiles are complete
+    if (warp == kTmaWarp && lane == 0 && n > 0) {
+        const int pre = min(2 * n, NS);
+        for (int i = 0; i < pre; ++i) {
+            umma::mbar_arrive_expect_tx(&sm.full[i], kT);
 #pragma unroll
-        for (int i = 0; i < kRowsPerWarp; ++i) {
-            const int r = warp * kRowsPerWarp + i, seen = r0 + r + lk - lq + 1;   // keys 0 .. seen - 1
-            float a = 0.0f;
-#pragma unroll 16
-            for (int d = 0; d < D; ++d) a = fmaf(sq[r][d], sk[lane][d], a);
-            a = t0 + lane < min(seen, end) ? a * scale : -INFINITY;
-            float mt = a;
+            for (int c = 0; c < D / 64; ++c)
+                umma::tma_load_2d(skv + i * kT + c * (kTile * 128), (i & 1) ? &tv : &tk, (h * D + 64 * c) * 2,
+                                  k0 + (i >> 1) * kTile, &sm.full[i]);
+        }
+        loads = pre;
+    }
+    umma::fence_before_sync();
+    __syncthreads();
+    umma::fence_after_sync();
+
+    if (n > 0 && warp == kTmaWarp) {
+        if (lane == 0) {
+            for (int i = loads; i < 2 * n; ++i) {                      // K_0, V_0, K_1, V_1, ...
+                const int s = i % NS;
+                if (!wait(&sm.empty[s], (uint32_t)((i / NS + 1) & 1))) break;
+                umma::mbar_arrive_expect_tx(&sm.full[s], kT);
 #pragma unroll
-            for (int x = 16; x >= 1; x >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, x));
-            const float m1 = fmaxf(m[i], mt);
-            const float ref = m1 > -INFINITY ? m1 : 0.0f;
-            const float f = expf(m[i] - ref), p = expf(a - ref);
-            float ps = p;
+                for (int c = 0; c < D / 64; ++c)
+                    umma::tma_load_2d(skv + s * kT + c * (kTile * 128), (i & 1) ? &tv : &tk, (h * D + 64 * c) * 2,
+                                      k0 + (i >> 1) * kTile, &sm.full[s]);
+                loads = i + 1;
+            }
+        }
+    } else if (n > 0 && warp == kMmaWarp) {
+        if (lane == 0) {
+            constexpr uint32_t id_s = umma::instr_desc(1, 1, kTile, kTile);
+            constexpr uint32_t id_o = umma::instr_desc(1, 1, kTile, D) | (1u << 16);      // B is MN-major
+            const uint32_t q_addr = umma::smem_addr(sq), kv_addr = umma::smem_addr(skv);
+            auto scores = [&](int t, int i) {                           // S_t = Q_t K_i^T
+                const uint64_t ad = desc_k(q_addr + t * kT), bd = desc_k(kv_addr + ((2 * i) % NS) * kT);
 #pragma unroll
-            for (int x = 16; x >= 1; x >>= 1) ps += __shfl_xor_sync(0xffffffffu, ps, x);
-            m[i] = m1;
-            l[i] = l[i] * f + ps;
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t step = (uint32_t)((kk >> 2) * (kTile * 128) + (kk & 3) * 32) >> 4;
+                    umma::mma_bf16(tmem + kS + t * kTile, ad + step, bd + step, id_s, kk != 0);
+                }
+                umma::mma_commit(&sm.sfull[t]);
+            };
+            bool ok = wait(&sm.full[0], 0);
+            if (ok) {
+                umma::fence_after_sync();
+                for (int t = 0; t < nt; ++t) scores(t, 0);
+                umma::mma_commit(&sm.empty[0]);
+                issued = true;
+            }
+            for (int i = 0; i < n && ok; ++i) {
+                const int sv = (2 * i + 1) % NS, sk = (2 * i + 2) % NS;
+                const bool more = i + 1 < n;
+                ok = wait(&sm.full[sv], (uint32_t)(((2 * i + 1) / NS) & 1)) &&
+                     (!more || wait(&sm.full[sk], (uint32_t)(((2 * i + 2) / NS) & 1)));
+                for (int t = 0; t < nt && ok; ++t) {
+                    if (!(ok = wait(&sm.pfull[t], (uint32_t)(i & 1)))) break;
+                    umma::fence_after_sync();
+                    const uint64_t bd = desc_mn(kv_addr + sv * kT);
 #pragma unroll
-            for (int e = 0; e < E; ++e) acc[i][e] *= f;
-            for (int t = 0; t < min(kTile, min(seen, end) - t0); ++t) {
-                const float pt = __shfl_sync(0xffffffffu, p, t);
+                    for (int kk = 0; kk < kTile / 16; ++kk)             // 16 keys: 2 groups of 8 rows
+                        umma::mma_bf16_ta(tmem + kO + t * kTile, tmem + kS + t * kTile + kk * 8, bd + (kk * 2048 >> 4), id_o,
+                                          (i | kk) != 0);
+                    if (t == nt - 1) umma::mma_commit(&sm.empty[sv]);
+                    if (more) {
+                        scores(t, i + 1);
+                        if (t == nt - 1) umma::mma_commit(&sm.empty[sk]);
+                    } else {
+                        umma::mma_commit(&sm.odone[t]);
+                    }
+                }
+            }
+        }
+    } else if (work && warp < kMmaWarp && (warp >> 2) < nt) {
+        const int t = warp >> 2;
+        const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+        const uint32_t ts = tmem + lanes + kS + t * kTile, to = tmem + lanes + kO + t * kTile;
+        const long long idx = row0 + t * kTile + (warp & 3) * 32 + lane;
+        const bool in = idx < rows;
+        const int p = in ? (int)(idx / G) : 0, g = in ? (int)(idx - (long long)p * G) : 0;
+        const int lim = in ? p + off : -1;                              // last key seen
+        // tiles from here on are masked for some row of the tile
+        const int first_masked = (int)((row0 + t * kTile) / G) + off;
+        const float c = a.scale != 0.0f ? fabsf(a.scale) * 1.4426950408889634f : 1.0f;
+        float m = -INFINITY, l = 0.0f;
+        bool ok = true;
+        for (int i = 0; i < n; ++i) {
+            // (the vote keeps the warp together where a wait runs out)
+            if (!(ok = __all_sync(0xffffffffu, wait(&sm.sfull[t], (uint32_t)(i & 1))))) break;
+            umma::fence_after_sync();
+            uint32_t s[4][32];
 #pragma unroll
-                for (int e = 0; e < E; ++e) acc[i][e] = fmaf(pt, bf16_bits_to_float(sv[t][lane + 32 * e]), acc[i][e]);
+            for (int x = 0; x < 4; ++x) umma::tmem_ld32(ts + 32 * x, s[x]);
+            umma::tmem_ld_wait();
+            if (i * kTile + kTile - 1 > first_masked || !in) {
+                const int seen = lim - i * kTile;                       // columns 0 .. seen
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+#pragma unroll
+                    for (int y = 0; y < 32; ++y)
+                        if (32 * x + y > seen) s[x][y] = 0xFF800000u;
+            }
+            float mx[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                mx[x] = __uint_as_float(s[x][0]);
+#pragma unroll
+                for (int y = 1; y < 32; ++y) mx[x] = fmaxf(mx[x], __uint_as_float(s[x][y]));
+            }
+            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+            if (i == 0) {
+                m = top > -INFINITY ? top : 0.0f;
+            } else {
+                const bool move = (top - m) * c > kRescale;
+                if (__any_sync(0xffffffffu, move)) {                    // O_t is complete up to tile i - 1
+                    const float f = move ? ex2((m - top) * c) : 1.0f;
+                    if (move) m = top;
+                    l *= f;
+#pragma unroll
+                    for (int x = 0; x < D / 32; ++x) {
+                        uint32_t o[32];
+                        umma::tmem_ld32(to + 32 * x, o);
+                        umma::tmem_ld_wait();
+#pragma unroll
+                        for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+                        umma::tmem_st32(to + 32 * x, o);
+                    }
+                }
+            }
+            const float mc = -m * c;
+            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                uint32_t w[32];
+#pragma unroll
+                for (int y = 0; y < 32; ++y) {
+                    const float p0 = ex2(fmaf(__uint_as_float(s[2 * x + (y >> 4)][(2 * y) & 31]), c, mc));
+                    const float p1 = ex2(fmaf(__uint_as_float(s[2 * x + (y >> 4)][(2 * y + 1) & 31]), c, mc));
+                    sum[y & 1] += p0;
+                    sum[2 + (y & 1)] += p1;
+                    w[y] = pack_bf16(p0, p1);
+                }
+                umma::tmem_st32(ts + 32 * x, w);
+            }
+            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            umma::tmem_st_wait();
+            umma::fence_before_sync();
+            umma::mbar_arrive(&sm.pfull[t]);
+        }
+        // ---- epilogue: o = O / l ----
+        if (ok && n > 0) ok = __all_sync(0xffffffffu, wait(&sm.odone[t], 0));
+        if (ok) {
+            umma::fence_after_sync();
+            const size_t head = (size_t)(h * G + g) * D;
+            uint16_t *orow = a.o + (size_t)(q0 + p) * a.ldo + head;
+            const float inv = lim >= 0 ? 1.0f / l : 0.0f;
+            bool fine = true;
+#pragma unroll
+            for (int x = 0; x < D / 32; ++x) {
+                uint32_t o[32];
+                if (n > 0) {
+                    umma::tmem_ld32(to + 32 * x, o);
+                    umma::tmem_ld_wait();
+                }
+                uint32_t w[16];
+#pragma unroll
+                for (int y = 0; y < 16; ++y) {
+                    const float o0 = lim >= 0 ? __uint_as_float(o[2 * y]) * inv : 0.0f;
+                    const float o1 = lim >= 0 ? __uint_as_float(o[2 * y + 1]) * inv : 0.0f;
+                    fine = fine && isfinite(o0) && isfinite(o1);
+                    w[y] = pack_bf16(o0, o1);
+                }
+                if (in)
+#pragma unroll
+                    for (int y = 0; y < 4; ++y)
+                        reinterpret_cast<uint4 *>(orow + 32 * x)[y] = make_uint4(w[4 * y], w[4 * y + 1], w[4 * y + 2], w[4 * y + 3]);
+            }
+            uint32_t again = __ballot_sync(0xffffffffu, in && !fine);
+            while (again) {
+                const int who = __ffs(again) - 1;
+                again &= again - 1;
+                const int pw = __shfl_sync(0xffffffffu, p, who), gw = __shfl_sync(0xffffffffu, g, who);
+                const size_t hw = (size_t)(h * G + gw) * D;
+                __syncwarp();
+                row_again<D>(a, h, a.q + (size_t)(q0 + pw) * a.ldq + hw, k0, pw + off, a.o + (size_t)(q0 + pw) * a.ldo + hw);
             }
         }
     }
-#pragma unroll
-    for (int i = 0; i < kRowsPerWarp; ++i) {
-        const int r = r0 + warp * kRowsPerWarp + i;
-        if (r >= lq) continue;
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-            o[(size_t)(q0 + r) * ldo + (size_t)j * D + lane + 32 * e] =
-                float_to_bf16_bits(l[i] > 0.0f ? acc[i][e] / l[i] : 0.0f);
+
+    // after a timeout: copies and products in flight finish (bounded) before
+    // the memory is released
+    __syncthreads();
+    if (sm.timeout) {
+        if (warp == kTmaWarp && lane == 0)
+            for (int i = max(0, loads - NS); i < loads; ++i)
+                umma::mbar_wait(&sm.full[i % NS], (uint32_t)((i / NS) & 1), kWaitLimit);
+        if (warp == kMmaWarp && lane == 0 && issued) {
+            umma::mma_commit(&sm.drain);
+            umma::mbar_wait(&sm.drain, 0, kWaitLimit);
+        }
+        if (tid == 0) flag(a.st, QSPEC_ERR_TIMEOUT);
     }
+    umma::fence_before_sync();
+    __syncthreads();
+    if (warp == kMmaWarp) umma::tmem_free(tmem, kCols);
+}
+
+template <int D>
+int launch(const Args &a, cudaStream_t stream) {
+    const long long units = (long long)a.q_rows * a.G / (2 * kTile) + a.B;
+    if (units * a.H >= (1LL << 31)) return QSPEC_ERR_SHAPE;
+    // no key rows: no copy is issued, and the maps only have to be valid
+    const bool none = a.k_rows == 0;
+    CUtensorMap tk, tv;
+    const int cols = (none ? a.H * a.G : a.H) * D * 2;
+    if (byte_tmap_sw128(&tk, none ? a.q : a.k, none ? a.q_rows : a.k_rows, cols, (size_t)(none ? a.ldq : a.ldk) * 2, kTile) ||
+        byte_tmap_sw128(&tv, none ? a.q : a.v, none ? a.q_rows : a.k_rows, cols, (size_t)(none ? a.ldq : a.ldv) * 2, kTile))
+        return QSPEC_ERR_UNSUPPORTED;
+    auto kern = attn_prompt_kernel<D>;
+    int rc = smem_limit_once(reinterpret_cast<const void *>(kern), (int)smem_total<D>());
+    if (rc) return rc;
+    return launch_pdl("qspec_attn_prompt", kern, dim3((unsigned)(units * a.H)), dim3(kThreads), smem_total<D>(), stream, tk,
+                      tv, a, kWaitLimit);
 }
 
 }  // namespace apr
@@ -131,10 +484,7 @@ extern "C" int qspec_attn_prompt(const uint16_t *q_bf16, int ldq, const uint16_t
         return QSPEC_ERR_ALIGN;
     int rc = check_device();
     if (rc || q_rows == 0) return rc;
-    const long long tiles = (long long)q_rows / apr::kTile + B;
-    if (tiles >= (1LL << 31)) return QSPEC_ERR_SHAPE;
-    auto kern = D == 128 ? apr::simple_kernel<128> : apr::simple_kernel<64>;
-    return launch_pdl("qspec_attn_prompt", kern, dim3((unsigned)tiles, (unsigned)Hq), dim3(apr::kThreads), 0,
-                      as_cuda(stream), q_bf16, ldq, k_bf16, ldk, v_bf16, ldv, q_start, k_start, q_rows, k_rows, B, Hq,
-                      H, scale, o_bf16, ldo, dev_status);
+    const apr::Args a{q_bf16, k_bf16, v_bf16, q_start, k_start, o_bf16, dev_status, ldq, ldk, ldv,
+                      ldo,    q_rows, k_rows, B,       H,       Hq / H, scale};
+    return D == 128 ? apr::launch<128>(a, as_cuda(stream)) : apr::launch<64>(a, as_cuda(stream));
 }
