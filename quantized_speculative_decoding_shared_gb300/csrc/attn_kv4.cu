@@ -1,37 +1,52 @@
 // attn_kv4.cu -- attention of the newest rows of every sequence over the 4-bit
-// KV cache (draft steps and verify passes).
+// KV cache (draft steps and verify passes), on the Blackwell tensor cores.
 //
 //   a_t = scale s_t (sum_d q_d c_td - z_t sum_d q_d),  p = softmax(a),
 //   o = sum_t p_t s_t (c_t - z_t)
 //
-// The R G query rows that read one KV head are taken together, kRows = 8 NT of
-// them per pass.  Products run as warp MMAs with the cache on the row side,
-// 16 positions by 8 query rows, so that few query rows waste little:
-//   S^T (positions x rows) = K Q^T:  a K word's eight codes become four bf16
-//     pairs 128 + c by a shift and one logic operation each (the order of d is
-//     free: Q is permuted the same way once), and (128 + z) sum q is taken off
-//     the fp32 sum;
-//   O^T (d x rows) += V^T P^T:  V's codes of two positions side by side, minus
-//     (128 + z) exactly in bf16; P^T = p s is S^T's fragment transposed 8 x 8.
-// Codes and scale words come through a ring of cp.async stages that each warp
-// keeps for itself: no barrier between warps inside a segment.  The
-// softmax reference m moves only when a score passes it by more than 2^8.
+// The R G query rows that read one KV head are taken together, N (16, 32 or 64)
+// of them per pass, as the narrow side of the products; 128 cache positions are
+// the wide one:
+//   S^T (positions x rows) = K Q^T in fp16: a code c in the low bits of an fp16
+//     lane IS the number c 2^-24 (a subnormal), one nibble higher 16 c 2^-24, so eight
+//     codes take one shift and four ANDs on their way into tensor memory (thread
+//     = position).  Each row of Q is scaled by a power of two to at most 2^15
+//     (exact: bf16 has 8 bits, fp16 11, and what falls below 2^-24 is below 2^-39
+//     of the row's largest), in the order of d that the unpacked codes have, times 1/16
+//     against 16 c.  z enters as one more K step: z against -sum q in three fp16 parts.
+//   O^T (d x rows) += V^T P^T in bf16: V's codes as 128 + c by one logic operation, minus
+//     (128 + z) exactly; P^T = p s with the range of fp32 (in fp16 the weights of
+//     far positions would round to subnormals).  Both operands lie in shared memory
+//     position by position, an MN-major layout without swizzle: 16-byte pieces of
+//     consecutive positions side by side.
+// Three groups of four warps take the tiles in turn (thread = position: unpack K,
+// unpack V while S^T is formed, then the softmax); one lane issues the products of
+// S^T, one those of O^T (each waits for its own operands, so that the tensor cores
+// have the other's meanwhile: at these widths a product takes some 55 clocks
+// whatever N is, 17 of them a tile), one the copies.
+//
+// The softmax reference of a row is its score at the segment's first position, and stays:
+// p, its sum and O are floating point and lose nothing while no score passes
+// it by 2^96.  A segment where one does is taken again by a plain path.
 //
 // Work is split by the lengths on the device: all (sequence, head, row block)
-// tasks, cut into chunks of 64 positions, are laid end to end and every CTA
+// tasks, cut into tiles of 128 positions, are laid end to end and every CTA
 // takes an equal share.  A task that several CTAs share is joined by the last
 // of them to finish, in the order of the parts, so that the bits do not
 // depend on who is last.
 //
-// Bound: HBM for one row tile (D / 2 + 4 bytes per position, head and side);
-// with more rows the warp MMAs and the integer work of unpacking.
+// Bound: HBM (D / 2 + 4 bytes per position, head and side) and, close to it, the
+// issue slots of unpacking (about 0.1 warp instructions per code) and of N scores
+// per position.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include <cuda_fp16.h>
 
 #include "qspec_device.cuh"
 #include "qspec_host.h"
+#include "umma.cuh"
 
 namespace qspec {
 
@@ -40,28 +55,46 @@ namespace {
 namespace akv {
 
 constexpr int kMaxR = QSPEC_MAX_GAMMA + 1;
-constexpr int kWarps = 4, kThreads = kWarps * 32;
-constexpr int kTile = 16;                       // positions per MMA tile
-constexpr int kChunk = kWarps * kTile;          // positions per unit of work
-constexpr int kMaxSms = 160;
-constexpr float kNone = -1.0e30f;               // running reference before any score
-constexpr float kMove = 8.0f;                   // log2 of the largest p
+constexpr int kTok = 128;                       // positions per tile
+constexpr int kGroups = 3, kWorkWarps = 4 * kGroups, kWork = 32 * kWorkWarps;
+constexpr int kScoreWarp = kWorkWarps, kValueWarp = kScoreWarp + 1, kLoadWarp = kValueWarp + 1;   // one lane each: S^T, O^T products, copies
+constexpr int kThreads = kWork + 96;
+constexpr int kMaxCtas = 160;                   // one per SM
+constexpr int kMaxN = 64, kMaxD = 128;
+constexpr float kNone = -1.0e30f;               // log2 of the sum of a row that sees nothing
+constexpr float kOver = 7.9228162514264338e28f; // 2^96: a thread's sum of p from where a segment is taken again
 
-// CTAs per SM (registers: the O^T accumulators are 4 NT D / 16 per thread)
-template <int NT>
-constexpr int per_sm() { return NT == 1 ? 4 : NT == 2 ? 3 : 2; }
-constexpr int kMaxCtas = kMaxSms * 4;
-constexpr int kMaxRowsPerSm = 2 * 32;           // max over NT of per_sm * 8 NT
-constexpr int kMaxD = 128;
-
+constexpr int kStages = 3;                      // tiles of codes in flight
+constexpr int kVBuf = kTok * kMaxD * 2;         // V operand (D = 64: the products' rows 64 .. 127 read the rest, unused)
 template <int D>
-constexpr int stage_bytes() { return 2 * kTile * (D / 2) + 2 * kTile * 4; }
-constexpr int kStages = 6;
-template <int D, int NT>
+constexpr int side_bytes() { return kTok * D / 2; }
+template <int N>
+constexpr int p_bytes() { return kTok * N * 2; }
+template <int D, int N>
+constexpr int q_bytes() { return N * (D + 16) * 2; }
+
+struct Join {                                   // a task to join: its parts (0: nothing to do)
+    int parts, c0, nq, b, task;
+};
+
+template <int N>
+struct Ctl {
+    uint64_t full[kStages], empty[kStages];     // codes landed; unpacked
+    uint64_t kfull[kGroups], sfull[kGroups], pfull[kGroups], vfull[kGroups], pdone[kGroups];   // K in tensor memory, S^T, P^T, V, O^T += done
+    uint64_t qfull, ref, odone, drain[2];       // per segment: Q written, reference known, O^T complete
+    float4 back[N / 2];                         // score of rows n, n + 1: {back, back'}({s u - ref, s u' - ref'}), as {back, back', -ref, -ref'}
+    float lse[N], inv[N];
+    float lsum[kWorkWarps][N];
+    long long orow[N];                          // the rows' places in q and o
+    int seen[N];                                // positions that a row sees
+    uint32_t tmem;
+    int timeout, over;
+    Join join[2];                               // the task that the CTA continues, the one that it begins
+};
+
+template <int D, int N>
 constexpr size_t smem_bytes() {
-    // the ring, and over it at the end of a segment the warps' O (rows padded by 4)
-    return std::max((size_t)kWarps * kStages * stage_bytes<D>(), (size_t)kWarps * 8 * NT * (D + 4) * 4) +
-           (size_t)kWarps * 8 * NT * 2 * 4;
+    return 1024 + (size_t)kStages * 2 * side_bytes<D>() + kGroups * kVBuf + kGroups * p_bytes<N>() + q_bytes<D, N>() + sizeof(Ctl<N>);
 }
 
 struct Args {
@@ -74,7 +107,10 @@ struct Args {
     int *count;                                  // [kMaxCtas] arrivals at the task that a CTA begins
     float *part;                                 // partial results, two slots per CTA
     int ldq, ldo, B, R, G, H, T, blocks;         // blocks: row blocks per (sequence, head)
+    uint32_t g_mul;                              // n / G = umulhi(n, g_mul) for n < 17 G (G = 1: 0)
     float scale;
+
+    __device__ __forceinline__ int row_r(int n) const { return g_mul ? (int)__umulhi((uint32_t)n, g_mul) : n; }
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -87,79 +123,195 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
-__device__ __forceinline__ uint32_t bf2_sub(uint32_t a, uint32_t b) {
-    __nv_bfloat162 r = __hsub2(*reinterpret_cast<__nv_bfloat162 *>(&a), *reinterpret_cast<__nv_bfloat162 *>(&b));
-    return *reinterpret_cast<uint32_t *>(&r);
+__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
 }
-__device__ __forceinline__ uint32_t code_pair(uint32_t w, int i) {   // bf16 pair 128 + (nibble i of each half)
-    return ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
+// two fp32 values in a register pair, and the packed operations on them
+__device__ __forceinline__ uint64_t f2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float lo32(uint64_t v) { return __uint_as_float((uint32_t)v); }
+__device__ __forceinline__ float hi32(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
 }
 __device__ __forceinline__ float lo_half(uint32_t w) { return __half2float(__ushort_as_half((uint16_t)(w & 0xFFFFu))); }
 __device__ __forceinline__ float hi_half(uint32_t w) { return __half2float(__ushort_as_half((uint16_t)(w >> 16))); }
-// 128 + z; the clamp keeps a bad word at an unseen place from reaching the
-// rows that do not see it as NaN (0 times NaN)
-__device__ __forceinline__ float zero_point(uint32_t w) { return 128.0f + fminf(fmaxf(hi_half(w), 0.0f), 15.0f); }
 
-__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                    uint32_t b1) {
+__device__ __forceinline__ void tma_load_3d(void *dst, const void *tmap, int x, int y, int z, uint64_t *bar) {
     asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n" ::
+            "r"(umma::smem_addr(dst)),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(umma::smem_addr(bar))
+        : "memory");
 }
-__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
-    uint32_t y;
-    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
-    return y;
+__device__ __forceinline__ void bar_sync(int id, int threads) {
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
-__device__ __forceinline__ uint32_t saddr(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool in) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+// the 16-byte piece c of position t in a tile of codes as the copy left it: rows of 64 bytes in
+// the 64-byte swizzle, rows of 32 bytes in the 32-byte one
+template <int D>
+__device__ __forceinline__ uint4 code_piece(const uint8_t *side, int t, int c) {
+    if constexpr (D == 128) return *reinterpret_cast<const uint4 *>(side + t * 64 + ((c ^ ((t >> 1) & 3)) << 4));
+    return *reinterpret_cast<const uint4 *>(side + t * 32 + ((c ^ ((t >> 2) & 1)) << 4));
 }
-__device__ __forceinline__ void copy4(uint32_t dst, const void *src, bool in) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(in ? 4 : 0) : "memory");
+// d of place x of an operand's piece of eight: the order that unpacking gives
+__device__ __forceinline__ int place_d(int x) { return (x >> 1) | ((x & 1) << 2); }
+
+// Sums over the warp's lanes of v[0 .. N - 1]: lane i gets the sum of v[(N / 32) i ..] (N / 32
+// values), or for N = 16 of v[i / 2].  Each exchange halves the values a lane still carries.
+template <int N>
+__device__ __forceinline__ void lane_sums(float (&v)[N], int lane) {
+    constexpr int kLast = N >= 32 ? N / 32 : 1;
+#pragma unroll
+    for (int o = 16, k = N; o >= 1; o >>= 1) {
+        if (k > kLast) {
+            k >>= 1;
+#pragma unroll
+            for (int i = 0; i < N / 2; ++i)
+                if (i < k) {
+                    const bool up = lane & o;
+                    const float give = up ? v[i] : v[i + k], keep = up ? v[i + k] : v[i];
+                    v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+                }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kLast; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+        }
+    }
 }
 
-// MMA row of position x (0..15) of a tile: rows 2 i, 2 i + 1, 8 + 2 i, 9 + 2 i are
-// positions i, 4 + i, 8 + i, 12 + i, which spreads a thread's V rows over the banks
-__device__ __forceinline__ int mma_row(int x) { return (x & 8) | ((x & 3) << 1) | ((x >> 2) & 1); }
+// A row over positions [p0, p1) in the plain order by one warp; o normalised.  Returns log2 of
+// the sum of exponentials.
+template <int D>
+__device__ __noinline__ float plain_row(const Args &a, const uint16_t *qrow, size_t head, int p0, int p1, float (&o)[D / 32]) {
+    constexpr int E = D / 32;
+    const int lane = threadIdx.x & 31;
+    float qv[E], m = -INFINITY, l = 0.0f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        qv[e] = bf16_bits_to_float(qrow[lane * E + e]);
+        o[e] = 0.0f;
+    }
+    for (int t = p0; t < p1; ++t) {
+        const uint32_t kw = __ldg(a.ks + head + t), vw = __ldg(a.vs + head + t);
+        const float ks = lo_half(kw), kz = hi_half(kw), vs = lo_half(vw), vz = hi_half(vw);
+        float s = 0.0f, v[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const int d = lane * E + e, sh = 4 * (d & 1);
+            const size_t at = (head + t) * (D / 2) + d / 2;
+            s = fmaf(qv[e], (float)((a.kc[at] >> sh) & 15) - kz, s);
+            v[e] = vs * ((float)((a.vc[at] >> sh) & 15) - vz);
+        }
+#pragma unroll
+        for (int x = 16; x >= 1; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
+        s *= ks * a.scale * 1.4426950408889634f;
+        const float m1 = fmaxf(m, s), ref = m1 > -INFINITY ? m1 : 0.0f, f = ex2(m - ref), p = ex2(s - ref);
+        m = m1;
+        l = l * f + p;
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = fmaf(p, v[e], o[e] * f);
+    }
+    if (l == 0.0f) return kNone;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] /= l;
+    return m + log2f(l);
+}
 
-template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, per_sm<NT>()) attn_kv4_kernel(const __grid_constant__ Args a) {
-    constexpr int kRows = 8 * NT;
-    constexpr int kWords = D / 32;              // K words per thread and position, V words x 2 ... (D / 64)
-    constexpr int kSteps = D / 16;              // MMA steps of S, and 16-row tiles of O^T
-    constexpr int kStage = stage_bytes<D>(), kSide = kTile * (D / 2);
-    extern __shared__ __align__(16) uint8_t smem[];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g8 = lane >> 2, t4 = lane & 3;
-    uint8_t *ring = smem + (size_t)warp * kStages * kStage;
-    float *so = reinterpret_cast<float *>(smem);                                   // [warp][row][D + 4]
-    float *sml = reinterpret_cast<float *>(smem + smem_bytes<D, NT>()) - kWarps * kRows * 2;   // [warp][row]{m, l}
-    __shared__ int last_flag;
+template <int D, int N>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_kv4_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
+                    const __grid_constant__ Args a, uint32_t wait_limit) {
+    constexpr int kSide = side_bytes<D>(), kP = p_bytes<N>();
+    constexpr int kSteps = D / 16;                               // MMA steps of S^T (one more holds z)
+    constexpr uint32_t cS = 0, cK = kGroups * N, cO = cK + kGroups * 80;   // the groups' S^T and K operands (80 columns each), O^T
+    constexpr uint32_t kCols = 512;
+    static_assert(cO + N <= kCols, "tensor memory");
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    // (an offset, not a rounded address: the compiler keeps seeing shared memory)
+    uint8_t *codes = smem_raw + ((1024u - (umma::smem_addr(smem_raw) & 1023u)) & 1023u);
+    uint8_t *sv = codes + kStages * 2 * kSide, *sp = sv + kGroups * kVBuf, *sq = sp + kGroups * kP;
+    Ctl<N> &sm = *reinterpret_cast<Ctl<N> *>(sq + q_bytes<D, N>());
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
+    if (warp == kScoreWarp) umma::tmem_alloc(&sm.tmem, kCols);
+    if (tid == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            umma::mbar_init(&sm.full[s], 1);
+            umma::mbar_init(&sm.empty[s], 4);
+        }
+        for (int s = 0; s < kGroups; ++s) {
+            umma::mbar_init(&sm.kfull[s], 4);
+            umma::mbar_init(&sm.sfull[s], 1);
+            umma::mbar_init(&sm.pfull[s], 4);
+            umma::mbar_init(&sm.vfull[s], 4);
+            umma::mbar_init(&sm.pdone[s], 1);
+        }
+        umma::mbar_init(&sm.qfull, kWorkWarps);
+        umma::mbar_init(&sm.ref, 1);
+        umma::mbar_init(&sm.odone, 1);
+        umma::mbar_init(&sm.drain[0], 1);
+        umma::mbar_init(&sm.drain[1], 1);
+        sm.timeout = 0;
+        sm.over = 0;
+        sm.join[0].parts = sm.join[1].parts = 0;
+        umma::mbar_fence_init();
+    }
     pdl_launch_dependents();
     pdl_wait();
-    // ---- this CTA's share of the chunks (every warp finds it for itself) ----
-    const int tasks = a.H * a.blocks;           // per sequence
-    auto chunks_of = [&](int b) -> int {
-        const int n = __ldg(a.len + b);
-        return n < 0 || n > a.T ? 0 : max(1, (n + kChunk - 1) / kChunk);
+    umma::fence_before_sync();
+    __syncthreads();
+    umma::fence_after_sync();
+    const uint32_t tmem = sm.tmem;
+    // A wait that runs out is remembered; from then on no wait waits and nothing
+    // more is issued, and every warp walks to the end past the same barriers.
+    auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
+        if (umma::mbar_try_wait(bar, parity & 1)) return true;
+        if (*reinterpret_cast<volatile int *>(&sm.timeout)) return false;
+        if (umma::mbar_wait(bar, parity & 1, wait_limit)) return true;
+        *reinterpret_cast<volatile int *>(&sm.timeout) = 1;
+        return false;
     };
+
+    // ---- this CTA's share of the tiles (every warp finds it for itself) ----
+    const int tasks = a.H * a.blocks;           // per sequence
+    auto tiles_of = [&](int b) -> int {
+        const int n = __ldg(a.len + b);
+        return n < 0 || n > a.T ? 0 : max(1, (n + kTok - 1) / kTok);
+    };
+    const int mine = lane < a.B ? tiles_of(lane) : 0;            // the first 32 sequences', kept
     long long total = 0;
     for (int b0 = 0; b0 < a.B; b0 += 32) {
-        const int c = b0 + lane < a.B ? chunks_of(b0 + lane) : 0;
-        if (blockIdx.x == 0 && b0 + lane < a.B && c == 0) flag(a.st, QSPEC_ERR_RANGE);
+        const int c = b0 == 0 ? mine : b0 + lane < a.B ? tiles_of(b0 + lane) : 0;
+        if (blockIdx.x == 0 && warp == 0 && b0 + lane < a.B && c == 0) flag(a.st, QSPEC_ERR_RANGE);
         total += __reduce_add_sync(0xffffffffu, c);
     }
     total *= tasks;
     const long long nc = min((long long)gridDim.x, total);
-    if (blockIdx.x >= nc) return;
-    long long at = blockIdx.x * total / nc;
-    const long long end = (blockIdx.x + 1) * total / nc;
+    const bool any = blockIdx.x < nc;
+    long long at = any ? blockIdx.x * total / nc : 0;
+    const long long end = any ? (blockIdx.x + 1) * total / nc : 0;
     int b = 0;
-    long long prefix = 0;                        // items before sequence b
-    for (int b0 = 0; b0 < a.B; b0 += 32) {
-        const int c = b0 + lane < a.B ? chunks_of(b0 + lane) : 0;
+    long long prefix = 0;                        // tiles before sequence b
+    for (int b0 = 0; b0 < a.B && any; b0 += 32) {
+        const int c = b0 == 0 ? mine : b0 + lane < a.B ? tiles_of(b0 + lane) : 0;
         int upto = c;
 #pragma unroll
         for (int x = 1; x < 32; x <<= 1) {
@@ -175,346 +327,537 @@ __global__ void __launch_bounds__(kThreads, per_sm<NT>()) attn_kv4_kernel(const 
         }
         prefix += (long long)__shfl_sync(0xffffffffu, upto, 31) * tasks;
     }
-    int chunks = chunks_of(b);
-    int task = (int)((at - prefix) / chunks), chunk = (int)((at - prefix) - (long long)task * chunks);
-
-    while (at < end) {
-        // ---- one segment: chunks [chunk, chunk + n_ch) of a task ----
-        const int n_ch = (int)min((long long)(chunks - chunk), end - at);
-        const int len = __ldg(a.len + b), h = task / a.blocks, row0 = (task - h * a.blocks) * kRows;
-        const int nq = min(kRows, a.R * a.G - row0);
-        const int p0 = chunk * kChunk, p1 = min(len, p0 + n_ch * kChunk);
-        const size_t head = ((size_t)b * a.H + h) * a.T;
-        const int tiles = max(0, (p1 - p0 + kTile - 1) / kTile);
-        auto issue = [&](int i, int stage) {                         // this warp's tile i: positions p0 + 16 (4 i + warp)
-            const int pt = p0 + kTile * (kWarps * i + warp);
-            if (pt < p1) {
-                const uint32_t dst = saddr(ring + stage * kStage);
-                constexpr int kPer = D / 32;                          // 16-byte pieces per position
-#pragma unroll
-                for (int e = 0; e < kTile * kPer / 32; ++e) {
-                    const int x = (e * 32 + lane) / kPer, c = (e * 32 + lane) % kPer;
-                    const bool in = pt + x < p1;
-                    const size_t src = (head + (in ? pt + x : p0)) * (D / 2) + 16 * c;
-                    copy16(dst + mma_row(x) * (D / 2) + 16 * c, a.kc + src, in);
-                    copy16(dst + kSide + x * (D / 2) + 16 * (D == 128 ? c ^ (x & 2) : c), a.vc + src, in);
-                }
-                const int x = lane & 15;
-                const bool in = pt + x < p1;
-                copy4(dst + 2 * kSide + (lane & 16) * 4 + mma_row(x) * 4, (lane < 16 ? a.ks : a.vs) + head + (in ? pt + x : p0),
-                      in);
-            }
-            asm volatile("cp.async.commit_group;" ::: "memory");
-        };
-        const int mine = (tiles - warp + kWarps - 1) / kWarps;       // tiles of this warp (0 or fewer: none)
-#pragma unroll
-        for (int s = 0; s < kStages - 1; ++s) issue(s, s);
-
-        // ---- Q fragments (k order: pairs (i, i + 4) of a word's eight d) and sum q ----
-        uint32_t qf[NT][kSteps][2];
-        float qs[NT][2];
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            const int n = row0 + 8 * j + g8, r = n / a.G, gg = n - r * a.G;
-            float sum = 0.0f;
-#pragma unroll
-            for (int w = 0; w < kWords; ++w) {
-                uint4 x = make_uint4(0, 0, 0, 0);
-                if (8 * j + g8 < nq)
-                    x = __ldg(reinterpret_cast<const uint4 *>(a.q + (size_t)(b * a.R + r) * a.ldq + (size_t)(h * a.G + gg) * D +
-                                                              (D / 4) * t4 + 8 * w));
-                const uint32_t v[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) sum += __uint_as_float(v[e] << 16) + __uint_as_float(v[e] & 0xFFFF0000u);
-                qf[j][2 * w][0] = __byte_perm(x.x, x.z, 0x5410);
-                qf[j][2 * w][1] = __byte_perm(x.x, x.z, 0x7632);
-                qf[j][2 * w + 1][0] = __byte_perm(x.y, x.w, 0x5410);
-                qf[j][2 * w + 1][1] = __byte_perm(x.y, x.w, 0x7632);
-            }
-            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-            qs[j][0] = __shfl_sync(0xffffffffu, sum, 8 * t4);        // rows 2 t, 2 t + 1: the S^T columns of this thread
-            qs[j][1] = __shfl_sync(0xffffffffu, sum, 8 * t4 + 4);
-        }
-        const float cs = a.scale * 1.4426950408889634f;
-        float m[NT][2], l[NT][2], acc[kSteps][NT][4];
-        int seen[NT][2];                                              // positions that a row sees
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                m[j][e] = kNone;
-                l[j][e] = 0.0f;
-                seen[j][e] = len - a.R + 1 + (row0 + 8 * j + 2 * t4 + e) / a.G;
-            }
-#pragma unroll
-        for (int i = 0; i < kSteps; ++i)
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.0f;
-
-        for (int i = 0; i < mine; ++i) {
-            asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
-            __syncwarp();
-            issue(i + kStages - 1, (i + kStages - 1) % kStages);
-            const uint8_t *stg = ring + (i % kStages) * kStage;
-            const uint32_t *szk = reinterpret_cast<const uint32_t *>(stg + 2 * kSide), *szv = szk + kTile;
-            // ---- S^T = K Q^T ----
-            float s[NT][4];
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) s[j][e] = 0.0f;
-            uint32_t kw[2][kWords];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const uint8_t *src = stg + (g8 + 8 * e) * (D / 2) + t4 * (D / 8);
-                if constexpr (D == 128) {
-                    const uint4 x = *reinterpret_cast<const uint4 *>(src);
-                    kw[e][0] = x.x, kw[e][1] = x.y, kw[e][2] = x.z, kw[e][3] = x.w;
-                } else {
-                    const uint2 x = *reinterpret_cast<const uint2 *>(src);
-                    kw[e][0] = x.x, kw[e][1] = x.y;
-                }
-            }
-#pragma unroll
-            for (int k = 0; k < kSteps; ++k) {
-                const int w = k >> 1, f = 2 * (k & 1);
-                const uint32_t a0 = code_pair(kw[0][w], f), a1 = code_pair(kw[1][w], f), a2 = code_pair(kw[0][w], f + 1),
-                               a3 = code_pair(kw[1][w], f + 1);
-#pragma unroll
-                for (int j = 0; j < NT; ++j) mma(s[j], a0, a1, a2, a3, qf[j][k][0], qf[j][k][1]);
-            }
-            const uint32_t k0w = szk[g8], k1w = szk[g8 + 8];
-            const float sk[2] = {lo_half(k0w) * cs, lo_half(k1w) * cs}, zk[2] = {128.0f + hi_half(k0w), 128.0f + hi_half(k1w)};
-            // scores in log2 units; places that a row does not see
-            const int pt = p0 + kTile * (kWarps * i + warp);
-            const bool edge = pt + kTile > len - a.R + 1;
-            const int pos = pt + ((g8 & 1) << 2) + (g8 >> 1);         // position of MMA row g8 (row g8 + 8: + 8)
-            bool move = false;
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    s[j][e] = sk[e >> 1] * fmaf(-zk[e >> 1], qs[j][e & 1], s[j][e]);
-                    if (edge && pos + 8 * (e >> 1) >= seen[j][e & 1]) s[j][e] = -INFINITY;
-                    move |= s[j][e] > m[j][e & 1] + kMove;
-                }
-            if (__any_sync(0xffffffffu, move)) {
-#pragma unroll
-                for (int j = 0; j < NT; ++j)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float top = fmaxf(s[j][e], s[j][e + 2]);
-#pragma unroll
-                        for (int x = 4; x <= 16; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-                        if (top > m[j][e] + kMove) {
-                            const float f = ex2(m[j][e] - top);
-                            m[j][e] = top;
-                            l[j][e] *= f;
-#pragma unroll
-                            for (int k = 0; k < kSteps; ++k) {
-                                acc[k][j][e] *= f;
-                                acc[k][j][e + 2] *= f;
-                            }
-                        }
-                    }
-            }
-            // ---- p, l, and P^T fragments ----
-            const float v0 = lo_half(szv[g8]), v1 = lo_half(szv[g8 + 8]);
-            uint32_t pf[NT][2];
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                float p[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    p[e] = ex2(s[j][e] - m[j][e & 1]);
-                    l[j][e & 1] += p[e];
-                }
-                float w[4] = {p[0] * v0, p[1] * v0, p[2] * v1, p[3] * v1};
-                if (edge)                                             // an unseen place's scale may be anything
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) w[e] = p[e] == 0.0f ? 0.0f : w[e];
-                pf[j][0] = transpose8x8(pack_bf16(w[0], w[1]));
-                pf[j][1] = transpose8x8(pack_bf16(w[2], w[3]));
-            }
-            // ---- O^T += V^T P^T: MMA rows 2 t, 2 t + 1 and 8 + 2 t, 9 + 2 t of the tile ----
-            const uint2 za = *reinterpret_cast<const uint2 *>(szv + 2 * t4), zb = *reinterpret_cast<const uint2 *>(szv + 8 + 2 * t4);
-            const uint32_t zz0 = pack_bf16(zero_point(za.x), zero_point(za.y)), zz1 = pack_bf16(zero_point(zb.x), zero_point(zb.y));
-            const uint8_t *vsrc = stg + kSide + t4 * (D / 2) + (D == 128 ? ((8 * g8) ^ ((t4 & 2) << 4)) : 4 * g8);
-            uint32_t vw[4][D / 64];
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {                             // positions t, 4 + t, 8 + t, 12 + t
-                if constexpr (D == 128) {
-                    const uint2 y = *reinterpret_cast<const uint2 *>(vsrc + x * 4 * (D / 2));
-                    vw[x][0] = y.x, vw[x][1] = y.y;
-                } else {
-                    vw[x][0] = *reinterpret_cast<const uint32_t *>(vsrc + x * 4 * (D / 2));
-                }
-            }
-#pragma unroll
-            for (int w = 0; w < D / 64; ++w) {
-                const uint32_t l0 = __byte_perm(vw[0][w], vw[1][w], 0x5410), h0 = __byte_perm(vw[0][w], vw[1][w], 0x7632),
-                               l1 = __byte_perm(vw[2][w], vw[3][w], 0x5410), h1 = __byte_perm(vw[2][w], vw[3][w], 0x7632);
-#pragma unroll
-                for (int f = 0; f < 4; ++f) {
-                    const uint32_t a0 = bf2_sub(code_pair(l0, f), zz0), a1 = bf2_sub(code_pair(h0, f), zz0),
-                                   a2 = bf2_sub(code_pair(l1, f), zz1), a3 = bf2_sub(code_pair(h1, f), zz1);
-#pragma unroll
-                    for (int j = 0; j < NT; ++j) mma(acc[4 * w + f][j], a0, a1, a2, a3, pf[j][0], pf[j][1]);
-                }
-            }
-        }
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
-
-        // ---- the warps' results joined: rows 2 t, 2 t + 1 of each 8, d = (D / 8) g + ... ----
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-#pragma unroll
-                for (int x = 4; x <= 16; x <<= 1) l[j][e] += __shfl_xor_sync(0xffffffffu, l[j][e], x);
-                if (g8 == 0)
-                    *reinterpret_cast<float2 *>(sml + (warp * kRows + 8 * j + 2 * t4 + e) * 2) = make_float2(m[j][e], l[j][e]);
-            }
-        __syncthreads();                                              // every warp is done with its ring
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int n = 8 * j + 2 * t4 + e;
-                float top = kNone;
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sml[(w * kRows + n) * 2]);
-                const float f = ex2(m[j][e] - top);
-                float *dst = so + (size_t)(warp * kRows + n) * (D + 4) + (D / 8) * g8;
-#pragma unroll
-                for (int w = 0; w < D / 64; ++w) {                    // word w: d 0..3 in MMA row g, 4..7 in row g + 8
-                    *reinterpret_cast<float4 *>(dst + 8 * w) = make_float4(acc[4 * w][j][e] * f, acc[4 * w + 1][j][e] * f,
-                                                                           acc[4 * w + 2][j][e] * f, acc[4 * w + 3][j][e] * f);
-                    *reinterpret_cast<float4 *>(dst + 8 * w + 4) =
-                        make_float4(acc[4 * w][j][e + 2] * f, acc[4 * w + 1][j][e + 2] * f, acc[4 * w + 2][j][e + 2] * f,
-                                    acc[4 * w + 3][j][e + 2] * f);
-                }
-            }
-        __syncthreads();
-        const long long ts = prefix + (long long)task * chunks;       // the task's first item
-        const bool whole = n_ch == chunks;
-        const int c0 = (int)(((ts + 1) * nc + total - 1) / total) - 1, c1 = (int)(((ts + chunks) * nc + total - 1) / total) - 1;
-        constexpr int kSlot = kRows * (D + 2);
-        auto out_row = [&](int n) {
-            const int r = (row0 + n) / a.G, gg = (row0 + n) - r * a.G;
-            return a.o + (size_t)(b * a.R + r) * a.ldo + (size_t)(h * a.G + gg) * D;
-        };
-        float *slot = a.part + ((size_t)blockIdx.x * 2 + ((int)blockIdx.x == c0 ? 1 : 0)) * kSlot;
-        for (int n = warp; n < nq; n += kWarps) {                      // a warp per row, four d per lane
-            float top = kNone, sum = 0.0f;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sml[(w * kRows + n) * 2]);
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) sum += sml[(w * kRows + n) * 2 + 1] * ex2(sml[(w * kRows + n) * 2] - top);
-            if (4 * lane < D) {
-                float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) {
-                    const float4 y = *reinterpret_cast<const float4 *>(so + (size_t)(w * kRows + n) * (D + 4) + 4 * lane);
-                    x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
-                }
-                if (whole) {
-                    const float inv = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;   // NaN stays
-                    *reinterpret_cast<uint2 *>(out_row(n) + 4 * lane) =
-                        make_uint2(pack_bf16(x.x * inv, x.y * inv), pack_bf16(x.z * inv, x.w * inv));
-                } else {
-                    __stcg(reinterpret_cast<float4 *>(slot + n * D + 4 * lane), x);
-                }
-            }
-            if (!whole && lane == 0) __stcg(reinterpret_cast<float2 *>(slot + kRows * D + 2 * n), make_float2(top, sum));
-        }
-        if (!whole) {
-            __syncthreads();
-            if (tid == 0) {
-                __threadfence();
-                const int done = atomicAdd(a.count + c0, 1);
-                last_flag = done == c1 - c0;
-                if (last_flag) {
-                    a.count[c0] = 0;                                   // ready for the next call
-                    __threadfence();
-                }
-            }
-            __syncthreads();
-            if (last_flag) {
-                auto part = [&](int c) { return a.part + ((size_t)c * 2 + (c == c0 ? 1 : 0)) * kSlot; };
-                for (int n = warp; n < nq; n += kWarps) {
-                    float top = kNone;
-                    for (int c = c0 + lane; c <= c1; c += 32) top = fmaxf(top, __ldcg(part(c) + kRows * D + 2 * n));
-#pragma unroll
-                    for (int x = 16; x >= 1; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-                    float sum = 0.0f;
-                    float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    for (int cb = c0; cb <= c1; cb += 32) {
-                        float2 ml = make_float2(kNone, 0.0f);
-                        if (cb + lane <= c1) ml = __ldcg(reinterpret_cast<const float2 *>(part(cb + lane) + kRows * D + 2 * n));
-                        const float f = ex2(ml.x - top);
-                        const int cnt = min(32, c1 - cb + 1);
-#pragma unroll 8
-                        for (int c = 0; c < cnt; ++c) {
-                            const float fc = __shfl_sync(0xffffffffu, f, c);
-                            sum = fmaf(fc, __shfl_sync(0xffffffffu, ml.y, c), sum);
-                            if (4 * lane < D) {
-                                const float4 y = __ldcg(reinterpret_cast<const float4 *>(part(cb + c) + n * D + 4 * lane));
-                                x.x = fmaf(fc, y.x, x.x), x.y = fmaf(fc, y.y, x.y), x.z = fmaf(fc, y.z, x.z), x.w = fmaf(fc, y.w, x.w);
-                            }
-                        }
-                    }
-                    const float inv = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;
-                    if (4 * lane < D)
-                        *reinterpret_cast<uint2 *>(out_row(n) + 4 * lane) =
-                            make_uint2(pack_bf16(x.x * inv, x.y * inv), pack_bf16(x.z * inv, x.w * inv));
-                }
-            }
-        }
-        __syncthreads();                                              // shared memory free for the next segment
-        // ---- on to the next task ----
-        at += n_ch;
-        chunk = 0;
+    int nt_task = any ? tiles_of(b) : 1;         // tiles of the task
+    int task = any ? (int)((at - prefix) / nt_task) : 0, tile = any ? (int)((at - prefix) - (long long)task * nt_task) : 0;
+    auto next = [&](int n_t) {                   // on to the next task
+        at += n_t;
+        tile = 0;
         if (++task == tasks && at < end) {
             task = 0;
-            prefix += (long long)chunks * tasks;
-            do chunks = chunks_of(++b);
-            while (chunks == 0);
+            prefix += (long long)nt_task * tasks;
+            do nt_task = tiles_of(++b);
+            while (nt_task == 0);
+        }
+    };
+
+    int loads = 0;                               // tiles whose copies were issued
+    bool issued = false;
+    if (warp == kLoadWarp) {
+        if (lane == 0) {
+            while (at < end) {
+                const int n_t = (int)min((long long)(nt_task - tile), end - at), h = task / a.blocks;
+                for (int i = 0; i < n_t; ++i) {
+                    const int s = loads % kStages;
+                    if (loads >= kStages && !wait(&sm.empty[s], loads / kStages + 1)) break;
+                    if (*reinterpret_cast<volatile int *>(&sm.timeout)) break;
+                    umma::mbar_arrive_expect_tx(&sm.full[s], 2 * kSide);
+                    tma_load_3d(codes + s * 2 * kSide, &tk, 0, (tile + i) * kTok, b * a.H + h, &sm.full[s]);
+                    tma_load_3d(codes + s * 2 * kSide + kSide, &tv, 0, (tile + i) * kTok, b * a.H + h, &sm.full[s]);
+                    ++loads;
+                }
+                next(n_t);
+            }
+        }
+    } else if (warp == kScoreWarp) {
+        if (lane == 0) {
+            constexpr uint32_t id = umma::instr_desc(0, 0, kTok, N);                            // f16, f32 sums
+            const uint64_t qd = umma::smem_desc(umma::smem_addr(sq), N * 16, 128);
+            int g = 0;
+            bool ok = true;
+            for (int seg = 0; at < end; ++seg) {
+                const int n_t = (int)min((long long)(nt_task - tile), end - at);
+                ok = ok && wait(&sm.qfull, seg);
+                for (int i = 0; i < n_t && ok; ++i, ++g) {
+                    const int s = g % kGroups;
+                    ok = wait(&sm.kfull[s], g / kGroups);
+                    if (!ok) break;
+                    umma::fence_after_sync();
+#pragma unroll
+                    for (int kk = 0; kk < kSteps + 1; ++kk)
+                        umma::mma_bf16_ta(tmem + cS + s * N, tmem + cK + s * 80 + kk * 8, qd + (uint64_t)(kk * 2 * N), id, kk != 0);
+                    umma::mma_commit(&sm.sfull[s]);
+                    issued = true;
+                }
+                next(n_t);
+            }
+        }
+    } else if (warp == kValueWarp) {
+        if (lane == 0) {
+            constexpr uint32_t id = umma::instr_desc(1, 1, kTok, N) | (1u << 15) | (1u << 16);  // bf16, both MN-major
+            int g = 0;
+            bool ok = true;
+            while (at < end) {
+                const int n_t = (int)min((long long)(nt_task - tile), end - at);
+                for (int i = 0; i < n_t && ok; ++i, ++g) {
+                    const int s = g % kGroups;
+                    ok = wait(&sm.vfull[s], g / kGroups) && wait(&sm.pfull[s], g / kGroups);
+                    if (!ok) break;
+                    umma::fence_after_sync();
+                    const uint64_t vd = umma::smem_desc(umma::smem_addr(sv + s * kVBuf), 128, kTok * 16);
+                    const uint64_t pd = umma::smem_desc(umma::smem_addr(sp + s * kP), 128, kTok * 16);
+#pragma unroll
+                    for (int kk = 0; kk < kTok / 16; ++kk)
+                        umma::mma_bf16(tmem + cO, vd + kk * 16, pd + kk * 16, id, (i | kk) != 0);
+                    umma::mma_commit(&sm.pdone[s]);
+                    issued = true;
+                }
+                if (ok) umma::mma_commit(&sm.odone);
+                next(n_t);
+            }
+        }
+    } else {
+        const int grp = warp >> 2, tok = tid & (kTok - 1);
+        const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+        const uint32_t tK = tmem + lanes + cK + grp * 80, tS = tmem + lanes + cS + grp * N;
+        uint8_t *const v_dst = sv + grp * kVBuf + tok * 16, *const p_dst = sp + grp * kP + tok * 16;
+        // the z step's unused columns
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%1,%1,%1,%1,%1,%1,%1};\n" ::"r"(tK + D / 2), "r"(0u) : "memory");
+        umma::tmem_st_wait();
+        // pieces of Q of a segment: row n = item / (D / 8), eight d each
+        constexpr int kItems = (N * (D / 8) + kWork - 1) / kWork;
+        auto q_offset = [&](int sb, int st, int n, int ld) -> long long {      // row n of task st of sequence sb
+            const int hh = a.blocks == 1 ? st : st / a.blocks, nn = (st - hh * a.blocks) * N + n, r = a.row_r(nn);
+            return (long long)(sb * a.R + r) * ld + (long long)(hh * a.G + (nn - r * a.G)) * D;
+        };
+        uint4 qx[kItems];
+        auto fetch_q = [&](int sb, int st) {
+            const int left = a.R * a.G - (a.blocks == 1 ? 0 : (st % a.blocks) * N);
+#pragma unroll
+            for (int k = 0; k < kItems; ++k) {
+                const int it = k * kWork + tid, n = it / (D / 8);
+                qx[k] = make_uint4(0, 0, 0, 0);
+                if (n < N && n < left) qx[k] = __ldg(reinterpret_cast<const uint4 *>(a.q + q_offset(sb, st, n, a.ldq) + 8 * (it % (D / 8))));
+            }
+        };
+        if (at < end) fetch_q(b, task);
+        int g = 0;                                               // tiles of this CTA so far
+        for (int seg = 0; at < end; ++seg) {
+            const int n_t = (int)min((long long)(nt_task - tile), end - at);
+            const int len = __ldg(a.len + b), h = a.blocks == 1 ? task : task / a.blocks, row0 = (task - h * a.blocks) * N;
+            const int nq = min(N, a.R * a.G - row0);
+            const int p0 = tile * kTok;
+            const size_t head = ((size_t)b * a.H + h) * a.T;
+            // this group's tiles: i0, i0 + 3, ...; the scale words one tile ahead
+            const int i0 = (grp + kGroups - g % kGroups) % kGroups;
+            uint32_t kn = 0, vn = 0;
+            if (i0 < n_t && p0 + i0 * kTok + tok < len) {
+                kn = __ldg(a.ks + head + p0 + i0 * kTok + tok);
+                vn = __ldg(a.vs + head + p0 + i0 * kTok + tok);
+            }
+            // ---- Q, rows scaled to below 2^15, in the order of unpacked codes ----
+#pragma unroll
+            for (int k = 0; k < kItems; ++k) {
+                const int it = k * kWork + tid, n = it / (D / 8), w = it % (D / 8);
+                if (k * kWork + 32 * warp >= N * (D / 8)) break;
+                const uint32_t v[4] = {qx[k].x, qx[k].y, qx[k].z, qx[k].w};
+                uint32_t top = 0;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) top = max(top, max((v[e] >> 7) & 0xFFu, (v[e] >> 23) & 0xFFu));   // exponents
+#pragma unroll
+                for (int o = D / 16; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+                const int up = min(253, 268 - (int)min(top, 254u));   // exponent field of 2^(14 - exponent)
+                const float f = __uint_as_float((uint32_t)up << 23), f16 = f * 0.0625f;
+                float lo[4], hi[4], sum = 0.0f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    lo[e] = __uint_as_float(v[e] << 16);
+                    hi[e] = __uint_as_float(v[e] & 0xFFFF0000u);
+                    sum += lo[e] * f + hi[e] * f;
+                }
+                *reinterpret_cast<uint4 *>(sq + (w * N + n) * 16) =
+                    make_uint4(pack_half(lo[0] * f, lo[2] * f), pack_half(hi[0] * f16, hi[2] * f16),
+                               pack_half(lo[1] * f, lo[3] * f), pack_half(hi[1] * f16, hi[3] * f16));
+#pragma unroll
+                for (int o = D / 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                if (w == 0) {
+                    // z 2^-10 against -sum 2^-14 (the codes carry 2^-24), in three parts
+                    const float z0 = -sum * 6.103515625e-5f;
+                    const __half h0 = __float2half_rn(z0), h1 = __float2half_rn(z0 - __half2float(h0)),
+                                 h2 = __float2half_rn(z0 - __half2float(h0) - __half2float(h1));
+                    *reinterpret_cast<uint4 *>(sq + ((D / 8) * N + n) * 16) =
+                        make_uint4((uint32_t)__half_as_ushort(h0) | ((uint32_t)__half_as_ushort(h1) << 16),
+                                   (uint32_t)__half_as_ushort(h2), 0u, 0u);
+                    *reinterpret_cast<uint4 *>(sq + ((D / 8 + 1) * N + n) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                    reinterpret_cast<float *>(sm.back)[4 * (n >> 1) + (n & 1)] =
+                        __uint_as_float((uint32_t)(254 - up) << 23) * (a.scale * (1.4426950408889634f * 16777216.0f));
+                    sm.seen[n] = n < nq ? len - a.R + 1 + a.row_r(row0 + n) : 0;
+                    sm.orow[n] = n < nq ? q_offset(b, task, n, a.ldo) : 0;
+                }
+            }
+            umma::fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) umma::mbar_arrive(&sm.qfull);
+            bar_sync(1, kWork);
+            uint64_t l2[N / 2];
+#pragma unroll
+            for (int n = 0; n < N / 2; ++n) l2[n] = 0;
+            for (int i = i0; i < n_t; i += kGroups) {
+                const int gi = g + i, c = gi / kGroups, stage = gi % kStages, t = p0 + i * kTok + tok;
+                const uint32_t kw = kn, vw = vn;
+                kn = vn = 0;
+                if (i + kGroups < n_t && t + kGroups * kTok < len) {
+                    kn = __ldg(a.ks + head + t + kGroups * kTok);
+                    vn = __ldg(a.vs + head + t + kGroups * kTok);
+                }
+                // ---- K codes into tensor memory (S^T of the group's last tile is complete: the buffer is free) ----
+                wait(&sm.full[stage], gi / kStages);
+                const uint8_t *kcode = codes + stage * 2 * kSide;
+                uint4 x[D / 32];
+#pragma unroll
+                for (int y = 0; y < D / 32; ++y) x[y] = code_piece<D>(kcode, tok, y);
+#pragma unroll
+                for (int y = 0; y < D / 64; ++y) {
+                    uint32_t r[32];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const uint4 &xx = x[2 * y + (k >> 2)];
+                        const uint32_t w = (k & 3) == 0 ? xx.x : (k & 3) == 1 ? xx.y : (k & 3) == 2 ? xx.z : xx.w, v = w >> 8;
+                        r[4 * k] = w & 0x000F000Fu;
+                        r[4 * k + 1] = w & 0x00F000F0u;
+                        r[4 * k + 2] = v & 0x000F000Fu;
+                        r[4 * k + 3] = v & 0x00F000F0u;
+                    }
+                    umma::tmem_st32(tK + 32 * y, r);
+                }
+                {
+                    const uint32_t z = __half_as_ushort(__float2half_rn(hi_half(kw) * 0.0009765625f));
+                    asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%0], {%1,%2};\n" ::"r"(tK + D / 2), "r"(z | (z << 16)), "r"(z)
+                                 : "memory");
+                }
+                umma::tmem_st_wait();
+                umma::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) umma::mbar_arrive(&sm.kfull[grp]);
+                // ---- V into its operand layout, once the group's last tile's products have read it ----
+                // (128 + z) as a bf16 pair: fp16 z + 1024 has the integer z in its low bits.  Whatever the
+                // word holds, it is finite: a bad word at an unseen place does not reach other rows as 0 times NaN
+                const uint32_t z = (uint32_t)__half_as_ushort(__hadd(__ushort_as_half((uint16_t)(vw >> 16)), __ushort_as_half(0x6400))) & 15u;
+                const uint32_t zz = 0x43004300u | z | (z << 16);
+                const __nv_bfloat162 z2 = *reinterpret_cast<const __nv_bfloat162 *>(&zz);
+#pragma unroll
+                for (int y = 0; y < D / 32; ++y) x[y] = code_piece<D>(kcode + kSide, tok, y);
+                // the next copy into the stage comes by the async proxy: these reads are fenced against it
+                umma::fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) umma::mbar_arrive(&sm.empty[stage]);
+                if (c > 0) wait(&sm.pdone[grp], c - 1);
+#pragma unroll
+                for (int y = 0; y < D / 32; ++y) {
+                    const uint32_t ww[4] = {x[y].x, x[y].y, x[y].z, x[y].w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        uint32_t r[4];
+#pragma unroll
+                        for (int f = 0; f < 4; ++f) {
+                            const uint32_t cc = ((ww[k] >> (4 * f)) & 0x000F000Fu) | 0x43004300u;
+                            const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&cc), z2);
+                            r[f] = *reinterpret_cast<const uint32_t *>(&v);
+                        }
+                        *reinterpret_cast<uint4 *>(v_dst + (4 * y + k) * (kTok * 16)) = make_uint4(r[0], r[1], r[2], r[3]);
+                    }
+                }
+                umma::fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) umma::mbar_arrive(&sm.vfull[grp]);
+                // ---- scores, p, P^T ----
+                const float sk = lo_half(kw), svv = lo_half(vw);
+                wait(&sm.sfull[grp], c);
+                umma::fence_after_sync();
+                if (i == 0 && (warp & 3) == 0) {                  // the first position's lane sets the reference
+#pragma unroll
+                    for (int n0 = 0; n0 < N; n0 += 16) {
+                        uint32_t u[16];
+                        umma::tmem_ld16(tS + n0, u);
+                        umma::tmem_ld_wait();
+                        if (lane == 0)
+#pragma unroll
+                            for (int k = 0; k < 16; k += 2)
+                                reinterpret_cast<float2 *>(sm.back)[n0 + k + 1] = make_float2(-sk * __uint_as_float(u[k]), -sk * __uint_as_float(u[k + 1]));
+                    }
+                    if (lane == 0) umma::mbar_arrive(&sm.ref);
+                }
+                if (i < kGroups) wait(&sm.ref, seg);
+                const uint64_t sk2 = f2(sk, sk), sv2 = f2(svv, svv);
+                auto weights = [&](auto edge_c) {
+                    constexpr bool kEdge = decltype(edge_c)::value;
+                    constexpr int kC = N < 32 ? 16 : 32;
+#pragma unroll
+                    for (int n0 = 0; n0 < N; n0 += kC) {
+                        if (n0 >= nq) {                           // rows past nq hold nothing
+#pragma unroll
+                            for (int k8 = 0; k8 < kC; k8 += 8)
+                                *reinterpret_cast<uint4 *>(p_dst + ((n0 + k8) / 8) * (kTok * 16)) = make_uint4(0u, 0u, 0u, 0u);
+                            continue;
+                        }
+                        uint32_t u[kC];
+                        if constexpr (kC == 16)
+                            umma::tmem_ld16(tS + n0, u);
+                        else
+                            umma::tmem_ld32(tS + n0, u);
+                        umma::tmem_ld_wait();
+#pragma unroll
+                        for (int k8 = 0; k8 < kC; k8 += 8) {
+                            uint32_t w[4] = {0u, 0u, 0u, 0u};
+                            if (n0 + k8 < nq) {                   // (eight rows at a time)
+#pragma unroll
+                                for (int k = 0; k < 8; k += 2) {
+                                    const int n = n0 + k8 + k;
+                                    const ulonglong2 br = *reinterpret_cast<const ulonglong2 *>(&sm.back[n / 2]);
+                                    const uint64_t d = mul2(br.x, fma2(sk2, f2(__uint_as_float(u[k8 + k]), __uint_as_float(u[k8 + k + 1])), br.y));
+                                    float d0 = lo32(d), d1 = hi32(d);
+                                    if (kEdge) {
+                                        if (t >= sm.seen[n]) d0 = -INFINITY;
+                                        if (t >= sm.seen[n + 1]) d1 = -INFINITY;
+                                    }
+                                    const float p0v = ex2(d0), p1v = ex2(d1);
+                                    const uint64_t pp = f2(p0v, p1v), ws = mul2(pp, sv2);
+                                    l2[n / 2] = add2(l2[n / 2], pp);
+                                    // an unseen place's scale may be anything
+                                    w[k / 2] = pack_bf16(kEdge && p0v == 0.0f ? 0.0f : lo32(ws), kEdge && p1v == 0.0f ? 0.0f : hi32(ws));
+                                }
+                            }
+                            *reinterpret_cast<uint4 *>(p_dst + ((n0 + k8) / 8) * (kTok * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                    }
+                };
+                if (p0 + (i + 1) * kTok > len - a.R + 1)          // some row does not see some of it
+                    weights(std::true_type{});
+                else
+                    weights(std::false_type{});
+                umma::fence_before_sync();
+                umma::fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) umma::mbar_arrive(&sm.pfull[grp]);
+            }
+            g += n_t;
+            // ---- sums of p ----
+            {
+                float l[N];
+                bool over = false;
+#pragma unroll
+                for (int n = 0; n < N / 2; ++n) {
+                    l[2 * n] = lo32(l2[n]);
+                    l[2 * n + 1] = hi32(l2[n]);
+                    over |= l[2 * n] > kOver || l[2 * n + 1] > kOver;
+                }
+                if (over) sm.over = 1;
+                lane_sums<N>(l, lane);
+                if constexpr (N >= 32) {
+#pragma unroll
+                    for (int e = 0; e < N / 32; ++e) sm.lsum[warp][lane * (N / 32) + e] = l[e];
+                } else {
+                    if ((lane & 1) == 0) sm.lsum[warp][lane >> 1] = l[0];
+                }
+            }
+            bar_sync(1, kWork);
+            if (tid < N) {
+                float sum = 0.0f;
+#pragma unroll
+                for (int w = 0; w < kWorkWarps; ++w) sum += sm.lsum[w][tid];
+                const float back = reinterpret_cast<const float *>(sm.back)[4 * (tid >> 1) + (tid & 1)],
+                            ref = -reinterpret_cast<const float *>(sm.back)[4 * (tid >> 1) + 2 + (tid & 1)];
+                sm.inv[tid] = sum == 0.0f ? 0.0f : 1.0f / sum;                 // (NaN stays)
+                sm.lse[tid] = sum == 0.0f ? kNone : fmaf(back, ref, log2f(sum));
+            }
+            const bool whole = n_t == nt_task;
+            const long long ts = prefix + (long long)task * nt_task;      // the task's first tile
+            const int c0 = (int)(((ts + 1) * nc + total - 1) / total) - 1, c1 = (int)(((ts + nt_task) * nc + total - 1) / total) - 1;
+            const int seg_b = b, seg_task = task;
+            next(n_t);
+            if (at < end) fetch_q(b, task);                       // the next segment's Q, under this one's end
+            wait(&sm.odone, seg);
+            umma::fence_after_sync();
+            bar_sync(1, kWork);
+            // ---- results: to the output, or to this CTA's slot where others have parts of the task ----
+            constexpr int kSlot = N * (D + 1);
+            float *slot = a.part + ((size_t)blockIdx.x * 2 + ((int)blockIdx.x == c0 ? 1 : 0)) * kSlot;
+            if (sm.over) {
+                for (int n = warp; n < nq; n += kWorkWarps) {
+                    float o[D / 32];
+                    const float lse = plain_row<D>(a, a.q + q_offset(seg_b, seg_task, n, a.ldq), head, p0,
+                                                   min(sm.seen[n], min(len, p0 + n_t * kTok)), o);
+#pragma unroll
+                    for (int e = 0; e < D / 32; ++e) {
+                        if (whole)
+                            a.o[sm.orow[n] + lane * (D / 32) + e] = float_to_bf16_bits(o[e]);
+                        else
+                            __stcg(slot + n * D + lane * (D / 32) + e, o[e]);
+                    }
+                    if (!whole && lane == 0) __stcg(slot + N * D + n, lse);
+                }
+            } else if (32 * (warp & 3) < D) {                      // thread = d; each group every third eight rows
+                const int L = 32 * (warp & 3) + lane, d = (L & ~7) | place_d(L & 7);
+                for (int n0 = 8 * grp; n0 < nq; n0 += 8 * kGroups) {
+                    uint32_t u[8];
+                    umma::tmem_ld_cols<8>(tmem + lanes + cO + n0, u);
+                    umma::tmem_ld_wait();
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const int n = n0 + k;
+                        const float o = sm.lse[n] == kNone ? 0.0f : __uint_as_float(u[k]) * sm.inv[n];
+                        if (n < nq) {
+                            if (whole)
+                                a.o[sm.orow[n] + d] = float_to_bf16_bits(o);
+                            else
+                                __stcg(slot + n * D + d, o);
+                        }
+                    }
+                }
+                umma::fence_before_sync();
+                if (!whole && warp == 0)
+                    for (int n = lane; n < nq; n += 32) __stcg(slot + N * D + n, sm.lse[n]);
+            }
+            bar_sync(1, kWork);
+            if (tid == 0) {
+                sm.over = 0;
+                if (!whole) {                                      // (the answer is looked at when all tiles are done)
+                    __threadfence();
+                    const bool last = atomicAdd(a.count + c0, 1) == c1 - c0;
+                    if (last) a.count[c0] = 0;                     // ready for the next call
+                    Join &j = sm.join[(int)blockIdx.x == c0 ? 1 : 0];
+                    j.parts = last ? c1 - c0 + 1 : 0;
+                    j.c0 = c0;
+                    j.nq = nq;
+                    j.b = seg_b;
+                    j.task = seg_task;
+                }
+            }
+        }
+        // ---- tasks of which this CTA was the last to finish a part ----
+        if (tid == 0) __threadfence();
+        bar_sync(1, kWork);
+#pragma unroll 1
+        for (int e = 0; e < 2; ++e) {
+            const Join j = sm.join[e];
+            if (j.parts == 0) continue;
+            constexpr int kSlot = N * (D + 1), kFew = 8;
+            float *wgt = reinterpret_cast<float *>(sv);             // [part][N], in the V operands' place
+            auto part = [&](int c) { return a.part + ((size_t)(j.c0 + c) * 2 + (c == 0 ? 1 : 0)) * kSlot; };
+            if (j.parts <= kFew) {                                  // a thread per row
+                if (tid < j.nq) {
+                    float v[kFew], top = kNone, sum = 0.0f;
+#pragma unroll
+                    for (int c = 0; c < kFew; ++c) v[c] = c < j.parts ? __ldcg(part(c) + N * D + tid) : kNone;
+#pragma unroll
+                    for (int c = 0; c < kFew; ++c) top = fmaxf(top, v[c]);
+#pragma unroll
+                    for (int c = 0; c < kFew; ++c) {
+                        v[c] = v[c] == kNone ? 0.0f : ex2(v[c] - top);          // (NaN stays)
+                        sum += v[c];
+                    }
+                    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+                    for (int c = 0; c < kFew; ++c)
+                        if (c < j.parts) wgt[c * N + tid] = v[c] * inv;
+                }
+            } else {                                                // a warp per row
+                for (int n = warp; n < j.nq; n += kWorkWarps) {
+                    float v[(kMaxCtas + 31) / 32], top = kNone, sum = 0.0f;
+#pragma unroll
+                    for (int k = 0; k < (kMaxCtas + 31) / 32; ++k) {
+                        v[k] = 32 * k + lane < j.parts ? __ldcg(part(32 * k + lane) + N * D + n) : kNone;
+                        top = fmaxf(top, v[k]);
+                    }
+#pragma unroll
+                    for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+#pragma unroll
+                    for (int k = 0; k < (kMaxCtas + 31) / 32; ++k) {
+                        v[k] = v[k] == kNone ? 0.0f : ex2(v[k] - top);
+                        sum += v[k];
+                    }
+#pragma unroll
+                    for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+                    for (int k = 0; k < (kMaxCtas + 31) / 32; ++k)
+                        if (32 * k + lane < j.parts) wgt[(32 * k + lane) * N + n] = v[k] * inv;
+                }
+            }
+            bar_sync(1, kWork);
+            constexpr int kEach = (N * (D / 4) + kWork - 1) / kWork, kBatch = kEach < 3 ? 4 : 2;   // loads in flight: kEach x kBatch
+            float4 x[kEach];
+#pragma unroll
+            for (int k = 0; k < kEach; ++k) x[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            for (int cb = 0; cb < j.parts; cb += kBatch) {
+                float4 y[kBatch][kEach];
+#pragma unroll
+                for (int c = 0; c < kBatch; ++c)
+#pragma unroll
+                    for (int k = 0; k < kEach; ++k) {
+                        const int it = k * kWork + tid;
+                        y[c][k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        if (cb + c < j.parts && it < j.nq * (D / 4)) y[c][k] = __ldcg(reinterpret_cast<const float4 *>(part(cb + c)) + it);
+                    }
+#pragma unroll
+                for (int c = 0; c < kBatch; ++c)
+#pragma unroll
+                    for (int k = 0; k < kEach; ++k) {
+                        const int it = k * kWork + tid;
+                        if (cb + c < j.parts && it < j.nq * (D / 4)) {
+                            const float w = wgt[(cb + c) * N + it / (D / 4)];
+                            x[k].x = fmaf(w, y[c][k].x, x[k].x), x[k].y = fmaf(w, y[c][k].y, x[k].y);
+                            x[k].z = fmaf(w, y[c][k].z, x[k].z), x[k].w = fmaf(w, y[c][k].w, x[k].w);
+                        }
+                    }
+            }
+#pragma unroll
+            for (int k = 0; k < kEach; ++k) {
+                const int it = k * kWork + tid, n = it / (D / 4);
+                if (n < j.nq)
+                    *reinterpret_cast<uint2 *>(a.o + q_offset(j.b, j.task, n, a.ldo) + 4 * (it % (D / 4))) =
+                        make_uint2(pack_bf16(x[k].x, x[k].y), pack_bf16(x[k].z, x[k].w));
+            }
+            bar_sync(1, kWork);
         }
     }
+
+    // after a timeout: copies and products in flight finish (bounded) before
+    // the memory is released
+    __syncthreads();
+    if (sm.timeout) {
+        if (warp == kLoadWarp && lane == 0)
+            for (int i = max(0, loads - kStages); i < loads; ++i)
+                umma::mbar_wait(&sm.full[i % kStages], (uint32_t)((i / kStages) & 1), kWaitLimit);
+        if ((warp == kScoreWarp || warp == kValueWarp) && lane == 0 && issued) {
+            umma::mma_commit(&sm.drain[warp - kScoreWarp]);
+            umma::mbar_wait(&sm.drain[warp - kScoreWarp], 0, kWaitLimit);
+        }
+        if (tid == 0) flag(a.st, QSPEC_ERR_TIMEOUT);
+    }
+    umma::fence_before_sync();
+    __syncthreads();
+    if (warp == kScoreWarp) umma::tmem_free(tmem, kCols);
 }
 
 bool sizes_ok(int B, int R, int Hq, int H, int D) {
     return B >= 1 && R >= 1 && R <= kMaxR && H >= 1 && Hq >= H && Hq % H == 0 && (D == 64 || D == 128) &&
-           (long long)B * R * Hq < (1LL << 28);
+           Hq / H <= 8192 && (long long)B * R * Hq < (1LL << 28);
 }
 
 constexpr size_t kCountBytes = kMaxCtas * sizeof(int);
+constexpr size_t kPartBytes = (size_t)kMaxCtas * 2 * kMaxN * (kMaxD + 1) * sizeof(float);
 
-template <int D, int NT>
+template <int D, int N>
 int launch(Args a, cudaStream_t stream) {
-    a.blocks = (a.R * a.G + 8 * NT - 1) / (8 * NT);
-    auto kern = attn_kv4_kernel<D, NT>;
-    int rc = smem_limit_once(reinterpret_cast<const void *>(kern), (int)smem_bytes<D, NT>(), true);
+    a.blocks = (a.R * a.G + N - 1) / N;
+    CUtensorMap tk, tv;
+    if (code_tmap(&tk, a.kc, D / 2, a.T, a.B * a.H, kTok) || code_tmap(&tv, a.vc, D / 2, a.T, a.B * a.H, kTok))
+        return QSPEC_ERR_UNSUPPORTED;
+    auto kern = attn_kv4_kernel<D, N>;
+    int rc = smem_limit_once(reinterpret_cast<const void *>(kern), (int)smem_bytes<D, N>());
     if (rc) return rc;
-    const long long most = (long long)a.B * a.H * a.blocks * std::max(1, (a.T + kChunk - 1) / kChunk);   // chunks at full lengths
-    const unsigned grid = (unsigned)std::min<long long>((long long)std::min(sm_count(), kMaxSms) * per_sm<NT>(), most);
-    return launch_pdl("qspec_attn_kv4", kern, dim3(grid), dim3(kThreads), smem_bytes<D, NT>(), stream, a);
+    const long long most = (long long)a.B * a.H * a.blocks * std::max(1, (a.T + kTok - 1) / kTok);   // tiles at full lengths
+    const unsigned grid = (unsigned)std::min<long long>(std::min(sm_count(), kMaxCtas), most);
+    return launch_pdl("qspec_attn_kv4", kern, dim3(grid), dim3(kThreads), smem_bytes<D, N>(), stream, tk, tv, a, kWaitLimit);
 }
 
-// row tiles per pass: the fewest passes over the cache with at most four, evenly filled
+// rows per pass: the fewest passes over the cache, then the narrowest that holds them
 template <int D>
 int dispatch(const Args &a, cudaStream_t stream) {
-    const int tiles = (a.R * a.G + 7) / 8, passes = (tiles + 3) / 4;
-    switch ((tiles + passes - 1) / passes) {
-        case 1: return launch<D, 1>(a, stream);
-        case 2: return launch<D, 2>(a, stream);
-        case 3: return launch<D, 3>(a, stream);
-        default: return launch<D, 4>(a, stream);
-    }
+    const int rows = a.R * a.G, passes = (rows + kMaxN - 1) / kMaxN, each = (rows + passes - 1) / passes;
+    if (each <= 16) return launch<D, 16>(a, stream);
+    if (each <= 32) return launch<D, 32>(a, stream);
+    return launch<D, 64>(a, stream);
 }
 
 }  // namespace akv
@@ -526,10 +869,8 @@ int dispatch(const Args &a, cudaStream_t stream) {
 using namespace qspec;
 
 extern "C" size_t qspec_attn_kv4_workspace_bytes(int B, int R, int Hq, int H, int D) {
-    // the same for every shape: arrival counts, then the partial results of every CTA that can be resident
-    return akv::sizes_ok(B, R, Hq, H, D)
-               ? akv::kCountBytes + (size_t)akv::kMaxSms * akv::kMaxRowsPerSm * 2 * (akv::kMaxD + 2) * sizeof(float)
-               : 0;
+    // the same for every shape: arrival counts, then two partial results per CTA
+    return akv::sizes_ok(B, R, Hq, H, D) ? akv::kCountBytes + akv::kPartBytes : 0;
 }
 
 extern "C" int qspec_attn_kv4(const uint16_t *q_bf16, int ldq, const uint8_t *k_codes, const uint32_t *k_sz,
@@ -537,8 +878,8 @@ extern "C" int qspec_attn_kv4(const uint16_t *q_bf16, int ldq, const uint8_t *k_
                               int H, int T, int D, float scale, uint16_t *o_bf16, int ldo, void *workspace,
                               size_t ws_bytes, int32_t *dev_status, qspec_stream_t stream) {
     if (!q_bf16 || !k_codes || !k_sz || !v_codes || !v_sz || !len || !o_bf16 || !workspace) return QSPEC_ERR_NULL;
-    if (!akv::sizes_ok(B, R, Hq, H, D) || T < 1 || T > (1 << 30) || !std::isfinite(scale) || ldq < (long long)Hq * D ||
-        ldo < (long long)Hq * D)
+    if (!akv::sizes_ok(B, R, Hq, H, D) || T < 1 || T > (1 << 30) || (long long)B * H >= (1LL << 31) ||
+        !std::isfinite(scale) || ldq < (long long)Hq * D || ldo < (long long)Hq * D)
         return QSPEC_ERR_SHAPE;
     if (ldq % 8 || ldo % 8 || !aligned(q_bf16, 16) || !aligned(o_bf16, 16) || !aligned(k_codes, 16) ||
         !aligned(v_codes, 16) || !aligned(k_sz, 4) || !aligned(v_sz, 4) || !aligned(len, 4) || !aligned(workspace, 16))
@@ -548,6 +889,6 @@ extern "C" int qspec_attn_kv4(const uint16_t *q_bf16, int ldq, const uint8_t *k_
     if (rc) return rc;
     const akv::Args a{q_bf16, k_codes, v_codes, k_sz, v_sz, len, o_bf16, dev_status, reinterpret_cast<int *>(workspace),
                       reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + akv::kCountBytes), ldq, ldo, B, R,
-                      Hq / H, H, T, 1, scale};
+                      Hq / H, H, T, 1, Hq == H ? 0u : (uint32_t)((1ull << 32) / (Hq / H) + 1), scale};
     return D == 128 ? akv::dispatch<128>(a, as_cuda(stream)) : akv::dispatch<64>(a, as_cuda(stream));
 }

@@ -128,7 +128,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                        uint32_t wait_limit) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     constexpr int kT = tile_bytes<D>(), NS = ring<D>();
-    uint8_t *sq = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    // (an offset, not a rounded address: the compiler keeps seeing shared memory)
+    uint8_t *sq = smem_raw + ((1024u - (umma::smem_addr(smem_raw) & 1023u)) & 1023u);
     uint8_t *skv = sq + 2 * kT;
     Ctl &sm = *reinterpret_cast<Ctl *>(skv + NS * kT);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;

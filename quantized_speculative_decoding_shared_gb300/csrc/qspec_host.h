@@ -76,6 +76,11 @@ int weight_tmap(CUtensorMap *out, const uint8_t *packed, int N, int K, int box_r
 // the matrix give zeros (not cached).
 int byte_tmap_sw128(CUtensorMap *out, const void *base, int rows, int cols, size_t pitch, int box_rows);
 
+// 3-D TMA map over a 4-bit cache's codes [BH][T][row_bytes] (row_bytes 64 or
+// 32): boxes of one row's bytes x box_rows positions, swizzled over the row's
+// width, positions past T read as zeros (not cached).
+int code_tmap(CUtensorMap *out, const void *base, int row_bytes, int T, int BH, int box_rows);
+
 // Polls of a bounded barrier wait in the tensor-core kernels (each poll
 // suspends for a hardware-chosen time); a wait that runs out sets
 // QSPEC_ERR_TIMEOUT.
