@@ -30,7 +30,8 @@
 // it by 2^96.  A segment where one does is taken again by a plain path.
 //
 // Work is split by the lengths on the device: all (sequence, head, row block)
-// tasks, cut into tiles of 128 positions, are laid end to end and every CTA
+// tasks, cut into tiles of 128 positions, are laid end to end, each with a few
+// empty tiles in front that stand for a segment's fixed cost, and every CTA
 // takes an equal share.  A task that several CTAs share is joined by the last
 // of them to finish, in the order of the parts, so that the bits do not
 // depend on who is last.
@@ -306,26 +307,53 @@ __global__ void __launch_bounds__(kThreads, 1)
     total *= tasks;
     const long long nc = min((long long)gridDim.x, total);
     const bool any = blockIdx.x < nc;
-    long long at = any ? blockIdx.x * total / nc : 0;
-    const long long end = any ? (blockIdx.x + 1) * total / nc : 0;
-    int b = 0;
-    long long prefix = 0;                        // tiles before sequence b
-    for (int b0 = 0; b0 < a.B && any; b0 += 32) {
+    // Beginning and ending a segment (Q, the first tile's way through the products, sums, results) takes as
+    // long as some six tiles; where a CTA has fewer than twelve, half of them: few tiles are better spread.
+    const int lead = (int)min(6ll, total / (2ll * gridDim.x));
+    // Tiles before share i: a border among a task's leading empty tiles is its first tile.
+    long long valid = 0;                         // sequences with tasks
+    for (int b0 = 0; b0 < a.B; b0 += 32) {
         const int c = b0 == 0 ? mine : b0 + lane < a.B ? tiles_of(b0 + lane) : 0;
-        int upto = c;
+        valid += __popc(__ballot_sync(0xffffffffu, c > 0));
+    }
+    const long long total_v = total + valid * tasks * lead;
+    int b = 0;                                   // of the share's first tile
+    long long prefix = 0, before = 0;            // tiles, and tasks, before sequence b
+    auto border = [&](long long i, int &sb, long long &sprefix, long long &sbefore) -> long long {
+        const long long v = i * total_v / nc;
+        sprefix = sbefore = 0;
+        for (int b0 = 0; b0 < a.B; b0 += 32) {
+            const int c = b0 == 0 ? mine : b0 + lane < a.B ? tiles_of(b0 + lane) : 0;
+            int upto = c, some = c > 0;
 #pragma unroll
-        for (int x = 1; x < 32; x <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, upto, x);
-            if (lane >= x) upto += y;
+            for (int x = 1; x < 32; x <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, upto, x), z = __shfl_up_sync(0xffffffffu, some, x);
+                if (lane >= x) {
+                    upto += y;
+                    some += z;
+                }
+            }
+            const long long v_end = sprefix + sbefore * lead + ((long long)upto + (long long)some * lead) * tasks;
+            const uint32_t past = __ballot_sync(0xffffffffu, v_end > v);
+            if (past) {
+                const int who = __ffs(past) - 1, cw = __shfl_sync(0xffffffffu, c, who);
+                sb = b0 + who;
+                sprefix += (long long)(__shfl_sync(0xffffffffu, upto, who) - cw) * tasks;
+                sbefore += (long long)(__shfl_sync(0xffffffffu, some, who) - 1) * tasks;
+                const long long in = v - sprefix - sbefore * lead, t = in / (cw + lead);
+                return sprefix + t * cw + max(0ll, in - t * (cw + lead) - lead);
+            }
+            sprefix += (long long)__shfl_sync(0xffffffffu, upto, 31) * tasks;
+            sbefore += (long long)__shfl_sync(0xffffffffu, some, 31) * tasks;
         }
-        const uint32_t past = __ballot_sync(0xffffffffu, prefix + (long long)upto * tasks > at);
-        if (past) {
-            const int who = __ffs(past) - 1;
-            b = b0 + who;
-            prefix += (long long)(__shfl_sync(0xffffffffu, upto, who) - __shfl_sync(0xffffffffu, c, who)) * tasks;
-            break;
-        }
-        prefix += (long long)__shfl_sync(0xffffffffu, upto, 31) * tasks;
+        return total;
+    };
+    long long at = 0, end = 0;
+    if (any) {
+        int sb;
+        long long sp, sn;
+        end = border(blockIdx.x + 1, sb, sp, sn);
+        at = border(blockIdx.x, b, prefix, before);
     }
     int nt_task = any ? tiles_of(b) : 1;         // tiles of the task
     int task = any ? (int)((at - prefix) / nt_task) : 0, tile = any ? (int)((at - prefix) - (long long)task * nt_task) : 0;
@@ -335,6 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (++task == tasks && at < end) {
             task = 0;
             prefix += (long long)nt_task * tasks;
+            before += tasks;
             do nt_task = tiles_of(++b);
             while (nt_task == 0);
         }
@@ -660,8 +689,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 sm.lse[tid] = sum == 0.0f ? kNone : fmaf(back, ref, log2f(sum));
             }
             const bool whole = n_t == nt_task;
-            const long long ts = prefix + (long long)task * nt_task;      // the task's first tile
-            const int c0 = (int)(((ts + 1) * nc + total - 1) / total) - 1, c1 = (int)(((ts + nt_task) * nc + total - 1) / total) - 1;
+            // the CTAs whose shares hold the task's first and last tile
+            const long long ts = prefix + (long long)task * nt_task + (before + task + 1) * lead;
+            const int c0 = (int)(((ts + 1) * nc + total_v - 1) / total_v) - 1,
+                      c1 = (int)(((ts + nt_task) * nc + total_v - 1) / total_v) - 1;
             const int seg_b = b, seg_task = task;
             next(n_t);
             if (at < end) fetch_q(b, task);                       // the next segment's Q, under this one's end
@@ -690,16 +721,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int n0 = 8 * grp; n0 < nq; n0 += 8 * kGroups) {
                     uint32_t u[8];
                     umma::tmem_ld_cols<8>(tmem + lanes + cO + n0, u);
+                    float inv[8], lse[8];
+                    long long row[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        inv[k] = sm.inv[n0 + k];
+                        lse[k] = sm.lse[n0 + k];
+                        row[k] = whole ? sm.orow[n0 + k] : 0;
+                    }
                     umma::tmem_ld_wait();
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
-                        const int n = n0 + k;
-                        const float o = sm.lse[n] == kNone ? 0.0f : __uint_as_float(u[k]) * sm.inv[n];
-                        if (n < nq) {
+                        const float o = lse[k] == kNone ? 0.0f : __uint_as_float(u[k]) * inv[k];
+                        if (n0 + k < nq) {
                             if (whole)
-                                a.o[sm.orow[n] + d] = float_to_bf16_bits(o);
+                                a.o[row[k] + d] = float_to_bf16_bits(o);
                             else
-                                __stcg(slot + n * D + d, o);
+                                __stcg(slot + (n0 + k) * D + d, o);
                         }
                     }
                 }
