@@ -308,8 +308,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const long long nc = min((long long)gridDim.x, total);
     const bool any = blockIdx.x < nc;
     // Beginning and ending a segment (Q, the first tile's way through the products, sums, results) takes as
-    // long as some six tiles; where a CTA has fewer than twelve, half of them: few tiles are better spread.
-    const int lead = (int)min(6ll, total / (2ll * gridDim.x));
+    // long as some eight tiles (measured: 4, 6, 8, 11, 15 give 41.8, 40.6, 38.1, 38.2, 38.1 us at 32 sequences,
+    // gamma 8); where a CTA has fewer than sixteen, half of them: few tiles are better spread.
+    const int lead = (int)min(8ll, total / (2ll * gridDim.x));
     // Tiles before share i: a border among a task's leading empty tiles is its first tile.
     long long valid = 0;                         // sequences with tasks
     for (int b0 = 0; b0 < a.B; b0 += 32) {
