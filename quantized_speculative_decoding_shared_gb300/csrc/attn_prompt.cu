@@ -35,7 +35,10 @@ namespace apr {
 constexpr int kTile = 128;                      // query rows per tile, keys per tile
 constexpr int kSoftmax = 256;                   // softmax threads: 128 per row tile
 constexpr int kMmaWarp = kSoftmax / 32, kTmaWarp = kMmaWarp + 1;
-constexpr int kThreads = kSoftmax + 64;
+constexpr int kThreads = kSoftmax + 128;       // (two warps idle: register shares are set by four warps)
+// registers per thread: 384 threads start with 168 and share 64512
+constexpr int kRegsStart = 168, kRegsSoftmax = 216, kRegsRest = 64;
+static_assert(kSoftmax * kRegsSoftmax + 128 * kRegsRest <= kThreads * kRegsStart, "register shares");
 constexpr uint32_t kCols = 512;                 // tensor memory: S0, S1 (128 columns each), O0, O1 (D each)
 constexpr uint32_t kS = 0, kO = 256;
 constexpr float kRescale = 8.0f;                // log2 of the largest p
@@ -75,6 +78,30 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+// two fp32 values in a register pair, and the packed operations on them
+__device__ __forceinline__ uint64_t f2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float lo32(uint64_t v) { return __uint_as_float((uint32_t)v); }
+__device__ __forceinline__ float hi32(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
 }
 
 // K-major operand, 128-byte swizzle: 8 rows x 128 bytes per 1024-byte atom, the
@@ -212,6 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int loads = 0;
     bool issued = false;
     auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
+        if (umma::mbar_try_wait(bar, parity)) return true;
         if (*reinterpret_cast<volatile int *>(&sm.timeout)) return false;
         if (umma::mbar_wait(bar, parity, wait_limit)) return true;
         *reinterpret_cast<volatile int *>(&sm.timeout) = 1;
@@ -253,8 +281,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     umma::fence_after_sync();
 
-    if (n > 0 && warp == kTmaWarp) {
-        if (lane == 0) {
+    if (warp >= kMmaWarp) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
+        if (n > 0 && warp == kTmaWarp && lane == 0) {
             for (int i = loads; i < 2 * n; ++i) {                      // K_0, V_0, K_1, V_1, ...
                 const int s = i % NS;
                 if (!wait(&sm.empty[s], (uint32_t)((i / NS + 1) & 1))) break;
@@ -265,9 +294,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                       k0 + (i >> 1) * kTile, &sm.full[s]);
                 loads = i + 1;
             }
-        }
-    } else if (n > 0 && warp == kMmaWarp) {
-        if (lane == 0) {
+        } else if (n > 0 && warp == kMmaWarp && lane == 0) {
             constexpr uint32_t id_s = umma::instr_desc(1, 1, kTile, kTile);
             constexpr uint32_t id_o = umma::instr_desc(1, 1, kTile, D) | (1u << 16);      // B is MN-major
             const uint32_t q_addr = umma::smem_addr(sq), kv_addr = umma::smem_addr(skv);
@@ -310,7 +337,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         }
-    } else if (work && warp < kMmaWarp && (warp >> 2) < nt) {
+    } else {
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+      if (work && (warp >> 2) < nt) {
         const int t = warp >> 2;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t ts = tmem + lanes + kS + t * kTile, to = tmem + lanes + kO + t * kTile;
@@ -342,9 +371,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             float mx[4];
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-                mx[x] = __uint_as_float(s[x][0]);
+                mx[x] = fmaxf(__uint_as_float(s[x][0]), __uint_as_float(s[x][1]));
 #pragma unroll
-                for (int y = 1; y < 32; ++y) mx[x] = fmaxf(mx[x], __uint_as_float(s[x][y]));
+                for (int y = 2; y < 32; y += 2) mx[x] = max3(mx[x], __uint_as_float(s[x][y]), __uint_as_float(s[x][y + 1]));
             }
             const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
             if (i == 0) {
@@ -366,22 +395,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            const float mc = -m * c;
-            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            const uint64_t cc = f2(c, c), mc = f2(-m * c, -m * c);
+            uint64_t sum[4] = {0, 0, 0, 0};
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 uint32_t w[32];
 #pragma unroll
                 for (int y = 0; y < 32; ++y) {
-                    const float p0 = ex2(fmaf(__uint_as_float(s[2 * x + (y >> 4)][(2 * y) & 31]), c, mc));
-                    const float p1 = ex2(fmaf(__uint_as_float(s[2 * x + (y >> 4)][(2 * y + 1) & 31]), c, mc));
-                    sum[y & 1] += p0;
-                    sum[2 + (y & 1)] += p1;
+                    const uint64_t d = fma2(f2(__uint_as_float(s[2 * x + (y >> 4)][(2 * y) & 31]), __uint_as_float(s[2 * x + (y >> 4)][(2 * y + 1) & 31])), cc, mc);
+                    const float p0 = ex2(lo32(d)), p1 = ex2(hi32(d));
+                    sum[y & 3] = add2(sum[y & 3], f2(p0, p1));
                     w[y] = pack_bf16(p0, p1);
                 }
                 umma::tmem_st32(ts + 32 * x, w);
             }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
+            l += lo32(sum[0]) + hi32(sum[0]);
             umma::tmem_st_wait();
             umma::fence_before_sync();
             umma::mbar_arrive(&sm.pfull[t]);
@@ -424,6 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 row_again<D>(a, h, a.q + (size_t)(q0 + pw) * a.ldq + hw, k0, pw + off, a.o + (size_t)(q0 + pw) * a.ldo + hw);
             }
         }
+      }
     }
 
     // after a timeout: copies and products in flight finish (bounded) before
