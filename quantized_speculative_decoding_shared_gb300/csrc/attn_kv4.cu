@@ -371,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
 
     int loads = 0;                               // tiles whose copies were issued
-    bool issued = false;
+    bool issued = false, elected = false;
     if (warp == kLoadWarp) {
         if (lane == 0) {
             while (at < end) {
@@ -389,7 +389,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
     } else if (warp == kScoreWarp) {
-        if (lane == 0) {
+        // (the whole warp walks the loop and one lane issues: the descriptors stay in uniform registers)
+        elected = umma::elect_one();
+        {
             constexpr uint32_t id = umma::instr_desc(0, 0, kTok, N);                            // f16, f32 sums
             const uint64_t qd = umma::smem_desc(umma::smem_addr(sq), N * 16, 128);
             int g = 0;
@@ -402,17 +404,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ok = wait(&sm.kfull[s], g / kGroups);
                     if (!ok) break;
                     umma::fence_after_sync();
+                    if (elected) {
 #pragma unroll
-                    for (int kk = 0; kk < kSteps + 1; ++kk)
-                        umma::mma_bf16_ta(tmem + cS + s * N, tmem + cK + s * 80 + kk * 8, qd + (uint64_t)(kk * 2 * N), id, kk != 0);
-                    umma::mma_commit(&sm.sfull[s]);
+                        for (int kk = 0; kk < kSteps + 1; ++kk)
+                            umma::mma_bf16_ta(tmem + cS + s * N, tmem + cK + s * 80 + kk * 8, qd + (uint64_t)(kk * 2 * N), id, kk != 0);
+                        umma::mma_commit(&sm.sfull[s]);
+                    }
+                    __syncwarp();
                     issued = true;
                 }
                 next(n_t);
             }
         }
     } else if (warp == kValueWarp) {
-        if (lane == 0) {
+        elected = umma::elect_one();
+        {
             constexpr uint32_t id = umma::instr_desc(1, 1, kTok, N) | (1u << 15) | (1u << 16);  // bf16, both MN-major
             int g = 0;
             bool ok = true;
@@ -425,13 +431,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     umma::fence_after_sync();
                     const uint64_t vd = umma::smem_desc(umma::smem_addr(sv + s * kVBuf), 128, kTok * 16);
                     const uint64_t pd = umma::smem_desc(umma::smem_addr(sp + s * kP), 128, kTok * 16);
+                    if (elected) {
 #pragma unroll
-                    for (int kk = 0; kk < kTok / 16; ++kk)
-                        umma::mma_bf16(tmem + cO, vd + kk * 16, pd + kk * 16, id, (i | kk) != 0);
-                    umma::mma_commit(&sm.pdone[s]);
+                        for (int kk = 0; kk < kTok / 16; ++kk)
+                            umma::mma_bf16(tmem + cO, vd + kk * 16, pd + kk * 16, id, (i | kk) != 0);
+                        umma::mma_commit(&sm.pdone[s]);
+                    }
+                    __syncwarp();
                     issued = true;
                 }
-                if (ok) umma::mma_commit(&sm.odone);
+                if (ok && elected) umma::mma_commit(&sm.odone);
+                __syncwarp();
                 next(n_t);
             }
         }
@@ -857,7 +867,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (warp == kLoadWarp && lane == 0)
             for (int i = max(0, loads - kStages); i < loads; ++i)
                 umma::mbar_wait(&sm.full[i % kStages], (uint32_t)((i / kStages) & 1), kWaitLimit);
-        if ((warp == kScoreWarp || warp == kValueWarp) && lane == 0 && issued) {
+        if ((warp == kScoreWarp || warp == kValueWarp) && elected && issued) {
             umma::mma_commit(&sm.drain[warp - kScoreWarp]);
             umma::mbar_wait(&sm.drain[warp - kScoreWarp], 0, kWaitLimit);
         }

@@ -84,6 +84,13 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, uint32
     return false;
 }
 
+// true in one lane of a converged warp (the same one each time)
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile("{.reg .pred p; elect.sync _|p, 0xFFFFFFFF; selp.u32 %0, 1, 0, p;}\n" : "=r"(one));
+    return one != 0;
+}
+
 // ---- MMA ----
 __device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                          uint32_t accumulate) {
