@@ -14,8 +14,7 @@
 //     (exact: bf16 has 8 bits, fp16 11, and what falls below 2^-24 is below 2^-39
 //     of the row's largest), in the order of d that the unpacked codes have, times 1/16
 //     against 16 c.  z enters as one more K step: z against -sum q in three fp16 parts.
-//   O^T (d x rows) += V^T P^T in bf16: V's codes as 128 + c by one logic operation, minus
-//     (128 + z) exactly; P^T = p s with the range of fp32 (in fp16 the weights of
+//   O^T (d x rows) += V^T P^T in bf16: c - z exactly; P^T = p s with the range of fp32 (in fp16 the weights of
 //     far positions would round to subnormals).  Both operands lie in shared memory
 //     position by position, an MN-major layout without swizzle: 16-byte pieces of
 //     consecutive positions side by side.
@@ -65,7 +64,10 @@ constexpr int kMaxN = 64, kMaxD = 128;
 constexpr float kNone = -1.0e30f;               // log2 of the sum of a row that sees nothing
 constexpr float kOver = 7.9228162514264338e28f; // 2^96: a thread's sum of p from where a segment is taken again
 
-constexpr int kStages = 3;                      // tiles of codes in flight
+// tiles of codes in flight: what shared memory has room for (3 at N = 16 left the groups waiting for copies)
+template <int N>
+constexpr int n_stages() { return N == 16 ? 6 : N == 32 ? 5 : 3; }
+constexpr int kMaxStages = 6;
 constexpr int kVBuf = kTok * kMaxD * 2;         // V operand (D = 64: the products' rows 64 .. 127 read the rest, unused)
 template <int D>
 constexpr int side_bytes() { return kTok * D / 2; }
@@ -80,7 +82,7 @@ struct Join {                                   // a task to join: its parts (0:
 
 template <int N>
 struct Ctl {
-    uint64_t full[kStages], empty[kStages];     // codes landed; unpacked
+    uint64_t full[kMaxStages], empty[kMaxStages];     // codes landed; unpacked
     uint64_t kfull[kGroups], sfull[kGroups], pfull[kGroups], vfull[kGroups], pdone[kGroups];   // K in tensor memory, S^T, P^T, V, O^T += done
     uint64_t qfull, ref, odone, drain[2];       // per segment: Q written, reference known, O^T complete
     float4 back[N / 2];                         // score of rows n, n + 1: {back, back'}({s u - ref, s u' - ref'}), as {back, back', -ref, -ref'}
@@ -95,7 +97,7 @@ struct Ctl {
 
 template <int D, int N>
 constexpr size_t smem_bytes() {
-    return 1024 + (size_t)kStages * 2 * side_bytes<D>() + kGroups * kVBuf + kGroups * p_bytes<N>() + q_bytes<D, N>() + sizeof(Ctl<N>);
+    return 1024 + (size_t)n_stages<N>() * 2 * side_bytes<D>() + kGroups * kVBuf + kGroups * p_bytes<N>() + q_bytes<D, N>() + sizeof(Ctl<N>);
 }
 
 struct Args {
@@ -240,7 +242,7 @@ template <int D, int N>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_kv4_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                     const __grid_constant__ Args a, uint32_t wait_limit) {
-    constexpr int kSide = side_bytes<D>(), kP = p_bytes<N>();
+    constexpr int kSide = side_bytes<D>(), kP = p_bytes<N>(), kStages = n_stages<N>();
     constexpr int kSteps = D / 16;                               // MMA steps of S^T (one more holds z)
     constexpr uint32_t cS = 0, cK = kGroups * N, cO = cK + kGroups * 80;   // the groups' S^T and K operands (80 columns each), O^T
     constexpr uint32_t kCols = 512;
@@ -568,12 +570,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 umma::fence_before_sync();
                 __syncwarp();
                 if (lane == 0) umma::mbar_arrive(&sm.kfull[grp]);
-                // ---- V into its operand layout, once the group's last tile's products have read it ----
-                // (128 + z) as a bf16 pair: fp16 z + 1024 has the integer z in its low bits.  Whatever the
-                // word holds, it is finite: a bad word at an unseen place does not reach other rows as 0 times NaN
-                const uint32_t z = (uint32_t)__half_as_ushort(__hadd(__ushort_as_half((uint16_t)(vw >> 16)), __ushort_as_half(0x6400))) & 15u;
-                const uint32_t zz = 0x43004300u | z | (z << 16);
-                const __nv_bfloat162 z2 = *reinterpret_cast<const __nv_bfloat162 *>(&zz);
+                // ---- V into its operand layout, once the products have read what was there ----
+                // The bits of a code at the bottom of a bf16 lane are c 2^-133 (a subnormal), one nibble higher
+                // 16 c 2^-133; one fused step brings them up by 2^127 and takes z off exactly: (c - z) 2^-6 and
+                // (c - z) 2^-2.  z = 0 .. 15 whatever the word holds (fp16 z + 1024 has the integer in its low
+                // bits): a bad word at an unseen place does not reach other rows as 0 times NaN.
+                const float z = (float)((uint32_t)__half_as_ushort(__hadd(__ushort_as_half((uint16_t)(vw >> 16)), __ushort_as_half(0x6400))) & 15u);
+                const __nv_bfloat162 up2 = __float2bfloat162_rn(1.7014118346046923e38f), z_lo = __float2bfloat162_rn(z * -0.015625f),
+                                     z_hi = __float2bfloat162_rn(z * -0.25f);
 #pragma unroll
                 for (int y = 0; y < D / 32; ++y) x[y] = code_piece<D>(kcode + kSide, tok, y);
                 // the next copy into the stage comes by the async proxy: these reads are fenced against it
@@ -586,11 +590,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t ww[4] = {x[y].x, x[y].y, x[y].z, x[y].w};
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
+                        const uint32_t cc[4] = {ww[k] & 0x000F000Fu, ww[k] & 0x00F000F0u, (ww[k] >> 8) & 0x000F000Fu, (ww[k] >> 8) & 0x00F000F0u};
                         uint32_t r[4];
 #pragma unroll
                         for (int f = 0; f < 4; ++f) {
-                            const uint32_t cc = ((ww[k] >> (4 * f)) & 0x000F000Fu) | 0x43004300u;
-                            const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&cc), z2);
+                            const __nv_bfloat162 v = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&cc[f]), up2, f & 1 ? z_hi : z_lo);
                             r[f] = *reinterpret_cast<const uint32_t *>(&v);
                         }
                         *reinterpret_cast<uint4 *>(v_dst + (4 * y + k) * (kTok * 16)) = make_uint4(r[0], r[1], r[2], r[3]);
@@ -729,6 +733,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             } else if (32 * (warp & 3) < D) {                      // thread = d; each group every third eight rows
                 const int L = 32 * (warp & 3) + lane, d = (L & ~7) | place_d(L & 7);
+                const float scale = L & 2 ? 4.0f : 64.0f;          // (the operand's 2^-2 and 2^-6)
                 for (int n0 = 8 * grp; n0 < nq; n0 += 8 * kGroups) {
                     uint32_t u[8];
                     umma::tmem_ld_cols<8>(tmem + lanes + cO + n0, u);
@@ -736,7 +741,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     long long row[8];
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
-                        inv[k] = sm.inv[n0 + k];
+                        inv[k] = sm.inv[n0 + k] * scale;
                         lse[k] = sm.lse[n0 + k];
                         row[k] = whole ? sm.orow[n0 + k] : 0;
                     }
