@@ -18,7 +18,7 @@
 //     far positions would round to subnormals).  Both operands lie in shared memory
 //     position by position, an MN-major layout without swizzle: 16-byte pieces of
 //     consecutive positions side by side.
-// Three groups of four warps take the tiles in turn (thread = position: unpack K,
+// Three or four groups of four warps take the tiles in turn (thread = position: unpack K,
 // unpack V while S^T is formed, then the softmax); one lane issues the products of
 // S^T, one those of O^T (each waits for its own operands, so that the tensor cores
 // have the other's meanwhile: at these widths a product takes some 55 clocks
@@ -56,18 +56,23 @@ namespace akv {
 
 constexpr int kMaxR = QSPEC_MAX_GAMMA + 1;
 constexpr int kTok = 128;                       // positions per tile
-constexpr int kGroups = 3, kWorkWarps = 4 * kGroups, kWork = 32 * kWorkWarps;
-constexpr int kScoreWarp = kWorkWarps, kValueWarp = kScoreWarp + 1, kLoadWarp = kValueWarp + 1;   // one lane each: S^T, O^T products, copies
-constexpr int kThreads = kWork + 96;
+// Groups of four warps: four where their registers (96 per thread then), V operands and copies have room
+template <int N>
+struct Cfg {
+    static constexpr int kGroups = N == 16 ? 4 : 3, kWorkWarps = 4 * kGroups, kWork = 32 * kWorkWarps;
+    static constexpr int kScoreWarp = kWorkWarps, kValueWarp = kScoreWarp + 1, kLoadWarp = kValueWarp + 1;   // one lane each: S^T, O^T products, copies
+    static constexpr int kThreads = kWork + 96;
+    // Tiles of codes in flight.  A stage always serves the same group: one whose next tile came into another
+    // group's stage could look at that stage's barrier a whole phase early, and take the phase before for its own.
+    static constexpr int kStages = kGroups;
+    static_assert(kStages % kGroups == 0, "a stage serves one group");
+};
 constexpr int kMaxCtas = 160;                   // one per SM
 constexpr int kMaxN = 64, kMaxD = 128;
 constexpr float kNone = -1.0e30f;               // log2 of the sum of a row that sees nothing
 constexpr float kOver = 7.9228162514264338e28f; // 2^96: a thread's sum of p from where a segment is taken again
 
-// tiles of codes in flight: what shared memory has room for (3 at N = 16 left the groups waiting for copies)
-template <int N>
-constexpr int n_stages() { return N == 16 ? 6 : N == 32 ? 5 : 3; }
-constexpr int kMaxStages = 6;
+constexpr int kMaxStages = 4;
 constexpr int kVBuf = kTok * kMaxD * 2;         // V operand (D = 64: the products' rows 64 .. 127 read the rest, unused)
 template <int D>
 constexpr int side_bytes() { return kTok * D / 2; }
@@ -82,6 +87,7 @@ struct Join {                                   // a task to join: its parts (0:
 
 template <int N>
 struct Ctl {
+    static constexpr int kGroups = Cfg<N>::kGroups, kWorkWarps = Cfg<N>::kWorkWarps;
     uint64_t full[kMaxStages], empty[kMaxStages];     // codes landed; unpacked
     uint64_t kfull[kGroups], sfull[kGroups], pfull[kGroups], vfull[kGroups], pdone[kGroups];   // K in tensor memory, S^T, P^T, V, O^T += done
     uint64_t qfull, ref, odone, drain[2];       // per segment: Q written, reference known, O^T complete
@@ -97,7 +103,7 @@ struct Ctl {
 
 template <int D, int N>
 constexpr size_t smem_bytes() {
-    return 1024 + (size_t)n_stages<N>() * 2 * side_bytes<D>() + kGroups * kVBuf + kGroups * p_bytes<N>() + q_bytes<D, N>() + sizeof(Ctl<N>);
+    return 1024 + (size_t)Cfg<N>::kStages * 2 * side_bytes<D>() + Cfg<N>::kGroups * (kVBuf + p_bytes<N>()) + q_bytes<D, N>() + sizeof(Ctl<N>);
 }
 
 struct Args {
@@ -239,10 +245,12 @@ __device__ __noinline__ float plain_row(const Args &a, const uint16_t *qrow, siz
 }
 
 template <int D, int N>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
     attn_kv4_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                     const __grid_constant__ Args a, uint32_t wait_limit) {
-    constexpr int kSide = side_bytes<D>(), kP = p_bytes<N>(), kStages = n_stages<N>();
+    constexpr int kSide = side_bytes<D>(), kP = p_bytes<N>(), kStages = Cfg<N>::kStages;
+    constexpr int kGroups = Cfg<N>::kGroups, kWorkWarps = Cfg<N>::kWorkWarps, kWork = Cfg<N>::kWork;
+    constexpr int kScoreWarp = Cfg<N>::kScoreWarp, kValueWarp = Cfg<N>::kValueWarp, kLoadWarp = Cfg<N>::kLoadWarp;
     constexpr int kSteps = D / 16;                               // MMA steps of S^T (one more holds z)
     constexpr uint32_t cS = 0, cK = kGroups * N, cO = cK + kGroups * 80;   // the groups' S^T and K operands (80 columns each), O^T
     constexpr uint32_t kCols = 512;
@@ -479,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int nq = min(N, a.R * a.G - row0);
             const int p0 = tile * kTok;
             const size_t head = ((size_t)b * a.H + h) * a.T;
-            // this group's tiles: i0, i0 + 3, ...; the scale words one tile ahead
+            // this group's tiles: i0, i0 + kGroups, ...; the scale words one tile ahead
             const int i0 = (grp + kGroups - g % kGroups) % kGroups;
             uint32_t kn = 0, vn = 0;
             if (i0 < n_t && p0 + i0 * kTok + tok < len) {
@@ -902,7 +910,7 @@ int launch(Args a, cudaStream_t stream) {
     if (rc) return rc;
     const long long most = (long long)a.B * a.H * a.blocks * std::max(1, (a.T + kTok - 1) / kTok);   // tiles at full lengths
     const unsigned grid = (unsigned)std::min<long long>(std::min(sm_count(), kMaxCtas), most);
-    return launch_pdl("qspec_attn_kv4", kern, dim3(grid), dim3(kThreads), smem_bytes<D, N>(), stream, tk, tv, a, kWaitLimit);
+    return launch_pdl("qspec_attn_kv4", kern, dim3(grid), dim3(Cfg<N>::kThreads), smem_bytes<D, N>(), stream, tk, tv, a, kWaitLimit);
 }
 
 // rows per pass: the fewest passes over the cache, then the narrowest that holds them
