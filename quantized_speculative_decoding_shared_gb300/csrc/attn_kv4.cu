@@ -18,7 +18,7 @@
 //     far positions would round to subnormals).  Both operands lie in shared memory
 //     position by position, an MN-major layout without swizzle: 16-byte pieces of
 //     consecutive positions side by side.
-// Three or four groups of four warps take the tiles in turn (thread = position: unpack K,
+// Three groups of four warps take the tiles in turn (thread = position: unpack K,
 // unpack V while S^T is formed, then the softmax); one lane issues the products of
 // S^T, one those of O^T (each waits for its own operands, so that the tensor cores
 // have the other's meanwhile: at these widths a product takes some 55 clocks
@@ -56,15 +56,14 @@ namespace akv {
 
 constexpr int kMaxR = QSPEC_MAX_GAMMA + 1;
 constexpr int kTok = 128;                       // positions per tile
-// Groups of four warps: four where their registers (96 per thread then), V operands and copies have room
 template <int N>
 struct Cfg {
-    static constexpr int kGroups = N == 16 ? 4 : 3, kWorkWarps = 4 * kGroups, kWork = 32 * kWorkWarps;
+    static constexpr int kGroups = 3, kWorkWarps = 4 * kGroups, kWork = 32 * kWorkWarps;
     static constexpr int kScoreWarp = kWorkWarps, kValueWarp = kScoreWarp + 1, kLoadWarp = kValueWarp + 1;   // one lane each: S^T, O^T products, copies
     static constexpr int kThreads = kWork + 96;
     // Tiles of codes in flight.  A stage always serves the same group: one whose next tile came into another
     // group's stage could look at that stage's barrier a whole phase early, and take the phase before for its own.
-    static constexpr int kStages = kGroups;
+    static constexpr int kStages = N == 16 ? 6 : 3;
     static_assert(kStages % kGroups == 0, "a stage serves one group");
 };
 constexpr int kMaxCtas = 160;                   // one per SM
@@ -72,7 +71,7 @@ constexpr int kMaxN = 64, kMaxD = 128;
 constexpr float kNone = -1.0e30f;               // log2 of the sum of a row that sees nothing
 constexpr float kOver = 7.9228162514264338e28f; // 2^96: a thread's sum of p from where a segment is taken again
 
-constexpr int kMaxStages = 4;
+constexpr int kMaxStages = 6;
 constexpr int kVBuf = kTok * kMaxD * 2;         // V operand (D = 64: the products' rows 64 .. 127 read the rest, unused)
 template <int D>
 constexpr int side_bytes() { return kTok * D / 2; }
@@ -315,7 +314,10 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
         total += __reduce_add_sync(0xffffffffu, c);
     }
     total *= tasks;
-    const long long nc = min((long long)gridDim.x, total);
+    // Few tiles: four to a CTA rather than one, since every part of a task more is another result to join (one
+    // sequence of 333 / 4000 positions, one row: 7.8 / 12.1 us with four, 9.5 / 13.7 us with one); with 64 rows a tile
+    // takes longer than its part in a join, and one is better (18.8 for 22.9 us at 4 sequences of 1000, gamma 8).
+    const long long nc = min((long long)gridDim.x, N == 64 ? total : max(total / 4, min(total, (long long)tasks)));
     const bool any = blockIdx.x < nc;
     // Beginning and ending a segment (Q, the first tile's way through the products, sums, results) takes as
     // long as some eight tiles (measured: 4, 6, 8, 11, 15 give 41.8, 40.6, 38.1, 38.2, 38.1 us at 32 sequences,
@@ -632,7 +634,7 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
                 const uint64_t sk2 = f2(sk, sk), sv2 = f2(svv, svv);
                 auto weights = [&](auto edge_c) {
                     constexpr bool kEdge = decltype(edge_c)::value;
-                    constexpr int kC = N < 32 ? 16 : 32;
+                    constexpr int kC = N == 32 ? 32 : 16;
 #pragma unroll
                     for (int n0 = 0; n0 < N; n0 += kC) {
                         if (n0 >= nq) {                           // rows past nq hold nothing
