@@ -300,6 +300,9 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
         return false;
     };
 
+    // (the votes keep an issuing warp together where a wait runs out)
+    auto all = [](bool mine) { return __all_sync(0xffffffffu, mine) != 0; };
+
     // ---- this CTA's share of the tiles (every warp finds it for itself) ----
     const int tasks = a.H * a.blocks;           // per sequence
     auto tiles_of = [&](int b) -> int {
@@ -410,10 +413,10 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
             bool ok = true;
             for (int seg = 0; at < end; ++seg) {
                 const int n_t = (int)min((long long)(nt_task - tile), end - at);
-                ok = ok && wait(&sm.qfull, seg);
+                ok = all(ok && wait(&sm.qfull, seg));
                 for (int i = 0; i < n_t && ok; ++i, ++g) {
                     const int s = g % kGroups;
-                    ok = wait(&sm.kfull[s], g / kGroups);
+                    ok = all(wait(&sm.kfull[s], g / kGroups));
                     if (!ok) break;
                     umma::fence_after_sync();
                     if (elected) {
@@ -438,7 +441,7 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
                 const int n_t = (int)min((long long)(nt_task - tile), end - at);
                 for (int i = 0; i < n_t && ok; ++i, ++g) {
                     const int s = g % kGroups;
-                    ok = wait(&sm.vfull[s], g / kGroups) && wait(&sm.pfull[s], g / kGroups);
+                    ok = all(wait(&sm.vfull[s], g / kGroups) && wait(&sm.pfull[s], g / kGroups));
                     if (!ok) break;
                     umma::fence_after_sync();
                     const uint64_t vd = umma::smem_desc(umma::smem_addr(sv + s * kVBuf), 128, kTok * 16);

@@ -8,14 +8,19 @@
 // takes two consecutive tiles, so each key tile of 128 rows is read once for 256
 // rows and both tiles end at nearly the same key.  Per key tile and row tile t:
 //   S_t = Q_t K^T (tcgen05, both operands in shared memory, S in tensor memory),
-//   the softmax warps of t read S_t (thread = row), keep a running reference m and
-//   sum l, and write p = 2^(c (s - m)) as bf16 over S_t in tensor memory,
+//   the softmax warps of t read S_t (thread = row) and write p = 2^(c s - m) as
+//   bf16 over S_t in tensor memory, in two halves, and keep the sum l,
 //   O_t += P_t V (P from tensor memory, V rows as they are: an MN-major operand).
 // The issuing lane interleaves the two tiles, so one tile's softmax runs under
-// the other's products.  m is only moved (and O_t rescaled, by the softmax
-// warps themselves) when a score passes it by more than 2^8: the completed
-// product S_t(i + 1) implies O_t += P_t(i) V has completed, so no other
-// synchronisation is needed for it.
+// the other's products.
+// The reference m is the row's maximum over the first key tile and after that follows
+// the sums instead of the maxima: where a tile's sum of p passes 2^12, the next tile
+// begins by moving m up (by a power of two, exactly) and rescaling l and O_t.  No
+// pass over the scores looks for their maximum, and nothing is lost meanwhile, p and O
+// being floating point; a score that passes m by some 2^90 within one tile ends
+// in a result that is not finite, and such rows are computed again.  The softmax
+// warps rescale O_t themselves: the completed product S_t(i + 1) implies that
+// O_t += P_t(i) V has completed, so no other synchronisation is needed for it.
 //
 // Bound: tensor cores (512 clocks per 128 x 128 tile at D = 128) with the exponentials
 // close behind (16384 per tile).
@@ -41,7 +46,7 @@ constexpr int kRegsStart = 168, kRegsSoftmax = 216, kRegsRest = 64;
 static_assert(kSoftmax * kRegsSoftmax + 128 * kRegsRest <= kThreads * kRegsStart, "register shares");
 constexpr uint32_t kCols = 512;                 // tensor memory: S0, S1 (128 columns each), O0, O1 (D each)
 constexpr uint32_t kS = 0, kO = 256;
-constexpr float kRescale = 8.0f;                // log2 of the largest p
+constexpr float kGrown = 4096.0f;               // a tile's sum of p from where the reference moves
 
 template <int D>
 constexpr int tile_bytes() { return kTile * D * 2; }
@@ -50,11 +55,13 @@ constexpr int ring() { return D == 128 ? 4 : 8; }
 
 struct Ctl {
     uint64_t full[8], empty[8];                 // K / V tiles: landed, read
-    uint64_t sfull[2], pfull[2], odone[2];      // S_t written, P_t written (and S_t read), O_t complete
+    uint64_t sfull[2], pfull[2][2], odone[2];   // S_t written, each half of P_t written (and S_t read), O_t complete
     uint64_t drain;
     uint32_t tmem;
     int timeout;
-    int unit[6];                                // b found, q0, lq, k0, lk, first flattened row
+    int found, q0, lq, k0, lk;                  // the unit's sequence (none: found is 0)
+    int left, p_last;                           // flattened rows from the unit's first on (at most 256); its last row's position
+    int p[2], g[2];                             // each tile's first row: position and head of the group
 };
 
 template <int D>
@@ -66,7 +73,10 @@ struct Args {
     uint16_t *o;
     int32_t *st;
     int ldq, ldk, ldv, ldo, q_rows, k_rows, B, H, G;
+    uint32_t g_mul;                             // n / G = umulhi(n, g_mul) for n < G + 128 (G = 1: 0)
     float scale;
+
+    __device__ __forceinline__ int over_g(int n) const { return g_mul ? (int)__umulhi((uint32_t)n, g_mul) : n; }
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -170,12 +180,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int t = 0; t < 2; ++t) {
             umma::mbar_init(&sm.sfull[t], 1);
-            umma::mbar_init(&sm.pfull[t], kTile);
+            umma::mbar_init(&sm.pfull[t][0], kTile);
+            umma::mbar_init(&sm.pfull[t][1], kTile);
             umma::mbar_init(&sm.odone[t], 1);
         }
         umma::mbar_init(&sm.drain, 1);
         sm.timeout = 0;
-        sm.unit[0] = -1;
+        sm.found = 0;
         umma::mbar_fence_init();
     }
     pdl_launch_dependents();
@@ -208,12 +219,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane >= x) upto += y;
             }
             if (left >= upto - units && left < upto) {
-                sm.unit[1] = q0;
-                sm.unit[2] = lq;
-                sm.unit[3] = k0;
-                sm.unit[4] = lk;
-                sm.unit[5] = units - 1 - (left - (upto - units));
-                sm.unit[0] = b;
+                const long long row0 = (long long)(units - 1 - (left - (upto - units))) * (2 * kTile), rows = (long long)lq * G;
+                sm.q0 = q0;
+                sm.lq = lq;
+                sm.k0 = k0;
+                sm.lk = lk;
+                sm.left = (int)min(rows - row0, 2ll * kTile);
+                sm.p_last = (int)((row0 + sm.left - 1) / G);
+                for (int t = 0; t < 2; ++t) {
+                    sm.p[t] = (int)((row0 + t * kTile) / G);
+                    sm.g[t] = (int)(row0 + t * kTile - (long long)sm.p[t] * G);
+                }
+                sm.found = 1;
             }
             const int total = __shfl_sync(0xffffffffu, upto, 31);
             left = left < total ? -1 : left - total;
@@ -227,14 +244,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncthreads();
     const uint32_t tmem = sm.tmem;
-    const bool work = sm.unit[0] >= 0;
-    const int q0 = sm.unit[1], lq = sm.unit[2], k0 = sm.unit[3], lk = sm.unit[4];
-    const long long row0 = (long long)sm.unit[5] * (2 * kTile), rows = (long long)lq * G;
-    const int off = lk - lq;
+    const bool work = sm.found != 0;
+    const int q0 = sm.q0, k0 = sm.k0, off = sm.lk - sm.lq, left = work ? sm.left : 0;
     // key tiles that the unit's last row sees
-    const int p_last = work ? (int)((min(row0 + 2 * kTile, rows) - 1) / G) : 0;
-    const int n = work ? max(0, (p_last + off + kTile) / kTile) : 0;
-    const int nt = work && row0 + kTile < rows ? 2 : 1;     // row tiles with rows
+    const int n = work ? max(0, (sm.p_last + off + kTile) / kTile) : 0;
+    const int nt = left > kTile ? 2 : 1;                    // row tiles with rows
 
     int loads = 0;
     bool issued = false, elected = false;
@@ -249,19 +263,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---- Q tiles into shared memory (both operands' swizzle); a negative scale
     // turns the signs, a zero one the values, so that the softmax has c > 0 ----
     if (work && n > 0 && warp < kMmaWarp) {
-        const int t = warp >> 2, w = tid & (kTile - 1);
+        // eight values per thread and step, D / 8 threads a row; every step's load is under way before the first is stored
+        const int t = warp >> 2, w = tid & (kTile - 1), ch = w % (D / 8), r0 = w / (D / 8);
+        constexpr int kStep = kTile / (D / 8), kSteps = D / 8;
         const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u, keep = a.scale != 0.0f ? 0xFFFFFFFFu : 0u;
-#pragma unroll 4
-        for (int it = 0; it < D / 8; ++it) {
-            const int e = it * kTile + w, r = e / (D / 8), ch = e % (D / 8);
-            const long long idx = row0 + t * kTile + r;
-            uint4 x = make_uint4(0, 0, 0, 0);
-            if (idx < rows) {
-                const int p = (int)(idx / G), g = (int)(idx - (long long)p * G);
-                x = *reinterpret_cast<const uint4 *>(a.q + (size_t)(q0 + p) * a.ldq + (size_t)(h * G + g) * D + ch * 8);
-            }
-            x = make_uint4((x.x ^ flip) & keep, (x.y ^ flip) & keep, (x.z ^ flip) & keep, (x.w ^ flip) & keep);
-            *reinterpret_cast<uint4 *>(sq + t * kT + (ch >> 3) * (kTile * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = x;
+        uint4 x[kSteps];
+#pragma unroll
+        for (int it = 0; it < kSteps; ++it) {
+            const int r = it * kStep + r0, gr = sm.g[t] + r, pr = a.over_g(gr);
+            x[it] = make_uint4(0, 0, 0, 0);
+            if (t * kTile + r < left)
+                x[it] = __ldg(reinterpret_cast<const uint4 *>(a.q + (size_t)(q0 + sm.p[t] + pr) * a.ldq + (size_t)(h * G + gr - pr * G) * D + ch * 8));
+        }
+#pragma unroll
+        for (int it = 0; it < kSteps; ++it) {
+            const int r = it * kStep + r0;
+            const uint4 y = make_uint4((x[it].x ^ flip) & keep, (x[it].y ^ flip) & keep, (x[it].z ^ flip) & keep, (x[it].w ^ flip) & keep);
+            *reinterpret_cast<uint4 *>(sq + t * kT + (ch >> 3) * (kTile * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = y;
         }
         umma::fence_proxy_async();
     }
@@ -313,7 +331,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 __syncwarp();
             };
-            bool ok = wait(&sm.full[0], 0);
+            // (the votes keep the warp together where a wait runs out)
+            auto all = [&](bool mine) { return __all_sync(0xffffffffu, mine) != 0; };
+            bool ok = all(wait(&sm.full[0], 0));
             if (ok) {
                 umma::fence_after_sync();
                 for (int t = 0; t < nt; ++t) scores(t, 0);
@@ -323,19 +343,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < n && ok; ++i) {
                 const int sv = (2 * i + 1) % NS, sk = (2 * i + 2) % NS;
                 const bool more = i + 1 < n;
-                ok = wait(&sm.full[sv], (uint32_t)(((2 * i + 1) / NS) & 1)) &&
-                     (!more || wait(&sm.full[sk], (uint32_t)(((2 * i + 2) / NS) & 1)));
+                ok = all(wait(&sm.full[sv], (uint32_t)(((2 * i + 1) / NS) & 1)) &&
+                         (!more || wait(&sm.full[sk], (uint32_t)(((2 * i + 2) / NS) & 1))));
                 for (int t = 0; t < nt && ok; ++t) {
-                    if (!(ok = wait(&sm.pfull[t], (uint32_t)(i & 1)))) break;
-                    umma::fence_after_sync();
                     const uint64_t bd = desc_mn(kv_addr + sv * kT);
-                    if (elected) {
+                    for (int half = 0; half < 2 && ok; ++half) {
+                        if (!(ok = all(wait(&sm.pfull[t][half], (uint32_t)(i & 1))))) break;
+                        umma::fence_after_sync();
+                        if (elected) {
 #pragma unroll
-                        for (int kk = 0; kk < kTile / 16; ++kk)         // 16 keys: 2 groups of 8 rows
-                            umma::mma_bf16_ta(tmem + kO + t * kTile, tmem + kS + t * kTile + kk * 8, bd + (kk * 2048 >> 4), id_o,
-                                              (i | kk) != 0);
-                        if (t == nt - 1) umma::mma_commit(&sm.empty[sv]);
+                            for (int k4 = 0; k4 < kTile / 32; ++k4) {   // 16 keys: 2 groups of 8 rows
+                                const int kk = half * (kTile / 32) + k4;
+                                umma::mma_bf16_ta(tmem + kO + t * kTile, tmem + kS + t * kTile + kk * 8, bd + (kk * 2048 >> 4), id_o,
+                                                  (i | kk) != 0);
+                            }
+                        }
                     }
+                    if (!ok) break;
+                    if (elected && t == nt - 1) umma::mma_commit(&sm.empty[sv]);
                     __syncwarp();
                     if (more) {
                         scores(t, i + 1);
@@ -352,19 +377,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int t = warp >> 2;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t ts = tmem + lanes + kS + t * kTile, to = tmem + lanes + kO + t * kTile;
-        const long long idx = row0 + t * kTile + (warp & 3) * 32 + lane;
-        const bool in = idx < rows;
-        const int p = in ? (int)(idx / G) : 0, g = in ? (int)(idx - (long long)p * G) : 0;
+        const int r = (warp & 3) * 32 + lane, gr = sm.g[t] + r, pr = a.over_g(gr);
+        const bool in = t * kTile + r < left;
+        const int p = in ? sm.p[t] + pr : 0, g = in ? gr - pr * G : 0;
         const int lim = in ? p + off : -1;                              // last key seen
         // tiles from here on are masked for some row of the tile
-        const int first_masked = (int)((row0 + t * kTile) / G) + off;
+        const int first_masked = sm.p[t] + off;
         const float c = a.scale != 0.0f ? fabsf(a.scale) * 1.4426950408889634f : 1.0f;
-        float m = -INFINITY, l = 0.0f;
+        const uint64_t cc = f2(c, c);
+        float m = 0.0f, l = 0.0f, last = 0.0f;                          // reference in log2 units; the last tile's sum
         bool ok = true;
         for (int i = 0; i < n; ++i) {
             // (the vote keeps the warp together where a wait runs out)
             if (!(ok = __all_sync(0xffffffffu, wait(&sm.sfull[t], (uint32_t)(i & 1))))) break;
             umma::fence_after_sync();
+            if (__any_sync(0xffffffffu, last > kGrown)) {               // O_t is complete up to tile i - 1
+                const int k = last > kGrown ? (int)(__float_as_uint(last) >> 23) - 127 : 0;
+                const float f = __uint_as_float((uint32_t)max(127 - k, 1) << 23);
+                m += (float)k;
+                l *= f;
+#pragma unroll
+                for (int x = 0; x < D / 16; ++x) {
+                    uint32_t o[16];
+                    umma::tmem_ld16(to + 16 * x, o);
+                    umma::tmem_ld_wait();
+#pragma unroll
+                    for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+                    umma::tmem_st16(to + 16 * x, o);
+                }
+            }
             uint32_t s[4][32];
 #pragma unroll
             for (int x = 0; x < 4; ++x) umma::tmem_ld32(ts + 32 * x, s[x]);
@@ -377,52 +418,39 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int y = 0; y < 32; ++y)
                         if (32 * x + y > seen) s[x][y] = 0xFF800000u;
             }
-            float mx[4];
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                mx[x] = fmaxf(__uint_as_float(s[x][0]), __uint_as_float(s[x][1]));
-#pragma unroll
-                for (int y = 2; y < 32; y += 2) mx[x] = max3(mx[x], __uint_as_float(s[x][y]), __uint_as_float(s[x][y + 1]));
-            }
-            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
             if (i == 0) {
-                m = top > -INFINITY ? top : 0.0f;
-            } else {
-                const bool move = (top - m) * c > kRescale;
-                if (__any_sync(0xffffffffu, move)) {                    // O_t is complete up to tile i - 1
-                    const float f = move ? ex2((m - top) * c) : 1.0f;
-                    if (move) m = top;
-                    l *= f;
+                float mx[8];
 #pragma unroll
-                    for (int x = 0; x < D / 32; ++x) {
-                        uint32_t o[32];
-                        umma::tmem_ld32(to + 32 * x, o);
-                        umma::tmem_ld_wait();
+                for (int x = 0; x < 8; ++x) {
+                    const uint32_t *v = &s[x >> 1][16 * (x & 1)];
+                    mx[x] = fmaxf(__uint_as_float(v[0]), __uint_as_float(v[1]));
 #pragma unroll
-                        for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
-                        umma::tmem_st32(to + 32 * x, o);
-                    }
+                    for (int y = 2; y < 16; y += 2) mx[x] = max3(mx[x], __uint_as_float(v[y]), __uint_as_float(v[y + 1]));
                 }
+                const float top = max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
+                m = top > -INFINITY ? top * c : 0.0f;
             }
-            const uint64_t cc = f2(c, c), mc = f2(-m * c, -m * c);
-            uint64_t sum[4] = {0, 0, 0, 0};
+            const uint64_t mm = f2(-m, -m);
+            last = 0.0f;
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
+                uint64_t sum[4] = {0, 0, 0, 0};
                 uint32_t w[32];
 #pragma unroll
                 for (int y = 0; y < 32; ++y) {
-                    const uint64_t d = fma2(f2(__uint_as_float(s[2 * x + (y >> 4)][(2 * y) & 31]), __uint_as_float(s[2 * x + (y >> 4)][(2 * y + 1) & 31])), cc, mc);
+                    const uint64_t d = fma2(f2(__uint_as_float(s[2 * x + (y >> 4)][(2 * y) & 31]), __uint_as_float(s[2 * x + (y >> 4)][(2 * y + 1) & 31])), cc, mm);
                     const float p0 = ex2(lo32(d)), p1 = ex2(hi32(d));
                     sum[y & 3] = add2(sum[y & 3], f2(p0, p1));
                     w[y] = pack_bf16(p0, p1);
                 }
                 umma::tmem_st32(ts + 32 * x, w);
+                sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
+                last += lo32(sum[0]) + hi32(sum[0]);
+                umma::tmem_st_wait();
+                umma::fence_before_sync();
+                umma::mbar_arrive(&sm.pfull[t][x]);
             }
-            sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
-            l += lo32(sum[0]) + hi32(sum[0]);
-            umma::tmem_st_wait();
-            umma::fence_before_sync();
-            umma::mbar_arrive(&sm.pfull[t]);
+            l += last;
         }
         // ---- epilogue: o = O / l ----
         if (ok && n > 0) ok = __all_sync(0xffffffffu, wait(&sm.odone[t], 0));
@@ -431,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const size_t head = (size_t)(h * G + g) * D;
             uint16_t *orow = a.o + (size_t)(q0 + p) * a.ldo + head;
             const float inv = lim >= 0 ? 1.0f / l : 0.0f;
-            bool fine = true;
+            bool fine = lim < 0 || (l > 0.0f && l < INFINITY);
 #pragma unroll
             for (int x = 0; x < D / 32; ++x) {
                 uint32_t o[32];
@@ -525,6 +553,6 @@ extern "C" int qspec_attn_prompt(const uint16_t *q_bf16, int ldq, const uint16_t
     int rc = check_device();
     if (rc || q_rows == 0) return rc;
     const apr::Args a{q_bf16, k_bf16, v_bf16, q_start, k_start, o_bf16, dev_status, ldq, ldk, ldv,
-                      ldo,    q_rows, k_rows, B,       H,       Hq / H, scale};
+                      ldo,    q_rows, k_rows, B,       H,       Hq / H, Hq == H ? 0u : (uint32_t)((1ull << 32) / (Hq / H) + 1), scale};
     return D == 128 ? apr::launch<128>(a, as_cuda(stream)) : apr::launch<64>(a, as_cuda(stream));
 }
