@@ -162,13 +162,6 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 __device__ __forceinline__ float lo_half(uint32_t w) { return __half2float(__ushort_as_half((uint16_t)(w & 0xFFFFu))); }
 __device__ __forceinline__ float hi_half(uint32_t w) { return __half2float(__ushort_as_half((uint16_t)(w >> 16))); }
 
-__device__ __forceinline__ void tma_load_3d(void *dst, const void *tmap, int x, int y, int z, uint64_t *bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n" ::
-            "r"(umma::smem_addr(dst)),
-        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(umma::smem_addr(bar))
-        : "memory");
-}
 __device__ __forceinline__ void bar_sync(int id, int threads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
@@ -396,8 +389,8 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
                     if (loads >= kStages && !wait(&sm.empty[s], loads / kStages + 1)) break;
                     if (*reinterpret_cast<volatile int *>(&sm.timeout)) break;
                     umma::mbar_arrive_expect_tx(&sm.full[s], 2 * kSide);
-                    tma_load_3d(codes + s * 2 * kSide, &tk, 0, (tile + i) * kTok, b * a.H + h, &sm.full[s]);
-                    tma_load_3d(codes + s * 2 * kSide + kSide, &tv, 0, (tile + i) * kTok, b * a.H + h, &sm.full[s]);
+                    umma::tma_load_3d(codes + s * 2 * kSide, &tk, 0, (tile + i) * kTok, b * a.H + h, &sm.full[s]);
+                    umma::tma_load_3d(codes + s * 2 * kSide + kSide, &tv, 0, (tile + i) * kTok, b * a.H + h, &sm.full[s]);
                     ++loads;
                 }
                 next(n_t);

@@ -40,7 +40,8 @@ namespace apr {
 constexpr int kTile = 128;                      // query rows per tile, keys per tile
 constexpr int kSoftmax = 256;                   // softmax threads: 128 per row tile
 constexpr int kMmaWarp = kSoftmax / 32, kTmaWarp = kMmaWarp + 1;
-constexpr int kThreads = kSoftmax + 128;       // (two warps idle: register shares are set by four warps)
+constexpr int kUnitWarp = kTmaWarp + 1;         // finds the units and fetches their Q (one more warp idles)
+constexpr int kThreads = kSoftmax + 128;
 // registers per thread: 384 threads start with 168 and share 64512
 constexpr int kRegsStart = 168, kRegsSoftmax = 216, kRegsRest = 64;
 static_assert(kSoftmax * kRegsSoftmax + 128 * kRegsRest <= kThreads * kRegsStart, "register shares");
@@ -53,27 +54,34 @@ constexpr int tile_bytes() { return kTile * D * 2; }
 template <int D>
 constexpr int ring() { return D == 128 ? 4 : 8; }
 
-struct Ctl {
-    uint64_t full[8], empty[8];                 // K / V tiles: landed, read
-    uint64_t sfull[2], pfull[2][2], odone[2];   // S_t written, each half of P_t written (and S_t read), O_t complete
-    uint64_t drain;
-    uint32_t tmem;
-    int timeout;
-    int found, q0, lq, k0, lk;                  // the unit's sequence (none: found is 0)
-    int left, p_last;                           // flattened rows from the unit's first on (at most 256); its last row's position
-    int p[2], g[2];                             // each tile's first row: position and head of the group
+struct Unit {
+    int h, q0, k0, off;                         // group of heads, the sequence's first rows, Lk - Lq
+    int first, left, n;                         // first position, positions from it on (to the sequence's end), key tiles; n < 0: no more units
 };
 
+struct Ctl {
+    uint64_t full[8], empty[8];                 // K / V tiles: landed, read
+    uint64_t ufull[2], uempty[2];               // units: published, done with
+    uint64_t qfull[2], qfree[2];                // Q tiles: written, read
+    uint64_t sfull[2], pfull[2][2], odone[2];   // S_t written, each half of P_t written (and S_t read), O_t complete
+    uint64_t drain;
+    Unit unit[2];
+    uint32_t tmem;
+    int timeout, q_count[2];
+};
+
+constexpr int kOutBytes = kSoftmax / 32 * 32 * 128;   // per softmax warp 32 rows x 64 values on their way out
 template <int D>
-constexpr size_t smem_total() { return 1024 + 2 * (size_t)tile_bytes<D>() + (size_t)ring<D>() * tile_bytes<D>() + sizeof(Ctl); }
+constexpr size_t smem_total() { return 1024 + 2 * (size_t)tile_bytes<D>() + (size_t)ring<D>() * tile_bytes<D>() + kOutBytes + sizeof(Ctl); }
 
 struct Args {
     const uint16_t *q, *k, *v;
     const int32_t *q_start, *k_start;
     uint16_t *o;
     int32_t *st;
-    int ldq, ldk, ldv, ldo, q_rows, k_rows, B, H, G;
-    uint32_t g_mul;                             // n / G = umulhi(n, g_mul) for n < G + 128 (G = 1: 0)
+    int ldq, ldk, ldv, ldo, q_rows, k_rows, B, H, G;   // H groups of G query heads
+    int share;                                  // groups to a KV head
+    uint32_t g_mul;                             // n / G = umulhi(n, g_mul) for n < 128 (G = 1: 0)
     float scale;
 
     __device__ __forceinline__ int over_g(int n) const { return g_mul ? (int)__umulhi((uint32_t)n, g_mul) : n; }
@@ -160,7 +168,8 @@ __device__ __noinline__ void row_again(const Args &a, int h, const uint16_t *qro
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-    attn_prompt_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
+    attn_prompt_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+                       const __grid_constant__ CUtensorMap tv,
                        const __grid_constant__ Args a,
                        uint32_t wait_limit) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -168,9 +177,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // (an offset, not a rounded address: the compiler keeps seeing shared memory)
     uint8_t *sq = smem_raw + ((1024u - (umma::smem_addr(smem_raw) & 1023u)) & 1023u);
     uint8_t *skv = sq + 2 * kT;
-    Ctl &sm = *reinterpret_cast<Ctl *>(skv + NS * kT);
+    uint8_t *so = skv + NS * kT;
+    Ctl &sm = *reinterpret_cast<Ctl *>(so + kOutBytes);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int h = blockIdx.x % a.H, G = a.G;
+    const int G = a.G, per_tile = kTile / G;                // positions to a row tile
 
     if (warp == kMmaWarp) umma::tmem_alloc(&sm.tmem, kCols);
     if (tid == 0) {
@@ -183,10 +193,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             umma::mbar_init(&sm.pfull[t][0], kTile);
             umma::mbar_init(&sm.pfull[t][1], kTile);
             umma::mbar_init(&sm.odone[t], 1);
+            umma::mbar_init(&sm.ufull[t], 1);
+            umma::mbar_init(&sm.uempty[t], kSoftmax / 32 + 2);          // softmax, products, copies
+            umma::mbar_init(&sm.qfull[t], 1);
+            umma::mbar_init(&sm.qfree[t], 1);
         }
         umma::mbar_init(&sm.drain, 1);
         sm.timeout = 0;
-        sm.found = 0;
         umma::mbar_fence_init();
     }
     pdl_launch_dependents();
@@ -194,202 +207,246 @@ __global__ void __launch_bounds__(kThreads, 1)
     umma::fence_before_sync();
     __syncthreads();
     umma::fence_after_sync();
-    // this CTA's unit of 256 flattened rows: the sequences in order, each one's
-    // last (longest) unit first
-    if (warp == kTmaWarp) {
-        int left = blockIdx.x / a.H;
-        for (int b0 = 0; b0 < a.B && left >= 0; b0 += 32) {
-            const int b = b0 + lane;
-            int q0 = 0, lq = 0, k0 = 0, lk = 0;
-            bool bad = false;
-            if (b < a.B) {
-                const int q1 = a.q_start[b + 1], k1 = a.k_start[b + 1];
-                q0 = a.q_start[b];
-                k0 = a.k_start[b];
-                bad = q0 < 0 || q1 < q0 || q1 > a.q_rows || k0 < 0 || k1 < k0 || k1 > a.k_rows;
-                lq = bad ? 0 : q1 - q0;
-                lk = bad ? 0 : k1 - k0;
-            }
-            if (bad) flag(a.st, QSPEC_ERR_RANGE);
-            const int units = (int)(((long long)lq * G + 2 * kTile - 1) / (2 * kTile));
-            int upto = units;
-#pragma unroll
-            for (int x = 1; x < 32; x <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, upto, x);
-                if (lane >= x) upto += y;
-            }
-            if (left >= upto - units && left < upto) {
-                const long long row0 = (long long)(units - 1 - (left - (upto - units))) * (2 * kTile), rows = (long long)lq * G;
-                sm.q0 = q0;
-                sm.lq = lq;
-                sm.k0 = k0;
-                sm.lk = lk;
-                sm.left = (int)min(rows - row0, 2ll * kTile);
-                sm.p_last = (int)((row0 + sm.left - 1) / G);
-                for (int t = 0; t < 2; ++t) {
-                    sm.p[t] = (int)((row0 + t * kTile) / G);
-                    sm.g[t] = (int)(row0 + t * kTile - (long long)sm.p[t] * G);
-                }
-                sm.found = 1;
-            }
-            const int total = __shfl_sync(0xffffffffu, upto, 31);
-            left = left < total ? -1 : left - total;
-        }
-        // the sequences that no CTA walks to are checked by the first one
-        if (blockIdx.x == 0)
-            for (int b = lane; b < a.B; b += 32)
-                if (a.q_start[b] < 0 || a.q_start[b + 1] < a.q_start[b] || a.q_start[b + 1] > a.q_rows ||
-                    a.k_start[b] < 0 || a.k_start[b + 1] < a.k_start[b] || a.k_start[b + 1] > a.k_rows)
-                    flag(a.st, QSPEC_ERR_RANGE);
-    }
-    __syncthreads();
     const uint32_t tmem = sm.tmem;
-    const bool work = sm.found != 0;
-    const int q0 = sm.q0, k0 = sm.k0, off = sm.lk - sm.lq, left = work ? sm.left : 0;
-    // key tiles that the unit's last row sees
-    const int n = work ? max(0, (sm.p_last + off + kTile) / kTile) : 0;
-    const int nt = left > kTile ? 2 : 1;                    // row tiles with rows
 
     int loads = 0;
     bool issued = false, elected = false;
-    auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
-        if (umma::mbar_try_wait(bar, parity)) return true;
+    auto wait = [&](uint64_t *bar, uint32_t phase) -> bool {
+        if (umma::mbar_try_wait(bar, phase & 1)) return true;
         if (*reinterpret_cast<volatile int *>(&sm.timeout)) return false;
-        if (umma::mbar_wait(bar, parity, wait_limit)) return true;
+        if (umma::mbar_wait(bar, phase & 1, wait_limit)) return true;
         *reinterpret_cast<volatile int *>(&sm.timeout) = 1;
         return false;
     };
-
-    // ---- Q tiles into shared memory (both operands' swizzle); a negative scale
-    // turns the signs, a zero one the values, so that the softmax has c > 0 ----
-    if (work && n > 0 && warp < kMmaWarp) {
-        // eight values per thread and step, D / 8 threads a row; every step's load is under way before the first is stored
-        const int t = warp >> 2, w = tid & (kTile - 1), ch = w % (D / 8), r0 = w / (D / 8);
-        constexpr int kStep = kTile / (D / 8), kSteps = D / 8;
-        const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u, keep = a.scale != 0.0f ? 0xFFFFFFFFu : 0u;
-        uint4 x[kSteps];
-#pragma unroll
-        for (int it = 0; it < kSteps; ++it) {
-            const int r = it * kStep + r0, gr = sm.g[t] + r, pr = a.over_g(gr);
-            x[it] = make_uint4(0, 0, 0, 0);
-            if (t * kTile + r < left)
-                x[it] = __ldg(reinterpret_cast<const uint4 *>(a.q + (size_t)(q0 + sm.p[t] + pr) * a.ldq + (size_t)(h * G + gr - pr * G) * D + ch * 8));
-        }
-#pragma unroll
-        for (int it = 0; it < kSteps; ++it) {
-            const int r = it * kStep + r0;
-            const uint4 y = make_uint4((x[it].x ^ flip) & keep, (x[it].y ^ flip) & keep, (x[it].z ^ flip) & keep, (x[it].w ^ flip) & keep);
-            *reinterpret_cast<uint4 *>(sq + t * kT + (ch >> 3) * (kTile * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = y;
-        }
-        umma::fence_proxy_async();
-    }
-    // the first tiles' copies go out before the Q tiles are complete
-    if (warp == kTmaWarp && lane == 0 && n > 0) {
-        const int pre = min(2 * n, NS);
-        for (int i = 0; i < pre; ++i) {
-            umma::mbar_arrive_expect_tx(&sm.full[i], kT);
-#pragma unroll
-            for (int c = 0; c < D / 64; ++c)
-                umma::tma_load_2d(skv + i * kT + c * (kTile * 128), (i & 1) ? &tv : &tk, (h * D + 64 * c) * 2,
-                                  k0 + (i >> 1) * kTile, &sm.full[i]);
-        }
-        loads = pre;
-    }
-    umma::fence_before_sync();
-    __syncthreads();
-    umma::fence_after_sync();
+    // (the votes keep a warp together where a wait runs out)
+    auto all = [](bool mine) { return __all_sync(0xffffffffu, mine) != 0; };
+    int span = 0;                                           // positions to a unit (of the warp that finds them)
+    auto tiles = [&](const Unit &u) { return u.left > per_tile ? 2 : 1; };  // row tiles with rows
 
     if (warp >= kMmaWarp) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
-        if (n > 0 && warp == kTmaWarp && lane == 0) {
-            for (int i = loads; i < 2 * n; ++i) {                      // K_0, V_0, K_1, V_1, ...
-                const int s = i % NS;
-                if (!wait(&sm.empty[s], (uint32_t)((i / NS + 1) & 1))) break;
-                umma::mbar_arrive_expect_tx(&sm.full[s], kT);
+        if (warp == kUnitWarp) {
+            // ---- units: level by level from the sequences' last ones (the longest), for up to 32 sequences;
+            // for more, sequence by sequence, each one's last unit first ----
+            {
+                int q0 = 0, lq = 0, k0 = 0, lk = 0;
+                auto fetch = [&](int b, bool report) {
+                    q0 = lq = k0 = lk = 0;
+                    if (b >= a.B) return;
+                    const int q1 = __ldg(a.q_start + b + 1), k1 = __ldg(a.k_start + b + 1);
+                    q0 = __ldg(a.q_start + b);
+                    k0 = __ldg(a.k_start + b);
+                    if (q0 < 0 || q1 < q0 || q1 > a.q_rows || k0 < 0 || k1 < k0 || k1 > a.k_rows) {
+                        if (report) flag(a.st, QSPEC_ERR_RANGE);
+                        return;
+                    }
+                    lq = q1 - q0;
+                    lk = k1 - k0;
+                };
+                auto units_of = [&](int positions) { return (lq + positions - 1) / positions; };
+                long long total[2] = {0, 0};                            // units of one tile, of two
+                for (int b0 = 0; b0 < a.B; b0 += 32) {
+                    fetch(b0 + lane, blockIdx.x == 0);
+                    total[0] += __reduce_add_sync(0xffffffffu, units_of(per_tile));
+                    total[1] += __reduce_add_sync(0xffffffffu, units_of(2 * per_tile));
+                }
+                if (a.B > 32) fetch(lane, false);
+                const bool one = total[0] * a.H <= gridDim.x;           // one tile each still leaves SMs idle
+                span = one ? per_tile : 2 * per_tile;
+                const long long end = (one ? total[0] : total[1]) * a.H;
+                int count[2] = {0, 0};                                  // Q tiles fetched
+                bool ok = true;
+                for (int k = 0;; ++k) {
+                    const long long id = (long long)k * gridDim.x + (k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+                    const bool more = id < end;
+                    if (k >= 2 && !all(wait(&sm.uempty[k & 1], (k >> 1) - 1))) break;
+                    Unit &u = sm.unit[k & 1];
+                    bool mine = false;
+                    int index = 0;
+                    if (more) {
+                        int rank = (int)(id / a.H);
+                        if (a.B <= 32) {
+                            const int units = units_of(span);
+                            auto from = [&](int level) { return (int)__reduce_add_sync(0xffffffffu, max(0, units - level)); };   // units at level and above
+                            int lo = 0, hi = (int)__reduce_max_sync(0xffffffffu, units);
+                            while (hi - lo > 1) {
+                                const int mid = (lo + hi) >> 1;
+                                if (from(mid) > rank)
+                                    lo = mid;
+                                else
+                                    hi = mid;
+                            }
+                            rank -= from(lo + 1);
+                            const uint32_t there = __ballot_sync(0xffffffffu, units > lo);
+                            mine = units > lo && __popc(there & ((1u << lane) - 1)) == rank;
+                            index = lo;
+                        } else {
+                            for (int b0 = 0; b0 < a.B && rank >= 0; b0 += 32) {
+                                fetch(b0 + lane, false);
+                                const int units = units_of(span);
+                                int upto = units;
 #pragma unroll
-                for (int c = 0; c < D / 64; ++c)
-                    umma::tma_load_2d(skv + s * kT + c * (kTile * 128), (i & 1) ? &tv : &tk, (h * D + 64 * c) * 2,
-                                      k0 + (i >> 1) * kTile, &sm.full[s]);
-                loads = i + 1;
+                                for (int x = 1; x < 32; x <<= 1) {
+                                    const int y = __shfl_up_sync(0xffffffffu, upto, x);
+                                    if (lane >= x) upto += y;
+                                }
+                                const int sum = __shfl_sync(0xffffffffu, upto, 31);
+                                mine = rank >= upto - units && rank < upto;
+                                index = units - 1 - (rank - (upto - units));
+                                rank = rank < sum ? -1 : rank - sum;
+                            }
+                        }
+                    }
+                    if (mine) {
+                        u.h = (int)(id % a.H);
+                        u.q0 = q0;
+                        u.k0 = k0;
+                        u.off = lk - lq;
+                        u.first = index * span;
+                        u.left = min(lq - u.first, span);
+                        u.n = max(0, (u.first + u.left - 1 + u.off + kTile) / kTile);    // that its last row sees
+                    }
+                    if (!more && lane == 0) u.n = -1;
+                    __syncwarp();
+                    if (lane == 0) umma::mbar_arrive(&sm.ufull[k & 1]);
+                    if (!more) break;
+                    // its Q tiles: whole positions' heads in one box of 64 values each (rows past the sequence hold
+                    // whatever follows; their scores are all masked)
+                    for (int t = 0; t < tiles(u) && u.n > 0 && ok; ++t) {
+                        if (count[t] > 0 && !(ok = all(wait(&sm.qfree[t], count[t] - 1)))) break;
+                        if (lane == 0) {
+                            umma::mbar_arrive_expect_tx(&sm.qfull[t], per_tile * G * D * 2);
+#pragma unroll
+                            for (int c = 0; c < D / 64; ++c)
+                                umma::tma_load_3d(sq + t * kT + c * (kTile * 128), &tq, 128 * c, u.h * G, u.q0 + u.first + t * per_tile, &sm.qfull[t]);
+                        }
+                        ++count[t];
+                        __syncwarp();
+                    }
+                    if (!ok) break;
+                }
+                if (lane == 0)                                          // (for the drain after a timeout)
+                    for (int t = 0; t < 2; ++t) sm.q_count[t] = count[t];
             }
-        } else if (n > 0 && warp == kMmaWarp) {
+        } else if (warp == kTmaWarp) {
+            bool ok = true;
+            for (int k = 0; ok; ++k) {
+                if (!(ok = all(wait(&sm.ufull[k & 1], k >> 1)))) break;
+                const Unit &u = sm.unit[k & 1];
+                const int n = u.n, h = a.share == 1 ? u.h : u.h / a.share, k0 = u.k0;
+                if (n < 0) break;
+                for (int i = 0; i < 2 * n && ok; ++i, ++loads) {       // K_0, V_0, K_1, V_1, ...
+                    const int s = loads % NS;
+                    if (loads >= NS && !(ok = all(wait(&sm.empty[s], loads / NS - 1)))) break;
+                    if (lane == 0) {
+                        umma::mbar_arrive_expect_tx(&sm.full[s], kT);
+#pragma unroll
+                        for (int c = 0; c < D / 64; ++c)
+                            umma::tma_load_2d(skv + s * kT + c * (kTile * 128), (i & 1) ? &tv : &tk, (h * D + 64 * c) * 2,
+                                              k0 + (i >> 1) * kTile, &sm.full[s]);
+                    }
+                    __syncwarp();
+                }
+                if (lane == 0) umma::mbar_arrive(&sm.uempty[k & 1]);
+            }
+        } else if (warp == kMmaWarp) {
             constexpr uint32_t id_s = umma::instr_desc(1, 1, kTile, kTile);
             constexpr uint32_t id_o = umma::instr_desc(1, 1, kTile, D) | (1u << 16);      // B is MN-major
             const uint32_t q_addr = umma::smem_addr(sq), kv_addr = umma::smem_addr(skv);
             // the whole warp walks the loop and one lane issues: with the loop inside the lane's branch the
             // descriptors were moved to uniform registers product by product (494 us for 427 at 8192 tokens)
             elected = umma::elect_one();
-            auto scores = [&](int t, int i) {                           // S_t = Q_t K_i^T
-                const uint64_t ad = desc_k(q_addr + t * kT), bd = desc_k(kv_addr + ((2 * i) % NS) * kT);
-                if (elected) {
-#pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint32_t step = (uint32_t)((kk >> 2) * (kTile * 128) + (kk & 3) * 32) >> 4;
-                        umma::mma_bf16(tmem + kS + t * kTile, ad + step, bd + step, id_s, kk != 0);
-                    }
-                    umma::mma_commit(&sm.sfull[t]);
-                }
+            int at = 0, seen[2] = {0, 0}, units[2] = {0, 0};            // copies used; key tiles and units of each row tile
+            bool ok = true;
+            for (int k = 0; ok; ++k) {
+                if (!(ok = all(wait(&sm.ufull[k & 1], k >> 1)))) break;
+                const int n = sm.unit[k & 1].n, nt = tiles(sm.unit[k & 1]);
                 __syncwarp();
-            };
-            // (the votes keep the warp together where a wait runs out)
-            auto all = [&](bool mine) { return __all_sync(0xffffffffu, mine) != 0; };
-            bool ok = all(wait(&sm.full[0], 0));
-            if (ok) {
-                umma::fence_after_sync();
-                for (int t = 0; t < nt; ++t) scores(t, 0);
-                if (elected) umma::mma_commit(&sm.empty[0]);
-                issued = true;
-            }
-            for (int i = 0; i < n && ok; ++i) {
-                const int sv = (2 * i + 1) % NS, sk = (2 * i + 2) % NS;
-                const bool more = i + 1 < n;
-                ok = all(wait(&sm.full[sv], (uint32_t)(((2 * i + 1) / NS) & 1)) &&
-                         (!more || wait(&sm.full[sk], (uint32_t)(((2 * i + 2) / NS) & 1))));
-                for (int t = 0; t < nt && ok; ++t) {
-                    const uint64_t bd = desc_mn(kv_addr + sv * kT);
-                    for (int half = 0; half < 2 && ok; ++half) {
-                        if (!(ok = all(wait(&sm.pfull[t][half], (uint32_t)(i & 1))))) break;
-                        umma::fence_after_sync();
-                        if (elected) {
+                if (lane == 0) umma::mbar_arrive(&sm.uempty[k & 1]);
+                if (n < 0) break;
+                if (n == 0) continue;
+                auto scores = [&](int t, int i) {                       // S_t = Q_t K_i^T
+                    const uint64_t ad = desc_k(q_addr + t * kT), bd = desc_k(kv_addr + ((at + 2 * i) % NS) * kT);
+                    if (elected) {
 #pragma unroll
-                            for (int k4 = 0; k4 < kTile / 32; ++k4) {   // 16 keys: 2 groups of 8 rows
-                                const int kk = half * (kTile / 32) + k4;
-                                umma::mma_bf16_ta(tmem + kO + t * kTile, tmem + kS + t * kTile + kk * 8, bd + (kk * 2048 >> 4), id_o,
-                                                  (i | kk) != 0);
+                        for (int kk = 0; kk < D / 16; ++kk) {
+                            const uint32_t step = (uint32_t)((kk >> 2) * (kTile * 128) + (kk & 3) * 32) >> 4;
+                            umma::mma_bf16(tmem + kS + t * kTile, ad + step, bd + step, id_s, kk != 0);
+                        }
+                        umma::mma_commit(&sm.sfull[t]);
+                        if (i == n - 1) umma::mma_commit(&sm.qfree[t]);
+                    }
+                    __syncwarp();
+                };
+                ok = all(wait(&sm.full[at % NS], at / NS));
+                for (int t = 0; t < nt && ok; ++t) {
+                    if (!(ok = all(wait(&sm.qfull[t], units[t]++)))) break;
+                    umma::fence_after_sync();
+                    issued = true;
+                    scores(t, 0);
+                }
+                if (ok && elected) umma::mma_commit(&sm.empty[at % NS]);
+                for (int i = 0; i < n && ok; ++i) {
+                    const int iv = at + 2 * i + 1, ik = iv + 1;
+                    const bool more = i + 1 < n;
+                    ok = all(wait(&sm.full[iv % NS], iv / NS) && (!more || wait(&sm.full[ik % NS], ik / NS)));
+                    for (int t = 0; t < nt && ok; ++t) {
+                        const uint64_t bd = desc_mn(kv_addr + (iv % NS) * kT);
+                        for (int half = 0; half < 2 && ok; ++half) {
+                            if (!(ok = all(wait(&sm.pfull[t][half], seen[t] + i)))) break;
+                            umma::fence_after_sync();
+                            if (elected) {
+#pragma unroll
+                                for (int k4 = 0; k4 < kTile / 32; ++k4) {   // 16 keys: 2 groups of 8 rows
+                                    const int kk = half * (kTile / 32) + k4;
+                                    umma::mma_bf16_ta(tmem + kO + t * kTile, tmem + kS + t * kTile + kk * 8, bd + (kk * 2048 >> 4), id_o,
+                                                      (i | kk) != 0);
+                                }
                             }
                         }
-                    }
-                    if (!ok) break;
-                    if (elected && t == nt - 1) umma::mma_commit(&sm.empty[sv]);
-                    __syncwarp();
-                    if (more) {
-                        scores(t, i + 1);
-                        if (t == nt - 1 && elected) umma::mma_commit(&sm.empty[sk]);
-                    } else {
-                        if (elected) umma::mma_commit(&sm.odone[t]);
+                        if (!ok) break;
+                        if (elected && t == nt - 1) umma::mma_commit(&sm.empty[iv % NS]);
+                        __syncwarp();
+                        if (more) {
+                            scores(t, i + 1);
+                            if (t == nt - 1 && elected) umma::mma_commit(&sm.empty[ik % NS]);
+                        } else {
+                            if (elected) umma::mma_commit(&sm.odone[t]);
+                        }
+                        __syncwarp();
                     }
                 }
+                at += 2 * n;
+                for (int t = 0; t < nt; ++t) seen[t] += n;
             }
         }
     } else {
       asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-      if (work && (warp >> 2) < nt) {
-        const int t = warp >> 2;
-        const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-        const uint32_t ts = tmem + lanes + kS + t * kTile, to = tmem + lanes + kO + t * kTile;
-        const int r = (warp & 3) * 32 + lane, gr = sm.g[t] + r, pr = a.over_g(gr);
-        const bool in = t * kTile + r < left;
-        const int p = in ? sm.p[t] + pr : 0, g = in ? gr - pr * G : 0;
+      const int t = warp >> 2;
+      const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+      const uint32_t ts = tmem + lanes + kS + t * kTile, to = tmem + lanes + kO + t * kTile;
+      // a zero scale: as good as zero times any score, and a masked one stays minus infinity
+      const float c = a.scale != 0.0f ? a.scale * 1.4426950408889634f : 1.0e-30f;
+      const uint64_t cc = f2(c, c);
+      int tiles_seen = 0, units_seen = 0;
+      bool ok = true;
+      for (int k = 0; ok; ++k) {
+        if (!(ok = all(wait(&sm.ufull[k & 1], k >> 1)))) break;
+        const Unit u = sm.unit[k & 1];
+        __syncwarp();
+        if (lane == 0) umma::mbar_arrive(&sm.uempty[k & 1]);
+        if (u.n < 0) break;
+        if (t >= tiles(u)) continue;
+        const int n = u.n, h = u.h, q0 = u.q0, k0 = u.k0, off = u.off;
+        const int r = (warp & 3) * 32 + lane, pr = a.over_g(r), p_first = u.first + t * per_tile;
+        const bool in = pr < per_tile && t * per_tile + pr < u.left;
+        const int p = in ? p_first + pr : 0, g = in ? r - pr * G : 0;
         const int lim = in ? p + off : -1;                              // last key seen
         // tiles from here on are masked for some row of the tile
-        const int first_masked = sm.p[t] + off;
-        const float c = a.scale != 0.0f ? fabsf(a.scale) * 1.4426950408889634f : 1.0f;
-        const uint64_t cc = f2(c, c);
+        const int first_masked = p_first + off;
         float m = 0.0f, l = 0.0f, last = 0.0f;                          // reference in log2 units; the last tile's sum
-        bool ok = true;
         for (int i = 0; i < n; ++i) {
-            // (the vote keeps the warp together where a wait runs out)
-            if (!(ok = __all_sync(0xffffffffu, wait(&sm.sfull[t], (uint32_t)(i & 1))))) break;
+            if (!(ok = all(wait(&sm.sfull[t], tiles_seen + i)))) break;
             umma::fence_after_sync();
             if (__any_sync(0xffffffffu, last > kGrown)) {               // O_t is complete up to tile i - 1
                 const int k = last > kGrown ? (int)(__float_as_uint(last) >> 23) - 127 : 0;
@@ -412,23 +469,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             umma::tmem_ld_wait();
             if (i * kTile + kTile - 1 > first_masked || !in) {
                 const int seen = lim - i * kTile;                       // columns 0 .. seen
+                const uint32_t hidden = c < 0.0f ? 0x7F800000u : 0xFF800000u;   // c times it is minus infinity
 #pragma unroll
                 for (int x = 0; x < 4; ++x)
 #pragma unroll
                     for (int y = 0; y < 32; ++y)
-                        if (32 * x + y > seen) s[x][y] = 0xFF800000u;
+                        if (32 * x + y > seen) s[x][y] = hidden;
             }
             if (i == 0) {
+                const uint32_t turn = c < 0.0f ? 0x80000000u : 0u;
+                auto at = [&](uint32_t v) { return __uint_as_float(v ^ turn); };
                 float mx[8];
 #pragma unroll
                 for (int x = 0; x < 8; ++x) {
                     const uint32_t *v = &s[x >> 1][16 * (x & 1)];
-                    mx[x] = fmaxf(__uint_as_float(v[0]), __uint_as_float(v[1]));
+                    mx[x] = fmaxf(at(v[0]), at(v[1]));
 #pragma unroll
-                    for (int y = 2; y < 16; y += 2) mx[x] = max3(mx[x], __uint_as_float(v[y]), __uint_as_float(v[y + 1]));
+                    for (int y = 2; y < 16; y += 2) mx[x] = max3(mx[x], at(v[y]), at(v[y + 1]));
                 }
                 const float top = max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
-                m = top > -INFINITY ? top * c : 0.0f;
+                m = top > -INFINITY ? top * fabsf(c) : 0.0f;
             }
             const uint64_t mm = f2(-m, -m);
             last = 0.0f;
@@ -453,32 +513,49 @@ __global__ void __launch_bounds__(kThreads, 1)
             l += last;
         }
         // ---- epilogue: o = O / l ----
-        if (ok && n > 0) ok = __all_sync(0xffffffffu, wait(&sm.odone[t], 0));
+        if (ok && n > 0) ok = all(wait(&sm.odone[t], units_seen));
+        tiles_seen += n;
+        units_seen += n > 0;
         if (ok) {
             umma::fence_after_sync();
-            const size_t head = (size_t)(h * G + g) * D;
-            uint16_t *orow = a.o + (size_t)(q0 + p) * a.ldo + head;
+            const size_t at = (size_t)(q0 + p) * a.ldo + (size_t)(h * G + g) * D;     // this row's place in o
             const float inv = lim >= 0 ? 1.0f / l : 0.0f;
             bool fine = lim < 0 || (l > 0.0f && l < INFINITY);
+            const uint32_t inside = __ballot_sync(0xffffffffu, in);
+            uint8_t *buf = so + warp * (32 * 128);
 #pragma unroll
-            for (int x = 0; x < D / 32; ++x) {
-                uint32_t o[32];
-                if (n > 0) {
-                    umma::tmem_ld32(to + 32 * x, o);
-                    umma::tmem_ld_wait();
+            for (int x = 0; x < D / 64; ++x) {
+                // 64 values of each row through shared memory, so that eight lanes write one row's 128 bytes (rows
+                // written by their own threads: 32 places per store, 2.9 us a tile instead of 0.9)
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    uint32_t o[32];
+                    if (n > 0) {
+                        umma::tmem_ld32(to + 64 * x + 32 * y, o);
+                        umma::tmem_ld_wait();
+                    }
+                    uint32_t w[16];
+#pragma unroll
+                    for (int z = 0; z < 16; ++z) {
+                        const float o0 = lim >= 0 ? __uint_as_float(o[2 * z]) * inv : 0.0f;
+                        const float o1 = lim >= 0 ? __uint_as_float(o[2 * z + 1]) * inv : 0.0f;
+                        fine = fine && isfinite(o0) && isfinite(o1);
+                        w[z] = pack_bf16(o0, o1);
+                    }
+#pragma unroll
+                    for (int z = 0; z < 4; ++z)
+                        *reinterpret_cast<uint4 *>(buf + lane * 128 + (((4 * y + z) ^ (lane & 7)) << 4)) =
+                            make_uint4(w[4 * z], w[4 * z + 1], w[4 * z + 2], w[4 * z + 3]);
                 }
-                uint32_t w[16];
+                __syncwarp();
 #pragma unroll
-                for (int y = 0; y < 16; ++y) {
-                    const float o0 = lim >= 0 ? __uint_as_float(o[2 * y]) * inv : 0.0f;
-                    const float o1 = lim >= 0 ? __uint_as_float(o[2 * y + 1]) * inv : 0.0f;
-                    fine = fine && isfinite(o0) && isfinite(o1);
-                    w[y] = pack_bf16(o0, o1);
+                for (int z = 0; z < 8; ++z) {
+                    const int row = 4 * z + (lane >> 3), ch = lane & 7;
+                    const uint4 v = *reinterpret_cast<const uint4 *>(buf + row * 128 + ((ch ^ (row & 7)) << 4));
+                    const size_t dst = __shfl_sync(0xffffffffu, at, row);
+                    if (inside >> row & 1) *reinterpret_cast<uint4 *>(a.o + dst + 64 * x + 8 * ch) = v;
                 }
-                if (in)
-#pragma unroll
-                    for (int y = 0; y < 4; ++y)
-                        reinterpret_cast<uint4 *>(orow + 32 * x)[y] = make_uint4(w[4 * y], w[4 * y + 1], w[4 * y + 2], w[4 * y + 3]);
+                __syncwarp();
             }
             uint32_t again = __ballot_sync(0xffffffffu, in && !fine);
             while (again) {
@@ -487,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int pw = __shfl_sync(0xffffffffu, p, who), gw = __shfl_sync(0xffffffffu, g, who);
                 const size_t hw = (size_t)(h * G + gw) * D;
                 __syncwarp();
-                row_again<D>(a, h, a.q + (size_t)(q0 + pw) * a.ldq + hw, k0, pw + off, a.o + (size_t)(q0 + pw) * a.ldo + hw);
+                row_again<D>(a, h / a.share, a.q + (size_t)(q0 + pw) * a.ldq + hw, k0, pw + off, a.o + (size_t)(q0 + pw) * a.ldo + hw);
             }
         }
       }
@@ -500,6 +577,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (warp == kTmaWarp && lane == 0)
             for (int i = max(0, loads - NS); i < loads; ++i)
                 umma::mbar_wait(&sm.full[i % NS], (uint32_t)((i / NS) & 1), kWaitLimit);
+        if (warp == kUnitWarp && lane == 0)
+            for (int t = 0; t < 2; ++t)
+                if (sm.q_count[t] > 0) umma::mbar_wait(&sm.qfull[t], (uint32_t)((sm.q_count[t] - 1) & 1), kWaitLimit);
         if (warp == kMmaWarp && elected && issued) {
             umma::mma_commit(&sm.drain);
             umma::mbar_wait(&sm.drain, 0, kWaitLimit);
@@ -513,20 +593,22 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <int D>
 int launch(const Args &a, cudaStream_t stream) {
-    const long long units = (long long)a.q_rows * a.G / (2 * kTile) + a.B;
+    const long long units = (long long)a.q_rows / (kTile / a.G) + a.B;      // at most, of one tile
     if (units * a.H >= (1LL << 31)) return QSPEC_ERR_SHAPE;
     // no key rows: no copy is issued, and the maps only have to be valid
     const bool none = a.k_rows == 0;
     CUtensorMap tk, tv;
-    const int cols = (none ? a.H * a.G : a.H) * D * 2;
+    const int cols = (none ? a.H * a.G : a.H / a.share) * D * 2;
     if (byte_tmap_sw128(&tk, none ? a.q : a.k, none ? a.q_rows : a.k_rows, cols, (size_t)(none ? a.ldq : a.ldk) * 2, kTile) ||
         byte_tmap_sw128(&tv, none ? a.q : a.v, none ? a.q_rows : a.k_rows, cols, (size_t)(none ? a.ldq : a.ldv) * 2, kTile))
         return QSPEC_ERR_UNSUPPORTED;
+    CUtensorMap tq;
+    if (row_box_tmap_sw128(&tq, a.q, D * 2, a.H * a.G, a.q_rows, (size_t)a.ldq * 2, a.G, kTile / a.G)) return QSPEC_ERR_UNSUPPORTED;
     auto kern = attn_prompt_kernel<D>;
     int rc = smem_limit_once(reinterpret_cast<const void *>(kern), (int)smem_total<D>());
     if (rc) return rc;
-    return launch_pdl("qspec_attn_prompt", kern, dim3((unsigned)(units * a.H)), dim3(kThreads), smem_total<D>(), stream, tk,
-                      tv, a, kWaitLimit);
+    return launch_pdl("qspec_attn_prompt", kern, dim3((unsigned)std::min<long long>(sm_count(), units * a.H)), dim3(kThreads), smem_total<D>(), stream, tq,
+                      tk, tv, a, kWaitLimit);
 }
 
 }  // namespace apr
@@ -552,7 +634,11 @@ extern "C" int qspec_attn_prompt(const uint16_t *q_bf16, int ldq, const uint16_t
         return QSPEC_ERR_ALIGN;
     int rc = check_device();
     if (rc || q_rows == 0) return rc;
-    const apr::Args a{q_bf16, k_bf16, v_bf16, q_start, k_start, o_bf16, dev_status, ldq, ldk, ldv,
-                      ldo,    q_rows, k_rows, B,       H,       Hq / H, Hq == H ? 0u : (uint32_t)((1ull << 32) / (Hq / H) + 1), scale};
+    // heads to a row tile: all of a KV head's up to 128, else the largest equal part
+    int G = Hq / H, share = 1;
+    while (G / share > apr::kTile || G % share) ++share;
+    G /= share;
+    const apr::Args a{q_bf16, k_bf16, v_bf16, q_start, k_start, o_bf16, dev_status, ldq, ldk, ldv, ldo, q_rows, k_rows, B,
+                      H * share, G, share, G == 1 ? 0u : (uint32_t)((1ull << 32) / G + 1), scale};
     return D == 128 ? apr::launch<128>(a, as_cuda(stream)) : apr::launch<64>(a, as_cuda(stream));
 }

@@ -76,6 +76,12 @@ int weight_tmap(CUtensorMap *out, const uint8_t *packed, int N, int K, int box_r
 // the matrix give zeros (not cached).
 int byte_tmap_sw128(CUtensorMap *out, const void *base, int rows, int cols, size_t pitch, int box_rows);
 
+// 3-D TMA map over rows of heads [rows][heads][head_bytes], rows `pitch` bytes
+// apart: boxes of 128 bytes x box_heads heads x box_rows rows, 128-byte
+// swizzle, rows past the tensor read as zeros (not cached).
+int row_box_tmap_sw128(CUtensorMap *out, const void *base, int head_bytes, int heads, int rows, size_t pitch, int box_heads,
+                       int box_rows);
+
 // 3-D TMA map over a 4-bit cache's codes [BH][T][row_bytes] (row_bytes 64 or
 // 32): boxes of one row's bytes x box_rows positions, swizzled over the row's
 // width, positions past T read as zeros (not cached).

@@ -92,6 +92,24 @@ int byte_tmap_sw128(CUtensorMap *out, const void *base, int rows, int cols, size
     return r == CUDA_SUCCESS ? QSPEC_OK : QSPEC_ERR_UNSUPPORTED;
 }
 
+// 3-D TMA map over rows of heads: [rows][heads][head_bytes], rows `pitch` bytes
+// apart: boxes of 128 bytes x box_heads heads x box_rows rows, 128-byte swizzle,
+// rows past the tensor read as zeros.  Not cached.
+int row_box_tmap_sw128(CUtensorMap *out, const void *base, int head_bytes, int heads, int rows, size_t pitch, int box_heads,
+                       int box_rows) {
+    EncodeTiled fn = encoder();
+    if (!fn) return QSPEC_ERR_UNSUPPORTED;
+    const cuuint64_t dims[3] = {(cuuint64_t)head_bytes, (cuuint64_t)heads, (cuuint64_t)rows};
+    const cuuint64_t strides[2] = {(cuuint64_t)head_bytes, (cuuint64_t)pitch};
+    const cuuint32_t box[3] = {128, (cuuint32_t)box_heads, (cuuint32_t)box_rows};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    std::memset(out, 0, sizeof(*out));
+    CUresult r = fn(out, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? QSPEC_OK : QSPEC_ERR_UNSUPPORTED;
+}
+
 // 3-D TMA map over the codes of a 4-bit cache [BH][T][row_bytes], row_bytes 64
 // or 32: boxes of one row's bytes x box_rows positions, swizzled over the row's
 // width, positions past T read as zeros.  Not cached.
