@@ -26,13 +26,48 @@ constexpr int kMaxK = 32768;
 __device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-    return (uint32_t)float_to_bf16_bits(a) | ((uint32_t)float_to_bf16_bits(b) << 16);
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+    return r;
 }
-// four E4M3 codes, element 0 in the low byte
-__device__ __forceinline__ uint32_t pack_e4m3(float a, float b, float c, float d) {
-    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
-    return lo | (hi << 16);
+__device__ __forceinline__ uint32_t add_bf16(uint32_t a, uint32_t b) {      // two bf16 sums, each rounded once
+    uint32_t d;
+    asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+// two fp32 values in a register pair, and packed operations on them
+__device__ __forceinline__ uint64_t f2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t both(uint32_t w) { return f2(lo_f(w), hi_f(w)); }
+__device__ __forceinline__ float lo32(uint64_t v) { return __uint_as_float((uint32_t)v); }
+__device__ __forceinline__ float hi32(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+// max(a, |b|, |c|) and max(a, b) that keep a NaN (a >= 0)
+__device__ __forceinline__ float max_abs(float a, float b, float c) {
+    float d;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+// two E4M3 codes, the first in the low byte
+__device__ __forceinline__ uint32_t pack_e4m3(uint64_t v) {
+    return __nv_cvt_float2_to_fp8x2(make_float2(lo32(v), hi32(v)), __NV_SATFINITE, __NV_E4M3);
 }
 
 // sum and maximum over the TPR threads of a row (all rows of a CTA take part)
@@ -41,7 +76,7 @@ __device__ __forceinline__ void row_reduce(float &sum, float &mx, float2 *red) {
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) {
         sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, o));
     }
     if constexpr (TPR > 32) {
         constexpr int kW = TPR / 32;
@@ -55,7 +90,7 @@ __device__ __forceinline__ void row_reduce(float &sum, float &mx, float2 *red) {
 #pragma unroll
         for (int o = kW / 2; o >= 1; o >>= 1) {
             sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, o));
         }
     }
 }
@@ -94,40 +129,51 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR)
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int i = t + j * TPR;
-            uint32_t a[4] = {hv[j].x, hv[j].y, hv[j].z, hv[j].w};
-            const uint32_t b[4] = {rv[j].x, rv[j].y, rv[j].z, rv[j].w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) a[e] = pack_bf16(lo_f(a[e]) + lo_f(b[e]), hi_f(a[e]) + hi_f(b[e]));
-            hv[j] = make_uint4(a[0], a[1], a[2], a[3]);
+            hv[j] = make_uint4(add_bf16(hv[j].x, rv[j].x), add_bf16(hv[j].y, rv[j].y), add_bf16(hv[j].z, rv[j].z),
+                               add_bf16(hv[j].w, rv[j].w));
             if (row_ok && i < n8) reinterpret_cast<uint4 *>(h + (size_t)m * ldh)[i] = hv[j];
         }
     }
-    // sum h^2 and max |h w|.  Where the squares or products of finite values
-    // pass fp32 (|h| above 1e19), the row is taken again times 2^-80.
-    float down = 1.0f, ss, amax;
-#pragma unroll 1
-    for (int pass = 0; pass < 2; ++pass) {
+    // sum h^2 and max |h w|; the products stay in registers for the codes
+    uint64_t a[NV][4], sq = 0;
+    float amax = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const uint32_t hw[4] = {hv[j].x, hv[j].y, hv[j].z, hv[j].w}, ww[4] = {wv[j].x, wv[j].y, wv[j].z, wv[j].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint64_t v = both(hw[e]);
+            sq = fma2(v, v, sq);
+            a[j][e] = mul2(v, both(ww[e]));
+            amax = max_abs(amax, lo32(a[j][e]), hi32(a[j][e]));
+        }
+    }
+    float ss = lo32(sq) + hi32(sq), down = 1.0f;
+    row_reduce<TPR>(ss, amax, red);
+    // Where the squares or products of finite values pass fp32 (|h| above 1e19),
+    // the row is read and taken again times 2^-80.
+    const bool again = !(ss < INFINITY && amax < INFINITY);
+    if (TPR > 32 ? again : __any_sync(0xffffffffu, again)) {
+        if (again) down = 8.271806125530277e-25f;        // 2^-80
+        const uint16_t *row = res != nullptr ? h + (size_t)m * ldh : x + (size_t)m * ldx;
         ss = 0.0f;
         amax = 0.0f;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const uint32_t a[4] = {hv[j].x, hv[j].y, hv[j].z, hv[j].w};
-            const uint32_t b[4] = {wv[j].x, wv[j].y, wv[j].z, wv[j].w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const float h0 = lo_f(a[e]) * down, h1 = hi_f(a[e]) * down;
-                ss = fmaf(h0, h0, ss);
-                ss = fmaf(h1, h1, ss);
-                const float p0 = fabsf(h0 * lo_f(b[e])), p1 = fabsf(h1 * hi_f(b[e]));
-                amax = fmaxf(amax, fmaxf(p0 < INFINITY ? p0 : INFINITY, p1 < INFINITY ? p1 : INFINITY));   // NaN counts as inf
+                const int i = 4 * (t + j * TPR) + e;
+                const bool in = row_ok && i < 4 * n8;
+                const uint64_t v = mul2(both(in ? reinterpret_cast<const uint32_t *>(row)[i] : 0u), f2(down, down));
+                ss = fmaf(lo32(v), lo32(v), fmaf(hi32(v), hi32(v), ss));
+                a[j][e] = mul2(v, both(in ? reinterpret_cast<const uint32_t *>(w)[i] : 0u));
+                amax = max_abs(amax, lo32(a[j][e]), hi32(a[j][e]));
             }
         }
         row_reduce<TPR>(ss, amax, red);
-        const bool again = pass == 0 && !(ss < INFINITY && amax < INFINITY);
-        if (TPR > 32 ? !again : !__any_sync(0xffffffffu, again)) break;
-        down = again ? 8.271806125530277e-25f : 1.0f;    // 2^-80
     }
     if (!row_ok) return;
+    if (!(amax < INFINITY)) amax = INFINITY;             // (NaN too)
     const float rstd = rsqrtf(fmaf(ss, 1.0f / (float)K, eps * down * down));
     // y = a rstd; codes a (448 / max |a|), where 448 / max |a| would pass fp32
     // with a brought up first
@@ -137,22 +183,24 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR)
     for (int j = 0; j < NV; ++j) {
         const int i = t + j * TPR;
         if (i >= n8) continue;
-        const uint32_t a[4] = {hv[j].x, hv[j].y, hv[j].z, hv[j].w};
-        const uint32_t b[4] = {wv[j].x, wv[j].y, wv[j].z, wv[j].w};
-        float p[8];
+        if (y != nullptr) {
+            uint32_t o[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint64_t v = mul2(a[j][e], f2(rstd, rstd));
+                o[e] = pack_bf16(lo32(v), hi32(v));
+            }
+            reinterpret_cast<uint4 *>(y + (size_t)m * ldy)[i] = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+        uint32_t code[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            p[2 * e] = lo_f(a[e]) * down * lo_f(b[e]);
-            p[2 * e + 1] = hi_f(a[e]) * down * hi_f(b[e]);
+            if (up != 1.0f) a[j][e] = mul2(a[j][e], f2(up, up));
+            code[e] = pack_e4m3(mul2(a[j][e], f2(inv, inv)));
         }
         reinterpret_cast<uint2 *>(xq + (size_t)m * K)[i] =
-            amax > 0.0f ? make_uint2(pack_e4m3(p[0] * up * inv, p[1] * up * inv, p[2] * up * inv, p[3] * up * inv),
-                                     pack_e4m3(p[4] * up * inv, p[5] * up * inv, p[6] * up * inv, p[7] * up * inv))
+            amax > 0.0f ? make_uint2(code[0] | code[1] << 16, code[2] | code[3] << 16)
                         : make_uint2(0u, 0u);         // no code of -0 in a row of zeros
-        if (y != nullptr)
-            reinterpret_cast<uint4 *>(y + (size_t)m * ldy)[i] =
-                make_uint4(pack_bf16(p[0] * rstd, p[1] * rstd), pack_bf16(p[2] * rstd, p[3] * rstd),
-                           pack_bf16(p[4] * rstd, p[5] * rstd), pack_bf16(p[6] * rstd, p[7] * rstd));
     }
     if (t == 0) {
         const float s = __fdiv_rn(amax * rstd, 448.0f);
