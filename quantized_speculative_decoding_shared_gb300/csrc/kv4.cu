@@ -8,8 +8,10 @@
 // it exactly) or at least 2^-10 from one for |x / s| < 16 (far beyond the
 // step's error): rint gives what the IEEE quotient gives.
 //
-// Pure streaming, bound by HBM: 16 bytes (8 values) per thread, D / 8 threads
-// per head row, K and V in the same thread so that a row's two loads overlap.
+// Pure streaming.  A warp takes one head of R consecutive rows of K or of V, L =
+// D / 8 lanes to a head row, 16 bytes (8 values) to a lane and kRounds rows one
+// after another: its codes and its scale words are then runs of R positions in the
+// cache, and the loads of all rounds are in flight together.
 #include <algorithm>
 #include <cuda_fp16.h>
 
@@ -22,28 +24,61 @@ namespace {
 
 namespace kv4 {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128, kWarps = kThreads / 32;
+constexpr int kRounds = 4;                       // head rows per group of lanes
+constexpr int kStage = 1024;                     // sequences whose starts are searched in shared memory
 
 struct Rows {
     const int32_t *start, *base;
     int rows, B, H, T;
 };
 
-// The position of packed row m in its sequence b, or -1: rows of no sequence,
-// and sequences whose ranges do not hold (flagged at the sequence's first row).
-__device__ __forceinline__ int locate(const Rows &r, int m, int &b) {
+// what a warp works on, and its lanes' share of it
+template <int D>
+struct Part {
+    static constexpr int L = D / 8, G = 32 / L, R = G * kRounds;
+    int m0, hd, l, g;
+    bool v, in;                                  // V, not K; there are such rows
+
+    __device__ __forceinline__ Part(const Rows &r) {
+        const uint32_t unit = blockIdx.x * kWarps + (threadIdx.x >> 5), u = unit >> 1, block = u / (uint32_t)r.H;
+        const int lane = threadIdx.x & 31;
+        v = unit & 1;
+        hd = (int)(u - block * (uint32_t)r.H);
+        in = (long long)block * R < r.rows;
+        m0 = in ? (int)block * R : 0;
+        l = lane % L;
+        g = lane / L;
+    }
+    // the packed row of round i (of lanes j = 0 .. R - 1 that look the rows up: place j)
+    __device__ __forceinline__ int row(int i) const { return m0 + g * kRounds + i; }
+};
+
+// the sequences' first rows into shared memory; a binary search there is short
+// against one in global memory, whose steps each wait for the last (8191 rows
+// of 7 sequences: 14.6 us a call with the search per thread in global memory)
+__device__ __forceinline__ const int32_t *stage_starts(const Rows &r, int32_t *buf) {
+    if (r.B > kStage) return r.start;
+    for (int i = threadIdx.x; i <= r.B; i += kThreads) buf[i] = __ldg(r.start + i);
+    __syncthreads();
+    return buf;
+}
+
+// The place (sequence, head, position) of packed row m in the cache, or -1: rows of
+// no sequence, and sequences whose ranges do not hold (flagged by check_ranges).
+__device__ __forceinline__ long long locate(const Rows &r, const int32_t *start, int m, int hd) {
+    if (m >= r.rows) return -1;
     int lo = 0, hi = r.B;                        // last b with start[b] <= m
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (__ldg(r.start + mid) <= m)
+        if (start[mid] <= m)
             lo = mid;
         else
             hi = mid;
     }
-    b = lo;
-    const int s0 = __ldg(r.start + lo), s1 = __ldg(r.start + lo + 1), p0 = __ldg(r.base + lo);
+    const int s0 = start[lo], s1 = start[lo + 1], p0 = __ldg(r.base + lo);
     if (m < s0 || m >= s1 || s0 < 0 || s1 > r.rows || p0 < 0 || (long long)p0 + (s1 - s0) > r.T) return -1;
-    return p0 + (m - s0);
+    return ((long long)lo * r.H + hd) * r.T + p0 + (m - s0);
 }
 
 // every sequence's ranges, by the first CTA (so that one without rows of its
@@ -58,47 +93,79 @@ __device__ __forceinline__ void check_ranges(const Rows &r, int32_t *st) {
     if (bad) flag(st, QSPEC_ERR_RANGE);
 }
 
-// 8 values of a head row held by L = D / 8 consecutive lanes -> their codes as
-// nibbles, and the row's scale word
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {          // of two bf16 values each
+    uint32_t d;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t f2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ float lo32(uint64_t v) { return __uint_as_float((uint32_t)v); }
+__device__ __forceinline__ float hi32(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
+
+// 8 values of a head row held by L consecutive lanes -> their codes as nibbles,
+// and the row's scale word
 template <int L>
 __device__ __forceinline__ uint32_t quantise(const uint4 &v, uint32_t &word, bool &bad) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    float f[8];
+    // (max(0, -min), max(0, max)) as two bf16 values, exact
+    const uint32_t n = 0x80008000u;
+    const uint32_t top = max2(max2(w[0], w[1]), max2(w[2], w[3]));
+    const uint32_t low = max2(max2(w[0] ^ n, w[1] ^ n), max2(w[2] ^ n, w[3] ^ n));
+    uint32_t ends = max2(max2(__byte_perm(low, top, 0x5410), __byte_perm(low, top, 0x7632)), 0u);
+#pragma unroll
+    for (int o = L / 2; o >= 1; o >>= 1) ends = max2(ends, __shfl_xor_sync(0xffffffffu, ends, o));
+    const float below = __uint_as_float(ends << 16), above = __uint_as_float(ends & 0xFFFF0000u);
+    const __half sh = __float2half_rn(__fdiv_rn(__fadd_rn(above, below), 15.0f));
+    const float s = __half2float(sh);
+    const float y = s > 0.0f ? __frcp_rn(s) : 0.0f;
+    // rint by the addition of 1.5 x 2^23: the integer is then in the low bits.  q stays below 32: s is at
+    // least half of (hi - lo) / 15 where it is not 0
+    constexpr float kInt = 12582912.0f;
+    auto quot = [&](uint64_t x) {
+        const uint64_t q0 = mul2(x, f2(y, y));
+        return add2(fma2(fma2(q0, f2(-s, -s), x), f2(y, y), q0), f2(kInt, kInt));
+    };
+    const uint32_t z = s > 0.0f ? (uint32_t)min((int)(__float_as_uint(lo32(quot(f2(below, below)))) & 0xFFu), 15) : 0u;
+    // integers i and i + 4 of the eight in one register, then shifted in by nibbles
+    uint32_t nan = 0, c[4];
+    uint64_t t[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        f[2 * i] = __uint_as_float(w[i] << 16);
-        f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        const float x0 = __uint_as_float(w[i] << 16), x1 = __uint_as_float(w[i] & 0xFFFF0000u);
+        nan |= (x0 != x0) | (x1 != x1);
+        t[i] = quot(f2(x0, x1));
     }
-    float lo = 0.0f, hi = 0.0f;
-    bool nan = false;
+    const uint32_t zz = z * 0x10001u;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        lo = fminf(lo, f[i]);
-        hi = fmaxf(hi, f[i]);
-        nan |= f[i] != f[i];
+    for (int i = 0; i < 4; ++i) {
+        const uint64_t a = t[i >> 1], b = t[2 + (i >> 1)];
+        const uint32_t both = __byte_perm(__float_as_uint(i & 1 ? hi32(a) : lo32(a)), __float_as_uint(i & 1 ? hi32(b) : lo32(b)), 0x5410);
+        uint32_t d;
+        asm("{ .reg .b32 x; add.s16x2 x, %1, %2; min.relu.s16x2 %0, x, %3; }" : "=r"(d) : "r"(both), "r"(zz), "r"(0x000F000Fu));
+        c[i] = d;
     }
-#pragma unroll
-    for (int o = L / 2; o >= 1; o >>= 1) {
-        lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-    }
-    const __half sh = __float2half_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.0f));
-    const float s = __half2float(sh);
-    bad |= nan || !(s < INFINITY);
-    const float y = s > 0.0f ? __frcp_rn(s) : 0.0f;
-    auto quot = [&](float x) {
-        const float q0 = __fmul_rn(x, y);
-        return rintf(__fmaf_rn(__fmaf_rn(-q0, s, x), y, q0));
-    };
-    const float z = s > 0.0f ? fminf(fmaxf(quot(-lo), 0.0f), 15.0f) : 0.0f;
-    uint32_t nib = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float c = s > 0.0f ? fminf(fmaxf(quot(f[i]) + z, 0.0f), 15.0f) : 0.0f;
-        nib |= (uint32_t)(int)c << (4 * i);
-    }
-    word = (uint32_t)__half_as_ushort(sh) | ((uint32_t)__half_as_ushort(__float2half_rn(z)) << 16);
-    return nib;
+    bad |= nan != 0 || !(s < INFINITY);
+    word = (uint32_t)__half_as_ushort(sh) | ((uint32_t)__half_as_ushort(__ushort2half_rn((unsigned short)z)) << 16);
+    return s > 0.0f ? (c[0] | c[1] << 4) | (c[2] << 8 | c[3] << 12) : 0u;
 }
 
 template <int D>
@@ -106,45 +173,60 @@ __global__ void __launch_bounds__(kThreads)
     append_kernel(const uint16_t *__restrict__ k, int ldk, const uint16_t *__restrict__ v, int ldv, Rows r,
                   uint32_t *__restrict__ kc, uint32_t *__restrict__ ks, uint32_t *__restrict__ vc,
                   uint32_t *__restrict__ vs, int32_t *st) {
-    constexpr int L = D / 8;
+    constexpr int L = Part<D>::L;
+    __shared__ int32_t buf[kStage + 1];
     pdl_launch_dependents();
+    const Part<D> p(r);
     pdl_wait();
     check_ranges(r, st);
-    const long long item = ((long long)blockIdx.x * kThreads + threadIdx.x) / L;
-    const int l = threadIdx.x % L;
-    const int m = (int)(item / r.H), hd = (int)(item - (long long)m * r.H);
-    int b = 0;
-    const int pos = m < r.rows ? locate(r, m, b) : -1;
-    uint4 kv = make_uint4(0, 0, 0, 0), vv = kv;
-    if (pos >= 0) {
-        kv = __ldcs(reinterpret_cast<const uint4 *>(k + (size_t)m * ldk + (size_t)hd * D) + l);
-        vv = __ldcs(reinterpret_cast<const uint4 *>(v + (size_t)m * ldv + (size_t)hd * D) + l);
-    }
+    const uint16_t *x = (p.v ? v : k) + (size_t)p.hd * D;
+    const int ld = p.v ? ldv : ldk;
+    uint4 in[kRounds];
+#pragma unroll
+    for (int i = 0; i < kRounds; ++i)
+        in[i] = p.in && p.row(i) < r.rows ? __ldcs(reinterpret_cast<const uint4 *>(x + (size_t)p.row(i) * ld) + p.l) : make_uint4(0, 0, 0, 0);
+    const int32_t *start = stage_starts(r, buf);
+    if (!p.in) return;
+    const int lane = threadIdx.x & 31;
+    const long long found = lane < Part<D>::R ? locate(r, start, p.m0 + lane, p.hd) : -1;
+    uint32_t *codes = p.v ? vc : kc, *sz = p.v ? vs : ks;
     bool bad = false;
-    uint32_t kw, vw;
-    const uint32_t kn = quantise<L>(kv, kw, bad), vn = quantise<L>(vv, vw, bad);
-    if (pos >= 0) {
-        const size_t at = ((size_t)b * r.H + hd) * r.T + pos;
-        kc[at * L + l] = kn;
-        vc[at * L + l] = vn;
-        if (l == 0) {
-            ks[at] = kw;
-            vs[at] = vw;
+    long long mine = -1;
+    uint32_t my_word = 0;
+#pragma unroll
+    for (int i = 0; i < kRounds; ++i) {
+        const long long at = __shfl_sync(0xffffffffu, found, p.g * kRounds + i);
+        uint32_t word;
+        bool b = false;
+        const uint32_t nib = quantise<L>(in[i], word, b);
+        if (at >= 0) {
+            codes[at * L + p.l] = nib;
+            bad |= b;
+        }
+        if (p.l == i) {
+            mine = at;
+            my_word = word;
         }
     }
+    if (mine >= 0) sz[mine] = my_word;           // R words side by side
     if (bad) flag(st, QSPEC_ERR_NONFINITE);
 }
 
-// 8 codes and a scale word -> 8 bf16 values s (c - z), each rounded once (the
-// product of an fp16 and a 4-bit integer is exact in fp32)
+// 8 codes and a scale word -> 8 bf16 values s (c - z), each rounded once (c - z
+// and the product of an fp16 and a 4-bit integer are exact in fp32)
 __device__ __forceinline__ uint4 values(uint32_t nib, uint32_t word) {
     const float s = __half2float(__ushort_as_half((uint16_t)(word & 0xFFFFu)));
     const float z = __half2float(__ushort_as_half((uint16_t)(word >> 16)));
+    // 2^23 + c by its bits, minus 2^23 + z
+    const float zi = -(8388608.0f + z);
+    const uint32_t even = nib & 0x0F0F0F0Fu, odd = (nib >> 4) & 0x0F0F0F0Fu;
     uint32_t o[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float a = s * ((float)((nib >> (8 * i)) & 15u) - z), c = s * ((float)((nib >> (8 * i + 4)) & 15u) - z);
-        o[i] = (uint32_t)float_to_bf16_bits(a) | ((uint32_t)float_to_bf16_bits(c) << 16);
+        const float a = __uint_as_float(__byte_perm(even, 0x4B000000u, 0x7440 | i));
+        const float c = __uint_as_float(__byte_perm(odd, 0x4B000000u, 0x7440 | i));
+        const uint64_t d = mul2(add2(f2(a, c), f2(zi, zi)), f2(s, s));
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o[i]) : "f"(hi32(d)), "f"(lo32(d)));
     }
     return make_uint4(o[0], o[1], o[2], o[3]);
 }
@@ -154,21 +236,37 @@ __global__ void __launch_bounds__(kThreads)
     load_kernel(const uint32_t *__restrict__ kc, const uint32_t *__restrict__ ks, const uint32_t *__restrict__ vc,
                 const uint32_t *__restrict__ vs, Rows r, uint16_t *__restrict__ k, int ldk, uint16_t *__restrict__ v,
                 int ldv, int32_t *st) {
-    constexpr int L = D / 8;
+    constexpr int L = Part<D>::L;
+    __shared__ int32_t buf[kStage + 1];
     pdl_launch_dependents();
+    const Part<D> p(r);
     pdl_wait();
     check_ranges(r, st);
-    const long long item = ((long long)blockIdx.x * kThreads + threadIdx.x) / L;
-    const int l = threadIdx.x % L;
-    const int m = (int)(item / r.H), hd = (int)(item - (long long)m * r.H);
-    if (m >= r.rows) return;
-    int b = 0;
-    const int pos = locate(r, m, b);
-    if (pos < 0) return;
-    const size_t at = ((size_t)b * r.H + hd) * r.T + pos;
-    const uint32_t kn = kc[at * L + l], vn = vc[at * L + l], kw = ks[at], vw = vs[at];
-    reinterpret_cast<uint4 *>(k + (size_t)m * ldk + (size_t)hd * D)[l] = values(kn, kw);
-    reinterpret_cast<uint4 *>(v + (size_t)m * ldv + (size_t)hd * D)[l] = values(vn, vw);
+    const int32_t *start = stage_starts(r, buf);
+    if (!p.in) return;
+    const int lane = threadIdx.x & 31;
+    const long long found = lane < Part<D>::R ? locate(r, start, p.m0 + lane, p.hd) : -1;
+    const uint32_t *codes = p.v ? vc : kc, *sz = p.v ? vs : ks;
+    uint32_t nib[kRounds], word[kRounds];
+    bool there[kRounds];
+#pragma unroll
+    for (int i = 0; i < kRounds; ++i) {
+        const long long at = __shfl_sync(0xffffffffu, found, p.g * kRounds + i);
+        there[i] = at >= 0;
+        nib[i] = there[i] ? __ldg(codes + at * L + p.l) : 0u;
+        word[i] = there[i] ? __ldg(sz + at) : 0u;
+    }
+    uint16_t *x = (p.v ? v : k) + (size_t)p.hd * D;
+    const int ld = p.v ? ldv : ldk;
+#pragma unroll
+    for (int i = 0; i < kRounds; ++i)
+        if (there[i]) reinterpret_cast<uint4 *>(x + (size_t)p.row(i) * ld)[p.l] = values(nib[i], word[i]);
+}
+
+// CTAs of a call
+template <int D>
+long long ctas(long long rows, int H) {
+    return ((rows + Part<D>::R - 1) / Part<D>::R * H * 2 + kWarps - 1) / kWarps;
 }
 
 // what both calls can refuse on the host
@@ -177,7 +275,7 @@ int check(const void *k, int ldk, const void *v, int ldv, const int32_t *start, 
     if (!start || !base || !kc || !ks || !vc || !vs || (rows > 0 && (!k || !v))) return QSPEC_ERR_NULL;
     if (rows < 0 || B < 1 || H < 1 || T < 1 || (D != 64 && D != 128)) return QSPEC_ERR_SHAPE;
     if (ldk < (long long)H * D || ldv < (long long)H * D) return QSPEC_ERR_SHAPE;
-    if ((long long)rows * H * (D / 8) / kThreads >= (1LL << 31) - 1) return QSPEC_ERR_SHAPE;
+    if ((D == 128 ? ctas<128>(rows, H) : ctas<64>(rows, H)) * kWarps >= 1LL << 32) return QSPEC_ERR_SHAPE;
     if (ldk % 8 || ldv % 8 || !aligned(k, 16) || !aligned(v, 16) || !aligned(kc, 16) || !aligned(vc, 16) ||
         !aligned(ks, 4) || !aligned(vs, 4) || !aligned(start, 4) || !aligned(base, 4))
         return QSPEC_ERR_ALIGN;
@@ -199,7 +297,7 @@ extern "C" int qspec_kv4_append(const uint16_t *k_bf16, int ldk, const uint16_t 
     int rc = kv4::check(k_bf16, ldk, v_bf16, ldv, row_start, base_pos, rows, B, H, T, D, k_codes, k_sz, v_codes, v_sz);
     if (rc || rows == 0) return rc;
     const kv4::Rows r{row_start, base_pos, rows, B, H, T};
-    const unsigned grid = (unsigned)(((long long)rows * H * (D / 8) + kv4::kThreads - 1) / kv4::kThreads);
+    const unsigned grid = (unsigned)(D == 128 ? kv4::ctas<128>(rows, H) : kv4::ctas<64>(rows, H));
     auto kern = D == 128 ? kv4::append_kernel<128> : kv4::append_kernel<64>;
     return launch_pdl("qspec_kv4_append", kern, dim3(grid), dim3(kv4::kThreads), 0, as_cuda(stream), k_bf16, ldk,
                       v_bf16, ldv, r, reinterpret_cast<uint32_t *>(k_codes), k_sz,
@@ -213,7 +311,7 @@ extern "C" int qspec_kv4_load(const uint8_t *k_codes, const uint32_t *k_sz, cons
     int rc = kv4::check(k_bf16, ldk, v_bf16, ldv, row_start, base_pos, rows, B, H, T, D, k_codes, k_sz, v_codes, v_sz);
     if (rc || rows == 0) return rc;
     const kv4::Rows r{row_start, base_pos, rows, B, H, T};
-    const unsigned grid = (unsigned)(((long long)rows * H * (D / 8) + kv4::kThreads - 1) / kv4::kThreads);
+    const unsigned grid = (unsigned)(D == 128 ? kv4::ctas<128>(rows, H) : kv4::ctas<64>(rows, H));
     auto kern = D == 128 ? kv4::load_kernel<128> : kv4::load_kernel<64>;
     return launch_pdl("qspec_kv4_load", kern, dim3(grid), dim3(kv4::kThreads), 0, as_cuda(stream),
                       reinterpret_cast<const uint32_t *>(k_codes), k_sz, reinterpret_cast<const uint32_t *>(v_codes),
