@@ -8,11 +8,15 @@
 // it exactly) or at least 2^-10 from one for |x / s| < 16 (far beyond the
 // step's error): rint gives what the IEEE quotient gives.
 //
-// Pure streaming.  A warp takes one head of R consecutive rows of K or of V, L =
-// D / 8 lanes to a head row, 16 bytes (8 values) to a lane and kRounds rows one
-// after another: its codes and its scale words are then runs of R positions in the
-// cache, and the loads of all rounds are in flight together.
+// Streaming: 2 D bytes of a head row against D / 2 + 4 of the cache.  Long prompts
+// come to HBM's rate on the way out and to the instructions issued on the way in
+// (32764 rows of 8 heads of 128: load 6.2 TB/s, append 4.6).  A warp takes one head of R
+// consecutive rows of K and of V, L = D / 8 lanes to a head row, 16 bytes (8 values)
+// to a lane and kRounds rows one after another: its codes and its scale words are
+// then runs of positions in the cache, the rows are looked up once, and the loads
+// of all rounds are in flight together.
 #include <algorithm>
+#include <climits>
 #include <cuda_fp16.h>
 
 #include "qspec_device.cuh"
@@ -25,7 +29,9 @@ namespace {
 namespace kv4 {
 
 constexpr int kThreads = 128, kWarps = kThreads / 32;
-constexpr int kRounds = 4;                       // head rows per group of lanes
+// head rows per group of lanes, of K and of V each: 8191 rows of 8 heads append in 11.7 us and load in 8.9 (four rounds:
+// 11.3 and 9.9), 80 rows in 2.3 and 2.3 (2.9 and 2.5); 8 warps a CTA the same within 0.2, 2 warps 1.5 us slower
+constexpr int kRounds = 2;
 constexpr int kStage = 1024;                     // sequences whose starts are searched in shared memory
 
 struct Rows {
@@ -38,13 +44,12 @@ template <int D>
 struct Part {
     static constexpr int L = D / 8, G = 32 / L, R = G * kRounds;
     int m0, hd, l, g;
-    bool v, in;                                  // V, not K; there are such rows
+    bool in;                                     // there are such rows
 
     __device__ __forceinline__ Part(const Rows &r) {
-        const uint32_t unit = blockIdx.x * kWarps + (threadIdx.x >> 5), u = unit >> 1, block = u / (uint32_t)r.H;
+        const uint32_t unit = blockIdx.x * kWarps + (threadIdx.x >> 5), block = unit / (uint32_t)r.H;
         const int lane = threadIdx.x & 31;
-        v = unit & 1;
-        hd = (int)(u - block * (uint32_t)r.H);
+        hd = (int)(unit - block * (uint32_t)r.H);
         in = (long long)block * R < r.rows;
         m0 = in ? (int)block * R : 0;
         l = lane % L;
@@ -55,8 +60,7 @@ struct Part {
 };
 
 // the sequences' first rows into shared memory; a binary search there is short
-// against one in global memory, whose steps each wait for the last (8191 rows
-// of 7 sequences: 14.6 us a call with the search per thread in global memory)
+// against one in global memory, whose steps each wait for the last
 __device__ __forceinline__ const int32_t *stage_starts(const Rows &r, int32_t *buf) {
     if (r.B > kStage) return r.start;
     for (int i = threadIdx.x; i <= r.B; i += kThreads) buf[i] = __ldg(r.start + i);
@@ -93,9 +97,9 @@ __device__ __forceinline__ void check_ranges(const Rows &r, int32_t *st) {
     if (bad) flag(st, QSPEC_ERR_RANGE);
 }
 
-__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {          // of two bf16 values each
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {          // of two bf16 values each, keeps a NaN
     uint32_t d;
-    asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
     return d;
 }
 __device__ __forceinline__ uint64_t f2(float a, float b) {
@@ -134,9 +138,14 @@ __device__ __forceinline__ uint32_t quantise(const uint4 &v, uint32_t &word, boo
 #pragma unroll
     for (int o = L / 2; o >= 1; o >>= 1) ends = max2(ends, __shfl_xor_sync(0xffffffffu, ends, o));
     const float below = __uint_as_float(ends << 16), above = __uint_as_float(ends & 0xFFFF0000u);
-    const __half sh = __float2half_rn(__fdiv_rn(__fadd_rn(above, below), 15.0f));
-    const float s = __half2float(sh);
-    const float y = s > 0.0f ? __frcp_rn(s) : 0.0f;
+    // (hi - lo) / 15, correctly rounded where it is a normal number (and 0 in fp16 where it is not): the residual
+    // of the product with the rounded 1 / 15 is exact, and one step with it rounds like the quotient
+    const float range = __fadd_rn(above, below), t0 = __fmul_rn(range, 1.0f / 15.0f);
+    const __half sh = __float2half_rn(__fmaf_rn(__fmaf_rn(t0, -15.0f, range), 1.0f / 15.0f, t0));
+    const float s = __half2float(sh);            // NaN where a value is not finite
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(s));
+    if (!(s > 0.0f)) y = 0.0f;
     // rint by the addition of 1.5 x 2^23: the integer is then in the low bits.  q stays below 32: s is at
     // least half of (hi - lo) / 15 where it is not 0
     constexpr float kInt = 12582912.0f;
@@ -146,14 +155,10 @@ __device__ __forceinline__ uint32_t quantise(const uint4 &v, uint32_t &word, boo
     };
     const uint32_t z = s > 0.0f ? (uint32_t)min((int)(__float_as_uint(lo32(quot(f2(below, below)))) & 0xFFu), 15) : 0u;
     // integers i and i + 4 of the eight in one register, then shifted in by nibbles
-    uint32_t nan = 0, c[4];
+    uint32_t c[4];
     uint64_t t[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float x0 = __uint_as_float(w[i] << 16), x1 = __uint_as_float(w[i] & 0xFFFF0000u);
-        nan |= (x0 != x0) | (x1 != x1);
-        t[i] = quot(f2(x0, x1));
-    }
+    for (int i = 0; i < 4; ++i) t[i] = quot(f2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u)));
     const uint32_t zz = z * 0x10001u;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -163,9 +168,24 @@ __device__ __forceinline__ uint32_t quantise(const uint4 &v, uint32_t &word, boo
         asm("{ .reg .b32 x; add.s16x2 x, %1, %2; min.relu.s16x2 %0, x, %3; }" : "=r"(d) : "r"(both), "r"(zz), "r"(0x000F000Fu));
         c[i] = d;
     }
-    bad |= nan != 0 || !(s < INFINITY);
+    bad |= !(s < INFINITY);
     word = (uint32_t)__half_as_ushort(sh) | ((uint32_t)__half_as_ushort(__ushort2half_rn((unsigned short)z)) << 16);
     return s > 0.0f ? (c[0] | c[1] << 4) | (c[2] << 8 | c[3] << 12) : 0u;
+}
+
+// A warp's rounds with their rows' places.  Where all R rows lie one after another in
+// one sequence (nearly always in a prompt) the places are steps from the first,
+// so the addresses are too (the instructions issued are what bounds these kernels).
+template <int D, class F>
+__device__ __forceinline__ void one_run(const Part<D> &p, long long found, F rounds) {
+    const int lane = threadIdx.x & 31;
+    const long long first = __shfl_sync(0xffffffffu, found, 0);
+    if (first >= 0 && __all_sync(0xffffffffu, lane >= Part<D>::R || found == first + lane)) {
+        const long long mine = first + p.g * kRounds;
+        rounds([=](int i) { return mine + i; });
+    } else {
+        rounds([=](int i) { return __shfl_sync(0xffffffffu, found, p.g * kRounds + i); });
+    }
 }
 
 template <int D>
@@ -179,36 +199,44 @@ __global__ void __launch_bounds__(kThreads)
     const Part<D> p(r);
     pdl_wait();
     check_ranges(r, st);
-    const uint16_t *x = (p.v ? v : k) + (size_t)p.hd * D;
-    const int ld = p.v ? ldv : ldk;
-    uint4 in[kRounds];
+    uint4 in[2][kRounds];
 #pragma unroll
-    for (int i = 0; i < kRounds; ++i)
-        in[i] = p.in && p.row(i) < r.rows ? __ldcs(reinterpret_cast<const uint4 *>(x + (size_t)p.row(i) * ld) + p.l) : make_uint4(0, 0, 0, 0);
+    for (int i = 0; i < kRounds; ++i) {
+        const bool there = p.in && p.row(i) < r.rows;
+        const size_t m = (size_t)p.row(i);
+        in[0][i] = there ? __ldcs(reinterpret_cast<const uint4 *>(k + m * ldk + (size_t)p.hd * D) + p.l) : make_uint4(0, 0, 0, 0);
+        in[1][i] = there ? __ldcs(reinterpret_cast<const uint4 *>(v + m * ldv + (size_t)p.hd * D) + p.l) : make_uint4(0, 0, 0, 0);
+    }
     const int32_t *start = stage_starts(r, buf);
     if (!p.in) return;
     const int lane = threadIdx.x & 31;
     const long long found = lane < Part<D>::R ? locate(r, start, p.m0 + lane, p.hd) : -1;
-    uint32_t *codes = p.v ? vc : kc, *sz = p.v ? vs : ks;
     bool bad = false;
-    long long mine = -1;
-    uint32_t my_word = 0;
+    uint32_t word[2] = {0, 0};                   // of the row that this lane writes
+    auto rounds = [&](auto place) {
 #pragma unroll
-    for (int i = 0; i < kRounds; ++i) {
-        const long long at = __shfl_sync(0xffffffffu, found, p.g * kRounds + i);
-        uint32_t word;
-        bool b = false;
-        const uint32_t nib = quantise<L>(in[i], word, b);
-        if (at >= 0) {
-            codes[at * L + p.l] = nib;
-            bad |= b;
+        for (int i = 0; i < kRounds; ++i) {
+            const long long at = place(i);
+            bool b = false;
+            uint32_t kw, vw;
+            const uint32_t kn = quantise<L>(in[0][i], kw, b), vn = quantise<L>(in[1][i], vw, b);
+            if (at >= 0) {
+                kc[at * L + p.l] = kn;
+                vc[at * L + p.l] = vn;
+                bad |= b;
+            }
+            if (p.l == i) {
+                word[0] = kw;
+                word[1] = vw;
+            }
         }
-        if (p.l == i) {
-            mine = at;
-            my_word = word;
-        }
+    };
+    const long long mine = __shfl_sync(0xffffffffu, found, (p.g * kRounds + p.l) & 31);
+    one_run<D>(p, found, rounds);
+    if (p.l < kRounds && mine >= 0) {            // R words side by side
+        ks[mine] = word[0];
+        vs[mine] = word[1];
     }
-    if (mine >= 0) sz[mine] = my_word;           // R words side by side
     if (bad) flag(st, QSPEC_ERR_NONFINITE);
 }
 
@@ -246,34 +274,40 @@ __global__ void __launch_bounds__(kThreads)
     if (!p.in) return;
     const int lane = threadIdx.x & 31;
     const long long found = lane < Part<D>::R ? locate(r, start, p.m0 + lane, p.hd) : -1;
-    const uint32_t *codes = p.v ? vc : kc, *sz = p.v ? vs : ks;
-    uint32_t nib[kRounds], word[kRounds];
-    bool there[kRounds];
+    auto rounds = [&](auto place) {
+        uint32_t kn[kRounds], vn[kRounds], kw[kRounds], vw[kRounds];
+        bool there[kRounds];
 #pragma unroll
-    for (int i = 0; i < kRounds; ++i) {
-        const long long at = __shfl_sync(0xffffffffu, found, p.g * kRounds + i);
-        there[i] = at >= 0;
-        nib[i] = there[i] ? __ldg(codes + at * L + p.l) : 0u;
-        word[i] = there[i] ? __ldg(sz + at) : 0u;
-    }
-    uint16_t *x = (p.v ? v : k) + (size_t)p.hd * D;
-    const int ld = p.v ? ldv : ldk;
+        for (int i = 0; i < kRounds; ++i) {
+            const long long at = place(i);
+            there[i] = at >= 0;
+            kn[i] = there[i] ? __ldg(kc + at * L + p.l) : 0u;
+            vn[i] = there[i] ? __ldg(vc + at * L + p.l) : 0u;
+            kw[i] = there[i] ? __ldg(ks + at) : 0u;
+            vw[i] = there[i] ? __ldg(vs + at) : 0u;
+        }
 #pragma unroll
-    for (int i = 0; i < kRounds; ++i)
-        if (there[i]) reinterpret_cast<uint4 *>(x + (size_t)p.row(i) * ld)[p.l] = values(nib[i], word[i]);
+        for (int i = 0; i < kRounds; ++i)
+            if (there[i]) {
+                const size_t m = (size_t)p.row(i);
+                reinterpret_cast<uint4 *>(k + m * ldk + (size_t)p.hd * D)[p.l] = values(kn[i], kw[i]);
+                reinterpret_cast<uint4 *>(v + m * ldv + (size_t)p.hd * D)[p.l] = values(vn[i], vw[i]);
+            }
+    };
+    one_run<D>(p, found, rounds);
 }
 
 // CTAs of a call
 template <int D>
 long long ctas(long long rows, int H) {
-    return ((rows + Part<D>::R - 1) / Part<D>::R * H * 2 + kWarps - 1) / kWarps;
+    return ((rows + Part<D>::R - 1) / Part<D>::R * H + kWarps - 1) / kWarps;
 }
 
 // what both calls can refuse on the host
 int check(const void *k, int ldk, const void *v, int ldv, const int32_t *start, const int32_t *base, int rows, int B,
           int H, int T, int D, const void *kc, const void *ks, const void *vc, const void *vs) {
     if (!start || !base || !kc || !ks || !vc || !vs || (rows > 0 && (!k || !v))) return QSPEC_ERR_NULL;
-    if (rows < 0 || B < 1 || H < 1 || T < 1 || (D != 64 && D != 128)) return QSPEC_ERR_SHAPE;
+    if (rows < 0 || rows > INT_MAX - 64 || B < 1 || H < 1 || T < 1 || (D != 64 && D != 128)) return QSPEC_ERR_SHAPE;
     if (ldk < (long long)H * D || ldv < (long long)H * D) return QSPEC_ERR_SHAPE;
     if ((D == 128 ? ctas<128>(rows, H) : ctas<64>(rows, H)) * kWarps >= 1LL << 32) return QSPEC_ERR_SHAPE;
     if (ldk % 8 || ldv % 8 || !aligned(k, 16) || !aligned(v, 16) || !aligned(kc, 16) || !aligned(vc, 16) ||
