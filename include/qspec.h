@@ -456,9 +456,11 @@ size_t qspec_attn_kv4_workspace_bytes(int B, int R, int Hq, int H, int D);
  *                              Its first use needs it zeroed; every call leaves it
  *                              ready for the next, of any shape that fits.  Calls
  *                              that may overlap on the GPU need one each.
- * 1 <= R <= 17, Hq a multiple of H, D 64 or 128; q, o and the codes 16-byte
+ * 1 <= R <= 17, Hq a multiple of H (Hq / H <= 8192), D 64 or 128, T <= 2^30,
+ * B H ceil(R (Hq / H) / 64) (ceil(T / 128) + 8) < 2^30; q, o and the codes 16-byte
  * aligned, ldq, ldo multiples of 8.  Device errors: QSPEC_ERR_RANGE (len[b]
- * outside [0, T]; that sequence's outputs are left untouched).
+ * outside [0, T]; that sequence's outputs are left untouched),
+ * QSPEC_ERR_TIMEOUT (a wait inside the kernel ran out).
  */
 int qspec_attn_kv4(const uint16_t *q_bf16, int ldq, const uint8_t *k_codes, const uint32_t *k_sz,
                    const uint8_t *v_codes, const uint32_t *v_sz, const int32_t *len, int B, int R,

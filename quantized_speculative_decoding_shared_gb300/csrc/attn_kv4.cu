@@ -59,8 +59,11 @@ constexpr int kTok = 128;                       // positions per tile
 template <int N>
 struct Cfg {
     static constexpr int kGroups = 3, kWorkWarps = 4 * kGroups, kWork = 32 * kWorkWarps;
-    static constexpr int kScoreWarp = kWorkWarps, kValueWarp = kScoreWarp + 1, kLoadWarp = kValueWarp + 1;   // one lane each: S^T, O^T products, copies
-    static constexpr int kThreads = kWork + 96;
+    static constexpr int kScoreWarp = kWorkWarps, kValueWarp = kScoreWarp + 1, kLoadWarp = kValueWarp + 1, kTellWarp = kLoadWarp + 1;   // one lane each: S^T, O^T products, copies, finished parts
+    static constexpr int kThreads = kWork + 128;
+    // registers per thread: all start with 128 and share what that makes
+    static constexpr int kRegsWork = 144, kRegsRest = 64;
+    static_assert(kThreads * 128 <= 65536 && kWork * kRegsWork + 128 * kRegsRest <= kThreads * 128, "register shares");
     // Tiles of codes in flight.  A stage always serves the same group: one whose next tile came into another
     // group's stage could look at that stage's barrier a whole phase early, and take the phase before for its own.
     static constexpr int kStages = N == 16 ? 6 : 3;
@@ -90,6 +93,7 @@ struct Ctl {
     uint64_t full[kMaxStages], empty[kMaxStages];     // codes landed; unpacked
     uint64_t kfull[kGroups], sfull[kGroups], pfull[kGroups], vfull[kGroups], pdone[kGroups];   // K in tensor memory, S^T, P^T, V, O^T += done
     uint64_t qfull, ref, odone, drain[2];       // per segment: Q written, reference known, O^T complete
+    uint64_t stored[2];                         // once: results of the part of a task that the CTA continues, begins
     float4 back[N / 2];                         // score of rows n, n + 1: {back, back'}({s u - ref, s u' - ref'}), as {back, back', -ref, -ref'}
     float lse[N], inv[N];
     float lsum[kWorkWarps][N];
@@ -242,7 +246,7 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
                     const __grid_constant__ Args a, uint32_t wait_limit) {
     constexpr int kSide = side_bytes<D>(), kP = p_bytes<N>(), kStages = Cfg<N>::kStages;
     constexpr int kGroups = Cfg<N>::kGroups, kWorkWarps = Cfg<N>::kWorkWarps, kWork = Cfg<N>::kWork;
-    constexpr int kScoreWarp = Cfg<N>::kScoreWarp, kValueWarp = Cfg<N>::kValueWarp, kLoadWarp = Cfg<N>::kLoadWarp;
+    constexpr int kScoreWarp = Cfg<N>::kScoreWarp, kValueWarp = Cfg<N>::kValueWarp, kLoadWarp = Cfg<N>::kLoadWarp, kTellWarp = Cfg<N>::kTellWarp;
     constexpr int kSteps = D / 16;                               // MMA steps of S^T (one more holds z)
     constexpr uint32_t cS = 0, cK = kGroups * N, cO = cK + kGroups * 80;   // the groups' S^T and K operands (80 columns each), O^T
     constexpr uint32_t kCols = 512;
@@ -270,6 +274,8 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
         umma::mbar_init(&sm.qfull, kWorkWarps);
         umma::mbar_init(&sm.ref, 1);
         umma::mbar_init(&sm.odone, 1);
+        umma::mbar_init(&sm.stored[0], kWorkWarps);
+        umma::mbar_init(&sm.stored[1], kWorkWarps);
         umma::mbar_init(&sm.drain[0], 1);
         umma::mbar_init(&sm.drain[1], 1);
         sm.timeout = 0;
@@ -296,107 +302,140 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
     // (the votes keep an issuing warp together where a wait runs out)
     auto all = [](bool mine) { return __all_sync(0xffffffffu, mine) != 0; };
 
-    // ---- this CTA's share of the tiles (every warp finds it for itself) ----
+    // ---- this CTA's share of the tiles (every warp finds it for itself; 32-bit numbers, the host sees to it: with
+    // 64-bit divisions this took 2 us) ----
     const int tasks = a.H * a.blocks;           // per sequence
-    auto tiles_of = [&](int b) -> int {
-        const int n = __ldg(a.len + b);
-        return n < 0 || n > a.T ? 0 : max(1, (n + kTok - 1) / kTok);
+    auto tiles_in = [&](int n) { return n < 0 || n > a.T ? 0 : max(1, (n + kTok - 1) / kTok); };
+    auto tiles_of = [&](int b) { return tiles_in(__ldg(a.len + b)); };
+    auto scan = [&](int c) {                    // inclusive, over the lanes
+#pragma unroll
+        for (int x = 1; x < 32; x <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, c, x);
+            if (lane >= x) c += y;
+        }
+        return c;
     };
-    const int mine = lane < a.B ? tiles_of(lane) : 0;            // the first 32 sequences', kept
-    long long total = 0;
-    for (int b0 = 0; b0 < a.B; b0 += 32) {
-        const int c = b0 == 0 ? mine : b0 + lane < a.B ? tiles_of(b0 + lane) : 0;
+    const int my_len = lane < a.B ? __ldg(a.len + lane) : -1, mine = tiles_in(my_len), mine_upto = scan(mine);   // the first 32 sequences', kept
+    auto len_of = [&](int b) { return b < 32 ? __shfl_sync(0xffffffffu, my_len, b) : __ldg(a.len + b); };
+    if (blockIdx.x == 0 && warp == 0 && lane < a.B && mine == 0) flag(a.st, QSPEC_ERR_RANGE);
+    int total = __shfl_sync(0xffffffffu, mine_upto, 31), valid = __popc(__ballot_sync(0xffffffffu, mine > 0));   // tiles; sequences with tasks
+    for (int b0 = 32; b0 < a.B; b0 += 32) {
+        const int c = b0 + lane < a.B ? tiles_of(b0 + lane) : 0;
         if (blockIdx.x == 0 && warp == 0 && b0 + lane < a.B && c == 0) flag(a.st, QSPEC_ERR_RANGE);
         total += __reduce_add_sync(0xffffffffu, c);
+        valid += __popc(__ballot_sync(0xffffffffu, c > 0));
     }
     total *= tasks;
     // Few tiles: four to a CTA rather than one, since every part of a task more is another result to join (one
     // sequence of 333 / 4000 positions, one row: 7.8 / 12.1 us with four, 9.5 / 13.7 us with one); with 64 rows a tile
     // takes longer than its part in a join, and one is better (18.8 for 22.9 us at 4 sequences of 1000, gamma 8).
-    const long long nc = min((long long)gridDim.x, N == 64 ? total : max(total / 4, min(total, (long long)tasks)));
-    const bool any = blockIdx.x < nc;
+    const int nc = min((int)gridDim.x, N == 64 ? total : max(total / 4, min(total, tasks)));
+    const bool any = (int)blockIdx.x < nc;
     // Beginning and ending a segment (Q, the first tile's way through the products, sums, results) takes as
     // long as some eight tiles (measured: 4, 6, 8, 11, 15 give 41.8, 40.6, 38.1, 38.2, 38.1 us at 32 sequences,
     // gamma 8); where a CTA has fewer than sixteen, half of them: few tiles are better spread.
-    const int lead = (int)min(8ll, total / (2ll * gridDim.x));
-    // Tiles before share i: a border among a task's leading empty tiles is its first tile.
-    long long valid = 0;                         // sequences with tasks
-    for (int b0 = 0; b0 < a.B; b0 += 32) {
-        const int c = b0 == 0 ? mine : b0 + lane < a.B ? tiles_of(b0 + lane) : 0;
-        valid += __popc(__ballot_sync(0xffffffffu, c > 0));
-    }
-    const long long total_v = total + valid * tasks * lead;
-    int b = 0;                                   // of the share's first tile
-    long long prefix = 0, before = 0;            // tiles, and tasks, before sequence b
-    auto border = [&](long long i, int &sb, long long &sprefix, long long &sbefore) -> long long {
-        const long long v = i * total_v / nc;
+    const int lead = (int)min(8u, (uint32_t)total / (2u * gridDim.x));
+    // Shares: borders i total_v / nc, rounded down (i times the remainder is below 160 x 160, and its quotient by nc
+    // at least 1 / 320 from an integer after the half: fp32 finds it).  A border among a task's leading empty
+    // tiles is its first tile.
+    const int total_v = total + valid * tasks * lead;
+    const int share = (int)((uint32_t)total_v / (uint32_t)max(nc, 1)), rest = total_v - share * nc;
+    const float per_nc = __fdividef(1.0f, (float)max(nc, 1));
+    auto border_v = [&](int i) { return i * share + (int)(((float)(i * rest) + 0.5f) * per_nc); };
+    auto border = [&](int v, int &sb, int &sprefix, int &sbefore, int &stask, int &stile) -> int {
         sprefix = sbefore = 0;
         for (int b0 = 0; b0 < a.B; b0 += 32) {
-            const int c = b0 == 0 ? mine : b0 + lane < a.B ? tiles_of(b0 + lane) : 0;
-            int upto = c, some = c > 0;
-#pragma unroll
-            for (int x = 1; x < 32; x <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, upto, x), z = __shfl_up_sync(0xffffffffu, some, x);
-                if (lane >= x) {
-                    upto += y;
-                    some += z;
-                }
-            }
-            const long long v_end = sprefix + sbefore * lead + ((long long)upto + (long long)some * lead) * tasks;
+            const int c = b0 == 0 ? mine : b0 + lane < a.B ? tiles_of(b0 + lane) : 0, upto = b0 == 0 ? mine_upto : scan(c);
+            const uint32_t there = __ballot_sync(0xffffffffu, c > 0);
+            const int v_end = sprefix + sbefore * lead + (upto + __popc(there & ((2u << lane) - 1)) * lead) * tasks;
             const uint32_t past = __ballot_sync(0xffffffffu, v_end > v);
             if (past) {
                 const int who = __ffs(past) - 1, cw = __shfl_sync(0xffffffffu, c, who);
                 sb = b0 + who;
-                sprefix += (long long)(__shfl_sync(0xffffffffu, upto, who) - cw) * tasks;
-                sbefore += (long long)(__shfl_sync(0xffffffffu, some, who) - 1) * tasks;
-                const long long in = v - sprefix - sbefore * lead, t = in / (cw + lead);
-                return sprefix + t * cw + max(0ll, in - t * (cw + lead) - lead);
+                sprefix += (__shfl_sync(0xffffffffu, upto, who) - cw) * tasks;
+                sbefore += __popc(there & ((1u << who) - 1)) * tasks;
+                const uint32_t in = (uint32_t)(v - sprefix - sbefore * lead);
+                stask = (int)(in / (uint32_t)(cw + lead));
+                stile = max(0, (int)in - stask * (cw + lead) - lead);
+                return sprefix + stask * cw + stile;
             }
-            sprefix += (long long)__shfl_sync(0xffffffffu, upto, 31) * tasks;
-            sbefore += (long long)__shfl_sync(0xffffffffu, some, 31) * tasks;
+            sprefix += __shfl_sync(0xffffffffu, upto, 31) * tasks;
+            sbefore += __popc(there) * tasks;
         }
         return total;
     };
-    long long at = 0, end = 0;
+    int b = 0, task = 0, tile = 0;               // of the share's first tile
+    int prefix = 0, before = 0;                  // tiles, and tasks, before sequence b
+    int at = 0, end = 0;
     if (any) {
-        int sb;
-        long long sp, sn;
-        end = border(blockIdx.x + 1, sb, sp, sn);
-        at = border(blockIdx.x, b, prefix, before);
+        end = border(border_v(blockIdx.x + 1), b, prefix, before, task, tile);
+        at = border(border_v(blockIdx.x), b, prefix, before, task, tile);
     }
-    int nt_task = any ? tiles_of(b) : 1;         // tiles of the task
-    int task = any ? (int)((at - prefix) / nt_task) : 0, tile = any ? (int)((at - prefix) - (long long)task * nt_task) : 0;
+    int len = len_of(b), nt_task = max(1, tiles_in(len));        // the sequence's length, its tasks' tiles
     auto next = [&](int n_t) {                   // on to the next task
         at += n_t;
         tile = 0;
         if (++task == tasks && at < end) {
             task = 0;
-            prefix += (long long)nt_task * tasks;
+            prefix += nt_task * tasks;
             before += tasks;
-            do nt_task = tiles_of(++b);
+            do nt_task = tiles_in(len = len_of(++b));
             while (nt_task == 0);
         }
     };
 
     int loads = 0;                               // tiles whose copies were issued
     bool issued = false, elected = false;
-    if (warp == kLoadWarp) {
-        if (lane == 0) {
-            while (at < end) {
-                const int n_t = (int)min((long long)(nt_task - tile), end - at), h = task / a.blocks;
-                for (int i = 0; i < n_t; ++i) {
-                    const int s = loads % kStages;
-                    if (loads >= kStages && !wait(&sm.empty[s], loads / kStages + 1)) break;
-                    if (*reinterpret_cast<volatile int *>(&sm.timeout)) break;
+    if (warp >= kWorkWarps) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Cfg<N>::kRegsRest));
+      if (warp == kLoadWarp) {
+        bool ok = true;
+        while (at < end) {
+            const int n_t = min(nt_task - tile, end - at), h = task / a.blocks;
+            for (int i = 0; i < n_t && ok; ++i) {
+                const int s = loads % kStages;
+                if (!(ok = all(loads < kStages || wait(&sm.empty[s], loads / kStages + 1)))) break;
+                if (lane == 0) {
                     umma::mbar_arrive_expect_tx(&sm.full[s], 2 * kSide);
                     umma::tma_load_3d(codes + s * 2 * kSide, &tk, 0, (tile + i) * kTok, b * a.H + h, &sm.full[s]);
                     umma::tma_load_3d(codes + s * 2 * kSide + kSide, &tv, 0, (tile + i) * kTok, b * a.H + h, &sm.full[s]);
-                    ++loads;
                 }
-                next(n_t);
+                __syncwarp();
+                ++loads;
             }
+            next(n_t);
         }
-    } else if (warp == kScoreWarp) {
+      } else if (warp == kTellWarp) {
+        // ---- parts of tasks that others have parts of, told once their results are stored (the fence and the
+        // answer would hold up the next segment for 1.4 us); told last: this CTA joins them when its tiles are done ----
+        while (at < end) {
+            const int n_t = min(nt_task - tile, end - at), begins = tile == 0;
+            if (n_t < nt_task) {
+                const int ts = prefix + task * nt_task + (before + task + 1) * lead;
+                auto holder = [&](int v) {                         // the CTA whose share has place v
+                    int i = (int)(__fdividef((float)nc, (float)total_v) * (float)(v + 1));     // within one
+                    while (border_v(i) > v) --i;
+                    while (border_v(i + 1) <= v) ++i;
+                    return i;
+                };
+                const int c0 = holder(ts);
+                Join j{holder(ts + nt_task - 1) - c0 + 1, c0, min(N, a.R * a.G - (task % a.blocks) * N), b, task};
+                wait(&sm.stored[begins], 0);
+                if (lane == 0) {
+                    __threadfence();
+                    if (atomicAdd(a.count + c0, 1) == j.parts - 1)
+                        a.count[c0] = 0;                           // ready for the next call
+                    else
+                        j.parts = 0;
+                    __threadfence();
+                    sm.join[begins] = j;
+                }
+                __syncwarp();
+            }
+            next(n_t);
+        }
+        bar_sync(2, kWork + 32);
+      } else if (warp == kScoreWarp) {
         // (the whole warp walks the loop and one lane issues: the descriptors stay in uniform registers)
         elected = umma::elect_one();
         {
@@ -405,7 +444,7 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
             int g = 0;
             bool ok = true;
             for (int seg = 0; at < end; ++seg) {
-                const int n_t = (int)min((long long)(nt_task - tile), end - at);
+                const int n_t = min(nt_task - tile, end - at);
                 ok = all(ok && wait(&sm.qfull, seg));
                 for (int i = 0; i < n_t && ok; ++i, ++g) {
                     const int s = g % kGroups;
@@ -424,14 +463,14 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
                 next(n_t);
             }
         }
-    } else if (warp == kValueWarp) {
+      } else if (warp == kValueWarp) {
         elected = umma::elect_one();
         {
             constexpr uint32_t id = umma::instr_desc(1, 1, kTok, N) | (1u << 15) | (1u << 16);  // bf16, both MN-major
             int g = 0;
             bool ok = true;
             while (at < end) {
-                const int n_t = (int)min((long long)(nt_task - tile), end - at);
+                const int n_t = min(nt_task - tile, end - at);
                 for (int i = 0; i < n_t && ok; ++i, ++g) {
                     const int s = g % kGroups;
                     ok = all(wait(&sm.vfull[s], g / kGroups) && wait(&sm.pfull[s], g / kGroups));
@@ -453,14 +492,13 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
                 next(n_t);
             }
         }
+      }
     } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Cfg<N>::kRegsWork));
         const int grp = warp >> 2, tok = tid & (kTok - 1);
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t tK = tmem + lanes + cK + grp * 80, tS = tmem + lanes + cS + grp * N;
         uint8_t *const v_dst = sv + grp * kVBuf + tok * 16, *const p_dst = sp + grp * kP + tok * 16;
-        // the z step's unused columns
-        asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%1,%1,%1,%1,%1,%1,%1};\n" ::"r"(tK + D / 2), "r"(0u) : "memory");
-        umma::tmem_st_wait();
         // pieces of Q of a segment: row n = item / (D / 8), eight d each
         constexpr int kItems = (N * (D / 8) + kWork - 1) / kWork;
         auto q_offset = [&](int sb, int st, int n, int ld) -> long long {      // row n of task st of sequence sb
@@ -478,10 +516,13 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
             }
         };
         if (at < end) fetch_q(b, task);
+        // the z step's unused columns
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%1,%1,%1,%1,%1,%1,%1};\n" ::"r"(tK + D / 2), "r"(0u) : "memory");
+        umma::tmem_st_wait();
         int g = 0;                                               // tiles of this CTA so far
         for (int seg = 0; at < end; ++seg) {
-            const int n_t = (int)min((long long)(nt_task - tile), end - at);
-            const int len = __ldg(a.len + b), h = a.blocks == 1 ? task : task / a.blocks, row0 = (task - h * a.blocks) * N;
+            const int n_t = min(nt_task - tile, end - at);
+            const int h = a.blocks == 1 ? task : task / a.blocks, row0 = (task - h * a.blocks) * N;
             const int nq = min(N, a.R * a.G - row0);
             const int p0 = tile * kTok;
             const size_t head = ((size_t)b * a.H + h) * a.T;
@@ -680,6 +721,10 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
                 if (lane == 0) umma::mbar_arrive(&sm.pfull[grp]);
             }
             g += n_t;
+            const bool whole = n_t == nt_task;
+            const int seg_b = b, seg_task = task, seg_len = len;
+            next(n_t);
+            if (at < end) fetch_q(b, task);                       // the next segment's Q, under this one's end
             // ---- sums of p ----
             {
                 float l[N];
@@ -709,25 +754,17 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
                 sm.inv[tid] = sum == 0.0f ? 0.0f : 1.0f / sum;                 // (NaN stays)
                 sm.lse[tid] = sum == 0.0f ? kNone : fmaf(back, ref, log2f(sum));
             }
-            const bool whole = n_t == nt_task;
-            // the CTAs whose shares hold the task's first and last tile
-            const long long ts = prefix + (long long)task * nt_task + (before + task + 1) * lead;
-            const int c0 = (int)(((ts + 1) * nc + total_v - 1) / total_v) - 1,
-                      c1 = (int)(((ts + nt_task) * nc + total_v - 1) / total_v) - 1;
-            const int seg_b = b, seg_task = task;
-            next(n_t);
-            if (at < end) fetch_q(b, task);                       // the next segment's Q, under this one's end
             wait(&sm.odone, seg);
             umma::fence_after_sync();
             bar_sync(1, kWork);
             // ---- results: to the output, or to this CTA's slot where others have parts of the task ----
             constexpr int kSlot = N * (D + 1);
-            float *slot = a.part + ((size_t)blockIdx.x * 2 + ((int)blockIdx.x == c0 ? 1 : 0)) * kSlot;
+            float *slot = a.part + ((size_t)blockIdx.x * 2 + (p0 == 0 ? 1 : 0)) * kSlot;   // (1: the task begins here)
             if (sm.over) {
                 for (int n = warp; n < nq; n += kWorkWarps) {
                     float o[D / 32];
                     const float lse = plain_row<D>(a, a.q + q_offset(seg_b, seg_task, n, a.ldq), head, p0,
-                                                   min(sm.seen[n], min(len, p0 + n_t * kTok)), o);
+                                                   min(sm.seen[n], min(seg_len, p0 + n_t * kTok)), o);
 #pragma unroll
                     for (int e = 0; e < D / 32; ++e) {
                         if (whole)
@@ -767,25 +804,13 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
                 if (!whole && warp == 0)
                     for (int n = lane; n < nq; n += 32) __stcg(slot + N * D + n, sm.lse[n]);
             }
+            __syncwarp();
+            if (!whole && lane == 0) umma::mbar_arrive(&sm.stored[p0 == 0]);
             bar_sync(1, kWork);
-            if (tid == 0) {
-                sm.over = 0;
-                if (!whole) {                                      // (the answer is looked at when all tiles are done)
-                    __threadfence();
-                    const bool last = atomicAdd(a.count + c0, 1) == c1 - c0;
-                    if (last) a.count[c0] = 0;                     // ready for the next call
-                    Join &j = sm.join[(int)blockIdx.x == c0 ? 1 : 0];
-                    j.parts = last ? c1 - c0 + 1 : 0;
-                    j.c0 = c0;
-                    j.nq = nq;
-                    j.b = seg_b;
-                    j.task = seg_task;
-                }
-            }
+            if (tid == 0) sm.over = 0;
         }
         // ---- tasks of which this CTA was the last to finish a part ----
-        if (tid == 0) __threadfence();
-        bar_sync(1, kWork);
+        bar_sync(2, kWork + 32);
 #pragma unroll 1
         for (int e = 0; e < 2; ++e) {
             const Join j = sm.join[e];
@@ -793,6 +818,19 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
             constexpr int kSlot = N * (D + 1), kFew = 8;
             float *wgt = reinterpret_cast<float *>(sv);             // [part][N], in the V operands' place
             auto part = [&](int c) { return a.part + ((size_t)(j.c0 + c) * 2 + (c == 0 ? 1 : 0)) * kSlot; };
+            constexpr int kEach = (N * (D / 4) + kWork - 1) / kWork, kBatch = kEach < 3 ? 4 : 2;   // loads in flight: kEach x kBatch
+            float4 x[kEach], y[kBatch][kEach];
+            auto fetch = [&](int cb) {
+#pragma unroll
+                for (int c = 0; c < kBatch; ++c)
+#pragma unroll
+                    for (int k = 0; k < kEach; ++k) {
+                        const int it = k * kWork + tid;
+                        y[c][k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        if (cb + c < j.parts && it < j.nq * (D / 4)) y[c][k] = __ldcg(reinterpret_cast<const float4 *>(part(cb + c)) + it);
+                    }
+            };
+            fetch(0);                                               // (under the weights)
             if (j.parts <= kFew) {                                  // a thread per row
                 if (tid < j.nq) {
                     float v[kFew], top = kNone, sum = 0.0f;
@@ -834,20 +872,10 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
                 }
             }
             bar_sync(1, kWork);
-            constexpr int kEach = (N * (D / 4) + kWork - 1) / kWork, kBatch = kEach < 3 ? 4 : 2;   // loads in flight: kEach x kBatch
-            float4 x[kEach];
 #pragma unroll
             for (int k = 0; k < kEach; ++k) x[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             for (int cb = 0; cb < j.parts; cb += kBatch) {
-                float4 y[kBatch][kEach];
-#pragma unroll
-                for (int c = 0; c < kBatch; ++c)
-#pragma unroll
-                    for (int k = 0; k < kEach; ++k) {
-                        const int it = k * kWork + tid;
-                        y[c][k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                        if (cb + c < j.parts && it < j.nq * (D / 4)) y[c][k] = __ldcg(reinterpret_cast<const float4 *>(part(cb + c)) + it);
-                    }
+                if (cb > 0) fetch(cb);
 #pragma unroll
                 for (int c = 0; c < kBatch; ++c)
 #pragma unroll
@@ -941,6 +969,9 @@ extern "C" int qspec_attn_kv4(const uint16_t *q_bf16, int ldq, const uint8_t *k_
     if (!akv::sizes_ok(B, R, Hq, H, D) || T < 1 || T > (1 << 30) || (long long)B * H >= (1LL << 31) ||
         !std::isfinite(scale) || ldq < (long long)Hq * D || ldo < (long long)Hq * D)
         return QSPEC_ERR_SHAPE;
+    // tiles of all tasks, the empty ones in front of each counted, are 32-bit numbers in the kernel
+    const long long passes = (R * (long long)(Hq / H) + akv::kMaxN - 1) / akv::kMaxN;
+    if (B * (long long)H * passes * ((T + akv::kTok - 1) / akv::kTok + 8) >= (1LL << 30)) return QSPEC_ERR_SHAPE;
     if (ldq % 8 || ldo % 8 || !aligned(q_bf16, 16) || !aligned(o_bf16, 16) || !aligned(k_codes, 16) ||
         !aligned(v_codes, 16) || !aligned(k_sz, 4) || !aligned(v_sz, 4) || !aligned(len, 4) || !aligned(workspace, 16))
         return QSPEC_ERR_ALIGN;
