@@ -3,7 +3,7 @@
 Tolerance of an output o = sum p v, with A = sum p |v|: the weights p s are
 rounded to bf16 (half a step, 2^-8), the exponential is within 2^-12, a score
 within d = 16 x 2^-24 x scale max_t s_t 143 sum |q| (fp32 sums of products with
-codes held as 128 + c), which counts twice (weight and sum): together
+codes held as 128 + c, or as smaller numbers), which counts twice (weight and sum): together
 (2^-8 + 2^-12 + 2 d) A; and the output is rounded to bf16: 2^-8 |o|."""
 import math
 
@@ -12,7 +12,7 @@ import torch
 
 from quantized_speculative_decoding_shared_gb300 import binding as q, synthetic as syn
 from gpuhelp import need_gpu, read_status, status
-from layerref import attention, random_cache, values
+from layerref import attention, random_cache, values, words
 
 pytestmark = pytest.mark.gpu
 
@@ -199,3 +199,36 @@ def test_another_stream_and_a_graph():
         g.replay()
         torch.cuda.synchronize()
         check(x, cache, lens, R, 0.1, out)
+
+
+@pytest.mark.parametrize("B,R,H,G,D,T", [(16, 1, 8, 4, 128, 4096), (16, 5, 8, 4, 128, 4090), (8, 9, 4, 7, 128, 4001),
+                                         (6, 17, 2, 8, 64, 5000), (70, 2, 3, 4, 64, 900), (100, 9, 1, 2, 128, 1300)])
+def test_several_tiles_of_a_group_and_several_tasks_of_a_share(B, R, H, G, D, T):
+    """Each width of the products with every stage used many times over, and shares that end and begin inside tasks."""
+    dev = need_gpu()
+    lens = [T - (b * 997) % (T - T // 8) for b in range(B)]
+    cache = random_cache(B, H, T, D, 21, dev)
+    x = queries(B * R, H * G, D, 22, dev)
+    st = status(dev)
+    o = q.attn_kv4(x, cache, ints(lens, dev), 1 / math.sqrt(D), dev_status=st)
+    assert read_status(st) == 0
+    check(x, cache, lens, R, 1 / math.sqrt(D), o)
+
+
+@pytest.mark.parametrize("R,G", [(1, 1), (5, 4), (9, 7)])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("at", [1, 130, 777])
+def test_a_score_far_above_the_first_position(R, G, D, at):
+    """The first position's score is far below a later one's: the segment is taken again."""
+    dev = need_gpu()
+    T = 800
+    cache = random_cache(1, 1, T, D, 31, dev, s_lo=0.01, s_hi=0.02)
+    # values 15 s = 3 at position `at`, -3 at the first, rows of ones: scores of 3 D and -3 D times the scale
+    cache[0][0, 0, at], cache[1][0, 0, at] = 0xFF, words(torch.tensor(0.2, device=dev), torch.tensor(0.0, device=dev))
+    cache[0][0, 0, 0], cache[1][0, 0, 0] = 0x00, words(torch.tensor(0.2, device=dev), torch.tensor(15.0, device=dev))
+    x = (queries(R, G, D, 32, dev).float() * 0.05 + 1.0).to(torch.bfloat16)
+    scale = 100.0 / (3 * D)
+    st = status(dev)
+    o = q.attn_kv4(x, cache, ints([T], dev), scale, dev_status=st)
+    assert read_status(st) == 0
+    check(x, cache, [T], R, scale, o)

@@ -206,3 +206,26 @@ def test_the_same_bits_another_stream_and_a_graph():
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, ref)
+
+
+@pytest.mark.parametrize("H,G,D,lens", [(1, 100, 64, [150, 3]), (1, 128, 128, [40, 1]), (1, 131, 64, [70]), (2, 160, 64, [33, 20]),
+                                        (1, 65, 128, [9, 260])])
+def test_many_heads_to_a_kv_head(H, G, D, lens):
+    """One position to a row tile, and heads that are taken in parts."""
+    run(lens, lens, H, G, D, 14)
+
+
+def test_many_sequences_of_two_tiles():
+    lens = [(b * 137) % 401 for b in range(40)]
+    run(lens, [n + (b * 53) % 90 for b, n in enumerate(lens)], 4, 4, 64, 15)
+
+
+def test_a_nan_among_heads_taken_in_parts():
+    """Rows that see a NaN give NaN, the rows before it what the formula gives."""
+    dev = need_gpu()
+    n, G, D = 40, 131, 64
+    x, k, v = heads(n, G, D, 1, dev), heads(n, 1, D, 2, dev), heads(n, 1, D, 3, dev)
+    v[30] = float("nan")
+    o = q.attn_prompt(x, k, v, starts([n], dev))
+    assert torch.all(torch.isnan(o[30:].float()))
+    check(x[:30], k[:30], v[:30], [30], [30], 1 / math.sqrt(D), o[:30])

@@ -162,3 +162,47 @@ def test_no_rows():
     q.kv4_append(cache, e, e, ints([0, 0, 0], dev), ints([0, 4], dev))
     k, v = q.kv4_load(cache, ints([0, 0, 0], dev), ints([0, 4], dev), 0)
     assert k.shape == (0, 2, 64) and torch.all(cache[0] == 0x5A)
+
+
+@pytest.mark.parametrize("B", [1023, 1024, 1025, 2500])
+def test_many_sequences_some_without_rows(B):
+    """Around the number of sequences that the kernels look up in shared memory; runs of empty ones."""
+    dev = need_gpu()
+    H, D, T = 2, 64, 8
+    lens = [0 if b % 7 in (1, 2, 3) else 1 + b % 5 for b in range(B)]
+    base = [b % 3 for b in range(B)]
+    n = sum(lens)
+    k, v = rows_of(n, H, D, 1, dev), rows_of(n, H, D, 2, dev)
+    cache, want = filled(B, H, T, D, dev), filled(B, H, T, D, dev)
+    st = status(dev)
+    q.kv4_append(cache, k, v, starts(lens, dev), ints(base, dev), dev_status=st)
+    assert read_status(st) == 0
+    expect(want, k, v, lens, base)
+    for got, ref in zip(cache, want):
+        assert torch.equal(got, ref)
+    ko, vo = q.kv4_load(cache, starts(lens, dev), ints(base, dev), n, dev_status=st)
+    assert read_status(st) == 0
+    b = torch.tensor([i for i, m in enumerate(lens) for _ in range(m)], device=dev)
+    p = torch.tensor([base[i] + j for i, m in enumerate(lens) for j in range(m)], device=dev)
+    for o, codes, sz in ((ko, cache[0], cache[1]), (vo, cache[2], cache[3])):
+        assert torch.equal(o, values(codes[b, :, p], sz[b, :, p]).to(torch.bfloat16))
+
+
+def test_rows_before_and_after_the_sequences():
+    """Rows of no sequence are left out on the way in and untouched on the way out."""
+    dev = need_gpu()
+    H, D, T = 3, 128, 32
+    k, v = rows_of(40, H, D, 1, dev), rows_of(40, H, D, 2, dev)
+    start, base = [3, 10, 30], [4, 1]
+    cache, want = filled(2, H, T, D, dev), filled(2, H, T, D, dev)
+    st = status(dev)
+    q.kv4_append(cache, k, v, ints(start, dev), ints(base, dev), dev_status=st)
+    assert read_status(st) == 0
+    expect(want, k[3:30], v[3:30], [7, 20], base)
+    for got, ref in zip(cache, want):
+        assert torch.equal(got, ref)
+    ko, vo = torch.full_like(k, 7.0), torch.full_like(v, 7.0)
+    rc = q.qspec_kv4_load(*cache, ints(start, dev), ints(base, dev), 40, 2, H, T, D, ko, H * D, vo, H * D, st)
+    assert rc == 0 and read_status(st) == 0
+    for o in (ko, vo):
+        assert torch.all(o[:3] == 7.0) and torch.all(o[30:] == 7.0) and not torch.any(torch.all((o[3:30] == 7.0).flatten(1), -1))

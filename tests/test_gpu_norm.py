@@ -132,3 +132,19 @@ def test_feeds_the_fp8_linear():
     ref = ((xq.view(torch.float8_e4m3fn).double() @ w8.view(torch.float8_e4m3fn).double().T)
            * sa.double()[:, None] * s8.double())
     assert torch.all((y.double() - ref).abs() <= 1e-2 * (1 + ref.abs()))     # the linear's own bound
+
+
+@pytest.mark.parametrize("K", [256, 4096, 32768])
+def test_large_magnitudes_with_a_residual(K):
+    """Squares that pass fp32 in some rows: those rows are read again from the sum that was written."""
+    dev = need_gpu()
+    x = syn.activations(5, K, 8, device=dev).float()
+    x[1:3] *= 2.0 ** 90
+    x = x.to(torch.bfloat16)
+    r = (syn.activations(5, K, 10, device=dev).float() * 2.0 ** 89).to(torch.bfloat16)
+    r[0] = syn.activations(1, K, 11, device=dev)[0]
+    w = syn.activations(1, K, 9, device=dev).view(K)
+    st = status(dev)
+    got = q.rmsnorm_fp8(x, w, EPS, residual=r, want_bf16=True, dev_status=st)
+    assert read_status(st) == 0
+    check(x, w, EPS, r, got)

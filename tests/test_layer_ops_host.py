@@ -105,3 +105,15 @@ def test_conveniences_refuse_what_they_cannot_pass_on():
         binding.kv4_append(cache, q, q, torch.zeros(2, dtype=torch.int32), torch.zeros(1, dtype=torch.int32))
     with pytest.raises(ValueError):
         binding.attn_kv4(q, cache, torch.zeros(1, dtype=torch.int32), 0.1)
+
+
+def test_sizes_past_what_the_kernels_count(lib):
+    """Row numbers of the cache calls and tile numbers of the attention are 32-bit ones."""
+    rows = dict(k=fake(), ldk=256, v=fake(), ldv=256, start=fake(), base=fake(), rows=2 ** 31 - 8, B=2, H=2, T=16, D=128,
+                kc=fake(), ks=fake(), vc=fake(), vs=fake(), st=None, s=None)
+    refuse(lib.qspec_kv4_append, rows, list(rows), [(SHAPE, {}), (SHAPE, dict(rows=2 ** 30, H=2 ** 12, ldk=2 ** 19, ldv=2 ** 19))])
+    need = binding.qspec_attn_kv4_workspace_bytes(1, 1, 8, 2, 128)
+    ok = dict(q=fake(), ldq=1024, kc=fake(), ks=fake(), vc=fake(), vs=fake(), len=fake(), B=1, R=1, Hq=8, H=2, T=64, D=128,
+              scale=0.1, o=fake(), ldo=1024, ws=fake(), n=need, st=None, s=None)
+    refuse(lib.qspec_attn_kv4, ok, list(ok), [(SHAPE, dict(T=2 ** 30 + 1)), (SHAPE, dict(B=64, T=2 ** 30)),
+                                              (SHAPE, dict(R=17, Hq=16384, ldq=2 ** 21, ldo=2 ** 21, T=2 ** 28))])
