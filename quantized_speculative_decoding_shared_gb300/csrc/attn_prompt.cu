@@ -116,6 +116,11 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
     return d;
 }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     uint64_t d;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
@@ -244,27 +249,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                     lk = k1 - k0;
                 };
                 auto units_of = [&](int positions) { return (lq + positions - 1) / positions; };
-                long long total[2] = {0, 0};                            // units of one tile, of two
+                int total[2] = {0, 0};                                  // units of one tile, of two (times H: the host keeps it
+                                                                        // below 2^31)
                 for (int b0 = 0; b0 < a.B; b0 += 32) {
                     fetch(b0 + lane, blockIdx.x == 0);
                     total[0] += __reduce_add_sync(0xffffffffu, units_of(per_tile));
                     total[1] += __reduce_add_sync(0xffffffffu, units_of(2 * per_tile));
                 }
                 if (a.B > 32) fetch(lane, false);
-                const bool one = total[0] * a.H <= gridDim.x;           // one tile each still leaves SMs idle
+                const bool one = (uint32_t)(total[0] * a.H) <= gridDim.x;           // one tile each still leaves SMs idle
                 span = one ? per_tile : 2 * per_tile;
-                const long long end = (one ? total[0] : total[1]) * a.H;
+                const uint32_t end = (uint32_t)((one ? total[0] : total[1]) * a.H);
                 int count[2] = {0, 0};                                  // Q tiles fetched
                 bool ok = true;
                 for (int k = 0;; ++k) {
-                    const long long id = (long long)k * gridDim.x + (k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+                    const uint32_t id = k * gridDim.x + (k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
                     const bool more = id < end;
                     if (k >= 2 && !all(wait(&sm.uempty[k & 1], (k >> 1) - 1))) break;
                     Unit &u = sm.unit[k & 1];
                     bool mine = false;
                     int index = 0;
+                    const uint32_t place = id / (uint32_t)a.H;
                     if (more) {
-                        int rank = (int)(id / a.H);
+                        int rank = (int)place;
                         if (a.B <= 32) {
                             const int units = units_of(span);
                             auto from = [&](int level) { return (int)__reduce_add_sync(0xffffffffu, max(0, units - level)); };   // units at level and above
@@ -298,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                     if (mine) {
-                        u.h = (int)(id % a.H);
+                        u.h = (int)(id - place * a.H);
                         u.q0 = q0;
                         u.k0 = k0;
                         u.off = lk - lq;
@@ -467,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int x = 0; x < 4; ++x) umma::tmem_ld32(ts + 32 * x, s[x]);
             umma::tmem_ld_wait();
-            if (i * kTile + kTile - 1 > first_masked || !in) {
+            if (i * kTile + kTile - 1 > first_masked) {                 // (rows of no position may hold anything)
                 const int seen = lim - i * kTile;                       // columns 0 .. seen
                 const uint32_t hidden = c < 0.0f ? 0x7F800000u : 0xFF800000u;   // c times it is minus infinity
 #pragma unroll
@@ -511,6 +518,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 umma::mbar_arrive(&sm.pfull[t][x]);
             }
             l += last;
+            if (!in) last = 0.0f;
         }
         // ---- epilogue: o = O / l ----
         if (ok && n > 0) ok = all(wait(&sm.odone[t], units_seen));
@@ -520,27 +528,27 @@ __global__ void __launch_bounds__(kThreads, 1)
             umma::fence_after_sync();
             const size_t at = (size_t)(q0 + p) * a.ldo + (size_t)(h * G + g) * D;     // this row's place in o
             const float inv = lim >= 0 ? 1.0f / l : 0.0f;
-            bool fine = lim < 0 || (l > 0.0f && l < INFINITY);
+            const uint64_t inv2 = f2(inv, inv);
+            const uint32_t keep = lim >= 0 ? 0xFFFFFFFFu : 0u;
+            uint64_t zero = 0;                                          // NaN from where some value is not finite
             const uint32_t inside = __ballot_sync(0xffffffffu, in);
             uint8_t *buf = so + warp * (32 * 128);
 #pragma unroll
             for (int x = 0; x < D / 64; ++x) {
                 // 64 values of each row through shared memory, so that eight lanes write one row's 128 bytes (rows
-                // written by their own threads: 32 places per store, 2.9 us a tile instead of 0.9)
+                // written by their own threads: 32 places per store)
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
-                    uint32_t o[32];
+                    uint32_t o[32], w[16];
                     if (n > 0) {
                         umma::tmem_ld32(to + 64 * x + 32 * y, o);
                         umma::tmem_ld_wait();
                     }
-                    uint32_t w[16];
 #pragma unroll
                     for (int z = 0; z < 16; ++z) {
-                        const float o0 = lim >= 0 ? __uint_as_float(o[2 * z]) * inv : 0.0f;
-                        const float o1 = lim >= 0 ? __uint_as_float(o[2 * z + 1]) * inv : 0.0f;
-                        fine = fine && isfinite(o0) && isfinite(o1);
-                        w[z] = pack_bf16(o0, o1);
+                        const uint64_t v = mul2(f2(__uint_as_float(o[2 * z]), __uint_as_float(o[2 * z + 1])), inv2);
+                        zero = fma2(v, 0, zero);
+                        w[z] = pack_bf16(lo32(v), hi32(v)) & keep;
                     }
 #pragma unroll
                     for (int z = 0; z < 4; ++z)
@@ -557,6 +565,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 __syncwarp();
             }
+            const bool fine = lim < 0 || (l > 0.0f && l < INFINITY && lo32(zero) + hi32(zero) == 0.0f);
             uint32_t again = __ballot_sync(0xffffffffu, in && !fine);
             while (again) {
                 const int who = __ffs(again) - 1;
