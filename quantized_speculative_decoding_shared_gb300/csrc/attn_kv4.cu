@@ -22,7 +22,8 @@
 // unpack V while S^T is formed, then the softmax); one lane issues the products of
 // S^T, one those of O^T (each waits for its own operands, so that the tensor cores
 // have the other's meanwhile: at these widths a product takes some 55 clocks
-// whatever N is, 17 of them a tile), one the copies.
+// whatever N is, 17 of them a tile), one the copies, and one tells other CTAs of
+// finished parts.
 //
 // The softmax reference of a row is its score at the segment's first position, and stays:
 // p, its sum and O are floating point and lose nothing while no score passes
@@ -35,9 +36,13 @@
 // of them to finish, in the order of the parts, so that the bits do not
 // depend on who is last.
 //
-// Bound: HBM (D / 2 + 4 bytes per position, head and side) and, close to it, the
-// issue slots of unpacking (about 0.1 warp instructions per code) and of N scores
-// per position.
+// Bound: the 17 products of a tile (935 of some 1170 clocks at 16 rows) and shared
+// memory (half its rate: codes in, V and P^T out and read by the products), HBM next:
+// 4 sequences of 65001 positions, 8 KV heads of 128, one row of 4 heads: 59.7 us, 4.2
+// TB/s of the D / 2 + 4 bytes per position, head and side (37.4 us at HBM's rate).  With
+// warp MMA (registers only) it was 63.5 us, and 43 for 21.4 at 16 sequences of up to
+// 4091 with 5 rows; 32 sequences, 9 rows, 7 heads to a KV head: 32.0 us.  Short calls
+// are the way through one tile: 6.6 us for one sequence of 333.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -61,7 +66,8 @@ struct Cfg {
     static constexpr int kGroups = 3, kWorkWarps = 4 * kGroups, kWork = 32 * kWorkWarps;
     static constexpr int kScoreWarp = kWorkWarps, kValueWarp = kScoreWarp + 1, kLoadWarp = kValueWarp + 1, kTellWarp = kLoadWarp + 1;   // one lane each: S^T, O^T products, copies, finished parts
     static constexpr int kThreads = kWork + 128;
-    // registers per thread: all start with 128 and share what that makes
+    // registers per thread: all start with 128 and share what that makes (with 128 for the working warps 64 rows
+    // spill their sums: 40.1 for 32.1 us at 32 sequences, 9 rows, 7 heads)
     static constexpr int kRegsWork = 144, kRegsRest = 64;
     static_assert(kThreads * 128 <= 65536 && kWork * kRegsWork + 128 * kRegsRest <= kThreads * 128, "register shares");
     // Tiles of codes in flight.  A stage always serves the same group: one whose next tile came into another
@@ -438,59 +444,55 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
       } else if (warp == kScoreWarp) {
         // (the whole warp walks the loop and one lane issues: the descriptors stay in uniform registers)
         elected = umma::elect_one();
-        {
-            constexpr uint32_t id = umma::instr_desc(0, 0, kTok, N);                            // f16, f32 sums
-            const uint64_t qd = umma::smem_desc(umma::smem_addr(sq), N * 16, 128);
-            int g = 0;
-            bool ok = true;
-            for (int seg = 0; at < end; ++seg) {
-                const int n_t = min(nt_task - tile, end - at);
-                ok = all(ok && wait(&sm.qfull, seg));
-                for (int i = 0; i < n_t && ok; ++i, ++g) {
-                    const int s = g % kGroups;
-                    ok = all(wait(&sm.kfull[s], g / kGroups));
-                    if (!ok) break;
-                    umma::fence_after_sync();
-                    if (elected) {
+        constexpr uint32_t id = umma::instr_desc(0, 0, kTok, N);                            // f16, f32 sums
+        const uint64_t qd = umma::smem_desc(umma::smem_addr(sq), N * 16, 128);
+        int g = 0;
+        bool ok = true;
+        for (int seg = 0; at < end; ++seg) {
+            const int n_t = min(nt_task - tile, end - at);
+            ok = all(ok && wait(&sm.qfull, seg));
+            for (int i = 0; i < n_t && ok; ++i, ++g) {
+                const int s = g % kGroups;
+                ok = all(wait(&sm.kfull[s], g / kGroups));
+                if (!ok) break;
+                umma::fence_after_sync();
+                if (elected) {
 #pragma unroll
-                        for (int kk = 0; kk < kSteps + 1; ++kk)
-                            umma::mma_bf16_ta(tmem + cS + s * N, tmem + cK + s * 80 + kk * 8, qd + (uint64_t)(kk * 2 * N), id, kk != 0);
-                        umma::mma_commit(&sm.sfull[s]);
-                    }
-                    __syncwarp();
-                    issued = true;
+                    for (int kk = 0; kk < kSteps + 1; ++kk)
+                        umma::mma_bf16_ta(tmem + cS + s * N, tmem + cK + s * 80 + kk * 8, qd + (uint64_t)(kk * 2 * N), id, kk != 0);
+                    umma::mma_commit(&sm.sfull[s]);
                 }
-                next(n_t);
+                __syncwarp();
+                issued = true;
             }
+            next(n_t);
         }
       } else if (warp == kValueWarp) {
         elected = umma::elect_one();
-        {
-            constexpr uint32_t id = umma::instr_desc(1, 1, kTok, N) | (1u << 15) | (1u << 16);  // bf16, both MN-major
-            int g = 0;
-            bool ok = true;
-            while (at < end) {
-                const int n_t = min(nt_task - tile, end - at);
-                for (int i = 0; i < n_t && ok; ++i, ++g) {
-                    const int s = g % kGroups;
-                    ok = all(wait(&sm.vfull[s], g / kGroups) && wait(&sm.pfull[s], g / kGroups));
-                    if (!ok) break;
-                    umma::fence_after_sync();
-                    const uint64_t vd = umma::smem_desc(umma::smem_addr(sv + s * kVBuf), 128, kTok * 16);
-                    const uint64_t pd = umma::smem_desc(umma::smem_addr(sp + s * kP), 128, kTok * 16);
-                    if (elected) {
+        constexpr uint32_t id = umma::instr_desc(1, 1, kTok, N) | (1u << 15) | (1u << 16);  // bf16, both MN-major
+        int g = 0;
+        bool ok = true;
+        while (at < end) {
+            const int n_t = min(nt_task - tile, end - at);
+            for (int i = 0; i < n_t && ok; ++i, ++g) {
+                const int s = g % kGroups;
+                ok = all(wait(&sm.vfull[s], g / kGroups) && wait(&sm.pfull[s], g / kGroups));
+                if (!ok) break;
+                umma::fence_after_sync();
+                const uint64_t vd = umma::smem_desc(umma::smem_addr(sv + s * kVBuf), 128, kTok * 16);
+                const uint64_t pd = umma::smem_desc(umma::smem_addr(sp + s * kP), 128, kTok * 16);
+                if (elected) {
 #pragma unroll
-                        for (int kk = 0; kk < kTok / 16; ++kk)
-                            umma::mma_bf16(tmem + cO, vd + kk * 16, pd + kk * 16, id, (i | kk) != 0);
-                        umma::mma_commit(&sm.pdone[s]);
-                    }
-                    __syncwarp();
-                    issued = true;
+                    for (int kk = 0; kk < kTok / 16; ++kk)
+                        umma::mma_bf16(tmem + cO, vd + kk * 16, pd + kk * 16, id, (i | kk) != 0);
+                    umma::mma_commit(&sm.pdone[s]);
                 }
-                if (ok && elected) umma::mma_commit(&sm.odone);
                 __syncwarp();
-                next(n_t);
+                issued = true;
             }
+            if (ok && elected) umma::mma_commit(&sm.odone);
+            __syncwarp();
+            next(n_t);
         }
       }
     } else {
