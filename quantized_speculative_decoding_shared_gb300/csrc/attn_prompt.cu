@@ -203,8 +203,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int t = 0; t < 2; ++t) {
             umma::mbar_init(&sm.sfull[t], 1);
-            umma::mbar_init(&sm.pfull[t][0], kTile);
-            umma::mbar_init(&sm.pfull[t][1], kTile);
+            umma::mbar_init(&sm.pfull[t][0], kTile / 32);
+            umma::mbar_init(&sm.pfull[t][1], kTile / 32);
             umma::mbar_init(&sm.odone[t], 1);
             umma::mbar_init(&sm.ufull[t], 1);
             umma::mbar_init(&sm.uempty[t], kSoftmax / 32 + 2);          // softmax, products, copies
@@ -404,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int i = 0; i < n && ok; ++i) {
                     const int iv = at + 2 * i + 1, ik = iv + 1;
                     const bool more = i + 1 < n;
-                    ok = all(wait(&sm.full[iv % NS], iv / NS) && (!more || wait(&sm.full[ik % NS], ik / NS)));
+                    ok = all(wait(&sm.full[iv % NS], iv / NS));
                     for (int t = 0; t < nt && ok; ++t) {
                         const uint64_t bd = desc_mn(kv_addr + (iv % NS) * kT);
                         for (int half = 0; half < 2 && ok; ++half) {
@@ -423,6 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (elected && t == nt - 1) umma::mma_commit(&sm.empty[iv % NS]);
                         __syncwarp();
                         if (more) {
+                            if (t == 0 && !(ok = all(wait(&sm.full[ik % NS], ik / NS)))) break;
                             scores(t, i + 1);
                             if (t == nt - 1 && elected) umma::mma_commit(&sm.empty[ik % NS]);
                         } else {
@@ -523,7 +524,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 last += lo32(sum[0]) + hi32(sum[0]);
                 umma::tmem_st_wait();
                 umma::fence_before_sync();
-                umma::mbar_arrive(&sm.pfull[t][x]);
+                __syncwarp();
+                if (lane == 0) umma::mbar_arrive(&sm.pfull[t][x]);   // (a thread each: the arrivals queue up)
             }
             l += last;
             if (!in) last = 0.0f;
