@@ -25,12 +25,15 @@
 // CTAs are persistent: one warp finds a CTA's units (the longest first) and fetches
 // their queries ahead, so the next unit's copies run under the present one's products.
 //
-// Bound: tensor cores (a pair of row tiles and a key tile are 2093 clocks of products
-// at D = 128) and, on top, the copies' writes to shared memory, whose whole rate the
-// score products take, and the chain of a tile's softmax: some 2800 clocks.  8192
-// tokens, 8 KV heads of 128 with 4 heads each: 345 to 360 us, 1530 to 1590 TFLOP/s
-// counting what the mask leaves; 7 sequences of 5003 tokens, 4 KV heads with 7 each:
-// 51.4 us; 3 of 301: 7.8 us.
+// Bound: tensor cores and shared memory at once (D = 128): a pair of row tiles and a
+// key tile are 2093 clocks of products (measured: 62 to 68 for N = 128) and 256 KB of
+// shared memory (128 of them Q and K for the scores, 64 V, 64 the copies' writes), 2048
+// clocks at 128 bytes each; together they take some 2650.  What adds shared-memory
+// operations costs more than it hides (8192 tokens, 342 us as it is): waits
+// that spin 398, weights handed over in three parts 374, two warpgroups to a row
+// tile 408; with the exponentials left out it was as long.  8192 tokens, 8 KV heads
+// of 128 with 4 heads each: 342 us, 1607 TFLOP/s counting what the mask leaves; 7 sequences
+// of 5003 tokens, 4 KV heads with 7 each: 51.8 us; 3 of 301: 7.8 us.
 #include <algorithm>
 #include <cmath>
 

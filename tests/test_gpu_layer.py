@@ -160,3 +160,43 @@ def test_command(capsys):
     from quantized_speculative_decoding_shared_gb300 import layer
     layer.main()
     assert "status 0" in capsys.readouterr().out
+
+
+def test_steps_and_prompts_in_a_graph():
+    """Draft steps, a verify pass and a prompt captured on a stream of their own give what the calls give."""
+    dev = need_gpu()
+    B, T, gamma, Hq, H, D = 2, 300, 2, 8, 2, 128
+    fp16 = lambda n, k, seed: (syn.activations(n, k, seed, device=dev).float() * 0.05).to(torch.float16)   # noqa: E731
+    layer = AttentionLayer(torch.ones(K, dtype=torch.bfloat16, device=dev), fp16((Hq + 2 * H) * D, K, 1), fp16(K, Hq * D, 2), Hq, H, D,
+                           B, T, EPS)
+    lens = [120, 33]
+    prompt, base, start = syn.activations(sum(lens), K, 3, device=dev), ints(lens, dev), starts(lens, dev)
+    res = syn.activations(sum(lens), K, 4, device=dev)
+    drafts = [syn.activations(B, K, 10 + i, device=dev) for i in range(gamma)]
+    rows = syn.activations(B * (gamma + 1), K, 20, device=dev)
+
+    def program():
+        out = list(layer.prompt(prompt, start, residual=res))
+        for i, x in enumerate(drafts):
+            out.append(layer.step(x, base + i)[0])
+        return out + [layer.step(rows, base)[0]]
+
+    want = [t.clone() for t in program()]
+    cache = [t.clone() for t in layer.cache]
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        got = program()
+    for _ in range(3):
+        for t in layer.cache:
+            t.zero_()
+        for t in got:
+            t.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        for a, b in zip(layer.cache, cache):                           # (the positions in use)
+            for i, n in enumerate(lens):
+                assert torch.equal(a[i, :, :n + gamma + 1], b[i, :, :n + gamma + 1])
+    assert read_status(layer.status) == 0
