@@ -101,7 +101,7 @@ struct Ctl {
     uint64_t qfull, ref, odone, drain[2];       // per segment: Q written, reference known, O^T complete
     uint64_t stored[2];                         // once: results of the part of a task that the CTA continues, begins
     float4 back[N / 2];                         // score of rows n, n + 1: {back, back'}({s u - ref, s u' - ref'}), as {back, back', -ref, -ref'}
-    float lse[N], inv[N];
+    alignas(16) float lse[N], inv[N];
     float lsum[kWorkWarps][N];
     long long orow[N];                          // the rows' places in q and o
     int seen[N];                                // positions that a row sees
@@ -535,34 +535,50 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
                 kn = __ldg(a.ks + head + p0 + i0 * kTok + tok);
                 vn = __ldg(a.vs + head + p0 + i0 * kTok + tok);
             }
-            // ---- Q, rows scaled to below 2^15, in the order of unpacked codes ----
+            // ---- Q, rows scaled to below 2^15, in the order of unpacked codes (a thread's pieces side by side: the
+            // exchanges of one after another took 0.3 us a piece) ----
+            uint32_t top[kItems];
+            float sum[kItems];
+#pragma unroll
+            for (int k = 0; k < kItems; ++k) {
+                const uint32_t v[4] = {qx[k].x, qx[k].y, qx[k].z, qx[k].w};
+                top[k] = 0;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) top[k] = max(top[k], max((v[e] >> 7) & 0xFFu, (v[e] >> 23) & 0xFFu));   // exponents
+            }
+#pragma unroll
+            for (int o = D / 16; o >= 1; o >>= 1)
+#pragma unroll
+                for (int k = 0; k < kItems; ++k) top[k] = max(top[k], __shfl_xor_sync(0xffffffffu, top[k], o));
 #pragma unroll
             for (int k = 0; k < kItems; ++k) {
                 const int it = k * kWork + tid, n = it / (D / 8), w = it % (D / 8);
-                if (k * kWork + 32 * warp >= N * (D / 8)) break;
                 const uint32_t v[4] = {qx[k].x, qx[k].y, qx[k].z, qx[k].w};
-                uint32_t top = 0;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) top = max(top, max((v[e] >> 7) & 0xFFu, (v[e] >> 23) & 0xFFu));   // exponents
-#pragma unroll
-                for (int o = D / 16; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-                const int up = min(253, 268 - (int)min(top, 254u));   // exponent field of 2^(14 - exponent)
-                const float f = __uint_as_float((uint32_t)up << 23), f16 = f * 0.0625f;
-                float lo[4], hi[4], sum = 0.0f;
+                top[k] = (uint32_t)min(253, 268 - (int)min(top[k], 254u));           // exponent field of 2^(14 - exponent)
+                const float f = __uint_as_float(top[k] << 23), f16 = f * 0.0625f;
+                float lo[4], hi[4];
+                sum[k] = 0.0f;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     lo[e] = __uint_as_float(v[e] << 16);
                     hi[e] = __uint_as_float(v[e] & 0xFFFF0000u);
-                    sum += lo[e] * f + hi[e] * f;
+                    sum[k] += lo[e] * f + hi[e] * f;
                 }
-                *reinterpret_cast<uint4 *>(sq + (w * N + n) * 16) =
-                    make_uint4(pack_half(lo[0] * f, lo[2] * f), pack_half(hi[0] * f16, hi[2] * f16),
-                               pack_half(lo[1] * f, lo[3] * f), pack_half(hi[1] * f16, hi[3] * f16));
+                if (n < N)
+                    *reinterpret_cast<uint4 *>(sq + (w * N + n) * 16) =
+                        make_uint4(pack_half(lo[0] * f, lo[2] * f), pack_half(hi[0] * f16, hi[2] * f16),
+                                   pack_half(lo[1] * f, lo[3] * f), pack_half(hi[1] * f16, hi[3] * f16));
+            }
 #pragma unroll
-                for (int o = D / 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                if (w == 0) {
+            for (int o = D / 16; o >= 1; o >>= 1)
+#pragma unroll
+                for (int k = 0; k < kItems; ++k) sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], o);
+#pragma unroll
+            for (int k = 0; k < kItems; ++k) {
+                const int it = k * kWork + tid, n = it / (D / 8);
+                if (it % (D / 8) == 0 && n < N) {
                     // z 2^-10 against -sum 2^-14 (the codes carry 2^-24), in three parts
-                    const float z0 = -sum * 6.103515625e-5f;
+                    const float z0 = -sum[k] * 6.103515625e-5f;
                     const __half h0 = __float2half_rn(z0), h1 = __float2half_rn(z0 - __half2float(h0)),
                                  h2 = __float2half_rn(z0 - __half2float(h0) - __half2float(h1));
                     *reinterpret_cast<uint4 *>(sq + ((D / 8) * N + n) * 16) =
@@ -570,7 +586,7 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
                                    (uint32_t)__half_as_ushort(h2), 0u, 0u);
                     *reinterpret_cast<uint4 *>(sq + ((D / 8 + 1) * N + n) * 16) = make_uint4(0u, 0u, 0u, 0u);
                     reinterpret_cast<float *>(sm.back)[4 * (n >> 1) + (n & 1)] =
-                        __uint_as_float((uint32_t)(254 - up) << 23) * (a.scale * (1.4426950408889634f * 16777216.0f));
+                        __uint_as_float((254u - top[k]) << 23) * (a.scale * (1.4426950408889634f * 16777216.0f));
                     sm.seen[n] = n < nq ? len - a.R + 1 + a.row_r(row0 + n) : 0;
                     sm.orow[n] = n < nq ? q_offset(b, task, n, a.ldo) : 0;
                 }
@@ -782,24 +798,21 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
                 for (int n0 = 8 * grp; n0 < nq; n0 += 8 * kGroups) {
                     uint32_t u[8];
                     umma::tmem_ld_cols<8>(tmem + lanes + cO + n0, u);
-                    float inv[8], lse[8];
-                    long long row[8];
+                    float inv[8];                                  // (0 where a row sees nothing; its sums are 0)
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        inv[k] = sm.inv[n0 + k] * scale;
-                        lse[k] = sm.lse[n0 + k];
-                        row[k] = whole ? sm.orow[n0 + k] : 0;
-                    }
+                    for (int k = 0; k < 8; k += 4) *reinterpret_cast<float4 *>(inv + k) = *reinterpret_cast<const float4 *>(sm.inv + n0 + k);
                     umma::tmem_ld_wait();
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const float o = lse[k] == kNone ? 0.0f : __uint_as_float(u[k]) * inv[k];
-                        if (n0 + k < nq) {
-                            if (whole)
-                                a.o[row[k] + d] = float_to_bf16_bits(o);
-                            else
-                                __stcg(slot + (n0 + k) * D + d, o);
-                        }
+                    for (int k = 0; k < 8; ++k) inv[k] = __uint_as_float(u[k]) * (inv[k] * scale);
+                    if (whole) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            if (n0 + k < nq) a.o[sm.orow[n0 + k] + d] = float_to_bf16_bits(inv[k]);
+                    } else {
+                        float *to = slot + n0 * D + d;
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            if (n0 + k < nq) __stcg(to + k * D, inv[k]);
                     }
                 }
                 umma::fence_before_sync();
