@@ -38,11 +38,11 @@
 //
 // Bound: the 17 products of a tile (935 of some 1170 clocks at 16 rows) and shared
 // memory (half its rate: codes in, V and P^T out and read by the products), HBM next:
-// 4 sequences of 65001 positions, 8 KV heads of 128, one row of 4 heads: 59.7 us, 4.2
+// 4 sequences of 65001 positions, 8 KV heads of 128, one row of 4 heads: 59.4 us, 4.3
 // TB/s of the D / 2 + 4 bytes per position, head and side (37.4 us at HBM's rate).  With
-// warp MMA (registers only) it was 63.5 us, and 43 for 21.4 at 16 sequences of up to
-// 4091 with 5 rows; 32 sequences, 9 rows, 7 heads to a KV head: 32.0 us.  Short calls
-// are the way through one tile: 6.6 us for one sequence of 333.
+// warp MMA (registers only) it was 63.5 us, and 43 for 21.3 at 16 sequences of up to
+// 4091 with 5 rows; 32 sequences, 9 rows, 7 heads to a KV head: 31.0 us.  Short calls
+// are the way through one tile: 6.5 us for one sequence of 333.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
