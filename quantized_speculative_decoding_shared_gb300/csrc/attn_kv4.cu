@@ -291,6 +291,7 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
     }
     pdl_launch_dependents();
     pdl_wait();
+    const int my_len = lane < a.B ? __ldg(a.len + lane) : -1;    // the first 32 sequences', kept (asked for before the barrier)
     umma::fence_before_sync();
     __syncthreads();
     umma::fence_after_sync();
@@ -321,7 +322,7 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
         }
         return c;
     };
-    const int my_len = lane < a.B ? __ldg(a.len + lane) : -1, mine = tiles_in(my_len), mine_upto = scan(mine);   // the first 32 sequences', kept
+    const int mine = tiles_in(my_len), mine_upto = scan(mine);
     auto len_of = [&](int b) { return b < 32 ? __shfl_sync(0xffffffffu, my_len, b) : __ldg(a.len + b); };
     if (blockIdx.x == 0 && warp == 0 && lane < a.B && mine == 0) flag(a.st, QSPEC_ERR_RANGE);
     int total = __shfl_sync(0xffffffffu, mine_upto, 31), valid = __popc(__ballot_sync(0xffffffffu, mine > 0));   // tiles; sequences with tasks

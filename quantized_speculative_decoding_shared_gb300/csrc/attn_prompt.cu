@@ -32,8 +32,9 @@
 // operations costs more than it hides (8192 tokens, 342 us as it is): waits
 // that spin 398, weights handed over in three parts 374, two warpgroups to a row
 // tile 408; with the exponentials left out it was as long.  8192 tokens, 8 KV heads
-// of 128 with 4 heads each: 342 us, 1607 TFLOP/s counting what the mask leaves; 7 sequences
-// of 5003 tokens, 4 KV heads with 7 each: 51.8 us; 3 of 301: 7.8 us.
+// of 128 with 4 heads each: 342 to 359 us from one GPU to another, up to 1607 TFLOP/s
+// counting what the mask leaves; 7 sequences of 5003 tokens, 4 KV heads with 7 each:
+// 51.4 us; 3 of 301: 7.5 us.
 #include <algorithm>
 #include <cmath>
 
@@ -220,6 +221,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     pdl_launch_dependents();
     pdl_wait();
+    // the first 32 sequences' rows (asked for before the barrier)
+    int4 rows = make_int4(0, 0, 0, 0);
+    if (warp == kUnitWarp && lane < a.B)
+        rows = make_int4(__ldg(a.q_start + lane), __ldg(a.q_start + lane + 1), __ldg(a.k_start + lane), __ldg(a.k_start + lane + 1));
     umma::fence_before_sync();
     __syncthreads();
     umma::fence_after_sync();
@@ -249,9 +254,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 auto fetch = [&](int b, bool report) {
                     q0 = lq = k0 = lk = 0;
                     if (b >= a.B) return;
-                    const int q1 = __ldg(a.q_start + b + 1), k1 = __ldg(a.k_start + b + 1);
-                    q0 = __ldg(a.q_start + b);
-                    k0 = __ldg(a.k_start + b);
+                    const int q1 = b < 32 ? rows.y : __ldg(a.q_start + b + 1), k1 = b < 32 ? rows.w : __ldg(a.k_start + b + 1);
+                    q0 = b < 32 ? rows.x : __ldg(a.q_start + b);
+                    k0 = b < 32 ? rows.z : __ldg(a.k_start + b);
                     if (q0 < 0 || q1 < q0 || q1 > a.q_rows || k0 < 0 || k1 < k0 || k1 > a.k_rows) {
                         if (report) flag(a.st, QSPEC_ERR_RANGE);
                         return;
