@@ -425,7 +425,7 @@ int qspec_rmsnorm_fp8(const uint16_t *x_bf16, int ldx, const uint16_t *res_bf16,
  * errors: QSPEC_ERR_RANGE when 0 <= row_start[b] <= row_start[b + 1] <= rows,
  * base_pos[b] >= 0 or base_pos[b] + (its rows) <= T does not hold (that
  * sequence is left untouched); append: QSPEC_ERR_NONFINITE (a NaN or inf, or
- * a scale beyond fp16).
+ * a scale beyond fp16: that row's entry is unspecified).
  */
 int qspec_kv4_append(const uint16_t *k_bf16, int ldk, const uint16_t *v_bf16, int ldv,
                      const int32_t *row_start, const int32_t *base_pos, int rows, int B, int H, int T,
@@ -478,8 +478,8 @@ int qspec_attn_kv4(const uint16_t *q_bf16, int ldq, const uint8_t *k_codes, cons
  *   q_bf16 uint16 [q_rows][ldq], k_bf16, v_bf16 uint16 [k_rows][ldk / ldv],
  *   o_bf16 uint16 [q_rows][ldo]   head j of row m at m ld + j D
  *   q_start, k_start int32 [B + 1] on the device
- * Scores, softmax statistics and sums in fp32; the weights exp(a - max) are rounded to
- * bf16 for the tensor cores.  Hq a multiple of H, D 64 or 128, pointers 16-byte
+ * Scores, softmax statistics and sums in fp32; the weights exp(a - reference of the
+ * row) are rounded to bf16 for the tensor cores.  Hq a multiple of H, D 64 or 128, pointers 16-byte
  * aligned, leading dimensions multiples of 8, at least the heads' width.
  * q_rows or k_rows may be 0.  Device errors: QSPEC_ERR_RANGE when
  * 0 <= start[b] <= start[b + 1] <= rows does not hold (that sequence is left
