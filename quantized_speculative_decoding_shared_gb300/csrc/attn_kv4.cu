@@ -338,10 +338,13 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
     // takes longer than its part in a join, and one is better (18.8 for 22.9 us at 4 sequences of 1000, gamma 8).
     const int nc = min((int)gridDim.x, N == 64 ? total : max(total / 4, min(total, tasks)));
     const bool any = (int)blockIdx.x < nc;
-    // Beginning and ending a segment (Q, the first tile's way through the products, sums, results) takes as
-    // long as some eight tiles (measured: 4, 6, 8, 11, 15 give 41.8, 40.6, 38.1, 38.2, 38.1 us at 32 sequences,
-    // gamma 8); where a CTA has fewer than sixteen, half of them: few tiles are better spread.
-    const int lead = (int)min(8u, (uint32_t)total / (2u * gridDim.x));
+    // Beginning and ending a segment (Q, the first tile's way through the products, sums, results) takes as long as
+    // some tiles.  Measured with 3 / 4 / 5 / 6 / 7 / 8: 16 sequences up to 4091, 5 rows of 4 heads 22.1 / 21.4 / 20.9 /
+    // 20.9 / 21.1 / 21.2 us, 64 up to 2048, one row 34.9 / 34.1 / 33.8 / 34.2 / 34.9 / 35.3; at 64 rows, where nearly all
+    // of a segment's own work grows with them, 32 sequences up to 4096, 9 rows of 7 heads 34.2 / 33.0 / 32.4 / 32.0 / 30.8 /
+    // 31.0.  Where a CTA has fewer than twice as many, half of them: few tiles are better spread.
+    constexpr uint32_t kLead = N == 64 ? 7 : 5;
+    const int lead = (int)min(kLead, (uint32_t)total / (2u * gridDim.x));
     // Shares: borders i total_v / nc, rounded down (i times the remainder is below 160 x 160, and its quotient by nc
     // at least 1 / 320 from an integer after the half: fp32 finds it).  A border among a task's leading empty
     // tiles is its first tile.
