@@ -31,7 +31,8 @@
 //
 // Work is split by the lengths on the device: all (sequence, head, row block)
 // tasks, cut into tiles of 128 positions, are laid end to end, each with a few
-// empty tiles in front that stand for a segment's fixed cost, and every CTA
+// empty tiles in front that stand for a segment's fixed cost (none where the tasks
+// are of one length and are taken in equal parts), and every CTA
 // takes an equal share.  A task that several CTAs share is joined by the last
 // of them to finish, in the order of the parts, so that the bits do not
 // depend on who is last.
@@ -40,9 +41,9 @@
 // memory (half its rate: codes in, V and P^T out and read by the products), HBM next:
 // 4 sequences of 65001 positions, 8 KV heads of 128, one row of 4 heads: 59.4 us, 4.3
 // TB/s of the D / 2 + 4 bytes per position, head and side (37.4 us at HBM's rate).  With
-// warp MMA (registers only) it was 63.5 us, and 43 for 21.3 at 16 sequences of up to
-// 4091 with 5 rows; 32 sequences, 9 rows, 7 heads to a KV head: 31.0 us.  Short calls
-// are the way through one tile: 6.5 us for one sequence of 333.
+// warp MMA (registers only) it was 63.5 us, and 43 for 21.0 at 16 sequences of up to
+// 4091 with 5 rows; 32 sequences, 9 rows, 7 heads to a KV head: 30.7 us.  Short calls
+// are the way through one tile: 6.4 us for one sequence of 333.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -326,17 +327,32 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
     auto len_of = [&](int b) { return b < 32 ? __shfl_sync(0xffffffffu, my_len, b) : __ldg(a.len + b); };
     if (blockIdx.x == 0 && warp == 0 && lane < a.B && mine == 0) flag(a.st, QSPEC_ERR_RANGE);
     int total = __shfl_sync(0xffffffffu, mine_upto, 31), valid = __popc(__ballot_sync(0xffffffffu, mine > 0));   // tiles; sequences with tasks
+    int most = __reduce_max_sync(0xffffffffu, mine);
     for (int b0 = 32; b0 < a.B; b0 += 32) {
         const int c = b0 + lane < a.B ? tiles_of(b0 + lane) : 0;
         if (blockIdx.x == 0 && warp == 0 && b0 + lane < a.B && c == 0) flag(a.st, QSPEC_ERR_RANGE);
         total += __reduce_add_sync(0xffffffffu, c);
         valid += __popc(__ballot_sync(0xffffffffu, c > 0));
+        most = max(most, __reduce_max_sync(0xffffffffu, c));
     }
+    const int each = valid * tasks;             // tasks in all
+    const bool even = total == most * valid && each > 0 && each <= (int)gridDim.x;
     total *= tasks;
-    // Few tiles: four to a CTA rather than one, since every part of a task more is another result to join (one
-    // sequence of 333 / 4000 positions, one row: 7.8 / 12.1 us with four, 9.5 / 13.7 us with one); with 64 rows a tile
-    // takes longer than its part in a join, and one is better (18.8 for 22.9 us at 4 sequences of 1000, gamma 8).
-    const int nc = min((int)gridDim.x, N == 64 ? total : max(total / 4, min(total, tasks)));
+    // CTAs that take part.  Tasks of one length (one sequence, or all alike), if there is a CTA for each: equal parts of
+    // every task, so that no CTA has the end of one and the beginning of another; parts of two tiles up to four parts,
+    // of about four for more (a part more is another result to join).  Against the rule below, with these parts / without, us:
+    // 16 sequences of 1000, one row 9.7 / 13.6; 8 of 2000, 5 rows of 4 heads 13.6 / 15.5, 9 rows of 7 15.5 / 19.7; one
+    // of 1000, one row 8.3 / 9.6.
+    int parts = 1;
+    if (even && most > 3) {                      // (quotients in fp32: exact for these divisors, and any would do)
+        const int fit = (int)__fdividef((float)gridDim.x + 0.25f, (float)each);
+        parts = max(1, min(min(fit, most / 2), max(4, (most + 3) / 4)));
+        const int tiles = (int)__fdividef((float)(most + parts - 1) + 0.25f, (float)parts);
+        parts = min(parts, (int)__fdividef((float)(most + tiles - 1) + 0.25f, (float)tiles));   // (no more than that length needs)
+    }
+    // Tasks of several lengths, few tiles: four to a CTA rather than one; with 64 rows a tile takes longer than its part in
+    // a join, and one is better.  (Equal numbers of parts are worse here: 4 of up to 1000, 5 rows, 16.7 for 13.7 us.)
+    const int nc = even ? each * parts : min((int)gridDim.x, N == 64 ? total : max(total / 4, min(total, tasks)));
     const bool any = (int)blockIdx.x < nc;
     // Beginning and ending a segment (Q, the first tile's way through the products, sums, results) takes as long as
     // some tiles.  Measured with 3 / 4 / 5 / 6 / 7 / 8: 16 sequences up to 4091, 5 rows of 4 heads 22.1 / 21.4 / 20.9 /
@@ -344,7 +360,7 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
     // of a segment's own work grows with them, 32 sequences up to 4096, 9 rows of 7 heads 34.2 / 33.0 / 32.4 / 32.0 / 30.8 /
     // 31.0.  Where a CTA has fewer than twice as many, half of them: few tiles are better spread.
     constexpr uint32_t kLead = N == 64 ? 7 : 5;
-    const int lead = (int)min(kLead, (uint32_t)total / (2u * gridDim.x));
+    const int lead = even ? 0 : (int)min(kLead, (uint32_t)total / (2u * gridDim.x));
     // Shares: borders i total_v / nc, rounded down (i times the remainder is below 160 x 160, and its quotient by nc
     // at least 1 / 320 from an integer after the half: fp32 finds it).  A border among a task's leading empty
     // tiles is its first tile.

@@ -232,3 +232,25 @@ def test_a_score_far_above_the_first_position(R, G, D, at):
     o = q.attn_kv4(x, cache, ints([T], dev), scale, dev_status=st)
     assert read_status(st) == 0
     check(x, cache, [T], R, scale, o)
+
+
+@pytest.mark.parametrize("B,R,H,G,D,n", [(1, 1, 8, 4, 128, 8100), (1, 5, 8, 4, 128, 1000), (16, 5, 8, 4, 128, 1000), (19, 1, 8, 4, 128, 515),
+                                         (8, 9, 4, 7, 128, 2000), (2, 3, 1, 2, 64, 513), (38, 17, 4, 8, 64, 700)])
+def test_sequences_of_one_length(B, R, H, G, D, n):
+    """Tasks in equal parts, whole tasks to a CTA, and the first size past that; an invalid sequence among them."""
+    dev = need_gpu()
+    lens = [n - b % 3 for b in range(B)]
+    cache = random_cache(B, H, n, D, 41, dev)
+    x = queries(B * R, H * G, D, 42, dev)
+    st = status(dev)
+    o = q.attn_kv4(x, cache, ints(lens, dev), 1 / math.sqrt(D), dev_status=st)
+    assert read_status(st) == 0
+    check(x, cache, lens, R, 1 / math.sqrt(D), o)
+    if B > 1:
+        lens[B // 2] = -1
+        o2 = q.attn_kv4(x, cache, ints(lens, dev), 1 / math.sqrt(D), out=torch.full_like(o, 9.0), dev_status=st)
+        assert read_status(st) == q.ERR_RANGE
+        lens[B // 2] = 0
+        assert torch.all(o2.view(B, R, -1)[B // 2] == 9.0)
+        o2.view(B, R, -1)[B // 2] = 0
+        check(x, cache, lens, R, 1 / math.sqrt(D), o2)
