@@ -31,8 +31,8 @@
 //
 // Work is split by the lengths on the device: all (sequence, head, row block)
 // tasks, cut into tiles of 128 positions, are laid end to end, each with a few
-// empty tiles in front that stand for a segment's fixed cost (none where the tasks
-// are of one length and are taken in equal parts), and every CTA
+// empty tiles in front that stand for a segment's fixed cost (or cut into parts of
+// their own, where there is a CTA for each), and every CTA
 // takes an equal share.  A task that several CTAs share is joined by the last
 // of them to finish, in the order of the parts, so that the bits do not
 // depend on who is last.
@@ -327,44 +327,58 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
     auto len_of = [&](int b) { return b < 32 ? __shfl_sync(0xffffffffu, my_len, b) : __ldg(a.len + b); };
     if (blockIdx.x == 0 && warp == 0 && lane < a.B && mine == 0) flag(a.st, QSPEC_ERR_RANGE);
     int total = __shfl_sync(0xffffffffu, mine_upto, 31), valid = __popc(__ballot_sync(0xffffffffu, mine > 0));   // tiles; sequences with tasks
-    int most = __reduce_max_sync(0xffffffffu, mine);
     for (int b0 = 32; b0 < a.B; b0 += 32) {
         const int c = b0 + lane < a.B ? tiles_of(b0 + lane) : 0;
         if (blockIdx.x == 0 && warp == 0 && b0 + lane < a.B && c == 0) flag(a.st, QSPEC_ERR_RANGE);
         total += __reduce_add_sync(0xffffffffu, c);
         valid += __popc(__ballot_sync(0xffffffffu, c > 0));
-        most = max(most, __reduce_max_sync(0xffffffffu, c));
     }
-    const int each = valid * tasks;             // tasks in all
-    const bool even = total == most * valid && each > 0 && each <= (int)gridDim.x;
     total *= tasks;
-    // CTAs that take part.  Tasks of one length (one sequence, or all alike), if there is a CTA for each: equal parts of
-    // every task, so that no CTA has the end of one and the beginning of another; parts of two tiles up to four parts,
-    // of about four for more (a part more is another result to join).  Against the rule below, with these parts / without, us:
-    // 16 sequences of 1000, one row 9.7 / 13.6; 8 of 2000, 5 rows of 4 heads 13.6 / 15.5, 9 rows of 7 15.5 / 19.7; one
-    // of 1000, one row 8.3 / 9.6.
-    int parts = 1;
-    if (even && most > 3) {                      // (quotients in fp32: exact for these divisors, and any would do)
-        const int fit = (int)__fdividef((float)gridDim.x + 0.25f, (float)each);
-        parts = max(1, min(min(fit, most / 2), max(4, (most + 3) / 4)));
-        const int tiles = (int)__fdividef((float)(most + parts - 1) + 0.25f, (float)parts);
-        parts = min(parts, (int)__fdividef((float)(most + tiles - 1) + 0.25f, (float)tiles));   // (no more than that length needs)
-    }
-    // Tasks of several lengths, few tiles: four to a CTA rather than one; with 64 rows a tile takes longer than its part in
-    // a join, and one is better.  (Equal numbers of parts are worse here: 4 of up to 1000, 5 rows, 16.7 for 13.7 us.)
-    const int nc = even ? each * parts : min((int)gridDim.x, N == 64 ? total : max(total / 4, min(total, tasks)));
-    const bool any = (int)blockIdx.x < nc;
+    const int each = valid * tasks;             // tasks in all
     // Beginning and ending a segment (Q, the first tile's way through the products, sums, results) takes as long as
     // some tiles.  Measured with 3 / 4 / 5 / 6 / 7 / 8: 16 sequences up to 4091, 5 rows of 4 heads 22.1 / 21.4 / 20.9 /
     // 20.9 / 21.1 / 21.2 us, 64 up to 2048, one row 34.9 / 34.1 / 33.8 / 34.2 / 34.9 / 35.3; at 64 rows, where nearly all
     // of a segment's own work grows with them, 32 sequences up to 4096, 9 rows of 7 heads 34.2 / 33.0 / 32.4 / 32.0 / 30.8 /
     // 31.0.  Where a CTA has fewer than twice as many, half of them: few tiles are better spread.
-    constexpr uint32_t kLead = N == 64 ? 7 : 5;
-    const int lead = even ? 0 : (int)min(kLead, (uint32_t)total / (2u * gridDim.x));
-    // Shares: borders i total_v / nc, rounded down (i times the remainder is below 160 x 160, and its quotient by nc
-    // at least 1 / 320 from an integer after the half: fp32 finds it).  A border among a task's leading empty
+    constexpr int kLead = N == 64 ? 7 : 5;
+    // Whole parts: if there is a CTA for each task, every task may be cut into parts of its own, so that no CTA has the
+    // end of one task and the beginning of another.  The parts are of `longest` tiles at most, the least that the CTAs
+    // are enough for, from two up (four parts of a task, then parts of four tiles: a part more is another result to
+    // join).  It is done where `longest` is no more than the equal share below would be with a segment's beginning
+    // counted.  With whole parts / with equal shares, us: 16 sequences of 1000, one row 9.9 / 13.6, of 125 to 1000 10.2 /
+    // 13.7; 8 of 250 to 2000, 5 rows of 4 heads 12.1 / 13.9, 9 rows of 7 15.0 / 24.3; one of 1000, one row 8.3 / 9.6.  Up
+    // to 32 sequences, whose lengths the lanes keep: keeping more cost every call 0.6 us.
+    // (quotients in fp32 where any near value would do; those that cut a task are whole numbers' own)
+    auto over = [](int n, int d) { return (int)__fdividef((float)n + 0.25f, (float)d); };
+    int longest = 0;                             // 0: equal shares
+    if (each > 0 && each <= (int)gridDim.x && a.B <= 32) {
+        const int most = __reduce_max_sync(0xffffffffu, mine), room = over(gridDim.x, tasks);
+        auto need = [&](int t) { return (int)__reduce_add_sync(0xffffffffu, over(mine + t - 1, t)); };
+        const int up = max(4, (most + 3) / 4), least = most <= 3 ? most : max(2, over(most + up - 1, up));
+        int hi = max(least, over(total + each * kLead, gridDim.x)), lo = least - 1;
+        if (need(hi) <= room) {
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (need(mid) <= room)
+                    hi = mid;
+                else
+                    lo = mid;
+            }
+            longest = hi;
+        }
+    }
+    const int mine_parts = longest > 0 ? (int)((uint32_t)(mine + longest - 1) / (uint32_t)longest) : 0, parts_upto = scan(mine_parts);
+    if (__shfl_sync(0xffffffffu, parts_upto, 31) * tasks > (int)gridDim.x) longest = 0;     // (a quotient one off, of millions)
+    int b = 0, task = 0, tile = 0;               // of the share's first tile
+    int prefix = 0, before = 0;                  // tiles, and tasks, before sequence b
+    int at = 0, end = 0;                         // tiles: counted from the first task's first (equal shares) or from the share's
+    int parts = 0, first_cta = 0;                // of this CTA's task (whole parts)
+    // Equal shares: borders i total_v / nc, rounded down (i times the remainder is below 160 x 160, and its quotient
+    // by nc at least 1 / 320 from an integer after the half: fp32 finds it).  A border among a task's leading empty
     // tiles is its first tile.
-    const int total_v = total + valid * tasks * lead;
+    const int nc = min((int)gridDim.x, total);
+    const int lead = (int)min((uint32_t)kLead, (uint32_t)total / (2u * gridDim.x));
+    const int total_v = total + each * lead;
     const int share = (int)((uint32_t)total_v / (uint32_t)max(nc, 1)), rest = total_v - share * nc;
     const float per_nc = __fdividef(1.0f, (float)max(nc, 1));
     auto border_v = [&](int i) { return i * share + (int)(((float)(i * rest) + 0.5f) * per_nc); };
@@ -390,10 +404,19 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
         }
         return total;
     };
-    int b = 0, task = 0, tile = 0;               // of the share's first tile
-    int prefix = 0, before = 0;                  // tiles, and tasks, before sequence b
-    int at = 0, end = 0;
-    if (any) {
+    if (longest > 0) {
+        const uint32_t past = __ballot_sync(0xffffffffu, parts_upto * tasks > (int)blockIdx.x);
+        if (past) {
+            b = __ffs(past) - 1;
+            parts = __shfl_sync(0xffffffffu, mine_parts, b);
+            const int first = (__shfl_sync(0xffffffffu, parts_upto, b) - parts) * tasks, tiles = __shfl_sync(0xffffffffu, mine, b);
+            task = (int)((uint32_t)(blockIdx.x - first) / (uint32_t)parts);
+            first_cta = first + task * parts;
+            const int part = (int)blockIdx.x - first_cta;
+            tile = (int)((uint32_t)(part * tiles) / (uint32_t)parts);
+            end = (int)((uint32_t)((part + 1) * tiles) / (uint32_t)parts) - tile;
+        }
+    } else if ((int)blockIdx.x < nc) {
         end = border(border_v(blockIdx.x + 1), b, prefix, before, task, tile);
         at = border(border_v(blockIdx.x), b, prefix, before, task, tile);
     }
@@ -444,8 +467,8 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
                     while (border_v(i + 1) <= v) ++i;
                     return i;
                 };
-                const int c0 = holder(ts);
-                Join j{holder(ts + nt_task - 1) - c0 + 1, c0, min(N, a.R * a.G - (task % a.blocks) * N), b, task};
+                const int c0 = longest > 0 ? first_cta : holder(ts);
+                Join j{longest > 0 ? parts : holder(ts + nt_task - 1) - c0 + 1, c0, min(N, a.R * a.G - (task % a.blocks) * N), b, task};
                 wait(&sm.stored[begins], 0);
                 if (lane == 0) {
                     __threadfence();
