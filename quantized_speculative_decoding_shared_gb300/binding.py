@@ -133,6 +133,17 @@ def _stream(stream):
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def on_stream(stream):
+    """The context in which what a call on `stream` (None, a torch stream or a raw handle) makes and fills belongs to
+    that stream: torch orders a fill, and hands freed memory out again, by the stream that was current."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _stream(stream)
+        stream = torch.cuda.ExternalStream(0 if handle == 1 else handle)    # (1: the legacy default stream by name)
+    return torch.cuda.stream(stream)
+
+
 def _check(rc: int, where: str):
     if rc != OK:
         detail = ""
@@ -530,8 +541,9 @@ def kv4_load(cache, row_start, base_pos, rows, dev_status=None, stream=None):
     _starts(row_start, B + 1, "row_start")
     _starts(base_pos, B, "base_pos")
     k_codes, k_sz, v_codes, v_sz = cache
-    k = torch.zeros((rows, H, D), dtype=torch.bfloat16, device=k_codes.device)
-    v = torch.zeros_like(k)
+    with on_stream(stream):
+        k = torch.zeros((rows, H, D), dtype=torch.bfloat16, device=k_codes.device)
+        v = torch.zeros_like(k)
     _check(qspec_kv4_load(k_codes, k_sz, v_codes, v_sz, row_start, base_pos, rows, B, H, T, D, k, H * D, v, H * D,
                           dev_status, stream), "qspec_kv4_load")
     return k, v

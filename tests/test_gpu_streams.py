@@ -1,0 +1,43 @@
+"""Calls on a stream that is not torch's current one, given as a stream object or as a raw handle.
+
+The current stream is kept busy meanwhile, so that a fill or an allocation of the call's own that went to it instead
+of the given stream would come after the kernel and show in the result."""
+import pytest
+import torch
+
+from quantized_speculative_decoding_shared_gb300 import binding as q, synthetic as syn
+from gpuhelp import need_gpu, read_status, status
+from layerref import random_cache
+
+pytestmark = pytest.mark.gpu
+BUSY = 20_000_000                               # clocks that the current stream is kept busy for: some 10 ms
+
+
+def ints(v, dev):
+    return torch.tensor(v, dtype=torch.int32, device=dev)
+
+
+def given(kind):
+    """A stream other than the current one, and what a call is given for it."""
+    s = torch.cuda.Stream()
+    return s, (s if kind == "object" else s.cuda_stream)
+
+
+def on_a_busy_device(call):
+    """The call's results, as they are once everything queued is done; the current stream is busy during the call."""
+    torch.cuda.synchronize()
+    torch.cuda._sleep(BUSY)
+    got = call()
+    torch.cuda.synchronize()
+    return got
+
+
+@pytest.mark.parametrize("kind", ["object", "handle"])
+def test_rows_read_back(kind):
+    dev = need_gpu()
+    cache = random_cache(2, 4, 64, 128, 3, dev)
+    start, base = ints([0, 40, 70], dev), ints([5, 30], dev)
+    want = q.kv4_load(cache, start, base, 70)
+    s, arg = given(kind)
+    got = on_a_busy_device(lambda: q.kv4_load(cache, start, base, 70, stream=arg))
+    assert all(torch.equal(a, b) for a, b in zip(got, want)) and torch.any(want[0] != 0)
