@@ -570,7 +570,7 @@ def attn_kv4(q, cache, length, scale, workspace=None, out=None, dev_status=None,
     if _heads(o, "out")[:3] != (rows, Hq, D):
         raise ValueError("out must be [%d][%d][%d]" % (rows, Hq, D))
     if workspace is None:
-        with torch.cuda.stream(stream) if isinstance(stream, torch.cuda.Stream) else contextlib.nullcontext():
+        with on_stream(stream):
             workspace = attn_kv4_workspace(B, R, Hq, H, D, q.device)
     k_codes, k_sz, v_codes, v_sz = cache
     _check(qspec_attn_kv4(q, ldq, k_codes, k_sz, v_codes, v_sz, length, B, R, Hq, H, T, D, scale, o,

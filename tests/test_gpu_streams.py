@@ -41,3 +41,23 @@ def test_rows_read_back(kind):
     s, arg = given(kind)
     got = on_a_busy_device(lambda: q.kv4_load(cache, start, base, 70, stream=arg))
     assert all(torch.equal(a, b) for a, b in zip(got, want)) and torch.any(want[0] != 0)
+
+
+@pytest.mark.parametrize("kind", ["object", "handle"])
+def test_cache_attention_with_a_workspace_of_its_own(kind):
+    """The workspace's counters are zeros when the kernel begins: the memory it comes from holds something else, and
+    several CTAs have parts of each task."""
+    dev = need_gpu()
+    B, R, H, G, D, T = 2, 3, 4, 2, 128, 3000
+    cache = random_cache(B, H, T, D, 4, dev)
+    x = syn.activations(B * R * H * G, D, 5, device=dev).view(B * R, H * G, D)
+    length = ints([3000, 2500], dev)
+    want = q.attn_kv4(x, cache, length, 0.1)
+    n = q.qspec_attn_kv4_workspace_bytes(B, R, H * G, H, D)
+    s, arg = given(kind)
+    with torch.cuda.stream(s):                          # (a block of the given stream's pool, and one of the current's)
+        torch.full((n,), 1, dtype=torch.uint8, device=dev)
+    torch.full((n,), 1, dtype=torch.uint8, device=dev)
+    st = status(dev)
+    got = on_a_busy_device(lambda: q.attn_kv4(x, cache, length, 0.1, dev_status=st, stream=arg))
+    assert read_status(st) == 0 and torch.equal(got, want)
