@@ -23,7 +23,11 @@ from . import binding as q
 
 class AttentionLayer:
     """Weights, cache and workspace of one layer; w_qkv fp16 [(Hq + 2 H) D][K], w_out fp16 [K][Hq D] (parents of
-    the E4M3 weights), w_norm bf16 [K]; B sequences of up to T positions, H KV heads of D."""
+    the E4M3 weights), w_norm bf16 [K]; B sequences of up to T positions, H KV heads of D.
+
+    Weights, cache and workspace are made on torch's current stream; prompt and step run on `stream` (None: the current
+    one), and all that they make belongs to it, their results included.  The cache and the workspace are one to the layer: calls on different
+    streams are ordered by the caller, as is a stream's first call after the making."""
 
     def __init__(self, w_norm, w_qkv, w_out, Hq, H, D, B, T, eps=1e-5):
         dev = w_norm.device
@@ -36,37 +40,38 @@ class AttentionLayer:
         self.workspace = q.attn_kv4_workspace(B, 1, Hq, H, D, device=dev)       # any number of rows
         self.each = torch.arange(B + 1, dtype=torch.int32, device=dev)
 
-    def _project(self, x, residual, stream):
-        xq, sa, h, _ = q.rmsnorm_fp8(x, self.w_norm, self.eps, residual=residual, dev_status=self.status, stream=stream)
-        y = q.linear_fp8(xq, sa, self.w_qkv, self.s_qkv, dev_status=self.status, stream=stream)
+    def _project(self, x, residual):
+        xq, sa, h, _ = q.rmsnorm_fp8(x, self.w_norm, self.eps, residual=residual, dev_status=self.status)
+        y = q.linear_fp8(xq, sa, self.w_qkv, self.s_qkv, dev_status=self.status)
         heads = y.view(x.shape[0], self.Hq + 2 * self.H, self.D)
         return h, heads[:, :self.Hq], heads[:, self.Hq:self.Hq + self.H], heads[:, self.Hq + self.H:]
 
-    def _out(self, o, stream):
-        xq, sa = q.quant_act_fp8(o.view(o.shape[0], self.Hq * self.D), dev_status=self.status, stream=stream)
-        return q.linear_fp8(xq, sa, self.w_out, self.s_out, dev_status=self.status, stream=stream)
+    def _out(self, o):
+        xq, sa = q.quant_act_fp8(o.view(o.shape[0], self.Hq * self.D), dev_status=self.status)
+        return q.linear_fp8(xq, sa, self.w_out, self.s_out, dev_status=self.status)
 
     def prompt(self, x, start, base=None, key_start=None, keys=None, residual=None, stream=None):
         """Packed prompt rows x bf16 [rows][K]; start int32 [B + 1].  With a prefix: base int32 [B] positions that the
         cache holds, key_start int32 [B + 1] = cumulated base + rows of each sequence, keys = its last value.
         Returns (y, h): the block's output and the residual stream (None without residual)."""
-        h, qr, k, v = self._project(x, residual, stream)
-        at = torch.zeros_like(self.each[:-1]) if base is None else base
-        q.kv4_append(self.cache, k, v, start, at, dev_status=self.status, stream=stream)
-        if base is not None:
-            k, v = q.kv4_load(self.cache, key_start, torch.zeros_like(at), keys, dev_status=self.status, stream=stream)
-        o = q.attn_prompt(qr, k, v, start, key_start if base is not None else None, dev_status=self.status, stream=stream)
-        return self._out(o, stream), h
+        with q.on_stream(stream):
+            h, qr, k, v = self._project(x, residual)
+            at = torch.zeros_like(self.each[:-1]) if base is None else base
+            q.kv4_append(self.cache, k, v, start, at, dev_status=self.status)
+            if base is not None:
+                k, v = q.kv4_load(self.cache, key_start, torch.zeros_like(at), keys, dev_status=self.status)
+            o = q.attn_prompt(qr, k, v, start, key_start if base is not None else None, dev_status=self.status)
+            return self._out(o), h
 
     def step(self, x, base, residual=None, stream=None):
         """R newest rows of every sequence, x bf16 [B R][K], at positions base[b], base[b] + 1, ...: R = 1 drafts,
         R = gamma + 1 verifies.  Returns (y, h)."""
         R = x.shape[0] // self.B
-        h, qr, k, v = self._project(x, residual, stream)
-        q.kv4_append(self.cache, k, v, self.each * R, base, dev_status=self.status, stream=stream)
-        o = q.attn_kv4(qr, self.cache, base + R, self.D ** -0.5, workspace=self.workspace, dev_status=self.status,
-                       stream=stream)
-        return self._out(o, stream), h
+        with q.on_stream(stream):
+            h, qr, k, v = self._project(x, residual)
+            q.kv4_append(self.cache, k, v, self.each * R, base, dev_status=self.status)
+            o = q.attn_kv4(qr, self.cache, base + R, self.D ** -0.5, workspace=self.workspace, dev_status=self.status)
+            return self._out(o), h
 
 
 def main():

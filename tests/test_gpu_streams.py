@@ -6,6 +6,7 @@ import pytest
 import torch
 
 from quantized_speculative_decoding_shared_gb300 import binding as q, synthetic as syn
+from quantized_speculative_decoding_shared_gb300.layer import AttentionLayer
 from gpuhelp import need_gpu, read_status, status
 from layerref import random_cache
 
@@ -61,3 +62,56 @@ def test_cache_attention_with_a_workspace_of_its_own(kind):
     st = status(dev)
     got = on_a_busy_device(lambda: q.attn_kv4(x, cache, length, 0.1, dev_status=st, stream=arg))
     assert read_status(st) == 0 and torch.equal(got, want)
+
+
+@pytest.mark.parametrize("kind", ["object", "handle"])
+def test_prompts_drafts_and_verify_of_a_layer(kind):
+    """A layer's program on a given stream, and what the current stream's allocations do meanwhile, leave the same bits
+    as the program on the current stream."""
+    dev = need_gpu()
+    B, T, gamma, K, Hq, H, D, lens = 3, 300, 3, 512, 8, 2, 128, [150, 1, 37]
+    w = torch.ones(K, dtype=torch.bfloat16, device=dev)
+    fp16 = lambda n, k, seed: (syn.activations(n, k, seed, device=dev).float() * 0.05).to(torch.float16)   # noqa: E731
+    layer = AttentionLayer(w, fp16((Hq + 2 * H) * D, K, 1), fp16(K, Hq * D, 2), Hq, H, D, B, T)
+    x, res = syn.activations(sum(lens), K, 3, device=dev), syn.activations(sum(lens), K, 4, device=dev)
+    start, at = ints([0, 150, 151, 188], dev), [ints([n + i for n in lens], dev) for i in range(gamma)]
+    held = ints([n + gamma + 1 for n in lens], dev)
+    more, start2, total = syn.activations(25, K, 30, device=dev), ints([0, 5, 5, 25], dev), [lens[0] + 9, lens[1] + 4, lens[2] + 24]
+    key_start, keys = ints([0, total[0], total[0] + total[1], sum(total)], dev), sum(total)
+    drafts = [syn.activations(B, K, 10 + i, device=dev) for i in range(gamma)]
+    rows = syn.activations(B * (gamma + 1), K, 20, device=dev)
+
+    def program(between=lambda: None, **kw):
+        out = list(layer.prompt(x, start, residual=res, **kw))
+        for d, p in zip(drafts, at):
+            between()
+            out.append(layer.step(d, p, **kw)[0])
+        between()
+        out.append(layer.step(rows, at[0], **kw)[0])
+        between()
+        out.append(layer.prompt(more, start2, base=held, key_start=key_start, keys=keys, **kw)[0])
+        between()
+        return out
+
+    want = program()
+    cache = [t.clone() for t in layer.cache]
+    s, arg = given(kind)
+    for late in (False, True):                              # the current stream late, the given one late
+        for t in layer.cache:
+            t.zero_()
+
+        def others():                                       # the current stream's memory, used again at once
+            for n in (16, 1024, 1 << 16, 1 << 18, 1 << 20):
+                torch.full((n,), 0xFF, dtype=torch.uint8, device=dev)
+
+        torch.cuda.synchronize()
+        if late:
+            with torch.cuda.stream(s):
+                torch.cuda._sleep(BUSY)
+        else:
+            torch.cuda._sleep(BUSY)
+        got = program(others, stream=arg)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        assert all(torch.equal(a, b) for a, b in zip(layer.cache, cache))
+    assert read_status(layer.status) == 0
