@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 import threading
 
@@ -142,6 +143,21 @@ def on_stream(stream):
         handle = _stream(stream)
         stream = torch.cuda.ExternalStream(0 if handle == 1 else handle)    # (1: the legacy default stream by name)
     return torch.cuda.stream(stream)
+
+
+def _allocates(call):
+    """A call that makes tensors: with `stream` given they are made on it (memory of the current stream's pool may still
+    be written by work queued there, and what a call drops on return would go back to that pool too early)."""
+    place = call.__code__.co_varnames.index("stream")
+
+    @functools.wraps(call)
+    def made(*args, **kw):
+        stream = args[place] if len(args) > place else kw.get("stream")
+        if stream is None:
+            return call(*args, **kw)
+        with on_stream(stream):
+            return call(*args, **kw)
+    return made
 
 
 def _check(rc: int, where: str):
@@ -317,6 +333,7 @@ def qspec_attn_prompt(q, ldq, k, ldk, v, ldv, q_start, k_start, q_rows, k_rows, 
 # ---------------------------------------------------------------------------
 # allocating conveniences (torch tensors in, torch tensors out)
 # ---------------------------------------------------------------------------
+@_allocates
 def pack_weights(codes, s, z, dev_status=None, stream=None):
     """codes uint8 [N][K], s / z fp16 [N][K/128] -> (packed uint8 [N][K/2], sz int32 [N][K/128])."""
     _need(codes, torch.uint8, "codes")
@@ -330,6 +347,7 @@ def pack_weights(codes, s, z, dev_status=None, stream=None):
     return packed, sz
 
 
+@_allocates
 def quant_act_int4(x, dev_status=None, stream=None):
     """x bf16 [M][K] -> (xq uint8 [M][K/2], sx fp32 [M][G], qs int32 [M][G])."""
     _need(x, torch.bfloat16, "x")
@@ -341,6 +359,7 @@ def quant_act_int4(x, dev_status=None, stream=None):
     return xq, sx, qs
 
 
+@_allocates
 def linear_w4a4(xq, sx, qs, packed, sz, want_I=False, out=None, dev_status=None, stream=None):
     M, N, K = xq.shape[0], packed.shape[0], packed.shape[1] * 2
     y = out if out is not None else torch.empty((M, N), dtype=torch.bfloat16, device=xq.device)
@@ -350,6 +369,7 @@ def linear_w4a4(xq, sx, qs, packed, sz, want_I=False, out=None, dev_status=None,
     return (y, I) if want_I else y
 
 
+@_allocates
 def linear_w4a4_bf16(x, packed, sz, want_I=False, out=None, dev_status=None, stream=None):
     """Quantise bf16 activations and run the W4A4 linear in one call:
     returns (y, xq, sx, qs) (and I when want_I), equal to quant_act_int4
@@ -368,6 +388,7 @@ def linear_w4a4_bf16(x, packed, sz, want_I=False, out=None, dev_status=None, str
     return (y, xq, sx, qs, I) if want_I else (y, xq, sx, qs)
 
 
+@_allocates
 def linear_w4a16(x, packed, sz, out=None, dev_status=None, stream=None):
     _need(x, torch.bfloat16, "x")
     M, K = x.shape
@@ -385,6 +406,7 @@ def verify_workspace(B, gamma, V, device="cuda"):
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
+@_allocates
 def verify_greedy(p, draft, workspace=None, dev_status=None, stream=None):
     B, g1, V = p.shape
     gamma = g1 - 1
@@ -396,6 +418,7 @@ def verify_greedy(p, draft, workspace=None, dev_status=None, stream=None):
     return n_acc, out
 
 
+@_allocates
 def verify_sample(p, q, draft, seed, rnd, workspace=None, dev_status=None, stream=None):
     B, g1, V = p.shape
     gamma = g1 - 1
@@ -414,6 +437,7 @@ def draft_workspace(B, V, device="cuda"):
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
+@_allocates
 def draft_sample(q, seed, rnd, step, workspace=None, dev_status=None, stream=None):
     """q bf16 [B][V] draft logits of draft position step (1..16) ->
     (token int32 [B], confidence fp32 [B], entropy fp32 [B])."""
@@ -435,6 +459,7 @@ def kv_overwrite(k_cache, v_cache, k_new, v_new, base_pos, n_acc, dev_status=Non
                               gamma, dev_status, stream), "qspec_kv_overwrite")
 
 
+@_allocates
 def quant_weights_fp8(w16, dev_status=None, stream=None):
     """Parent weights fp16 [N][K] -> (w8 uint8 [N][K] E4M3, s8 fp32 [N])."""
     _need(w16, torch.float16, "w16")
@@ -445,6 +470,7 @@ def quant_weights_fp8(w16, dev_status=None, stream=None):
     return w8, s8
 
 
+@_allocates
 def quant_act_fp8(x, dev_status=None, stream=None):
     """bf16 [M][K] -> (xq uint8 [M][K] E4M3, sa fp32 [M])."""
     _need(x, torch.bfloat16, "x")
@@ -455,6 +481,7 @@ def quant_act_fp8(x, dev_status=None, stream=None):
     return xq, sa
 
 
+@_allocates
 def linear_fp8(xq, sa, w8, s8, out=None, dev_status=None, stream=None):
     M, K = xq.shape
     N = w8.shape[0]
@@ -475,6 +502,7 @@ def _heads(t, name):
     return rows, H, D, (t.stride(0) if rows > 1 else H * D)
 
 
+@_allocates
 def rmsnorm_fp8(x, w, eps, residual=None, want_bf16=False, dev_status=None, stream=None):
     """x bf16 [M][K] (plus residual bf16 [M][K]) -> (xq uint8 [M][K] E4M3, sa fp32 [M], h bf16 [M][K] or
     None without a residual, y bf16 [M][K] or None without want_bf16)."""
@@ -535,15 +563,15 @@ def kv4_append(cache, k, v, row_start, base_pos, dev_status=None, stream=None):
                             dev_status, stream), "qspec_kv4_append")
 
 
+@_allocates
 def kv4_load(cache, row_start, base_pos, rows, dev_status=None, stream=None):
     """The rows of kv4_append back from the cache: (k, v) bf16 [rows][H][D].  Rows of no sequence are zeros."""
     B, H, T, D = _cache_shape(cache)
     _starts(row_start, B + 1, "row_start")
     _starts(base_pos, B, "base_pos")
     k_codes, k_sz, v_codes, v_sz = cache
-    with on_stream(stream):
-        k = torch.zeros((rows, H, D), dtype=torch.bfloat16, device=k_codes.device)
-        v = torch.zeros_like(k)
+    k = torch.zeros((rows, H, D), dtype=torch.bfloat16, device=k_codes.device)
+    v = torch.zeros_like(k)
     _check(qspec_kv4_load(k_codes, k_sz, v_codes, v_sz, row_start, base_pos, rows, B, H, T, D, k, H * D, v, H * D,
                           dev_status, stream), "qspec_kv4_load")
     return k, v
@@ -557,6 +585,7 @@ def attn_kv4_workspace(B, R, Hq, H, D, device="cuda"):
     return torch.zeros(n, dtype=torch.uint8, device=device)
 
 
+@_allocates
 def attn_kv4(q, cache, length, scale, workspace=None, out=None, dev_status=None, stream=None):
     """q bf16 [B R][Hq][D], the newest R rows of each sequence, over a 4-bit cache; length int32 [B] counts them.
     Returns o bf16 [B R][Hq][D]."""
@@ -570,14 +599,14 @@ def attn_kv4(q, cache, length, scale, workspace=None, out=None, dev_status=None,
     if _heads(o, "out")[:3] != (rows, Hq, D):
         raise ValueError("out must be [%d][%d][%d]" % (rows, Hq, D))
     if workspace is None:
-        with on_stream(stream):
-            workspace = attn_kv4_workspace(B, R, Hq, H, D, q.device)
+        workspace = attn_kv4_workspace(B, R, Hq, H, D, q.device)
     k_codes, k_sz, v_codes, v_sz = cache
     _check(qspec_attn_kv4(q, ldq, k_codes, k_sz, v_codes, v_sz, length, B, R, Hq, H, T, D, scale, o,
                           _heads(o, "out")[3], workspace, workspace.numel(), dev_status, stream), "qspec_attn_kv4")
     return o
 
 
+@_allocates
 def attn_prompt(q, k, v, q_start, k_start=None, scale=None, out=None, dev_status=None, stream=None):
     """Causal attention over packed prompts: q bf16 [q_rows][Hq][D], k and v bf16 [k_rows][H][D], q_start and
     k_start int32 [B + 1] (k_start None: the same).  scale None: 1 / sqrt(D).  Returns o bf16 [q_rows][Hq][D]."""

@@ -115,3 +115,62 @@ def test_prompts_drafts_and_verify_of_a_layer(kind):
         assert all(torch.equal(a, b) for a, b in zip(got, want))
         assert all(torch.equal(a, b) for a, b in zip(layer.cache, cache))
     assert read_status(layer.status) == 0
+
+
+def calls(dev):
+    """The calls that make their outputs, on inputs of a few rows."""
+    M, N, K, V = 5, 256, 512, 1000
+    x, w = syn.activations(M, K, 1, device=dev), torch.ones(K, dtype=torch.bfloat16, device=dev)
+    codes, sc, z = syn.weights(N, K, 2, device=dev)
+    packed, sz = q.pack_weights(codes, sc, z)
+    w16 = (syn.activations(N, K, 3, device=dev).float() * 0.05).to(torch.float16)
+    w8, s8 = q.quant_weights_fp8(w16)
+    x4, x8 = q.quant_act_int4(x), q.quant_act_fp8(x)
+    p = syn.activations(2 * 4, V, 4, device=dev).view(2, 4, V)
+    p3, p0, none, lens = p[:, :3].contiguous(), p[:, 0].contiguous(), ints([0, 0], dev), ints([70, 50], dev)
+    draft = ints([[1, 2, 3], [4, 5, 6]], dev)
+    h = syn.activations(70 * 8, 64, 6, device=dev).view(70, 8, 64)
+    cu = ints([0, 30, 70], dev)
+    cache = random_cache(2, 2, 70, 64, 3, dev)
+    return {
+        "pack_weights": lambda **kw: q.pack_weights(codes, sc, z, **kw),
+        "quant_act_int4": lambda **kw: q.quant_act_int4(x, **kw),
+        "linear_w4a4": lambda **kw: q.linear_w4a4(*x4, packed, sz, **kw),
+        "linear_w4a4_bf16": lambda **kw: q.linear_w4a4_bf16(x, packed, sz, **kw),
+        "linear_w4a16": lambda **kw: q.linear_w4a16(x, packed, sz, **kw),
+        "verify_greedy": lambda **kw: q.verify_greedy(p, draft, **kw),
+        "verify_sample": lambda **kw: q.verify_sample(p, p3, draft, 7, 1, **kw),
+        "draft_sample": lambda **kw: q.draft_sample(p0, 7, 1, 1, **kw),
+        "quant_weights_fp8": lambda **kw: q.quant_weights_fp8(w16, **kw),
+        "quant_act_fp8": lambda **kw: q.quant_act_fp8(x, **kw),
+        "linear_fp8": lambda **kw: q.linear_fp8(*x8, w8, s8, **kw),
+        "rmsnorm_fp8": lambda **kw: q.rmsnorm_fp8(x, w, 1e-5, residual=x, want_bf16=True, **kw),
+        "kv4_load": lambda **kw: q.kv4_load(cache, cu, none, 70, **kw),
+        "attn_kv4": lambda **kw: q.attn_kv4(h[:6], cache, lens, 0.1, **kw),
+        "attn_prompt": lambda **kw: q.attn_prompt(h, h[:, :2], h[:, 2:4], cu, **kw),
+    }
+
+
+@pytest.mark.parametrize("name", ["pack_weights", "quant_act_int4", "linear_w4a4", "linear_w4a4_bf16", "linear_w4a16", "verify_greedy",
+                                  "verify_sample", "draft_sample", "quant_weights_fp8", "quant_act_fp8", "linear_fp8", "rmsnorm_fp8",
+                                  "kv4_load", "attn_kv4", "attn_prompt"])
+@pytest.mark.parametrize("kind", ["object", "handle"])
+def test_outputs_are_memory_of_the_given_stream(name, kind):
+    """Memory that the current stream still writes (dropped by the program, its last fill queued) is not what a call on
+    another stream puts its results into."""
+    dev = need_gpu()
+    call = calls(dev)[name]
+    tensors = lambda r: list(r) if isinstance(r, tuple) else [r]            # noqa: E731
+    want = [t.clone() for t in tensors(call())]
+    s, arg = given(kind)
+
+    def fill():
+        for t in [torch.empty_like(t) for t in want]:
+            t.view(torch.uint8).fill_(0x11)
+
+    def fills_then_call():
+        fill()
+        return tensors(call(stream=arg))
+
+    got = on_a_busy_device(fills_then_call)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
