@@ -155,9 +155,11 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR)
     }
     float ss = lo32(sq) + hi32(sq), down = 1.0f;
     row_reduce<TPR>(ss, amax, red);
-    // Where the squares or products of finite values pass fp32 (|h| above 1e19),
-    // the row is read and taken again times 2^-80.
-    const bool again = !(ss < INFINITY && amax < INFINITY);
+    // Where the squares of finite values pass fp32 (|h| above 1e19), or the products
+    // with large weights, the row is read and taken again times 2^-80.  A sum of
+    // squares that did not pass it stands (times 2^-160 little would be left of it).
+    const bool again = !(ss < INFINITY && amax < INFINITY), stands = ss < INFINITY;
+    const float first = ss;
     if (TPR > 32 ? again : __any_sync(0xffffffffu, again)) {
         if (again) down = 8.271806125530277e-25f;        // 2^-80
         const uint16_t *row = res != nullptr ? h + (size_t)m * ldh : x + (size_t)m * ldx;
@@ -176,10 +178,12 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR)
             }
         }
         row_reduce<TPR>(ss, amax, red);
+        if (stands) ss = first;
     }
     if (!row_ok) return;
     if (!(amax < INFINITY)) amax = INFINITY;             // (NaN too)
-    const float rstd = rsqrtf(fmaf(ss, 1.0f / (float)K, eps * down * down));
+    const float of_ss = stands ? 1.0f : down;            // what ss was taken of: h times this
+    const float rstd = rsqrtf(fmaf(ss, 1.0f / (float)K, eps * of_ss * of_ss)) * (of_ss == down ? 1.0f : 1.2089258196146292e24f);   // (2^80)
     // y = a rstd; codes a (448 / max |a|), where 448 / max |a| would pass fp32
     // with a brought up first
     const float up = amax < 1.0e-30f ? 7.9228162514264338e28f : 1.0f;   // 2^96
