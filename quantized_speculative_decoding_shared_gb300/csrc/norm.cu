@@ -212,9 +212,9 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR)
                         : make_uint2(0u, 0u);         // no code of -0 in a row of zeros
     }
     if (t == 0) {
-        const float s = __fdiv_rn(amax * rstd, 448.0f);
-        sa[m] = s;
-        if (!(ss < INFINITY) || !(s < INFINITY)) flag(st, QSPEC_ERR_NONFINITE);
+        const float top = amax * rstd, s = __fdiv_rn(top, 448.0f);          // max |y|, in the bf16 output inf from the
+        sa[m] = s;                                                           // midpoint behind the largest bf16 value
+        if (!(ss < INFINITY) || !(top < (y != nullptr ? 3.3961775292304601e38f : INFINITY))) flag(st, QSPEC_ERR_NONFINITE);
     }
 }
 

@@ -41,3 +41,19 @@ def test_products_past_fp32(K, h, w):
     got = q.rmsnorm_fp8(x, ww, EPS, want_bf16=True, dev_status=st)
     assert read_status(st) == 0
     check(x, ww, EPS, got)
+
+
+@pytest.mark.parametrize("K", [128, 4096])
+def test_y_past_bf16(K):
+    """A y between the largest bf16 value and fp32's is finite for the codes; as a bf16 output it is inf, and flagged."""
+    dev = need_gpu()
+    x = torch.ones((1, K), device=dev)
+    x[0, K // 4:] = 1 - 2.0 ** -8                              # x / rms = 1.0029 where x = 1
+    w = torch.ones(K, device=dev)
+    w[0] = torch.finfo(torch.bfloat16).max                     # y = 1.0029 x 3.3895e38: past the midpoint 3.3962e38
+    x, w = x.to(torch.bfloat16), w.to(torch.bfloat16)
+    st = status(dev)
+    xq, sa, _, _ = q.rmsnorm_fp8(x, w, EPS, dev_status=st)
+    assert read_status(st) == 0 and torch.isfinite(sa).all() and int(xq[0, 0]) == 0x7E
+    _, _, _, y = q.rmsnorm_fp8(x, w, EPS, want_bf16=True, dev_status=st)
+    assert torch.isinf(y[0, 0]) and read_status(st) == q.ERR_NONFINITE
