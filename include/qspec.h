@@ -424,7 +424,8 @@ int qspec_rmsnorm_fp8(const uint16_t *x_bf16, int ldx, const uint16_t *res_bf16,
  * k_bf16, v_bf16 and the codes 16-byte aligned.  rows may be 0.  Device
  * errors: QSPEC_ERR_RANGE when 0 <= row_start[b] <= row_start[b + 1] <= rows,
  * base_pos[b] >= 0 or base_pos[b] + (its rows) <= T does not hold (that
- * sequence is left untouched); append: QSPEC_ERR_NONFINITE (a NaN or inf, or
+ * sequence is left untouched, the others are not affected; where starts that
+ * decrease put a row in the ranges of several, it is one of theirs); append: QSPEC_ERR_NONFINITE (a NaN or inf, or
  * a scale beyond fp16: that row's entry is unspecified).
  */
 int qspec_kv4_append(const uint16_t *k_bf16, int ldk, const uint16_t *v_bf16, int ldv,

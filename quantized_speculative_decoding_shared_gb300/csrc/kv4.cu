@@ -68,11 +68,19 @@ __device__ __forceinline__ const int32_t *stage_starts(const Rows &r, int32_t *b
     return buf;
 }
 
-// The place (sequence, head, position) of packed row m in the cache, or -1: rows of
-// no sequence, and sequences whose ranges do not hold (flagged by check_ranges).
-__device__ __forceinline__ long long locate(const Rows &r, const int32_t *start, int m, int hd) {
-    if (m >= r.rows) return -1;
-    int lo = 0, hi = r.B;                        // last b with start[b] <= m
+// The place (sequence, head, position) of packed row m in the cache if sequence b has it, or -1 (sequences
+// whose ranges do not hold, flagged by check_ranges, have none).
+__device__ __forceinline__ long long place_in(const Rows &r, const int32_t *start, int b, int m, int hd) {
+    const int s0 = start[b], s1 = start[b + 1], p0 = __ldg(r.base + b);
+    if (m < s0 || m >= s1 || s0 < 0 || s1 > r.rows || p0 < 0 || (long long)p0 + (s1 - s0) > r.T) return -1;
+    return ((long long)b * r.H + hd) * r.T + p0 + (m - s0);
+}
+// Of lane j < R the place of row m0 + j, or -1: rows of no sequence.
+template <int R>
+__device__ __forceinline__ long long locate(const Rows &r, const int32_t *start, int m0, int hd) {
+    const int lane = threadIdx.x & 31, m = m0 + lane;
+    const bool mine = lane < R && m < r.rows;
+    int lo = 0, hi = mine ? r.B : 0;             // last b with start[b] <= m
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (start[mid] <= m)
@@ -80,9 +88,22 @@ __device__ __forceinline__ long long locate(const Rows &r, const int32_t *start,
         else
             hi = mid;
     }
-    const int s0 = start[lo], s1 = start[lo + 1], p0 = __ldg(r.base + lo);
-    if (m < s0 || m >= s1 || s0 < 0 || s1 > r.rows || p0 < 0 || (long long)p0 + (s1 - s0) > r.T) return -1;
-    return ((long long)lo * r.H + hd) * r.T + p0 + (m - s0);
+    long long found = mine ? place_in(r, start, lo, m, hd) : -1;
+    // A start that does not hold can lead the search past a row's sequence: the lanes look at all of them
+    // then (and for rows between and after the sequences).
+    uint32_t lost = __ballot_sync(0xffffffffu, mine && found < 0);
+    while (lost) {
+        const int who = __ffs(lost) - 1;
+        lost &= lost - 1;
+        long long at = -1;
+        for (int b0 = 0; b0 < r.B && at < 0; b0 += 32) {
+            at = b0 + lane < r.B ? place_in(r, start, b0 + lane, m0 + who, hd) : -1;
+            const uint32_t has = __ballot_sync(0xffffffffu, at >= 0);
+            at = __shfl_sync(0xffffffffu, at, has ? __ffs(has) - 1 : 0);
+        }
+        if (lane == who) found = at;
+    }
+    return found;
 }
 
 // every sequence's ranges, by the first CTA (so that one without rows of its
@@ -209,8 +230,7 @@ __global__ void __launch_bounds__(kThreads)
     }
     const int32_t *start = stage_starts(r, buf);
     if (!p.in) return;
-    const int lane = threadIdx.x & 31;
-    const long long found = lane < Part<D>::R ? locate(r, start, p.m0 + lane, p.hd) : -1;
+    const long long found = locate<Part<D>::R>(r, start, p.m0, p.hd);
     bool bad = false;
     uint32_t word[2] = {0, 0};                   // of the row that this lane writes
     auto rounds = [&](auto place) {
@@ -272,8 +292,7 @@ __global__ void __launch_bounds__(kThreads)
     check_ranges(r, st);
     const int32_t *start = stage_starts(r, buf);
     if (!p.in) return;
-    const int lane = threadIdx.x & 31;
-    const long long found = lane < Part<D>::R ? locate(r, start, p.m0 + lane, p.hd) : -1;
+    const long long found = locate<Part<D>::R>(r, start, p.m0, p.hd);
     auto rounds = [&](auto place) {
         uint32_t kn[kRounds], vn[kRounds], kw[kRounds], vw[kRounds];
         bool there[kRounds];
