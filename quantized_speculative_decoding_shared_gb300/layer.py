@@ -66,7 +66,9 @@ class AttentionLayer:
     def step(self, x, base, residual=None, stream=None):
         """R newest rows of every sequence, x bf16 [B R][K], at positions base[b], base[b] + 1, ...: R = 1 drafts,
         R = gamma + 1 verifies.  Returns (y, h)."""
-        R = x.shape[0] // self.B
+        R, over = divmod(x.shape[0], self.B)
+        if over or not 1 <= R <= q.MAX_GAMMA + 1:
+            raise ValueError("x must hold 1 to %d rows for each of the %d sequences" % (q.MAX_GAMMA + 1, self.B))
         with q.on_stream(stream):
             h, qr, k, v = self._project(x, residual)
             q.kv4_append(self.cache, k, v, self.each * R, base, dev_status=self.status)
