@@ -54,6 +54,12 @@ class AttentionLayer:
         """Packed prompt rows x bf16 [rows][K]; start int32 [B + 1].  With a prefix: base int32 [B] positions that the
         cache holds, key_start int32 [B + 1] = cumulated base + rows of each sequence, keys = its last value.
         Returns (y, h): the block's output and the residual stream (None without residual)."""
+        if base is not None:
+            if key_start is None or not isinstance(keys, int) or keys < 0:
+                raise ValueError("a prefix needs key_start and the number of keys")
+            if (key_start.device != x.device or key_start.dtype != torch.int32 or key_start.numel() != self.B + 1
+                    or not key_start.is_contiguous()):
+                raise ValueError("key_start must be contiguous int32 [%d] next to x" % (self.B + 1))
         with q.on_stream(stream):
             h, qr, k, v = self._project(x, residual)
             at = torch.zeros_like(self.each[:-1]) if base is None else base

@@ -47,3 +47,15 @@ def test_step_refuses_before_it_writes(layer, rows):
     with pytest.raises(ValueError):
         layer.step(x(rows), torch.zeros(B, dtype=torch.int32))
     assert "kv4_append" not in made
+
+
+@pytest.mark.parametrize("change", [dict(key_start=None), dict(keys=None), dict(keys=-1), dict(keys=2.5),
+                                    dict(key_start=torch.zeros(B, dtype=torch.int32)),
+                                    dict(key_start=torch.zeros(B + 1, dtype=torch.int64))])
+def test_prompt_with_a_prefix_refuses_before_it_writes(layer, change):
+    layer, made = layer
+    starts = torch.zeros(B + 1, dtype=torch.int32)
+    prefix = dict(base=torch.zeros(B, dtype=torch.int32), key_start=starts, keys=6)
+    with pytest.raises(ValueError):
+        layer.prompt(x(6), starts, **dict(prefix, **change))
+    assert "kv4_append" not in made
