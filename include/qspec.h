@@ -389,7 +389,7 @@ int qspec_linear_fp8(const uint8_t *xq, const float *sa, const uint8_t *w8, cons
  *   xq       uint8  [M][K]     out: E4M3 codes, as qspec_linear_fp8 reads them
  *   sa       float  [M]        out: scales
  *   y_bf16   uint16 [M][ldy]   nullable out
- * K a multiple of 128, at most 32768; eps positive and finite
+ * M at least 1; K a multiple of 128, at most 32768; eps positive and finite
  * (QSPEC_ERR_SHAPE).  Leading dimensions are at least K and multiples of 8,
  * pointers 16-byte aligned (xq 8, sa 4).  Device errors: QSPEC_ERR_NONFINITE
  * (a NaN or inf among x, res, h, w or y).

@@ -61,6 +61,8 @@ class AttentionLayer:
                     or not key_start.is_contiguous()):
                 raise ValueError("key_start must be contiguous int32 [%d] next to x" % (self.B + 1))
         with q.on_stream(stream):
+            if x.shape[0] == 0:                          # (the linears take one row at least)
+                return x.new_empty((0, self.w_out.shape[0])), None if residual is None else torch.empty_like(x)
             h, qr, k, v = self._project(x, residual)
             at = torch.zeros_like(self.each[:-1]) if base is None else base
             q.kv4_append(self.cache, k, v, start, at, dev_status=self.status)

@@ -59,3 +59,14 @@ def test_prompt_with_a_prefix_refuses_before_it_writes(layer, change):
     with pytest.raises(ValueError):
         layer.prompt(x(6), starts, **dict(prefix, **change))
     assert "kv4_append" not in made
+
+
+@pytest.mark.parametrize("residual", [False, True])
+def test_a_prompt_without_rows(layer, residual):
+    """A step in which every sequence is empty: no rows out, and nothing called."""
+    layer, made = layer
+    starts = torch.zeros(B + 1, dtype=torch.int32)
+    for prefix in ({}, dict(base=torch.ones(B, dtype=torch.int32), key_start=starts, keys=3)):
+        y, h = layer.prompt(x(0), starts, residual=x(0) if residual else None, **prefix)
+        assert y.shape == (0, K) and y.dtype == torch.bfloat16 and made == []
+        assert h.shape == (0, K) if residual else h is None
