@@ -151,36 +151,176 @@ __device__ __forceinline__ uint64_t desc_mn(uint32_t saddr) {
     return umma::smem_desc(saddr, kTile * 128, 1024) | ((uint64_t)2 << 61);
 }
 
-// One row by a warp in the plain order, seen keys only: for rows whose result
-// is not finite.  A weight of 0 times a NaN or inf of an unseen key (a masked
-// place of the last key tiles) is the case that this mends.
+// the bits 15 and 31 of two bf16 values that are not finite
+__device__ __forceinline__ uint32_t not_finite(uint32_t w) { return ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u; }
+
+// Rows of a warp (its lanes `walk`) from the keys that each sees only, four together: eight lanes to a row, which take
+// every eighth 16 bytes of a key, staged eight keys at a time in the warp's 4 KB `buf`.  (Four lanes to a row are
+// faster here, but with the registers they need the kernel's own loop spills: 353 us for 344 at 8192 rows.)
+// `suspect`: the first key that holds something that is not finite; where some score has no softmax, nor has the row.
 template <int D>
-__device__ __noinline__ void row_again(const Args &a, int h, const uint16_t *qrow, int k0, int lim, uint16_t *orow) {
-    constexpr int E = D / 32;
-    const int lane = threadIdx.x & 31;
-    float qv[E], acc[E], m = -INFINITY, l = 0.0f;
+__device__ __noinline__ void rows_by_key(const Args &a, int hg, int q0, int k0, int off, int p, int g, int suspect, uint32_t walk, uint4 *buf) {
+    constexpr int kLanes = 8, C = D / (8 * kLanes), P = 4 * C;          // lanes to a row; their 16-byte pieces of it, pairs of values
+    constexpr int J = 8, L = J * D / 256;                               // keys at a time; a lane's loads of them
+    static_assert(2 * J * D * 2 <= kOutBytes / (kSoftmax / 32), "K and V of J keys in a warp's part");
+    const int lane = threadIdx.x & 31, part = lane % kLanes, h = hg / a.share;
+    const uint16_t *kc = a.k + (size_t)k0 * a.ldk + (size_t)h * D, *vc = a.v + (size_t)k0 * a.ldv + (size_t)h * D;
+    auto unpack = [](const uint4 &w, uint64_t *to) {
+        const uint32_t v[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-        qv[e] = bf16_bits_to_float(qrow[lane * E + e]);
-        acc[e] = 0.0f;
+        for (int i = 0; i < 4; ++i) to[i] = f2(__uint_as_float(v[i] << 16), __uint_as_float(v[i] & 0xFFFF0000u));
+    };
+    auto pairs = [&](const uint16_t *row, uint64_t (&to)[P]) {          // this lane's values of a row of D
+#pragma unroll
+        for (int i = 0; i < C; ++i) unpack(*reinterpret_cast<const uint4 *>(row + 8 * (kLanes * i + part)), to + 4 * i);
+    };
+    const float c = a.scale * 1.4426950408889634f;
+    auto score = [&](uint64_t s) {                                      // in log2 units
+        float v = lo32(s) + hi32(s);
+#pragma unroll
+        for (int x = 1; x < kLanes; x <<= 1) v += __shfl_xor_sync(0xffffffffu, v, x);
+        return v * c;
+    };
+    while (walk) {
+        int who = -1;                                                   // this row's lane in the mask, -1: none
+#pragma unroll
+        for (int r = 0; r < 32 / kLanes; ++r, walk &= walk - 1)
+            if (r == lane / kLanes && walk) who = __ffs(walk) - 1;
+        const int from = max(who, 0), pw = __shfl_sync(0xffffffffu, p, from), gw = __shfl_sync(0xffffffffu, g, from);
+        const int lim = who < 0 ? -1 : pw + off, most = __reduce_max_sync(0xffffffffu, lim);
+        const size_t hw = (size_t)(hg * a.G + gw) * D;
+        uint64_t q[P], acc[P];
+        pairs(a.q + (size_t)(q0 + pw) * a.ldq + hw, q);
+        float m = -INFINITY, l = 0.0f;
+        bool bad = false;
+        if (suspect <= most) {
+            uint64_t k[P], s = 0;
+            pairs(kc + (size_t)suspect * a.ldk, k);
+#pragma unroll
+            for (int i = 0; i < P; ++i) s = fma2(q[i], k[i], s);
+            bad = !(score(s) < INFINITY) && suspect <= lim;
+        }
+#pragma unroll
+        for (int i = 0; i < P; ++i) acc[i] = 0;
+        uint4 next[2][L];
+        auto fetch = [&](int j0) {                                      // (past the last key: that again, not used)
+#pragma unroll
+            for (int x = 0; x < L; ++x) {
+                const int it = x * 32 + lane, j = min(j0 + it / (D / 8), most), d = 8 * (it % (D / 8));
+                next[0][x] = *reinterpret_cast<const uint4 *>(kc + (size_t)j * a.ldk + d);
+                next[1][x] = *reinterpret_cast<const uint4 *>(vc + (size_t)j * a.ldv + d);
+            }
+        };
+        fetch(0);
+        for (int j0 = 0; j0 <= most && !__all_sync(0xffffffffu, bad || lim < j0); j0 += J) {
+            __syncwarp();
+#pragma unroll
+            for (int side = 0; side < 2; ++side)
+#pragma unroll
+                for (int x = 0; x < L; ++x) buf[side * (J * D / 8) + x * 32 + lane] = next[side][x];
+            __syncwarp();
+            fetch(j0 + J);
+            auto piece = [&](int side, int j, int i, uint64_t (&to)[4]) { unpack(buf[(side * J + j) * (D / 8) + kLanes * i + part], to); };
+            float s[J], m1 = m;
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                uint64_t two = 0;
+#pragma unroll
+                for (int i = 0; i < C; ++i) {
+                    uint64_t k[4];
+                    piece(0, j, i, k);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) two = fma2(q[4 * i + e], k[e], two);
+                }
+                s[j] = score(two);
+                if (j0 + j > lim) s[j] = -INFINITY;
+                bad |= !(s[j] < INFINITY);
+                m1 = fmaxf(m1, s[j]);
+            }
+            const float ref = m1 > -INFINITY ? m1 : 0.0f, f = ex2(m - ref);
+            m = m1;
+            l *= f;
+#pragma unroll
+            for (int i = 0; i < P; ++i) acc[i] = mul2(acc[i], f2(f, f));
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                if (j0 + j > lim) continue;                             // (0 times a NaN of an unseen key)
+                const float pj = ex2(s[j] - ref);
+                l += pj;
+#pragma unroll
+                for (int i = 0; i < C; ++i) {
+                    uint64_t v[4];
+                    piece(1, j, i, v);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[4 * i + e] = fma2(f2(pj, pj), v[e], acc[4 * i + e]);
+                }
+            }
+        }
+        if (who >= 0) {
+            const float inv = bad ? NAN : l == 0.0f ? 0.0f : 1.0f / l;
+            uint16_t *orow = a.o + (size_t)(q0 + pw) * a.ldo + hw + 8 * part;
+            auto out = [&](int i) { return pack_bf16(lo32(acc[i]) * inv, hi32(acc[i]) * inv); };
+#pragma unroll
+            for (int i = 0; i < C; ++i)
+                *reinterpret_cast<uint4 *>(orow + 8 * kLanes * i) = make_uint4(out(4 * i), out(4 * i + 1), out(4 * i + 2), out(4 * i + 3));
+        }
     }
-    for (int j = 0; j <= lim; ++j) {
-        const uint16_t *kr = a.k + (size_t)(k0 + j) * a.ldk + (size_t)h * D;
-        const uint16_t *vr = a.v + (size_t)(k0 + j) * a.ldv + (size_t)h * D;
-        float s = 0.0f;
+}
+
+// The rows `again` of a warp, whose results are not finite.  Three things make them so: the row sees such a value
+// and its result is right; a weight of 0 met a NaN or inf of an unseen key (a masked place of the last key
+// tiles); a score passed the reference by more than fp32 holds.  The last two are computed again.  The first is
+// told from them by one look at what the rows see, for all rows of the warp together: a NaN sum of weights comes
+// from a score, and a value of o from a seen V that is not finite in its dimension.  With every such row computed
+// again one NaN in an early row of V took 4096 rows from 0.10 ms to 100; it is 0.39, and 2.8 with a NaN half way, for
+// the rows before it in its own key tile.
+template <int D>
+__device__ __noinline__ void rows_again(const Args &a, int hg, int q0, int k0, int off, int p, int g, float l, uint32_t again) {
+    constexpr int C = D / 8, kKeys = 32 / C, kAhead = 8;                // lanes to a row, 16 bytes each; keys a load; loads
+    const int lane = threadIdx.x & 31, h = hg / a.share;
+    const size_t col = (size_t)h * D + 8 * (lane % C);
+    const uint16_t *kc = a.k + (size_t)k0 * a.ldk + col, *vc = a.v + (size_t)k0 * a.ldv + col;
+    auto at = [](const uint16_t *row) { return *reinterpret_cast<const uint4 *>(row); };
+    auto marks = [](const uint4 &w) { return make_uint4(not_finite(w.x), not_finite(w.y), not_finite(w.z), not_finite(w.w)); };
+    uint4 bad = make_uint4(0, 0, 0, 0);                                 // this lane's dimensions with such a value of V
+    uint32_t walk = 0;
+    int suspect = 0x7FFFFFFF, upto = 0;                                 // first such key of K; keys looked at
+    while (again) {                                                     // (rows further on see more)
+        const int who = __ffs(again) - 1;
+        again &= again - 1;
+        const int pw = __shfl_sync(0xffffffffu, p, who), gw = __shfl_sync(0xffffffffu, g, who), lim = pw + off;
+        const float lw = __shfl_sync(0xffffffffu, l, who);
+        if (lw == -1.0f) continue;                                      // (a score is NaN)
+        for (; upto <= lim; upto += kKeys * kAhead) {
+            uint4 kw[kAhead], vw[kAhead];
 #pragma unroll
-        for (int e = 0; e < E; ++e) s = fmaf(qv[e], bf16_bits_to_float(kr[lane * E + e]), s);
+            for (int i = 0; i < kAhead; ++i) {
+                const size_t j = min(upto + i * kKeys + lane / C, lim);
+                kw[i] = at(kc + j * a.ldk);
+                vw[i] = at(vc + j * a.ldv);
+            }
 #pragma unroll
-        for (int x = 16; x >= 1; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-        s *= a.scale;
-        const float m1 = fmaxf(m, s), ref = m1 > -INFINITY ? m1 : 0.0f, f = expf(m - ref), p = expf(s - ref);
-        m = m1;
-        l = l * f + p;
+            for (int i = 0; i < kAhead; ++i) {
+                const uint4 k = marks(kw[i]), v = marks(vw[i]);
+                if (k.x | k.y | k.z | k.w) suspect = min(suspect, min(upto + i * kKeys + lane / C, lim));
+                bad = make_uint4(bad.x | v.x, bad.y | v.y, bad.z | v.z, bad.w | v.w);
+            }
+        }
+        upto = lim + 1;
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = fmaf(p, bf16_bits_to_float(vr[lane * E + e]), acc[e] * f);
+        for (int o = C; o < 32; o <<= 1) {
+            bad.x |= __shfl_xor_sync(0xffffffffu, bad.x, o), bad.y |= __shfl_xor_sync(0xffffffffu, bad.y, o);
+            bad.z |= __shfl_xor_sync(0xffffffffu, bad.z, o), bad.w |= __shfl_xor_sync(0xffffffffu, bad.w, o);
+        }
+        const uint4 r = marks(at(a.o + (size_t)(q0 + pw) * a.ldo + (size_t)(hg * a.G + gw) * D + 8 * (lane % C)));
+        const bool other = !(lw > 0.0f && lw < INFINITY) || ((r.x & ~bad.x) | (r.y & ~bad.y) | (r.z & ~bad.z) | (r.w & ~bad.w));
+        if (__any_sync(0xffffffffu, other)) walk |= 1u << who;
     }
-#pragma unroll
-    for (int e = 0; e < E; ++e) orow[lane * E + e] = float_to_bf16_bits(l == 0.0f ? 0.0f : acc[e] / l);
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *so = smem_raw + ((1024u - (umma::smem_addr(smem_raw) & 1023u)) & 1023u) + (2 + ring<D>()) * tile_bytes<D>();
+    if (walk)
+        rows_by_key<D>(a, hg, q0, k0, off, p, g, __reduce_min_sync(0xffffffffu, suspect), walk,
+                       reinterpret_cast<uint4 *>(so + (threadIdx.x >> 5) * (32 * 128)));
 }
 
 template <int D>
@@ -547,6 +687,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const size_t at = (size_t)(q0 + p) * a.ldo + (size_t)(h * G + g) * D;     // this row's place in o
             const float inv = lim >= 0 ? 1.0f / l : 0.0f;
             const uint64_t inv2 = f2(inv, inv);
+            if (l != l && m < INFINITY) l = -1.0f;                      // a score is NaN, and so is all of the row
             const uint32_t keep = lim >= 0 ? 0xFFFFFFFFu : 0u;
             uint64_t zero = 0;                                          // NaN from where some value is not finite
             const uint32_t inside = __ballot_sync(0xffffffffu, in);
@@ -584,15 +725,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
             }
             const bool fine = lim < 0 || (l > 0.0f && l < INFINITY && lo32(zero) + hi32(zero) == 0.0f);
-            uint32_t again = __ballot_sync(0xffffffffu, in && !fine);
-            while (again) {
-                const int who = __ffs(again) - 1;
-                again &= again - 1;
-                const int pw = __shfl_sync(0xffffffffu, p, who), gw = __shfl_sync(0xffffffffu, g, who);
-                const size_t hw = (size_t)(h * G + gw) * D;
-                __syncwarp();
-                row_again<D>(a, h / a.share, a.q + (size_t)(q0 + pw) * a.ldq + hw, k0, pw + off, a.o + (size_t)(q0 + pw) * a.ldo + hw);
-            }
+            const uint32_t again = __ballot_sync(0xffffffffu, in && !fine);
+            if (again) rows_again<D>(a, h, q0, k0, off, p, g, l, again);
         }
       }
     }
