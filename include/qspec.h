@@ -520,6 +520,24 @@ int qspec_debug_linear_bounded(int kernel, const uint16_t *x_bf16, const uint8_t
                                int K, uint16_t *y_bf16, int ldy, uint32_t wait_limit, int stall,
                                int32_t *dev_status, qspec_stream_t stream);
 
+/*
+ * The same for the two attention kernels: the arguments of qspec_attn_kv4 and
+ * qspec_attn_prompt with a bound on the barrier waits (at least 1, else
+ * QSPEC_ERR_SHAPE) and `stall`, which makes the warp that issues the score
+ * products wait for what never comes.  After a timeout the outputs of that
+ * call are unspecified; qspec_attn_kv4's workspace is ready for the next call.
+ */
+int qspec_debug_attn_kv4_bounded(const uint16_t *q_bf16, int ldq, const uint8_t *k_codes, const uint32_t *k_sz,
+                                 const uint8_t *v_codes, const uint32_t *v_sz, const int32_t *len, int B, int R,
+                                 int Hq, int H, int T, int D, float scale, uint16_t *o_bf16, int ldo,
+                                 void *workspace, size_t ws_bytes, uint32_t wait_limit, int stall,
+                                 int32_t *dev_status, qspec_stream_t stream);
+int qspec_debug_attn_prompt_bounded(const uint16_t *q_bf16, int ldq, const uint16_t *k_bf16, int ldk,
+                                    const uint16_t *v_bf16, int ldv, const int32_t *q_start,
+                                    const int32_t *k_start, int q_rows, int k_rows, int B, int Hq, int H, int D,
+                                    float scale, uint16_t *o_bf16, int ldo, uint32_t wait_limit, int stall,
+                                    int32_t *dev_status, qspec_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

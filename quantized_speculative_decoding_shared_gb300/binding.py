@@ -39,7 +39,8 @@ EXPORTED = ["qspec_version", "qspec_status_string", "qspec_last_cuda_error", "qs
             "qspec_draft_sample", "qspec_debug_linear_bounded", "qspec_quant_weights_fp8",
             "qspec_quant_act_fp8", "qspec_linear_fp8", "qspec_linear_w4a16_kv",
             "qspec_rmsnorm_fp8", "qspec_kv4_append", "qspec_kv4_load", "qspec_attn_kv4_workspace_bytes",
-            "qspec_attn_kv4", "qspec_attn_prompt"]
+            "qspec_attn_kv4", "qspec_attn_prompt", "qspec_debug_attn_kv4_bounded",
+            "qspec_debug_attn_prompt_bounded"]
 KERNEL_W4A16_TC, KERNEL_W4A4_GEMV_TC, KERNEL_W4A4_TC = 0, 1, 2
 NOALLOC_SCRATCH_BYTES = 1 << 20
 
@@ -109,6 +110,10 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
                                 vp, vp], i32),
             "qspec_attn_prompt": ([vp, i32, vp, i32, vp, i32, vp, vp, i32, i32, i32, i32, i32, i32, f32, vp, i32,
                                    vp, vp], i32),
+            "qspec_debug_attn_kv4_bounded": ([vp, i32, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, f32, vp, i32,
+                                              vp, sz_t, ctypes.c_uint32, i32, vp, vp], i32),
+            "qspec_debug_attn_prompt_bounded": ([vp, i32, vp, i32, vp, i32, vp, vp, i32, i32, i32, i32, i32, i32, f32,
+                                                 vp, i32, ctypes.c_uint32, i32, vp, vp], i32),
         }
         for name, (args, res) in proto.items():
             f = getattr(lib, name)
@@ -328,6 +333,20 @@ def qspec_attn_prompt(q, ldq, k, ldk, v, ldv, q_start, k_start, q_rows, k_rows, 
     return load_library().qspec_attn_prompt(_ptr(q), ldq, _ptr(k), ldk, _ptr(v), ldv, _ptr(q_start),
                                             _ptr(k_start), q_rows, k_rows, B, Hq, H, D, scale, _ptr(o), ldo,
                                             _ptr(dev_status), _stream(stream))
+
+
+def qspec_debug_attn_kv4_bounded(q, ldq, k_codes, k_sz, v_codes, v_sz, length, B, R, Hq, H, T, D, scale, o, ldo,
+                                 workspace, ws_bytes, wait_limit, stall, dev_status=None, stream=None):
+    return load_library().qspec_debug_attn_kv4_bounded(
+        _ptr(q), ldq, _ptr(k_codes), _ptr(k_sz), _ptr(v_codes), _ptr(v_sz), _ptr(length), B, R, Hq, H, T, D, scale,
+        _ptr(o), ldo, _ptr(workspace), ws_bytes, wait_limit, stall, _ptr(dev_status), _stream(stream))
+
+
+def qspec_debug_attn_prompt_bounded(q, ldq, k, ldk, v, ldv, q_start, k_start, q_rows, k_rows, B, Hq, H, D, scale, o,
+                                    ldo, wait_limit, stall, dev_status=None, stream=None):
+    return load_library().qspec_debug_attn_prompt_bounded(
+        _ptr(q), ldq, _ptr(k), ldk, _ptr(v), ldv, _ptr(q_start), _ptr(k_start), q_rows, k_rows, B, Hq, H, D, scale,
+        _ptr(o), ldo, wait_limit, stall, _ptr(dev_status), _stream(stream))
 
 
 # ---------------------------------------------------------------------------

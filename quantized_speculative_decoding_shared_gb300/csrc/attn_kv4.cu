@@ -250,7 +250,7 @@ __device__ __noinline__ float plain_row(const Args &a, const uint16_t *qrow, siz
 template <int D, int N>
 __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
     attn_kv4_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
-                    const __grid_constant__ Args a, uint32_t wait_limit) {
+                    const __grid_constant__ Args a, uint32_t wait_limit, int stall) {
     constexpr int kSide = side_bytes<D>(), kP = p_bytes<N>(), kStages = Cfg<N>::kStages;
     constexpr int kGroups = Cfg<N>::kGroups, kWorkWarps = Cfg<N>::kWorkWarps, kWork = Cfg<N>::kWork;
     constexpr int kScoreWarp = Cfg<N>::kScoreWarp, kValueWarp = Cfg<N>::kValueWarp, kLoadWarp = Cfg<N>::kLoadWarp, kTellWarp = Cfg<N>::kTellWarp;
@@ -443,7 +443,11 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
             const int n_t = min(nt_task - tile, end - at), h = task / a.blocks;
             for (int i = 0; i < n_t && ok; ++i) {
                 const int s = loads % kStages;
-                if (!(ok = all(loads < kStages || wait(&sm.empty[s], loads / kStages + 1)))) break;
+                // (after a timeout the groups free stages that they did not wait for: a copy more would meet a barrier
+                // that still counts the last one; who frees a stage so has set the flag before)
+                if (!(ok = all(loads < kStages ||
+                               (wait(&sm.empty[s], loads / kStages + 1) && !*reinterpret_cast<volatile int *>(&sm.timeout)))))
+                    break;
                 if (lane == 0) {
                     umma::mbar_arrive_expect_tx(&sm.full[s], 2 * kSide);
                     umma::tma_load_3d(codes + s * 2 * kSide, &tk, 0, (tile + i) * kTok, b * a.H + h, &sm.full[s]);
@@ -490,7 +494,7 @@ __global__ void __launch_bounds__(Cfg<N>::kThreads, 1)
         constexpr uint32_t id = umma::instr_desc(0, 0, kTok, N);                            // f16, f32 sums
         const uint64_t qd = umma::smem_desc(umma::smem_addr(sq), N * 16, 128);
         int g = 0;
-        bool ok = true;
+        bool ok = !stall || all(wait(&sm.drain[0], 0));             // (tests: nothing arrives there before the end)
         for (int seg = 0; at < end; ++seg) {
             const int n_t = min(nt_task - tile, end - at);
             ok = all(ok && wait(&sm.qfull, seg));
@@ -984,7 +988,7 @@ constexpr size_t kCountBytes = kMaxCtas * sizeof(int);
 constexpr size_t kPartBytes = (size_t)kMaxCtas * 2 * kMaxN * (kMaxD + 1) * sizeof(float);
 
 template <int D, int N>
-int launch(Args a, cudaStream_t stream) {
+int launch(Args a, cudaStream_t stream, uint32_t wait_limit, int stall) {
     a.blocks = (a.R * a.G + N - 1) / N;
     CUtensorMap tk, tv;
     if (code_tmap(&tk, a.kc, D / 2, a.T, a.B * a.H, kTok) || code_tmap(&tv, a.vc, D / 2, a.T, a.B * a.H, kTok))
@@ -994,16 +998,17 @@ int launch(Args a, cudaStream_t stream) {
     if (rc) return rc;
     const long long most = (long long)a.B * a.H * a.blocks * std::max(1, (a.T + kTok - 1) / kTok);   // tiles at full lengths
     const unsigned grid = (unsigned)std::min<long long>(std::min(sm_count(), kMaxCtas), most);
-    return launch_pdl("qspec_attn_kv4", kern, dim3(grid), dim3(Cfg<N>::kThreads), smem_bytes<D, N>(), stream, tk, tv, a, kWaitLimit);
+    return launch_pdl("qspec_attn_kv4", kern, dim3(grid), dim3(Cfg<N>::kThreads), smem_bytes<D, N>(), stream, tk, tv, a,
+                      wait_limit, stall);
 }
 
 // rows per pass: the fewest passes over the cache, then the narrowest that holds them
 template <int D>
-int dispatch(const Args &a, cudaStream_t stream) {
+int dispatch(const Args &a, cudaStream_t stream, uint32_t wait_limit, int stall) {
     const int rows = a.R * a.G, passes = (rows + kMaxN - 1) / kMaxN, each = (rows + passes - 1) / passes;
-    if (each <= 16) return launch<D, 16>(a, stream);
-    if (each <= 32) return launch<D, 32>(a, stream);
-    return launch<D, 64>(a, stream);
+    if (each <= 16) return launch<D, 16>(a, stream, wait_limit, stall);
+    if (each <= 32) return launch<D, 32>(a, stream, wait_limit, stall);
+    return launch<D, 64>(a, stream, wait_limit, stall);
 }
 
 }  // namespace akv
@@ -1019,13 +1024,14 @@ extern "C" size_t qspec_attn_kv4_workspace_bytes(int B, int R, int Hq, int H, in
     return akv::sizes_ok(B, R, Hq, H, D) ? akv::kCountBytes + akv::kPartBytes : 0;
 }
 
-extern "C" int qspec_attn_kv4(const uint16_t *q_bf16, int ldq, const uint8_t *k_codes, const uint32_t *k_sz,
-                              const uint8_t *v_codes, const uint32_t *v_sz, const int32_t *len, int B, int R, int Hq,
-                              int H, int T, int D, float scale, uint16_t *o_bf16, int ldo, void *workspace,
-                              size_t ws_bytes, int32_t *dev_status, qspec_stream_t stream) {
+extern "C" int qspec_debug_attn_kv4_bounded(const uint16_t *q_bf16, int ldq, const uint8_t *k_codes, const uint32_t *k_sz,
+                                            const uint8_t *v_codes, const uint32_t *v_sz, const int32_t *len, int B, int R,
+                                            int Hq, int H, int T, int D, float scale, uint16_t *o_bf16, int ldo,
+                                            void *workspace, size_t ws_bytes, uint32_t wait_limit, int stall,
+                                            int32_t *dev_status, qspec_stream_t stream) {
     if (!q_bf16 || !k_codes || !k_sz || !v_codes || !v_sz || !len || !o_bf16 || !workspace) return QSPEC_ERR_NULL;
     if (!akv::sizes_ok(B, R, Hq, H, D) || T < 1 || T > (1 << 30) || (long long)B * H >= (1LL << 31) ||
-        !std::isfinite(scale) || ldq < (long long)Hq * D || ldo < (long long)Hq * D)
+        !std::isfinite(scale) || ldq < (long long)Hq * D || ldo < (long long)Hq * D || wait_limit < 1)
         return QSPEC_ERR_SHAPE;
     // tiles of all tasks, the empty ones in front of each counted, are 32-bit numbers in the kernel
     const long long passes = (R * (long long)(Hq / H) + akv::kMaxN - 1) / akv::kMaxN;
@@ -1039,5 +1045,14 @@ extern "C" int qspec_attn_kv4(const uint16_t *q_bf16, int ldq, const uint8_t *k_
     const akv::Args a{q_bf16, k_codes, v_codes, k_sz, v_sz, len, o_bf16, dev_status, reinterpret_cast<int *>(workspace),
                       reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + akv::kCountBytes), ldq, ldo, B, R,
                       Hq / H, H, T, 1, Hq == H ? 0u : (uint32_t)((1ull << 32) / (Hq / H) + 1), scale};
-    return D == 128 ? akv::dispatch<128>(a, as_cuda(stream)) : akv::dispatch<64>(a, as_cuda(stream));
+    return D == 128 ? akv::dispatch<128>(a, as_cuda(stream), wait_limit, stall)
+                    : akv::dispatch<64>(a, as_cuda(stream), wait_limit, stall);
+}
+
+extern "C" int qspec_attn_kv4(const uint16_t *q_bf16, int ldq, const uint8_t *k_codes, const uint32_t *k_sz,
+                              const uint8_t *v_codes, const uint32_t *v_sz, const int32_t *len, int B, int R, int Hq,
+                              int H, int T, int D, float scale, uint16_t *o_bf16, int ldo, void *workspace,
+                              size_t ws_bytes, int32_t *dev_status, qspec_stream_t stream) {
+    return qspec_debug_attn_kv4_bounded(q_bf16, ldq, k_codes, k_sz, v_codes, v_sz, len, B, R, Hq, H, T, D, scale, o_bf16,
+                                        ldo, workspace, ws_bytes, kWaitLimit, 0, dev_status, stream);
 }

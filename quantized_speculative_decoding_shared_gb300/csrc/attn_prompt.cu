@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     attn_prompt_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                        const __grid_constant__ CUtensorMap tv,
                        const __grid_constant__ Args a,
-                       uint32_t wait_limit) {
+                       uint32_t wait_limit, int stall) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     constexpr int kT = tile_bytes<D>(), NS = ring<D>();
     // (an offset, not a rounded address: the compiler keeps seeing shared memory)
@@ -520,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // descriptors were moved to uniform registers product by product (494 us for 427 at 8192 tokens)
             elected = umma::elect_one();
             int at = 0, seen[2] = {0, 0}, units[2] = {0, 0};            // copies used; key tiles and units of each row tile
-            bool ok = true;
+            bool ok = !stall || all(wait(&sm.drain, 0));                // (tests: nothing arrives there before the end)
             for (int k = 0; ok; ++k) {
                 if (!(ok = all(wait(&sm.ufull[k & 1], k >> 1)))) break;
                 const int n = sm.unit[k & 1].n, nt = tiles(sm.unit[k & 1]);
@@ -753,7 +753,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <int D>
-int launch(const Args &a, cudaStream_t stream) {
+int launch(const Args &a, cudaStream_t stream, uint32_t wait_limit, int stall) {
     const long long units = (long long)a.q_rows / (kTile / a.G) + a.B;      // at most, of one tile
     if (units * a.H >= (1LL << 31)) return QSPEC_ERR_SHAPE;
     // no key rows: no copy is issued, and the maps only have to be valid
@@ -769,7 +769,7 @@ int launch(const Args &a, cudaStream_t stream) {
     int rc = smem_limit_once(reinterpret_cast<const void *>(kern), (int)smem_total<D>());
     if (rc) return rc;
     return launch_pdl("qspec_attn_prompt", kern, dim3((unsigned)std::min<long long>(sm_count(), units * a.H)), dim3(kThreads), smem_total<D>(), stream, tq,
-                      tk, tv, a, kWaitLimit);
+                      tk, tv, a, wait_limit, stall);
 }
 
 }  // namespace apr
@@ -780,15 +780,16 @@ int launch(const Args &a, cudaStream_t stream) {
 
 using namespace qspec;
 
-extern "C" int qspec_attn_prompt(const uint16_t *q_bf16, int ldq, const uint16_t *k_bf16, int ldk,
-                                 const uint16_t *v_bf16, int ldv, const int32_t *q_start, const int32_t *k_start,
-                                 int q_rows, int k_rows, int B, int Hq, int H, int D, float scale, uint16_t *o_bf16,
-                                 int ldo, int32_t *dev_status, qspec_stream_t stream) {
+extern "C" int qspec_debug_attn_prompt_bounded(const uint16_t *q_bf16, int ldq, const uint16_t *k_bf16, int ldk,
+                                               const uint16_t *v_bf16, int ldv, const int32_t *q_start,
+                                               const int32_t *k_start, int q_rows, int k_rows, int B, int Hq, int H, int D,
+                                               float scale, uint16_t *o_bf16, int ldo, uint32_t wait_limit, int stall,
+                                               int32_t *dev_status, qspec_stream_t stream) {
     if (!q_start || !k_start || (q_rows > 0 && (!q_bf16 || !o_bf16)) || (k_rows > 0 && (!k_bf16 || !v_bf16)))
         return QSPEC_ERR_NULL;
     if (q_rows < 0 || k_rows < 0 || B < 1 || H < 1 || Hq < H || Hq % H || Hq > 65535 || (D != 64 && D != 128) ||
         !std::isfinite(scale) || ldq < (long long)Hq * D || ldo < (long long)Hq * D || ldk < (long long)H * D ||
-        ldv < (long long)H * D)
+        ldv < (long long)H * D || wait_limit < 1)
         return QSPEC_ERR_SHAPE;
     if ((ldq | ldk | ldv | ldo) % 8 || !aligned(q_bf16, 16) || !aligned(k_bf16, 16) || !aligned(v_bf16, 16) ||
         !aligned(o_bf16, 16) || !aligned(q_start, 4) || !aligned(k_start, 4))
@@ -801,5 +802,14 @@ extern "C" int qspec_attn_prompt(const uint16_t *q_bf16, int ldq, const uint16_t
     G /= share;
     const apr::Args a{q_bf16, k_bf16, v_bf16, q_start, k_start, o_bf16, dev_status, ldq, ldk, ldv, ldo, q_rows, k_rows, B,
                       H * share, G, share, G == 1 ? 0u : (uint32_t)((1ull << 32) / G + 1), scale};
-    return D == 128 ? apr::launch<128>(a, as_cuda(stream)) : apr::launch<64>(a, as_cuda(stream));
+    return D == 128 ? apr::launch<128>(a, as_cuda(stream), wait_limit, stall)
+                    : apr::launch<64>(a, as_cuda(stream), wait_limit, stall);
+}
+
+extern "C" int qspec_attn_prompt(const uint16_t *q_bf16, int ldq, const uint16_t *k_bf16, int ldk,
+                                 const uint16_t *v_bf16, int ldv, const int32_t *q_start, const int32_t *k_start,
+                                 int q_rows, int k_rows, int B, int Hq, int H, int D, float scale, uint16_t *o_bf16,
+                                 int ldo, int32_t *dev_status, qspec_stream_t stream) {
+    return qspec_debug_attn_prompt_bounded(q_bf16, ldq, k_bf16, ldk, v_bf16, ldv, q_start, k_start, q_rows, k_rows, B, Hq,
+                                           H, D, scale, o_bf16, ldo, kWaitLimit, 0, dev_status, stream);
 }
