@@ -10,7 +10,8 @@
 //   S_t = Q_t K^T (tcgen05, both operands in shared memory, S in tensor memory),
 //   the softmax warps of t read S_t (thread = row) and write p = 2^(c s - m) as
 //   bf16 over S_t in tensor memory, in two halves, and keep the sum l,
-//   O_t += P_t V (P from tensor memory, V rows as they are: an MN-major operand).
+//   O_t += P_t V (P from tensor memory, V rows as they are: an MN-major operand).  P is
+//   bf16 because V is (a product takes one type); its sum l is of the fp32 weights.
 // The issuing lane interleaves the two tiles, so one tile's softmax runs under
 // the other's products.
 // The reference m is the row's maximum over the first key tile and after that follows
@@ -32,9 +33,9 @@
 // operations costs more than it hides (8192 tokens, 342 us as it is): waits
 // that spin 398, weights handed over in three parts 374, two warpgroups to a row
 // tile 408; with the exponentials left out it was as long.  8192 tokens, 8 KV heads
-// of 128 with 4 heads each: 342 to 359 us from one GPU to another, up to 1607 TFLOP/s
-// counting what the mask leaves; 7 sequences of 5003 tokens, 4 KV heads with 7 each:
-// 51.4 us; 3 of 301: 7.5 us.
+// of 128 with 4 heads each: 365 to 373 us a call with new inputs, 342 to 359 in a
+// captured graph (from one GPU to another), that is 1480 to 1607 TFLOP/s counting what
+// the mask leaves; 7 sequences of 5003 tokens, 4 KV heads with 7 each: 50 us; 3 of 301: 7.5 us.
 #include <algorithm>
 #include <cmath>
 

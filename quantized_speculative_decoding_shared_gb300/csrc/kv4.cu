@@ -3,18 +3,22 @@
 // Per (row, head): lo = min(0, min x), hi = max(0, max x), s = fp16((hi - lo) / 15),
 // z = clamp(rint(-lo / s), 0, 15), code = clamp(rint(x / s) + z, 0, 15); 0 is in the
 // range, so it keeps an exact code.  The quotient x / s is one Newton step
-// from q0 = x y, y = 1 / s: fma(fma(-q0, s, x), y, q0).  x has 8 significant bits
-// and s 11, so x / s is either a half-integer exactly (then the step returns
-// it exactly) or at least 2^-10 from one for |x / s| < 16 (far beyond the
-// step's error): rint gives what the IEEE quotient gives.
+// from q0 = x y, y = 1 / s: fma(fma(-q0, s, x), y, q0).  x = X 2^a has 8 significant
+// bits and s = S 2^b 11, so x / s is either a half-integer exactly (then the step
+// returns it exactly) or at least 1 / 4094 from one, that is |2 X 2^a - (2 n + 1) S 2^b| / (2 S 2^b)
+// at its least (S = 2047, a = b + 3; over all X, S and a - b).  The step is off by some
+// 2^-19 where |x / s| < 32: rint gives what the IEEE quotient gives.  Quotients of 16 and more
+// come with scales that are fp16 subnormals only, and end at the clamp.
 //
 // Streaming: 2 D bytes of a head row against D / 2 + 4 of the cache.  Long prompts
-// come to HBM's rate on the way out and to the instructions issued on the way in
-// (32764 rows of 8 heads of 128: load 6.2 TB/s, append 4.6).  A warp takes one head of R
-// consecutive rows of K and of V, L = D / 8 lanes to a head row, 16 bytes (8 values)
-// to a lane and kRounds rows one after another: its codes and its scale words are
-// then runs of positions in the cache, the rows are looked up once, and the loads
-// of all rounds are in flight together.
+// come to HBM's rate on the way out (32764 rows of 8 heads of 128: load 6.2 TB/s,
+// append 4.6).  At 8191 rows (11.7 us in, 8.9 out) neither the issue slots (65 % used in
+// append) nor DRAM (28 %) is the bound but the way through a short-lived warp: a
+// search and its loads' latency in front of four head rows.  A warp takes one head
+// of R consecutive rows of K and of V, L = D / 8 lanes to a head row, 16 bytes (8
+// values) to a lane and kRounds rows one after another: its codes and its scale
+// words are then runs of positions in the cache, the rows are looked up once, and
+// the loads of all rounds are in flight together.
 #include <algorithm>
 #include <climits>
 #include <cuda_fp16.h>
@@ -196,7 +200,7 @@ __device__ __forceinline__ uint32_t quantise(const uint4 &v, uint32_t &word, boo
 
 // A warp's rounds with their rows' places.  Where all R rows lie one after another in
 // one sequence (nearly always in a prompt) the places are steps from the first,
-// so the addresses are too (the instructions issued are what bounds these kernels).
+// so the addresses are too (fewer instructions: 22.6 -> 20.0 us for 8191 rows in and out).
 template <int D, class F>
 __device__ __forceinline__ void one_run(const Part<D> &p, long long found, F rounds) {
     const int lane = threadIdx.x & 31;

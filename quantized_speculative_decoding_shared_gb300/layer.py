@@ -10,8 +10,9 @@ A prompt's rows attend each other in bf16, as the projection wrote them; the
 rows of a later prompt of the same sequences (a prefix in the cache) attend
 the cache's entries, read back by kv4_load.  A draft step is one row per
 sequence, a verify pass gamma + 1 rows whose entries overwrite the draft's
-(both from position `base`).  Rotary positions and the other half of the layer
-are the caller's.  ``python -m quantized_speculative_decoding_shared_gb300.layer``
+(both from position `base`).  The class holds no rotary positions and no biases: a
+model that has them makes the same calls, with its own step between the projection
+and kv4_append.  ``python -m quantized_speculative_decoding_shared_gb300.layer``
 runs prompts, draft steps and a verify pass on seeded inputs.
 """
 from __future__ import annotations

@@ -6,11 +6,11 @@ one verify pass in the W4A16 configuration over the gamma + 1 candidate rows
 of every sequence (M = B (gamma + 1)), the acceptance decision, and the
 overwrite of the accepted rows' KV-cache entries with the verify pass's.
 
-The model operations between the linears (attention, norms, activation
-functions, embeddings) are outside this library, so every linear reads its
-own seeded activations and the verification reads seeded target / draft
-logits: the round issues exactly the hot-path calls of a real round, on
-inputs of the real shapes.  All buffers are allocated once here; `run`
+The model operations between the linears (attention and norms, which
+`layer.py` runs; activation functions and embeddings, which this library does
+not have) are no part of it, so every linear reads its own seeded activations
+and the verification reads seeded target / draft logits: the round issues
+exactly the hot-path calls of a real round, on inputs of the real shapes.  All buffers are allocated once here; `run`
 only launches kernels (through the C ABI), so a round can be captured into
 a CUDA graph and replayed, with the round id (the verification's random
 stream) fixed per captured graph.
