@@ -174,3 +174,20 @@ def test_outputs_are_memory_of_the_given_stream(name, kind):
 
     got = on_a_busy_device(fills_then_call)
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("kind", ["zero", "legacy", "per thread", "default", "external"])
+def test_other_ways_to_name_a_stream(kind):
+    """The default stream by its handles and as an object, a thread's own stream, a handle wrapped as a stream."""
+    dev = need_gpu()
+    own = torch.cuda.Stream()
+    arg = {"zero": 0, "legacy": 1, "per thread": 2, "default": torch.cuda.default_stream(),
+           "external": torch.cuda.ExternalStream(own.cuda_stream)}[kind]
+    call = calls(dev)
+    for name in ("rmsnorm_fp8", "kv4_load", "attn_kv4"):
+        want = call[name]()
+        torch.cuda.synchronize()
+        got = call[name](stream=arg)
+        torch.cuda.synchronize()
+        for a, b in zip(*(t if isinstance(t, tuple) else (t,) for t in (got, want))):
+            assert torch.equal(a, b), name
