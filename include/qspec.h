@@ -491,6 +491,85 @@ int qspec_attn_prompt(const uint16_t *q_bf16, int ldq, const uint16_t *k_bf16, i
                       int q_rows, int k_rows, int B, int Hq, int H, int D, float scale,
                       uint16_t *o_bf16, int ldo, int32_t *dev_status, qspec_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * The feed-forward half of a decoder layer in E4M3 with a scale for each block
+ * of 128: an activation's scale belongs to one token and 128 values, a weight's
+ * to 128 x 128.  A block's scale is known as soon as its own values are, so the
+ * gated product quantises its output itself, which a scale per token (all of
+ * the output channels) does not allow.
+ *
+ *   xq uint8 [M][K]                      E4M3 codes of activations
+ *   sa float [K / 128][lds]              their scales: block g of token m at
+ *                                        g lds + m (lds >= M; nothing is read or
+ *                                        written past token M - 1)
+ *   w8 uint8 [N][K]                      E4M3 codes of weights
+ *   sw float [ceil(N / 128)][K / 128]    their scales
+ * K is a multiple of 128.  E4M3 and its rounding are those of the Q8 variant.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * The quantisers.  Per block s = amax / 448 (fp32, IEEE division), code =
+ * E4M3(v / s) (fp32 IEEE quotient); a block of zeros gives s = 0 and codes 0.
+ * Every bit is fixed.
+ *   w_fp16 uint16 [N][K] fp16 bits (16-byte aligned), w8 8-byte aligned; N >= 1
+ *     (the last blocks may hold fewer than 128 rows).
+ *   x_bf16 uint16 [M][ldx] (ldx >= K, ldx % 8 == 0, 16-byte aligned), xq 8-byte
+ *     aligned.
+ * Device errors: QSPEC_ERR_NONFINITE (a NaN or inf input: that block's scale is
+ * not finite either).
+ */
+int qspec_quant_weights_fp8_block(const uint16_t *w_fp16, int N, int K, uint8_t *w8, float *sw,
+                                  int32_t *dev_status, qspec_stream_t stream);
+int qspec_quant_act_fp8_block(const uint16_t *x_bf16, int M, int K, int ldx, uint8_t *xq, float *sa,
+                              int lds, int32_t *dev_status, qspec_stream_t stream);
+
+/*
+ * qspec_rmsnorm_fp8 with a scale for each block: h, y and every argument but sa
+ * and lds as there; per token m and block g of K
+ *   sa[g lds + m] = max |y| / 448 over the block, xq = E4M3(y / sa)
+ * (a block of zeros: sa = 0, codes 0), in fp32, y rounded once.  Device errors:
+ * QSPEC_ERR_NONFINITE as there.
+ */
+int qspec_rmsnorm_fp8_block(const uint16_t *x_bf16, int ldx, const uint16_t *res_bf16, int ldr,
+                            const uint16_t *w_bf16, float eps, int M, int K, uint16_t *h_bf16, int ldh,
+                            uint8_t *xq, float *sa, int lds, uint16_t *y_bf16, int ldy, int32_t *dev_status,
+                            qspec_stream_t stream);
+
+/*
+ * The linear on the tensor cores:
+ *   y[m][n] = bf16(sum_g sa[g][m] sw[n / 128][g] sum_{k in block g} E4M3(xq[m][k]) E4M3(w8[n][k]))
+ * each block's products summed by the tensor cores in fp32, the scaled sums added in
+ * fp32, rounded once.
+ *   y_bf16 uint16 [M][ldy] out (ldy >= N); xq, w8 16-byte aligned
+ * 1 <= M <= 2^22, 1 <= N <= 2^30.  Device errors: QSPEC_ERR_TIMEOUT (a bounded
+ * wait expired; the outputs are unspecified).
+ */
+int qspec_linear_fp8_block(const uint8_t *xq, const float *sa, int lds, const uint8_t *w8, const float *sw,
+                           int M, int N, int K, uint16_t *y_bf16, int ldy, int32_t *dev_status,
+                           qspec_stream_t stream);
+
+/*
+ * The gated product: gate and up projection, SiLU, product and quantisation in
+ * one kernel.  g and u are the sums of qspec_linear_fp8_block with the two sets
+ * of weights, not rounded:
+ *   h = g / (1 + exp(-g)) u                               (fp32)
+ *   sh[j ldh + m] = max |h| / 448 over channels 128 j .. 128 j + 127 of token m
+ *   hq = E4M3(h / sh)                                     (a block of zeros: 0)
+ * so that hq and sh are the xq and sa of the next qspec_linear_fp8_block (the down
+ * projection), h rounded once; and / or h in bf16, for a W4A16 linear.
+ *
+ *   w_gate, w_up uint8 [N][K], s_gate, s_up float [N / 128][K / 128]
+ *   hq    uint8  [M][N], sh float [N / 128][ldh]   out, nullable together (ldh >= M)
+ *   h_bf16 uint16 [M][ldy]                         out, nullable (ldy >= N)
+ * At least one output.  N and K multiples of 128, M <= 2^22, N <= 2^30; codes
+ * 16-byte aligned.  Device errors: QSPEC_ERR_NONFINITE (an h that is not finite,
+ * in bf16 where that output is asked for), QSPEC_ERR_TIMEOUT.
+ */
+int qspec_gated_fp8_block(const uint8_t *xq, const float *sa, int lds, const uint8_t *w_gate,
+                          const float *s_gate, const uint8_t *w_up, const float *s_up, int M, int N, int K,
+                          uint8_t *hq, float *sh, int ldh, uint16_t *h_bf16, int ldy, int32_t *dev_status,
+                          qspec_stream_t stream);
+
 /*
  * Diagnostic for tests of the bounded waits; the pages have no counterpart.
  * Runs one of the library's tensor-core linear kernels on the same arguments

@@ -40,7 +40,8 @@ EXPORTED = ["qspec_version", "qspec_status_string", "qspec_last_cuda_error", "qs
             "qspec_quant_act_fp8", "qspec_linear_fp8", "qspec_linear_w4a16_kv",
             "qspec_rmsnorm_fp8", "qspec_kv4_append", "qspec_kv4_load", "qspec_attn_kv4_workspace_bytes",
             "qspec_attn_kv4", "qspec_attn_prompt", "qspec_debug_attn_kv4_bounded",
-            "qspec_debug_attn_prompt_bounded"]
+            "qspec_debug_attn_prompt_bounded", "qspec_quant_weights_fp8_block", "qspec_quant_act_fp8_block",
+            "qspec_rmsnorm_fp8_block", "qspec_linear_fp8_block", "qspec_gated_fp8_block"]
 KERNEL_W4A16_TC, KERNEL_W4A4_GEMV_TC, KERNEL_W4A4_TC = 0, 1, 2
 NOALLOC_SCRATCH_BYTES = 1 << 20
 
@@ -114,6 +115,12 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
                                               vp, sz_t, ctypes.c_uint32, i32, vp, vp], i32),
             "qspec_debug_attn_prompt_bounded": ([vp, i32, vp, i32, vp, i32, vp, vp, i32, i32, i32, i32, i32, i32, f32,
                                                  vp, i32, ctypes.c_uint32, i32, vp, vp], i32),
+            "qspec_quant_weights_fp8_block": ([vp, i32, i32, vp, vp, vp, vp], i32),
+            "qspec_quant_act_fp8_block": ([vp, i32, i32, i32, vp, vp, i32, vp, vp], i32),
+            "qspec_rmsnorm_fp8_block": ([vp, i32, vp, i32, vp, f32, i32, i32, vp, i32, vp, vp, i32, vp, i32, vp, vp],
+                                        i32),
+            "qspec_linear_fp8_block": ([vp, vp, i32, vp, vp, i32, i32, i32, vp, i32, vp, vp], i32),
+            "qspec_gated_fp8_block": ([vp, vp, i32, vp, vp, vp, vp, i32, i32, i32, vp, vp, i32, vp, i32, vp, vp], i32),
         }
         for name, (args, res) in proto.items():
             f = getattr(lib, name)
@@ -347,6 +354,34 @@ def qspec_debug_attn_prompt_bounded(q, ldq, k, ldk, v, ldv, q_start, k_start, q_
     return load_library().qspec_debug_attn_prompt_bounded(
         _ptr(q), ldq, _ptr(k), ldk, _ptr(v), ldv, _ptr(q_start), _ptr(k_start), q_rows, k_rows, B, Hq, H, D, scale,
         _ptr(o), ldo, wait_limit, stall, _ptr(dev_status), _stream(stream))
+
+
+def qspec_quant_weights_fp8_block(w16, N, K, w8, sw, dev_status=None, stream=None):
+    return load_library().qspec_quant_weights_fp8_block(_ptr(w16), N, K, _ptr(w8), _ptr(sw), _ptr(dev_status),
+                                                        _stream(stream))
+
+
+def qspec_quant_act_fp8_block(x, M, K, ldx, xq, sa, lds, dev_status=None, stream=None):
+    return load_library().qspec_quant_act_fp8_block(_ptr(x), M, K, ldx, _ptr(xq), _ptr(sa), lds, _ptr(dev_status),
+                                                    _stream(stream))
+
+
+def qspec_rmsnorm_fp8_block(x, ldx, res, ldr, w, eps, M, K, h, ldh, xq, sa, lds, y, ldy, dev_status=None, stream=None):
+    return load_library().qspec_rmsnorm_fp8_block(_ptr(x), ldx, _ptr(res), ldr, _ptr(w), eps, M, K, _ptr(h), ldh,
+                                                  _ptr(xq), _ptr(sa), lds, _ptr(y), ldy, _ptr(dev_status),
+                                                  _stream(stream))
+
+
+def qspec_linear_fp8_block(xq, sa, lds, w8, sw, M, N, K, y, ldy, dev_status=None, stream=None):
+    return load_library().qspec_linear_fp8_block(_ptr(xq), _ptr(sa), lds, _ptr(w8), _ptr(sw), M, N, K, _ptr(y), ldy,
+                                                 _ptr(dev_status), _stream(stream))
+
+
+def qspec_gated_fp8_block(xq, sa, lds, w_gate, s_gate, w_up, s_up, M, N, K, hq, sh, ldh, h, ldy, dev_status=None,
+                          stream=None):
+    return load_library().qspec_gated_fp8_block(_ptr(xq), _ptr(sa), lds, _ptr(w_gate), _ptr(s_gate), _ptr(w_up),
+                                                _ptr(s_up), M, N, K, _ptr(hq), _ptr(sh), ldh, _ptr(h), ldy,
+                                                _ptr(dev_status), _stream(stream))
 
 
 # ---------------------------------------------------------------------------
@@ -645,3 +680,100 @@ def attn_prompt(q, k, v, q_start, k_start=None, scale=None, out=None, dev_status
                              D ** -0.5 if scale is None else scale, o, _heads(o, "out")[3], dev_status, stream),
            "qspec_attn_prompt")
     return o
+
+
+def _rows_of(t, name):
+    """A bf16 CUDA tensor [M][K] with contiguous rows: (M, K, leading dimension)."""
+    if t.device.type != "cuda" or t.dtype != torch.bfloat16 or t.dim() != 2 or (t.numel() and t.stride(1) != 1):
+        raise ValueError("%s must be a bf16 CUDA tensor [M][K] with contiguous rows" % name)
+    return t.shape[0], t.shape[1], (t.stride(0) if t.shape[0] > 1 else t.shape[1])
+
+
+def _block_codes(xq, sa):
+    """Codes uint8 [M][K] with scales fp32 [K / 128][M] (rows of scales may be strided): (M, K, lds)."""
+    _need(xq, torch.uint8, "xq")
+    M, K = xq.shape
+    if (sa.device.type != "cuda" or sa.dtype != torch.float32 or sa.shape != (K // GROUP, M)
+            or (M > 1 and sa.stride(1) != 1)):
+        raise ValueError("sa must be a fp32 CUDA tensor [%d][%d] with contiguous rows" % (K // GROUP, M))
+    return M, K, max(M, sa.stride(0))
+
+
+def _block_weights(w8, sw, K, name):
+    """Codes uint8 [N][K] with scales fp32 [ceil(N / 128)][K / 128]: N."""
+    _need(w8, torch.uint8, name)
+    _need(sw, torch.float32, "the scales of " + name)
+    if w8.dim() != 2 or w8.shape[1] != K or sw.shape != (-(-w8.shape[0] // GROUP), K // GROUP):
+        raise ValueError("%s must be [N][%d], its scales [ceil(N / 128)][%d]" % (name, K, K // GROUP))
+    return w8.shape[0]
+
+
+@_allocates
+def quant_weights_fp8_block(w16, dev_status=None, stream=None):
+    """Parent weights fp16 [N][K] -> (w8 uint8 [N][K] E4M3, sw fp32 [ceil(N / 128)][K / 128])."""
+    _need(w16, torch.float16, "w16")
+    N, K = w16.shape
+    w8 = torch.empty((N, K), dtype=torch.uint8, device=w16.device)
+    sw = torch.empty((-(-N // GROUP), K // GROUP), dtype=torch.float32, device=w16.device)
+    _check(qspec_quant_weights_fp8_block(w16, N, K, w8, sw, dev_status, stream), "qspec_quant_weights_fp8_block")
+    return w8, sw
+
+
+@_allocates
+def quant_act_fp8_block(x, dev_status=None, stream=None):
+    """bf16 [M][K] -> (xq uint8 [M][K] E4M3, sa fp32 [K / 128][M])."""
+    M, K, ldx = _rows_of(x, "x")
+    xq = torch.empty((M, K), dtype=torch.uint8, device=x.device)
+    sa = torch.empty((K // GROUP, M), dtype=torch.float32, device=x.device)
+    _check(qspec_quant_act_fp8_block(x, M, K, ldx, xq, sa, M, dev_status, stream), "qspec_quant_act_fp8_block")
+    return xq, sa
+
+
+@_allocates
+def rmsnorm_fp8_block(x, w, eps, residual=None, want_bf16=False, dev_status=None, stream=None):
+    """x bf16 [M][K] (plus residual bf16 [M][K]) -> (xq uint8 [M][K] E4M3, sa fp32 [K / 128][M], h bf16 [M][K] or
+    None without a residual, y bf16 [M][K] or None without want_bf16)."""
+    _need(w, torch.bfloat16, "w")
+    M, K, ldx = _rows_of(x, "x")
+    ldr = K if residual is None else _rows_of(residual, "residual")[2]
+    if residual is not None and residual.shape != x.shape:
+        raise ValueError("residual must be [%d][%d]" % (M, K))
+    if w.numel() != K:
+        raise ValueError("w must hold %d values" % K)
+    xq = torch.empty((M, K), dtype=torch.uint8, device=x.device)
+    sa = torch.empty((K // GROUP, M), dtype=torch.float32, device=x.device)
+    h = torch.empty((M, K), dtype=torch.bfloat16, device=x.device) if residual is not None else None
+    y = torch.empty((M, K), dtype=torch.bfloat16, device=x.device) if want_bf16 else None
+    _check(qspec_rmsnorm_fp8_block(x, ldx, residual, ldr, w, eps, M, K, h, K, xq, sa, M, y, K, dev_status, stream),
+           "qspec_rmsnorm_fp8_block")
+    return xq, sa, h, y
+
+
+@_allocates
+def linear_fp8_block(xq, sa, w8, sw, out=None, dev_status=None, stream=None):
+    """xq, sa as from quant_act_fp8_block (or the gated product), w8, sw as from quant_weights_fp8_block ->
+    y bf16 [M][N]."""
+    M, K, lds = _block_codes(xq, sa)
+    N = _block_weights(w8, sw, K, "w8")
+    y = out if out is not None else torch.empty((M, N), dtype=torch.bfloat16, device=xq.device)
+    if tuple(y.shape) != (M, N):
+        raise ValueError("out must be [%d][%d]" % (M, N))
+    _check(qspec_linear_fp8_block(xq, sa, lds, w8, sw, M, N, K, y, _rows_of(y, "out")[2], dev_status, stream),
+           "qspec_linear_fp8_block")
+    return y
+
+
+@_allocates
+def gated_fp8_block(xq, sa, w_gate, s_gate, w_up, s_up, want_fp8=True, want_bf16=False, dev_status=None, stream=None):
+    """silu(x W_gate^T) * (x W_up^T) -> (hq uint8 [M][N] E4M3, sh fp32 [N / 128][M], h bf16 [M][N]), each None where
+    it is not wanted."""
+    M, K, lds = _block_codes(xq, sa)
+    N = _block_weights(w_gate, s_gate, K, "w_gate")
+    if _block_weights(w_up, s_up, K, "w_up") != N:
+        raise ValueError("w_gate and w_up must have the same rows")
+    hq = torch.empty((M, N), dtype=torch.uint8, device=xq.device) if want_fp8 else None
+    sh = torch.empty((N // GROUP, M), dtype=torch.float32, device=xq.device) if want_fp8 else None
+    h = torch.empty((M, N), dtype=torch.bfloat16, device=xq.device) if want_bf16 else None
+    _check(qspec_gated_fp8_block(xq, sa, lds, w_gate, s_gate, w_up, s_up, M, N, K, hq, sh, M, h, N, dev_status, stream),
+           "qspec_gated_fp8_block")
+    return hq, sh, h

@@ -218,6 +218,136 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR)
     }
 }
 
+// The same with a scale for each block of 128: half a warp holds a block (16 lanes x 8 values), so its maximum takes
+// four shuffles and the row's reduction only the sum of squares.  Where the squares pass fp32 the sum is taken again
+// times 2^-160; a block whose products with the weights pass it is taken again times 2^-80, the other blocks stand.
+// Scales lie token by token, [K / 128][lds]: 4 bytes a block, next to those of the neighbouring rows' CTAs.
+template <int TPR, int NV>
+__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR)
+    rmsnorm_fp8_block_kernel(const uint16_t *x, int ldx, const uint16_t *res, int ldr, const uint16_t *__restrict__ w,
+                             float eps, int M, int K, uint16_t *h, int ldh, uint8_t *__restrict__ xq,
+                             float *__restrict__ sa, int lds, uint16_t *__restrict__ y, int ldy, int32_t *st) {
+    constexpr int kRows = TPR < 128 ? 128 / TPR : 1;
+    constexpr float kDown = 8.271806125530277e-25f, kUp = 1.2089258196146292e24f;      // 2^-80, 2^80
+    __shared__ float2 red[32];
+    const int t = threadIdx.x % TPR;
+    const int m = blockIdx.x * kRows + (TPR < 128 ? threadIdx.x / TPR : 0);
+    const int n8 = K / 8;
+    const bool row_ok = m < M;
+    pdl_launch_dependents();
+    pdl_wait();
+    uint4 hv[NV], wv[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int i = t + j * TPR;
+        const bool in = row_ok && i < n8;
+        hv[j] = in ? __ldcs(reinterpret_cast<const uint4 *>(x + (size_t)m * ldx) + i) : make_uint4(0, 0, 0, 0);
+        wv[j] = in ? __ldg(reinterpret_cast<const uint4 *>(w) + i) : make_uint4(0, 0, 0, 0);
+    }
+    if (res != nullptr) {
+        uint4 rv[NV];
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int i = t + j * TPR;
+            rv[j] = row_ok && i < n8 ? __ldcs(reinterpret_cast<const uint4 *>(res + (size_t)m * ldr) + i)
+                                     : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int i = t + j * TPR;
+            hv[j] = make_uint4(add_bf16(hv[j].x, rv[j].x), add_bf16(hv[j].y, rv[j].y), add_bf16(hv[j].z, rv[j].z),
+                               add_bf16(hv[j].w, rv[j].w));
+            if (row_ok && i < n8) reinterpret_cast<uint4 *>(h + (size_t)m * ldh)[i] = hv[j];
+        }
+    }
+    uint64_t a[NV][4], sq = 0;
+    float top[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const uint32_t hw[4] = {hv[j].x, hv[j].y, hv[j].z, hv[j].w}, ww[4] = {wv[j].x, wv[j].y, wv[j].z, wv[j].w};
+        top[j] = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint64_t v = both(hw[e]);
+            sq = fma2(v, v, sq);
+            a[j][e] = mul2(v, both(ww[e]));
+            top[j] = max_abs(top[j], lo32(a[j][e]), hi32(a[j][e]));
+        }
+#pragma unroll
+        for (int o = 8; o >= 1; o >>= 1) top[j] = max_nan(top[j], __shfl_xor_sync(0xffffffffu, top[j], o));
+    }
+    float ss = lo32(sq) + hi32(sq), none = 0.0f;
+    row_reduce<TPR>(ss, none, red);
+    const uint16_t *row = res != nullptr ? h + (size_t)m * ldh : x + (size_t)m * ldx;
+    const bool stands = ss < INFINITY;                    // (the same for a row's threads, and for TPR = 32 for a warp's)
+    if (!stands) {
+        ss = 0.0f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int i = 4 * (t + j * TPR) + e;
+                const uint64_t v = mul2(both(row_ok && i < 4 * n8 ? reinterpret_cast<const uint32_t *>(row)[i] : 0u), f2(kDown, kDown));
+                ss = fmaf(lo32(v), lo32(v), fmaf(hi32(v), hi32(v), ss));
+            }
+        row_reduce<TPR>(ss, none, red);
+    }
+    if (!row_ok) return;                                  // (whole warps: a row has at least one)
+    const float near = rsqrtf(fmaf(ss, 1.0f / (float)K, stands ? eps : eps * kDown * kDown));
+    // 1 / rms, for products as they are and for those times 2^-80
+    const float rstd = stands ? near : near * kDown, rstd_up = stands ? near * kUp : near;
+    bool bad = !(ss < INFINITY);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int i = t + j * TPR;
+        float by = rstd;
+        const bool again = !(top[j] < INFINITY);
+        if (__any_sync(0xffffffffu, again)) {
+            if (again) {
+                by = rstd_up;
+                top[j] = 0.0f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int at = 4 * i + e;
+                    const bool in = at < 4 * n8;
+                    a[j][e] = mul2(mul2(both(in ? reinterpret_cast<const uint32_t *>(row)[at] : 0u), f2(kDown, kDown)),
+                                   both(in ? reinterpret_cast<const uint32_t *>(w)[at] : 0u));
+                    top[j] = max_abs(top[j], lo32(a[j][e]), hi32(a[j][e]));
+                }
+            }
+#pragma unroll
+            for (int o = 8; o >= 1; o >>= 1) top[j] = max_nan(top[j], __shfl_xor_sync(0xffffffffu, top[j], o));
+            if (!(top[j] < INFINITY)) top[j] = INFINITY;          // (NaN too)
+        }
+        if (i >= n8) continue;
+        if (y != nullptr) {
+            uint32_t o[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint64_t v = mul2(a[j][e], f2(by, by));
+                o[e] = pack_bf16(lo32(v), hi32(v));
+            }
+            reinterpret_cast<uint4 *>(y + (size_t)m * ldy)[i] = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+        // codes a (448 / top), where 448 / top would pass fp32 with a brought up first
+        const float up = top[j] < 1.0e-30f ? 7.9228162514264338e28f : 1.0f;   // 2^96
+        const float inv = top[j] > 0.0f ? __fdiv_rn(448.0f, top[j] * up) : 0.0f;
+        uint32_t code[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (up != 1.0f) a[j][e] = mul2(a[j][e], f2(up, up));
+            code[e] = pack_e4m3(mul2(a[j][e], f2(inv, inv)));
+        }
+        reinterpret_cast<uint2 *>(xq + (size_t)m * K)[i] =
+            top[j] > 0.0f ? make_uint2(code[0] | code[1] << 16, code[2] | code[3] << 16)
+                          : make_uint2(0u, 0u);       // no code of -0 in a block of zeros
+        const float most = top[j] * by;                // max |y|, in the bf16 output inf from the midpoint behind the
+        bad |= !(most < (y != nullptr ? 3.3961775292304601e38f : INFINITY));   // largest bf16 value
+        if ((threadIdx.x & 15) == 0) sa[(size_t)(i / 16) * lds + m] = __fdiv_rn(most, 448.0f);
+    }
+    if (bad) flag(st, QSPEC_ERR_NONFINITE);
+}
+
 template <int TPR, int NV>
 int launch(const uint16_t *x, int ldx, const uint16_t *res, int ldr, const uint16_t *w, float eps, int M, int K,
            uint16_t *h, int ldh, uint8_t *xq, float *sa, uint16_t *y, int ldy, int32_t *st, cudaStream_t stream) {
@@ -225,6 +355,16 @@ int launch(const uint16_t *x, int ldx, const uint16_t *res, int ldr, const uint1
     return launch_pdl("qspec_rmsnorm_fp8", rmsnorm_fp8_kernel<TPR, NV>, dim3((unsigned)((M + kRows - 1) / kRows)),
                       dim3(TPR < 128 ? 128 : TPR), 0, stream, x, ldx, res, ldr, w, eps, M, K, h, ldh, xq, sa, y, ldy,
                       st);
+}
+
+template <int TPR, int NV>
+int launch_block(const uint16_t *x, int ldx, const uint16_t *res, int ldr, const uint16_t *w, float eps, int M, int K,
+                 uint16_t *h, int ldh, uint8_t *xq, float *sa, int lds, uint16_t *y, int ldy, int32_t *st,
+                 cudaStream_t stream) {
+    constexpr int kRows = TPR < 128 ? 128 / TPR : 1;
+    return launch_pdl("qspec_rmsnorm_fp8_block", rmsnorm_fp8_block_kernel<TPR, NV>,
+                      dim3((unsigned)((M + kRows - 1) / kRows)), dim3(TPR < 128 ? 128 : TPR), 0, stream, x, ldx, res,
+                      ldr, w, eps, M, K, h, ldh, xq, sa, lds, y, ldy, st);
 }
 
 }  // namespace nrm
@@ -260,4 +400,32 @@ extern "C" int qspec_rmsnorm_fp8(const uint16_t *x_bf16, int ldx, const uint16_t
     if (n8 <= 1024) return go(nrm::launch<512, 2>);
     if (n8 <= 2048) return go(nrm::launch<1024, 2>);
     return go(nrm::launch<1024, 4>);
+}
+
+extern "C" int qspec_rmsnorm_fp8_block(const uint16_t *x_bf16, int ldx, const uint16_t *res_bf16, int ldr,
+                                 const uint16_t *w_bf16, float eps, int M, int K, uint16_t *h_bf16, int ldh,
+                                 uint8_t *xq, float *sa, int lds, uint16_t *y_bf16, int ldy, int32_t *dev_status,
+                                 qspec_stream_t stream) {
+    if (!x_bf16 || !w_bf16 || !xq || !sa || (res_bf16 != nullptr) != (h_bf16 != nullptr)) return QSPEC_ERR_NULL;
+    if (M < 1 || K < kGroup || K % kGroup || K > nrm::kMaxK || !(eps > 0.0f) || !std::isfinite(eps) || ldx < K ||
+        lds < M ||
+        (res_bf16 && (ldr < K || ldh < K)) || (y_bf16 && ldy < K))
+        return QSPEC_ERR_SHAPE;
+    if (!aligned(x_bf16, 16) || !aligned(w_bf16, 16) || !aligned(xq, 8) || !aligned(sa, 4) || ldx % 8 ||
+        (res_bf16 && (!aligned(res_bf16, 16) || !aligned(h_bf16, 16) || ldr % 8 || ldh % 8)) ||
+        (y_bf16 && (!aligned(y_bf16, 16) || ldy % 8)))
+        return QSPEC_ERR_ALIGN;
+    int rc = check_device();
+    if (rc) return rc;
+    cudaStream_t s = as_cuda(stream);
+    auto go = [&](auto launcher) {
+        return launcher(x_bf16, ldx, res_bf16, ldr, w_bf16, eps, M, K, h_bf16, ldh, xq, sa, lds, y_bf16, ldy, dev_status,
+                        s);
+    };
+    const int n8 = K / 8;                        // (widths as in qspec_rmsnorm_fp8)
+    if (n8 <= 128) return go(nrm::launch_block<32, 4>);
+    if (n8 <= 512) return go(nrm::launch_block<256, 2>);
+    if (n8 <= 1024) return go(nrm::launch_block<512, 2>);
+    if (n8 <= 2048) return go(nrm::launch_block<1024, 2>);
+    return go(nrm::launch_block<1024, 4>);
 }

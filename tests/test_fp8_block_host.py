@@ -1,0 +1,85 @@
+"""Refusals of the E4M3 calls with block scales: on the host, before any launch (no GPU needed)."""
+import ctypes
+
+import pytest
+import torch
+
+from quantized_speculative_decoding_shared_gb300 import binding
+from quantized_speculative_decoding_shared_gb300 import build as qbuild
+
+V = ctypes.c_void_p
+NULL, SHAPE, ALIGN = 1, 2, 3
+
+
+@pytest.fixture(scope="module")
+def lib():
+    qbuild.build()
+    return binding.load_library()
+
+
+def at(n=0x1000):
+    """An aligned address that the calls must not touch."""
+    return V(n)
+
+
+def refuse(fn, ok, cases):
+    for want, change in cases:
+        a = dict(ok, **change)
+        assert fn(*a.values()) == want, change
+
+
+def test_quantisers(lib):
+    refuse(lib.qspec_quant_weights_fp8_block, dict(w=at(), N=3, K=256, w8=at(), sw=at(), st=None, s=None), [
+        (NULL, dict(w=None)), (NULL, dict(w8=None)), (NULL, dict(sw=None)), (SHAPE, dict(N=0)), (SHAPE, dict(K=0)),
+        (SHAPE, dict(K=200)), (SHAPE, dict(K=-128)), (SHAPE, dict(N=2 ** 31 - 1, K=2 ** 31 - 128)),
+        (ALIGN, dict(w=at(0x1008))), (ALIGN, dict(w8=at(0x1004))), (ALIGN, dict(sw=at(0x1002)))])
+    refuse(lib.qspec_quant_act_fp8_block, dict(x=at(), M=3, K=256, ldx=256, xq=at(), sa=at(), lds=3, st=None, s=None), [
+        (NULL, dict(x=None)), (NULL, dict(xq=None)), (NULL, dict(sa=None)), (SHAPE, dict(M=0)), (SHAPE, dict(K=100)),
+        (SHAPE, dict(ldx=248)), (SHAPE, dict(lds=2)), (SHAPE, dict(M=2 ** 31 - 1, lds=2 ** 31 - 1, K=2 ** 31 - 128, ldx=2 ** 31 - 8)),
+        (ALIGN, dict(ldx=260)), (ALIGN, dict(x=at(0x1008))), (ALIGN, dict(xq=at(0x1004))), (ALIGN, dict(sa=at(0x1001)))])
+
+
+def test_norm(lib):
+    ok = dict(x=at(), ldx=256, r=at(), ldr=256, w=at(), eps=1e-5, M=2, K=256, h=at(), ldh=256, xq=at(), sa=at(), lds=2,
+              y=at(), ldy=256, st=None, s=None)
+    refuse(lib.qspec_rmsnorm_fp8_block, ok, [
+        (NULL, dict(x=None)), (NULL, dict(w=None)), (NULL, dict(xq=None)), (NULL, dict(sa=None)), (NULL, dict(h=None)),
+        (NULL, dict(r=None)), (SHAPE, dict(M=0)), (SHAPE, dict(K=0)), (SHAPE, dict(K=200)), (SHAPE, dict(K=32896)),
+        (SHAPE, dict(eps=0.0)), (SHAPE, dict(eps=float("nan"))), (SHAPE, dict(eps=float("inf"))), (SHAPE, dict(lds=1)),
+        (SHAPE, dict(ldx=248)), (SHAPE, dict(ldr=248)), (SHAPE, dict(ldh=248)), (SHAPE, dict(ldy=248)),
+        (ALIGN, dict(ldx=257)), (ALIGN, dict(ldr=260)), (ALIGN, dict(ldh=258)), (ALIGN, dict(ldy=260)),
+        (ALIGN, dict(x=at(0x1008))), (ALIGN, dict(r=at(0x1002))), (ALIGN, dict(w=at(0x1004))), (ALIGN, dict(h=at(0x1008))),
+        (ALIGN, dict(xq=at(0x1004))), (ALIGN, dict(sa=at(0x1002))), (ALIGN, dict(y=at(0x1008)))])
+
+
+def test_linear(lib):
+    ok = dict(xq=at(), sa=at(), lds=5, w=at(), sw=at(), M=5, N=100, K=256, y=at(), ldy=100, st=None, s=None)
+    refuse(lib.qspec_linear_fp8_block, ok, [
+        (NULL, dict(xq=None)), (NULL, dict(sa=None)), (NULL, dict(w=None)), (NULL, dict(sw=None)), (NULL, dict(y=None)),
+        (SHAPE, dict(M=0)), (SHAPE, dict(N=0)), (SHAPE, dict(K=0)), (SHAPE, dict(K=130)), (SHAPE, dict(ldy=99)),
+        (SHAPE, dict(lds=4)), (SHAPE, dict(M=2 ** 22 + 1, lds=2 ** 23)), (SHAPE, dict(N=2 ** 30 + 1, ldy=2 ** 30 + 1)),
+        (ALIGN, dict(xq=at(0x1008))), (ALIGN, dict(w=at(0x1008))), (ALIGN, dict(sa=at(0x1002))),
+        (ALIGN, dict(sw=at(0x1002))), (ALIGN, dict(y=at(0x1001)))])
+
+
+def test_gated(lib):
+    ok = dict(xq=at(), sa=at(), lds=5, wg=at(), sg=at(), wu=at(), su=at(), M=5, N=128, K=256, hq=at(), sh=at(), ldh=5,
+              h=at(), ldy=128, st=None, s=None)
+    refuse(lib.qspec_gated_fp8_block, ok, [
+        (NULL, dict(xq=None)), (NULL, dict(sa=None)), (NULL, dict(wg=None)), (NULL, dict(sg=None)), (NULL, dict(wu=None)),
+        (NULL, dict(su=None)), (NULL, dict(hq=None)), (NULL, dict(sh=None)), (NULL, dict(hq=None, sh=None, h=None)),
+        (SHAPE, dict(M=0)), (SHAPE, dict(N=0)), (SHAPE, dict(N=100)), (SHAPE, dict(N=129)), (SHAPE, dict(K=130)),
+        (SHAPE, dict(lds=4)), (SHAPE, dict(ldh=4)), (SHAPE, dict(ldy=127)), (SHAPE, dict(M=2 ** 22 + 1, lds=2 ** 23, ldh=2 ** 23)),
+        (ALIGN, dict(xq=at(0x1008))), (ALIGN, dict(wg=at(0x1008))), (ALIGN, dict(wu=at(0x1004))),
+        (ALIGN, dict(sa=at(0x1002))), (ALIGN, dict(sg=at(0x1001))), (ALIGN, dict(su=at(0x1002))),
+        (ALIGN, dict(hq=at(0x1008))), (ALIGN, dict(sh=at(0x1002))), (ALIGN, dict(h=at(0x1001)))])
+
+
+def test_conveniences_refuse_what_they_cannot_pass_on():
+    x, u8 = torch.zeros((2, 256), dtype=torch.bfloat16), torch.zeros((2, 256), dtype=torch.uint8)
+    s = torch.zeros((2, 2))
+    for call in (lambda: binding.quant_act_fp8_block(x), lambda: binding.quant_weights_fp8_block(x.to(torch.float16)),
+                 lambda: binding.rmsnorm_fp8_block(x, x[0], 1e-5), lambda: binding.linear_fp8_block(u8, s, u8, s),
+                 lambda: binding.gated_fp8_block(u8, s, u8, s, u8, s)):
+        with pytest.raises(ValueError):
+            call()

@@ -1,0 +1,233 @@
+"""E4M3 with a scale for each block of 128: quantisers (every bit), the linear and the gated product (against 64 bits,
+the bounds of blockref.py)."""
+import pytest
+import torch
+
+from quantized_speculative_decoding_shared_gb300 import binding as q, synthetic as syn
+from blockref import (act_codes, act_values, check_bf16, check_codes, check_linear, gated, weight_codes, weight_values)
+from gpuhelp import need_gpu, read_status, status
+
+pytestmark = pytest.mark.gpu
+
+
+def acts(M, K, seed, dev, std=1.0):
+    """Rows of different sizes with outlier channels; some blocks of zeros."""
+    x = syn.activations(M, K, seed, device=dev, outlier_frac=0.01).float()
+    x *= (0.25 + torch.arange(M, device=dev)[:, None] % 5) * std
+    if M > 2:
+        x[1, :128] = 0.0
+    return x.to(torch.bfloat16)
+
+
+def parent(N, K, seed, dev, std=0.03):
+    w = syn.activations(N, K, seed, device=dev).float() * std
+    if N > 3:
+        w[: min(N, 128), K - 128:] = 0.0               # a block of zeros
+        w[N // 2] *= 16.0
+    return w.to(torch.float16)
+
+
+def same(a, b):
+    return torch.equal(a.cpu().view(torch.uint8), b.cpu().view(torch.uint8))
+
+
+@pytest.mark.parametrize("M,K", [(1, 128), (2, 384), (5, 4096), (33, 640), (40, 1152), (257, 14336), (3000, 1408)])
+def test_activation_codes(M, K):
+    dev = need_gpu()
+    x, st = acts(M, K, M + K, dev), status(dev)
+    xq, sa = q.quant_act_fp8_block(x, dev_status=st)
+    assert read_status(st) == 0
+    want = act_codes(x)
+    assert same(xq, want[0]) and same(sa, want[1])
+
+
+@pytest.mark.parametrize("N,K", [(1, 128), (127, 256), (128, 640), (129, 1152), (300, 4096), (1000, 384)])
+def test_weight_codes(N, K):
+    dev = need_gpu()
+    w, st = parent(N, K, N + K, dev), status(dev)
+    w8, sw = q.quant_weights_fp8_block(w, dev_status=st)
+    assert read_status(st) == 0
+    want = weight_codes(w)
+    assert same(w8, want[0]) and same(sw, want[1])
+
+
+@pytest.mark.parametrize("scale", [2.0 ** 120, 2.0 ** 79, 2.0 ** 70, 2.0 ** -60, 2.0 ** -73, 2.0 ** -90, 2.0 ** -126, 2.0 ** -133])
+def test_activation_codes_of_extreme_magnitudes(scale):
+    """Scales on both sides of where the quotient takes the division, subnormal ones among them."""
+    dev = need_gpu()
+    x = (acts(9, 512, 3, dev).float() * scale).to(torch.bfloat16)
+    st = status(dev)
+    xq, sa = q.quant_act_fp8_block(x, dev_status=st)
+    assert read_status(st) == 0
+    want = act_codes(x)
+    assert same(sa, want[1]) and same(xq, want[0])
+
+
+def test_every_bf16_value_over_several_scales():
+    """All finite bf16 values not above a block's maximum: code and quotient agree with the division."""
+    dev = need_gpu()
+    for top in (448.0, 1.0, 3.140625, 0.0087890625, 1.5e30, 2.0 ** -70):
+        top = torch.tensor(top).to(torch.bfloat16)
+        v = torch.arange(0, 1 << 16, dtype=torch.int32).to(torch.int16).view(torch.bfloat16)
+        v = v[torch.isfinite(v) & (v.abs() <= top)]
+        n = -(-len(v) // 127)
+        rows = torch.zeros((n, 128), dtype=torch.bfloat16)
+        rows[:, 0] = top
+        pad = torch.zeros(n * 127, dtype=torch.bfloat16)
+        pad[: len(v)] = v
+        rows[:, 1:] = pad.view(n, 127)
+        xq, sa = q.quant_act_fp8_block(rows.to(dev))
+        want = act_codes(rows)
+        assert same(xq, want[0]) and same(sa, want[1])
+
+
+def test_rows_and_scales_apart():
+    """Rows and rows of scales further apart than they are long: what lies between stays as it was."""
+    dev = need_gpu()
+    M, K, ldx, lds = 37, 640, 704, 41
+    wide = torch.full((M, ldx), float("nan"), dtype=torch.bfloat16, device=dev)
+    wide[:, :K] = acts(M, K, 1, dev)
+    xq = torch.empty((M, K), dtype=torch.uint8, device=dev)
+    sa = torch.full((K // 128, lds), -7.0, device=dev)
+    st = status(dev)
+    assert q.qspec_quant_act_fp8_block(wide, M, K, ldx, xq, sa, lds, st) == 0 and read_status(st) == 0
+    want = act_codes(wide[:, :K])
+    assert same(xq, want[0]) and same(sa[:, :M].contiguous(), want[1]) and torch.all(sa[:, M:] == -7.0)
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+def test_quantisers_flag_what_is_not_finite(value):
+    dev = need_gpu()
+    x = acts(20, 384, 5, dev)
+    want = act_codes(x)
+    x[7, 130] = value
+    st = status(dev)
+    xq, sa = q.quant_act_fp8_block(x, dev_status=st)
+    assert read_status(st) == q.ERR_NONFINITE and not torch.isfinite(sa[1, 7])
+    sa[1, 7] = want[1][1, 7]
+    assert same(sa, want[1]) and same(xq[8:], want[0][8:])            # the other blocks are what they were
+    w = parent(200, 256, 6, dev)
+    want = weight_codes(w)
+    w[150, 3] = value
+    st = status(dev)
+    w8, sw = q.quant_weights_fp8_block(w, dev_status=st)
+    assert read_status(st) == q.ERR_NONFINITE and not torch.isfinite(sw[1, 0])
+    assert same(w8[:128], want[0][:128]) and same(w8[:, 128:].contiguous(), want[0][:, 128:].contiguous())
+
+
+def codes(M, K, seed, dev):
+    return q.quant_act_fp8_block(acts(M, K, seed, dev))
+
+
+SHAPES = [(1, 128, 128), (1, 1, 128), (2, 300, 384), (1, 4096, 1152), (5, 1000, 4096), (15, 129, 14336), (16, 128, 256),
+          (17, 127, 640), (31, 640, 1408), (33, 257, 2048), (64, 384, 896), (65, 100, 1152), (80, 1024, 4096), (127, 130, 256),
+          (128, 512, 640), (129, 384, 512), (255, 256, 128), (257, 300, 1024), (288, 1152, 1408), (600, 640, 768), (1025, 257, 384)]
+
+
+@pytest.mark.parametrize("M,N,K", SHAPES)
+def test_linear(M, N, K):
+    dev = need_gpu()
+    xq, sa = codes(M, K, M, dev)
+    w8, sw = q.quant_weights_fp8_block(parent(N, K, N, dev))
+    st = status(dev)
+    y = q.linear_fp8_block(xq, sa, w8, sw, dev_status=st)
+    assert read_status(st) == 0
+    check_linear(y, act_values(xq, sa), weight_values(w8, sw))
+
+
+@pytest.mark.parametrize("M,N,K", [(M, -(-N // 128) * 128, K) for M, N, K in SHAPES])
+def test_gated(M, N, K):
+    dev = need_gpu()
+    xq, sa = codes(M, K, M + 1, dev)
+    wg, wu = (q.quant_weights_fp8_block(parent(N, K, N + i, dev)) for i in (1, 2))
+    st = status(dev)
+    hq, sh, h = q.gated_fp8_block(xq, sa, *wg, *wu, want_bf16=True, dev_status=st)
+    assert read_status(st) == 0
+    ref, d = gated(act_values(xq, sa), weight_values(*wg), weight_values(*wu))
+    check_codes(hq, sh, ref, d)
+    check_bf16(h, ref, d)
+    # one output without the other: the same bits
+    a, b = q.gated_fp8_block(xq, sa, *wg, *wu), q.gated_fp8_block(xq, sa, *wg, *wu, want_fp8=False, want_bf16=True)
+    assert torch.equal(a[0], hq) and torch.equal(a[1], sh) and a[2] is None
+    assert torch.equal(b[2], h) and b[0] is None and b[1] is None
+
+
+@pytest.mark.parametrize("M,std", [(5, 30.0), (40, 3000.0), (300, 30.0), (300, 3000.0)])
+def test_gated_far_from_zero(M, std):
+    """Gates where exp passes fp32 on one side and vanishes on the other."""
+    dev = need_gpu()
+    N, K = 256, 512
+    xq, sa = q.quant_act_fp8_block(acts(M, K, 8, dev, std=std))
+    wg, wu = (q.quant_weights_fp8_block(parent(N, K, i, dev)) for i in (1, 2))
+    st = status(dev)
+    hq, sh, h = q.gated_fp8_block(xq, sa, *wg, *wu, want_bf16=True, dev_status=st)
+    assert read_status(st) == 0
+    ref, d = gated(act_values(xq, sa), weight_values(*wg), weight_values(*wu))
+    check_codes(hq, sh, ref, d)
+    check_bf16(h, ref, d)
+
+
+@pytest.mark.parametrize("M", [3, 70, 300])
+def test_blocks_of_zeros(M):
+    """Scales of 0 in every row of weights and tokens: outputs, codes and scales of 0."""
+    dev = need_gpu()
+    N, K = 256, 384
+    xq, sa = q.quant_act_fp8_block(torch.zeros((M, K), dtype=torch.bfloat16, device=dev))
+    wg, wu = (q.quant_weights_fp8_block(parent(N, K, i, dev)) for i in (1, 2))
+    for a, b in ((xq, sa), codes(M, K, 9, dev)):
+        z = q.quant_weights_fp8_block(torch.zeros((N, K), dtype=torch.float16, device=dev)) if a is not xq else wg
+        assert torch.all(q.linear_fp8_block(a, b, *z) == 0)
+        hq, sh, h = q.gated_fp8_block(a, b, *z, *wu, want_bf16=True)
+        assert not hq.any() and not sh.any() and torch.all(h == 0)
+
+
+@pytest.mark.parametrize("M", [7, 64, 130, 513])
+def test_outputs_apart(M):
+    """Leading dimensions wider than the rows, odd ones among them, scales further apart than tokens: nothing else is
+    written, and what stands past the last token is not read."""
+    dev = need_gpu()
+    N, K, lds, ldh, ldy = 384, 640, M + 3, M + 5, 391
+    xq, sa0 = codes(M, K, 4, dev)
+    sa = torch.full((K // 128, lds), float("nan"), device=dev)
+    sa[:, :M] = sa0
+    wg, wu = (q.quant_weights_fp8_block(parent(N, K, i, dev)) for i in (1, 2))
+    y = torch.full((M, ldy), 7.0, dtype=torch.bfloat16, device=dev)
+    st = status(dev)
+    assert q.qspec_linear_fp8_block(xq, sa, lds, *wg, M, N - 1, K, y, ldy, st) == 0 and read_status(st) == 0
+    assert torch.all(y[:, N - 1:] == 7.0)
+    check_linear(y[:, :N - 1], act_values(xq, sa0), weight_values(*wg)[:N - 1])
+    hq = torch.full((M + 1, N), 9, dtype=torch.uint8, device=dev)
+    sh = torch.full((N // 128, ldh), -7.0, device=dev)
+    h = torch.full((M, ldy), 7.0, dtype=torch.bfloat16, device=dev)
+    assert q.qspec_gated_fp8_block(xq, sa, lds, *wg, *wu, M, N, K, hq, sh, ldh, h, ldy, st) == 0 and read_status(st) == 0
+    assert torch.all(hq[M] == 9) and torch.all(sh[:, M:] == -7.0) and torch.all(h[:, N:] == 7.0)
+    ref, d = gated(act_values(xq, sa0), weight_values(*wg), weight_values(*wu))
+    check_codes(hq[:M], sh[:, :M], ref, d)
+    check_bf16(h[:, :N], ref, d)
+
+
+@pytest.mark.parametrize("M", [2, 300])
+def test_products_that_pass_fp32_are_flagged(M):
+    dev = need_gpu()
+    N, K = 128, 256
+    x = torch.full((M, K), 2.0 ** 100, dtype=torch.bfloat16, device=dev)
+    x[0] = 1.0
+    xq, sa = q.quant_act_fp8_block(x)
+    w = q.quant_weights_fp8_block(torch.full((N, K), 1.0, dtype=torch.float16, device=dev))
+    st = status(dev)
+    hq, sh, _ = q.gated_fp8_block(xq, sa, *w, *w, dev_status=st)
+    assert read_status(st) == q.ERR_NONFINITE
+    assert not torch.isfinite(sh[0, 1:]).any()
+    ref, d = gated(act_values(xq[:1], sa[:, :1]), weight_values(*w), weight_values(*w))      # (the other rows are what they were)
+    check_codes(hq[:1], sh[:, :1], ref, d)
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 4096, 14336), (5, 14336, 4096), (288, 3584, 18944), (100, 18944, 3584)])
+def test_the_models_shapes_in_sampled_channels(M, N, K):
+    dev = need_gpu()
+    xq, sa = codes(M, K, 1, dev)
+    g = torch.Generator(device=dev).manual_seed(2)
+    w8, sw = q.quant_weights_fp8_block((torch.randn((N, K), generator=g, device=dev) * 0.02).to(torch.float16))
+    y = q.linear_fp8_block(xq, sa, w8, sw)
+    for n in (0, 128 * (N // 256), N - 128):
+        check_linear(y[:, n:n + 128], act_values(xq, sa), weight_values(w8[n:n + 128], sw[n // 128:n // 128 + 1]))
