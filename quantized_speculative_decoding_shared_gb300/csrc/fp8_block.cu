@@ -47,35 +47,67 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return d;
 }
 
+// two fp32 values in a register pair, and packed operations on them
+__device__ __forceinline__ uint64_t f2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float lo32(uint64_t v) { return __uint_as_float((uint32_t)v); }
+__device__ __forceinline__ float hi32(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+
+// a word of two fp16 or bf16 values
 template <bool kHalf>
-__device__ __forceinline__ void unpack(uint4 v, float (&f)[8]) {
+__device__ __forceinline__ uint64_t both(uint32_t w) {
+    if constexpr (kHalf) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+        return f2(f.x, f.y);
+    }
+    return f2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+template <bool kHalf>
+__device__ __forceinline__ float max_of(uint4 v, float amax) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        if constexpr (kHalf) {
-            f[2 * e] = __half2float(__ushort_as_half((uint16_t)(w[e] & 0xFFFFu)));
-            f[2 * e + 1] = __half2float(__ushort_as_half((uint16_t)(w[e] >> 16)));
-        } else {
-            f[2 * e] = __uint_as_float(w[e] << 16);
-            f[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
-        }
+        const uint64_t f = both<kHalf>(w[e]);
+        amax = max_abs(amax, lo32(f), hi32(f));
     }
+    return amax;
 }
 
-// the codes of 8 values over the scale s (not 0)
-__device__ __forceinline__ uint2 codes_of(const float (&f)[8], float s) {
-    const bool plain = s > 8.271806125530277e-25f && s < 1.2089258196146292e24f;     // 2^-80, 2^80
-    const float y = __frcp_rn(s);
+__device__ __forceinline__ uint32_t pack_e4m3(float a, float b) {          // the first in the low byte
+    return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+}
+
+// the codes of 8 values over the scale s; one of 0 stands for a block of zeros
+template <bool kHalf>
+__device__ __forceinline__ uint2 codes_of(uint4 v, float s, float y) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     uint32_t c[4];
+    if (s > 8.271806125530277e-25f && s < 1.2089258196146292e24f) {        // 2^-80, 2^80
+        const uint64_t yy = f2(y, y), ss = f2(-s, -s);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        float t[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const float v = f[2 * e + i], q = __fmul_rn(v, y);
-            t[i] = plain ? copysignf(__fmaf_rn(__fmaf_rn(-q, s, v), y, q), v) : __fdiv_rn(v, s);    // (-0 stays -0)
+        for (int e = 0; e < 4; ++e) {
+            const uint64_t f = both<kHalf>(w[e]), q = mul2(f, yy), t = fma2(fma2(q, ss, f), yy, q);
+            c[e] = pack_e4m3(copysignf(lo32(t), lo32(f)), copysignf(hi32(t), hi32(f)));      // (-0 stays -0)
         }
-        c[e] = __nv_cvt_float2_to_fp8x2(make_float2(t[0], t[1]), __NV_SATFINITE, __NV_E4M3);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint64_t f = both<kHalf>(w[e]);
+            c[e] = s == 0.0f ? 0u : pack_e4m3(__fdiv_rn(lo32(f), s), __fdiv_rn(hi32(f), s));
+        }
     }
     return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
 }
@@ -104,15 +136,12 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
         const int r = half / kBlocksX + i * (kHalves / kBlocksX), m = r0 + r;
-        float f[8], amax = 0.0f;
-        unpack<false>(v[i], f);
-#pragma unroll
-        for (int e = 0; e < 8; e += 2) amax = max_abs(amax, f[e], f[e + 1]);
+        float amax = max_of<false>(v[i], 0.0f);
 #pragma unroll
         for (int o = 8; o >= 1; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
         const float s = __fdiv_rn(amax, 448.0f);
         bad |= !(amax < INFINITY);
-        const uint2 c = amax == 0.0f ? make_uint2(0u, 0u) : codes_of(f, s);
+        const uint2 c = codes_of<false>(v[i], s, __frcp_rn(s));
         if (m < M && g < G) reinterpret_cast<uint2 *>(xq + (size_t)m * K + (size_t)g * kGroup)[lane] = c;
         if (lane == 0) scales[half % kBlocksX][r] = s;
     }
@@ -125,7 +154,7 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 // one 128 x 128 block per CTA, kept in registers between its load and its codes
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 3)
     quant_weights_kernel(const uint16_t *__restrict__ w, int N, int K, uint8_t *__restrict__ w8, float *__restrict__ sw,
                          int32_t *st) {
     constexpr int kPer = kGroup / kHalves;       // rows per half warp
@@ -143,12 +172,7 @@ __global__ void __launch_bounds__(kThreads)
     }
     float amax = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        float f[8];
-        unpack<true>(v[i], f);
-#pragma unroll
-        for (int e = 0; e < 8; e += 2) amax = max_abs(amax, f[e], f[e + 1]);
-    }
+    for (int i = 0; i < kPer; ++i) amax = max_of<true>(v[i], amax);
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
     if ((threadIdx.x & 31) == 0) red[warp] = amax;
@@ -156,14 +180,12 @@ __global__ void __launch_bounds__(kThreads)
     amax = red[0];
 #pragma unroll
     for (int i = 1; i < kThreads / 32; ++i) amax = max_nan(amax, red[i]);
-    const float s = __fdiv_rn(amax, 448.0f);
+    const float s = __fdiv_rn(amax, 448.0f), y = __frcp_rn(s);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         const int n = n0 + half + i * kHalves;
-        float f[8];
-        unpack<true>(v[i], f);
-        if (n < N) reinterpret_cast<uint2 *>(w8 + (size_t)n * K + (size_t)g * kGroup)[lane] =
-            amax == 0.0f ? make_uint2(0u, 0u) : codes_of(f, s);
+        const uint2 c = codes_of<true>(v[i], s, y);
+        if (n < N) reinterpret_cast<uint2 *>(w8 + (size_t)n * K + (size_t)g * kGroup)[lane] = c;
     }
     if (threadIdx.x == 0) {
         sw[(size_t)nb * G + g] = s;

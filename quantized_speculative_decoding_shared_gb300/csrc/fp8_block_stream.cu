@@ -18,8 +18,7 @@
 // that a scale needs is a warp's.
 #include <algorithm>
 
-#include "fp8_block.cuh"
-#include "qspec_host.h"
+#include "fp8_block_host.h"
 #include "umma.cuh"
 
 namespace qspec {
@@ -278,10 +277,9 @@ __global__ void __launch_bounds__(kThreads, (Cfg<BN, kGated>::kOcc))
                     asm("max.NaN.f32 %0, %0, %1;" : "+f"(amax) : "f"(other));
                 }
                 if (a.hq != nullptr) {
-                    const float s = __fdiv_rn(amax, 448.0f);
-                    reinterpret_cast<uint32_t *>(a.hq + (size_t)m * a.N + n0)[lane] =
-                        amax == 0.0f ? 0u : f8b::codes4(v[0][0], v[0][1], v[0][2], v[0][3], s);
-                    if (lane == 0) a.sh[(size_t)tile * a.ldh + m] = s;
+                    const f8b::Quant q(amax);
+                    reinterpret_cast<uint32_t *>(a.hq + (size_t)m * a.N + n0)[lane] = q.four(v[0][0], v[0][1], v[0][2], v[0][3]);
+                    if (lane == 0) a.sh[(size_t)tile * a.ldh + m] = q.s;
                 }
                 if (lane == 0 && !(amax < (a.y != nullptr ? 3.3961775292304601e38f : INFINITY))) flag(a.st, QSPEC_ERR_NONFINITE);
             }
@@ -329,7 +327,8 @@ int launch_any(const char *where, const uint8_t *xq, const uint8_t *w0, const ui
     if (a.M <= 16) return launch<16, kGated>(where, xq, w0, w1, a, st, kWaitLimit);
     if (a.M <= 32) return launch<32, kGated>(where, xq, w0, w1, a, st, kWaitLimit);
     if (a.M <= 64) return launch<64, kGated>(where, xq, w0, w1, a, st, kWaitLimit);
-    return launch<128, kGated>(where, xq, w0, w1, a, st, kWaitLimit);
+    if (a.M <= 128) return launch<128, kGated>(where, xq, w0, w1, a, st, kWaitLimit);
+    return f8b::launch_tile(where, xq, w0, w1, a, st, kWaitLimit);
 }
 
 }  // namespace f8s

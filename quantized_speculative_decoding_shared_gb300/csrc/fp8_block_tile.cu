@@ -1,0 +1,400 @@
+// fp8_block_tile.cu -- products of E4M3 codes with a scale for each block of 128
+// for many tokens (prompts, verify passes of large batches): the linear, and the gated
+// product.  Definitions: fp8_block_stream.cu.
+//
+// A pair of CTAs takes 256 tokens (the accumulator's lanes, 128 in each CTA) x
+// 256 channels (its columns; gated: 128 of the gate, 128 of the up projection), so that each
+// reads half of either operand: 64 bytes per clock for 128 x 256 x 128 products in 512.
+// Persistent: a pair goes through tiles in groups of 8 token tiles, whose operands
+// stay in L2 while the channels go by.
+// The tensor cores cannot scale a block's sums, so the products of a block (K = 128)
+// go into an accumulator of their own, two of them in turn (all of tensor memory), and
+// eight warps (thread = token, half the channels) add it to 128 sums in registers, times
+// the token's scale and the channels', while the next block's products run: 256 clocks of
+// reads and of packed products against 512 of the tensor cores.  The sums' way out (SiLU,
+// product, maxima, codes) has two blocks' products of the next tile beside it.
+// One lane of each CTA issues its copies, one of the even CTA the products; barriers of
+// filled stages and freed accumulators live in the even CTA, those of freed stages and
+// filled accumulators in both.
+#include <algorithm>
+
+#include "fp8_block_host.h"
+#include "umma.cuh"
+
+namespace qspec {
+
+namespace {
+
+namespace f8t {
+
+using f8b::Args;
+
+constexpr int kRows = 128, kCols = 256;              // of a CTA's accumulator
+constexpr int kWorkWarps = 8, kWork = 32 * kWorkWarps, kLoadWarp = 8, kMmaWarp = 9, kScaleWarp = 10, kThreads = kWork + 128;
+constexpr int kHalfStage = 128 * 128, kStage = 2 * kHalfStage;
+constexpr int kStages = 6;
+constexpr int kBatch = 4, kBatches = 4;              // scales: blocks per hand-over, hand-overs in flight
+constexpr int kGroupTiles = 8;                       // token tiles that go through the channels together
+// registers per thread: all start with 168; 128 sums and their operands need more, the issuing warps less
+constexpr int kRegsWork = 216, kRegsRest = 56;
+static_assert(kThreads * 168 <= 65536 && kWork * kRegsWork + 128 * kRegsRest <= kThreads * 168, "register shares");
+
+struct Ctl {
+    uint64_t full[kStages], empty[kStages];
+    uint64_t acc_full[2], acc_empty[2];
+    uint64_t scale_full[kBatches], scale_empty[kBatches];
+    uint64_t drain;
+    uint32_t tmem;
+    int timeout;
+    float token_scale[kBatches * kBatch][kRows], weight_scale[kBatches * kBatch][2];
+    float top[2][2][kRows];                          // gated: maxima of the two halves of the channels, two tiles' in turn
+};
+constexpr size_t kSmem = 1024 + (size_t)kStages * kStage + sizeof(Ctl);
+
+__device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr) {       // K-major, rows of 128 bytes, 128-byte swizzle
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)1 << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 |
+           (uint64_t)2 << 61;
+}
+__device__ __forceinline__ uint64_t f2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float lo32(uint64_t v) { return __uint_as_float((uint32_t)v); }
+__device__ __forceinline__ float hi32(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ float max_abs(float a, float b, float c) {          // keeps a NaN (a >= 0)
+    float d;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// 8 neighbouring values of a row to bf16, channels n .. n + 7 of N
+__device__ __forceinline__ void store8(uint16_t *row, int n, int N, bool wide, const float (&v)[8]) {
+    if (wide && n + 8 <= N) {
+        *reinterpret_cast<uint4 *>(row + n) =
+            make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (n + e < N) row[n + e] = float_to_bf16_bits(v[e]);
+    }
+}
+
+template <bool kGated>
+__global__ void __launch_bounds__(kThreads, 1)
+    tile_kernel(const __grid_constant__ CUtensorMap t0, const __grid_constant__ CUtensorMap t1,
+                const __grid_constant__ CUtensorMap tx, const __grid_constant__ Args a, int row_tiles, int col_tiles, int wide,
+                uint32_t wait_limit) {
+    constexpr int kChannels = kGated ? 128 : 256;                // channels of a tile
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *stages = smem_raw + ((1024u - (umma::smem_addr(smem_raw) & 1023u)) & 1023u);
+    Ctl &sm = *reinterpret_cast<Ctl *>(stages + (size_t)kStages * kStage);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = (int)umma::cluster_rank();
+    const int pair = (int)(blockIdx.x >> 1), pairs = (int)(gridDim.x >> 1);
+    const int G = a.K / kGroup, tiles = row_tiles * col_tiles;
+    volatile int *timeout = &sm.timeout;
+    auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
+        if (umma::mbar_try_wait(bar, parity & 1)) return true;
+        if (*timeout) return false;
+        if (umma::mbar_wait(bar, parity & 1, wait_limit)) return true;
+        *timeout = 1;
+        return false;
+    };
+    // tile t -> (token tile, channel tile)
+    auto place = [&](int t, int &rt, int &ct) {
+        const int in = kGroupTiles * col_tiles, g = t / in, r = t - g * in;
+        const int rows = min(kGroupTiles, row_tiles - g * kGroupTiles);
+        ct = r / rows;
+        rt = g * kGroupTiles + (r - ct * rows);
+    };
+
+    if (threadIdx.x == 0) {
+        sm.timeout = 0;
+        for (int i = 0; i < kStages; ++i) {
+            umma::mbar_init(&sm.full[i], 1);
+            umma::mbar_init(&sm.empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            umma::mbar_init(&sm.acc_full[i], 1);
+            umma::mbar_init(&sm.acc_empty[i], 2 * kWorkWarps);
+        }
+        for (int i = 0; i < kBatches; ++i) {
+            umma::mbar_init(&sm.scale_full[i], 1);
+            umma::mbar_init(&sm.scale_empty[i], kWorkWarps);
+        }
+        umma::mbar_init(&sm.drain, 1);
+        umma::mbar_fence_init();
+    }
+    if (warp == kMmaWarp) umma::tmem_alloc_pair(&sm.tmem, 2 * kCols);
+    if (warp == kLoadWarp && lane == 0) {
+        umma::prefetch_tmap(&t0);
+        if (kGated) umma::prefetch_tmap(&t1);
+        umma::prefetch_tmap(&tx);
+    }
+    umma::fence_before_sync();
+    umma::cluster_sync();
+    umma::fence_after_sync();
+    pdl_launch_dependents();
+    const uint32_t tmem = sm.tmem;
+    int loads = 0, issued = 0;                                    // blocks whose copies, whose products were issued
+
+    if (warp >= kWorkWarps) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
+        if (warp == kLoadWarp && lane == 0) {
+            const CUtensorMap *tw = kGated && rank == 1 ? &t1 : &t0;
+            pdl_wait();
+            bool ok = true;
+            for (int t = pair; t < tiles && ok; t += pairs) {
+                int rt, ct;
+                place(t, rt, ct);
+                const int m0 = rt * 2 * kRows + rank * kRows, n0 = ct * kChannels + (kGated ? 0 : rank * 128);
+                for (int g = 0; g < G; ++g) {
+                    const int s = loads % kStages;
+                    if (!(ok = loads < kStages || (wait(&sm.empty[s], (uint32_t)(loads / kStages + 1)) && !*timeout))) break;
+                    uint8_t *at = stages + (size_t)s * kStage;
+                    if (rank == 0) umma::mbar_arrive_expect_tx(&sm.full[s], 2 * kStage);      // both CTAs' bytes
+                    const uint32_t bar = umma::peer_addr(&sm.full[s], 0);
+                    umma::tma_load_2d_pair(at, &tx, g * kGroup, m0, bar);
+                    umma::tma_load_2d_pair(at + kHalfStage, tw, g * kGroup, n0, bar);
+                    ++loads;
+                }
+            }
+            // (the last arrivals of the even CTA's products on this CTA's barriers come before it ends)
+            for (int b = max(0, loads - kStages); b < loads; ++b) wait(&sm.empty[b % kStages], (uint32_t)(b / kStages));
+        } else if (warp == kMmaWarp && lane == 0 && rank == 0) {
+            constexpr uint32_t idesc = umma::instr_desc(0, 0, 2 * kRows, kCols);             // e4m3 x e4m3 -> f32
+            bool ok = true;
+            for (int t = pair; t < tiles && ok; t += pairs) {
+                for (int g = 0; g < G; ++g) {
+                    const int s = issued % kStages, b = issued & 1;
+                    if (!(ok = wait(&sm.full[s], (uint32_t)(issued / kStages)) && wait(&sm.acc_empty[b], (uint32_t)(issued / 2 + 1)) &&
+                               !*timeout))
+                        break;
+                    umma::fence_after_sync();
+                    const uint32_t at = umma::smem_addr(stages + (size_t)s * kStage);
+                    const uint64_t ad = desc_sw128(at), bd = desc_sw128(at + kHalfStage);
+#pragma unroll
+                    for (int kk = 0; kk < kGroup / 32; ++kk)      // K = 32 bytes per MMA: +2 in the address field
+                        umma::mma_e4m3_pair(tmem + b * kCols, ad + 2 * kk, bd + 2 * kk, idesc, kk != 0 ? 1u : 0u);
+                    umma::mma_commit_pair(&sm.empty[s], 3);
+                    umma::mma_commit_pair(&sm.acc_full[b], 3);
+                    ++issued;
+                }
+            }
+        } else if (warp == kScaleWarp) {
+            // the blocks' scales, some way ahead of the work (a load from L2 takes as long as two blocks)
+            const int blocks_n = (a.N + kGroup - 1) / kGroup;
+            int t = pair, g = 0, rt, ct;
+            place(t, rt, ct);
+            pdl_wait();
+            for (int base = 0; t < tiles; base += kBatch) {
+                float x[kBatch][kRows / 32], w[kBatch];
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u) {
+                    const bool some = t < tiles;
+                    const int m0 = rt * 2 * kRows + rank * kRows + lane;
+#pragma unroll
+                    for (int i = 0; i < kRows / 32; ++i)
+                        x[u][i] = some && m0 + 32 * i < a.M ? __ldg(a.sa + (size_t)g * a.lds + m0 + 32 * i) : 0.0f;
+                    // lane 0: of the lower half of the channels, or the gate; lane 1: of the upper half, or up
+                    const float *from = kGated && lane == 1 ? a.s1 : a.s0;
+                    w[u] = some && lane < 2 ? __ldg(from + (size_t)(kGated ? ct : min(2 * ct + lane, blocks_n - 1)) * G + g) : 0.0f;
+                    if (++g == G) {
+                        g = 0;
+                        if ((t += pairs) < tiles) place(t, rt, ct);
+                    }
+                }
+                const int slot = base / kBatch % kBatches;
+                if (!__all_sync(0xffffffffu, wait(&sm.scale_empty[slot], (uint32_t)(base / (kBatch * kBatches) + 1)))) break;
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u) {
+#pragma unroll
+                    for (int i = 0; i < kRows / 32; ++i) sm.token_scale[slot * kBatch + u][lane + 32 * i] = x[u][i];
+                    if (lane < 2) sm.weight_scale[slot * kBatch + u][lane] = w[u];
+                }
+                __syncwarp();
+                if (lane == 0) umma::mbar_arrive(&sm.scale_full[slot]);
+            }
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsWork));
+        // ---- thread = token; warps 0 .. 3 the lower half of the channels (gated: of both parts), 4 .. 7 the upper ----
+        const int half = warp >> 2, row = 32 * (warp & 3) + lane;
+        const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+        // columns of its four chunks of 32
+        auto column = [&](int c) { return kGated ? (c >> 1) * 128 + half * 64 + (c & 1) * 32 : half * 128 + c * 32; };
+        const uint32_t freed[2] = {umma::peer_addr(&sm.acc_empty[0], 0), umma::peer_addr(&sm.acc_empty[1], 0)};
+        int done = 0, parity = 0;
+        pdl_wait();
+        for (int t = pair; t < tiles; t += pairs) {
+            int rt, ct;
+            place(t, rt, ct);
+            const int m = rt * 2 * kRows + rank * kRows + row;
+            const bool in = m < a.M;
+            uint64_t acc[4][16];
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+                for (int j = 0; j < 16; ++j) acc[c][j] = 0;
+            bool ok = true;
+            for (int g = 0; g < G; ++g) {
+                const int b = done & 1, at = done % (kBatch * kBatches), slot = at / kBatch;
+                if (at % kBatch == 0 && !__all_sync(0xffffffffu, wait(&sm.scale_full[slot], (uint32_t)(done / (kBatch * kBatches))))) ok = false;
+                const float x = sm.token_scale[at][row];
+                const float s0 = x * sm.weight_scale[at][kGated ? 0 : half], s1 = kGated ? x * sm.weight_scale[at][1] : s0;
+                if (!(ok = ok && __all_sync(0xffffffffu, wait(&sm.acc_full[b], (uint32_t)(done >> 1))))) break;
+                umma::fence_after_sync();
+                // a chunk is on its way while the one before it is added
+                uint32_t d[2][32];
+                umma::tmem_ld32(tmem + lanes + b * kCols + column(0), d[0]);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    umma::tmem_ld_wait();
+                    if (c < 3) umma::tmem_ld32(tmem + lanes + b * kCols + column(c + 1), d[(c + 1) & 1]);
+                    if (c == 3) {
+                        umma::fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) {
+                            umma::mbar_arrive_relaxed_at(freed[b]);
+                            if (at % kBatch == kBatch - 1) umma::mbar_arrive(&sm.scale_empty[slot]);
+                        }
+                    }
+                    const uint64_t s = c < 2 ? f2(s0, s0) : f2(s1, s1);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        acc[c][j] = fma2(f2(__uint_as_float(d[c & 1][2 * j]), __uint_as_float(d[c & 1][2 * j + 1])), s, acc[c][j]);
+                }
+                ++done;
+            }
+            // ---- the sums' way out (after a timeout too, without stores: the warps meet in it) ----
+            if constexpr (!kGated) {
+                if (in && ok) {
+                    uint16_t *y = a.y + (size_t)m * a.ldy;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int j = 0; j < 16; j += 4) {
+                            const float v[8] = {lo32(acc[c][j]), hi32(acc[c][j]), lo32(acc[c][j + 1]), hi32(acc[c][j + 1]),
+                                                lo32(acc[c][j + 2]), hi32(acc[c][j + 2]), lo32(acc[c][j + 3]), hi32(acc[c][j + 3])};
+                            store8(y, ct * kChannels + column(c) + 2 * j, a.N, wide != 0, v);
+                        }
+                }
+            } else {
+                float amax = 0.0f;
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const float v0 = f8b::gated(lo32(acc[c][j]), lo32(acc[c + 2][j]));
+                        const float v1 = f8b::gated(hi32(acc[c][j]), hi32(acc[c + 2][j]));
+                        amax = max_abs(amax, v0, v1);
+                        acc[c][j] = f2(v0, v1);
+                    }
+                sm.top[parity][half][row] = amax;
+                asm volatile("bar.sync 1, %0;" ::"n"(kWork) : "memory");
+                amax = max_abs(amax, sm.top[parity][half ^ 1][row], 0.0f);
+                parity ^= 1;
+                if (in && ok) {
+                    const int n = ct * kChannels + half * 64;
+                    if (a.hq != nullptr) {
+                        const f8b::Quant q(amax);
+                        uint4 *out = reinterpret_cast<uint4 *>(a.hq + (size_t)m * a.N + n);
+#pragma unroll
+                        for (int c = 0; c < 2; ++c)
+#pragma unroll
+                            for (int j = 0; j < 16; j += 8) {
+                                uint32_t w[4];
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    w[e] = q.four(lo32(acc[c][j + 2 * e]), hi32(acc[c][j + 2 * e]), lo32(acc[c][j + 2 * e + 1]),
+                                                  hi32(acc[c][j + 2 * e + 1]));
+                                out[2 * c + j / 8] = make_uint4(w[0], w[1], w[2], w[3]);
+                            }
+                        if (half == 0) a.sh[(size_t)ct * a.ldh + m] = q.s;
+                    }
+                    if (a.y != nullptr) {
+                        uint16_t *y = a.y + (size_t)m * a.ldy;
+#pragma unroll
+                        for (int c = 0; c < 2; ++c)
+#pragma unroll
+                            for (int j = 0; j < 16; j += 4) {
+                                const float v[8] = {lo32(acc[c][j]), hi32(acc[c][j]), lo32(acc[c][j + 1]), hi32(acc[c][j + 1]),
+                                                    lo32(acc[c][j + 2]), hi32(acc[c][j + 2]), lo32(acc[c][j + 3]), hi32(acc[c][j + 3])};
+                                store8(y, n + c * 32 + 2 * j, a.N, wide != 0, v);
+                            }
+                    }
+                    if (half == 0 && !(amax < (a.y != nullptr ? 3.3961775292304601e38f : INFINITY))) flag(a.st, QSPEC_ERR_NONFINITE);
+                }
+            }
+        }
+    }
+
+    // The pair ends together: a CTA's barriers and operands are used by its neighbour's copies and products.  After a
+    // timeout (of either CTA: what it does not do runs out in the other) the issuers have stopped; the products in
+    // flight are waited for, and the copies: by their barriers in the even CTA, whose bytes are both CTAs', then by
+    // time (a copy takes microseconds), as a barrier that lacks one CTA's copies never completes.
+    __syncthreads();
+    if (*timeout) {
+        if (rank == 0 && warp == kMmaWarp && lane == 0 && issued > 0) {
+            umma::mma_commit_pair(&sm.drain, 1);
+            umma::mbar_wait(&sm.drain, 0, kWaitLimit);
+        }
+        if (warp == kLoadWarp && lane == 0) {
+            if (rank == 0)
+                for (int b = max(0, loads - kStages); b < loads; ++b)
+                    umma::mbar_wait(&sm.full[b % kStages], (uint32_t)((b / kStages) & 1), 1u << 12);
+            for (int i = 0; i < 64; ++i) __nanosleep(10000);
+        }
+        if (threadIdx.x == 0) flag(a.st, QSPEC_ERR_TIMEOUT);
+    }
+    umma::fence_before_sync();
+    umma::cluster_sync();
+    if (warp == kMmaWarp) umma::tmem_free_pair(tmem, 2 * kCols);
+}
+
+template <bool kGated>
+int launch(const char *where, const uint8_t *xq, const uint8_t *w0, const uint8_t *w1, const Args &a, cudaStream_t stream,
+           uint32_t wait_limit) {
+    CUtensorMap t0, t1, tx;
+    if (byte_tmap_sw128(&t0, w0, a.N, a.K, (size_t)a.K, 128) || (kGated && byte_tmap_sw128(&t1, w1, a.N, a.K, (size_t)a.K, 128)) ||
+        byte_tmap_sw128(&tx, xq, a.M, a.K, (size_t)a.K, 128))
+        return QSPEC_ERR_UNSUPPORTED;
+    if (!kGated) t1 = t0;
+    auto kern = tile_kernel<kGated>;
+    int rc = smem_limit_once(reinterpret_cast<const void *>(kern), (int)kSmem);
+    if (rc) return rc;
+    constexpr int kChannels = kGated ? 128 : 256;
+    const int row_tiles = (a.M + 2 * kRows - 1) / (2 * kRows), col_tiles = (a.N + kChannels - 1) / kChannels;
+    const long long tiles = (long long)row_tiles * col_tiles;
+    const int pairs = (int)std::min<long long>(tiles, sm_count() / 2);
+    const int wide = a.y != nullptr && aligned(a.y, 16) && a.ldy % 8 == 0;
+    return launch_pdl_cluster(where, kern, dim3((unsigned)(2 * pairs)), dim3(kThreads), kSmem, stream, 2, t0, t1, tx, a, row_tiles,
+                              col_tiles, wide, wait_limit);
+}
+
+}  // namespace f8t
+
+}  // namespace
+
+namespace f8b {
+
+int launch_tile(const char *where, const uint8_t *xq, const uint8_t *w0, const uint8_t *w1, const Args &a, cudaStream_t stream,
+                uint32_t wait_limit) {
+    return w1 != nullptr ? f8t::launch<true>(where, xq, w0, w1, a, stream, wait_limit)
+                         : f8t::launch<false>(where, xq, w0, w1, a, stream, wait_limit);
+}
+
+}  // namespace f8b
+
+}  // namespace qspec

@@ -121,7 +121,7 @@ def codes(M, K, seed, dev):
 
 SHAPES = [(1, 128, 128), (1, 1, 128), (2, 300, 384), (1, 4096, 1152), (5, 1000, 4096), (15, 129, 14336), (16, 128, 256),
           (17, 127, 640), (31, 640, 1408), (33, 257, 2048), (64, 384, 896), (65, 100, 1152), (80, 1024, 4096), (127, 130, 256),
-          (128, 512, 640), (129, 384, 512), (255, 256, 128), (257, 300, 1024), (288, 1152, 1408), (600, 640, 768), (1025, 257, 384)]
+          (128, 512, 640), (129, 384, 512), (255, 256, 128), (257, 300, 1024), (288, 1152, 1408), (600, 640, 768), (1025, 257, 384), (2500, 2560, 256)]
 
 
 @pytest.mark.parametrize("M,N,K", SHAPES)
