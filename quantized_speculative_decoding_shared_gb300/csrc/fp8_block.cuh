@@ -21,26 +21,26 @@ struct Args {
     int lds, M, N, K, ldy, ldh;
 };
 
-// silu(g) u.  exp(-g) passes fp32 below -88.7: 1 / inf is the limit 0; a NaN stays one.
+// h = silu(g) u = g u / (1 + exp(-g)).  exp(-g) passes fp32 below -88.7: 1 / inf is the limit 0; a NaN stays one.
 __device__ __forceinline__ float gated(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
 
 // A block's scale and what its codes are taken with: E4M3(v up inv), inv = 448 / (up max |v|), up = 2^96 where 448 / max
-// |v| would pass fp32.  Within 2 x 2^-24 of v / s in the quotient.  A maximum of 0 gives the codes 0.
+// |v| would pass fp32.  Within 2 x 2^-24 of v / s in the quotient.  A scale of 0 has the codes 0.
 struct Quant {
     float s, inv, up;
     __device__ __forceinline__ explicit Quant(float amax) {
         up = amax < 1.0e-30f ? 7.9228162514264338e28f : 1.0f;
         s = __fdiv_rn(amax, 448.0f);
-        inv = amax > 0.0f ? __fdiv_rn(448.0f, amax * up) : 0.0f;
-    }
-    // two codes, the first in the low byte
-    __device__ __forceinline__ uint32_t two(float a, float b) const {
-        return __nv_cvt_float2_to_fp8x2(make_float2(a * up * inv, b * up * inv), __NV_SATFINITE, __NV_E4M3);
-    }
-    __device__ __forceinline__ uint32_t four(float a, float b, float c, float d) const {
-        return s == 0.0f ? 0u : two(a, b) | two(c, d) << 16;
+        inv = s > 0.0f ? __fdiv_rn(448.0f, amax * up) : 0.0f;
     }
 };
+
+// four codes, the first in the low byte
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+    return lo | hi << 16;
+}
 
 }  // namespace f8b
 }  // namespace qspec

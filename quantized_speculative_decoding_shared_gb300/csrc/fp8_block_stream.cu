@@ -278,7 +278,8 @@ __global__ void __launch_bounds__(kThreads, (Cfg<BN, kGated>::kOcc))
                 }
                 if (a.hq != nullptr) {
                     const f8b::Quant q(amax);
-                    reinterpret_cast<uint32_t *>(a.hq + (size_t)m * a.N + n0)[lane] = q.four(v[0][0], v[0][1], v[0][2], v[0][3]);
+                    reinterpret_cast<uint32_t *>(a.hq + (size_t)m * a.N + n0)[lane] =
+                        q.s == 0.0f ? 0u : f8b::codes4(v[0][0] * q.up * q.inv, v[0][1] * q.up * q.inv, v[0][2] * q.up * q.inv, v[0][3] * q.up * q.inv);
                     if (lane == 0) a.sh[(size_t)tile * a.ldh + m] = q.s;
                 }
                 if (lane == 0 && !(amax < (a.y != nullptr ? 3.3961775292304601e38f : INFINITY))) flag(a.st, QSPEC_ERR_NONFINITE);

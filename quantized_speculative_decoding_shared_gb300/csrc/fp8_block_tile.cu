@@ -14,8 +14,8 @@
 // reads and of packed products against 512 of the tensor cores.  The sums' way out (SiLU,
 // product, maxima, codes) has two blocks' products of the next tile beside it.
 // One lane of each CTA issues its copies, one of the even CTA the products; barriers of
-// filled stages and freed accumulators live in the even CTA, those of freed stages and
-// filled accumulators in both.
+// filled stages and freed accumulators live in the even CTA, those of finished products
+// (a stage free, an accumulator full) in both.
 #include <algorithm>
 
 #include "fp8_block_host.h"
@@ -36,12 +36,12 @@ constexpr int kStages = 6;
 constexpr int kBatch = 4, kBatches = 4;              // scales: blocks per hand-over, hand-overs in flight
 constexpr int kGroupTiles = 8;                       // token tiles that go through the channels together
 // registers per thread: all start with 168; 128 sums and their operands need more, the issuing warps less
-constexpr int kRegsWork = 216, kRegsRest = 56;
+constexpr int kRegsWork = 200, kRegsRest = 96;
 static_assert(kThreads * 168 <= 65536 && kWork * kRegsWork + 128 * kRegsRest <= kThreads * 168, "register shares");
 
 struct Ctl {
-    uint64_t full[kStages], empty[kStages];
-    uint64_t acc_full[2], acc_empty[2];
+    uint64_t full[kStages], done[kStages];           // a stage's copies landed; its products done: stage free, sums there
+    uint64_t acc_empty[2];
     uint64_t scale_full[kBatches], scale_empty[kBatches];
     uint64_t drain;
     uint32_t tmem;
@@ -65,6 +65,26 @@ __device__ __forceinline__ float hi32(uint64_t v) { return __uint_as_float((uint
 __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
     uint64_t d;
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float min_of(float a, float b, float c) {           // keeps a NaN
+    float d;
+    asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
@@ -111,11 +131,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         *timeout = 1;
         return false;
     };
+    auto all = [](bool mine) { return __all_sync(0xffffffffu, mine) != 0; };
     // tile t -> (token tile, channel tile)
     auto place = [&](int t, int &rt, int &ct) {
         const int in = kGroupTiles * col_tiles, g = t / in, r = t - g * in;
         const int rows = min(kGroupTiles, row_tiles - g * kGroupTiles);
-        ct = r / rows;
+        ct = rows == kGroupTiles ? r / kGroupTiles : r / rows;
         rt = g * kGroupTiles + (r - ct * rows);
     };
 
@@ -123,12 +144,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         sm.timeout = 0;
         for (int i = 0; i < kStages; ++i) {
             umma::mbar_init(&sm.full[i], 1);
-            umma::mbar_init(&sm.empty[i], 1);
+            umma::mbar_init(&sm.done[i], 1);
         }
-        for (int i = 0; i < 2; ++i) {
-            umma::mbar_init(&sm.acc_full[i], 1);
-            umma::mbar_init(&sm.acc_empty[i], 2 * kWorkWarps);
-        }
+        for (int i = 0; i < 2; ++i) umma::mbar_init(&sm.acc_empty[i], 2 * kWorkWarps);
         for (int i = 0; i < kBatches; ++i) {
             umma::mbar_init(&sm.scale_full[i], 1);
             umma::mbar_init(&sm.scale_empty[i], kWorkWarps);
@@ -151,46 +169,63 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp >= kWorkWarps) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
-        if (warp == kLoadWarp && lane == 0) {
+        // (the issuing warps go through their loops whole and elect a lane where it counts: a lane's own loop is
+        // slower by the divergence that the compiler allows for at every step)
+        if (warp == kLoadWarp) {
             const CUtensorMap *tw = kGated && rank == 1 ? &t1 : &t0;
+            const bool elected = umma::elect_one();
             pdl_wait();
             bool ok = true;
+            int s = 0, turn = 0;                                  // the stage, and how often it was filled before
             for (int t = pair; t < tiles && ok; t += pairs) {
                 int rt, ct;
                 place(t, rt, ct);
                 const int m0 = rt * 2 * kRows + rank * kRows, n0 = ct * kChannels + (kGated ? 0 : rank * 128);
                 for (int g = 0; g < G; ++g) {
-                    const int s = loads % kStages;
-                    if (!(ok = loads < kStages || (wait(&sm.empty[s], (uint32_t)(loads / kStages + 1)) && !*timeout))) break;
-                    uint8_t *at = stages + (size_t)s * kStage;
-                    if (rank == 0) umma::mbar_arrive_expect_tx(&sm.full[s], 2 * kStage);      // both CTAs' bytes
-                    const uint32_t bar = umma::peer_addr(&sm.full[s], 0);
-                    umma::tma_load_2d_pair(at, &tx, g * kGroup, m0, bar);
-                    umma::tma_load_2d_pair(at + kHalfStage, tw, g * kGroup, n0, bar);
+                    if (!(ok = turn == 0 || all(wait(&sm.done[s], (uint32_t)(turn + 1))))) break;
+                    if (elected) {
+                        uint8_t *at = stages + (size_t)s * kStage;
+                        if (rank == 0) umma::mbar_arrive_expect_tx(&sm.full[s], 2 * kStage);      // both CTAs' bytes
+                        const uint32_t bar = umma::peer_addr(&sm.full[s], 0);
+                        umma::tma_load_2d_pair(at, &tx, g * kGroup, m0, bar);
+                        umma::tma_load_2d_pair(at + kHalfStage, tw, g * kGroup, n0, bar);
+                    }
+                    __syncwarp();
                     ++loads;
+                    if (++s == kStages) {
+                        s = 0;
+                        ++turn;
+                    }
                 }
             }
             // (the last arrivals of the even CTA's products on this CTA's barriers come before it ends)
-            for (int b = max(0, loads - kStages); b < loads; ++b) wait(&sm.empty[b % kStages], (uint32_t)(b / kStages));
-        } else if (warp == kMmaWarp && lane == 0 && rank == 0) {
+            for (int b = max(0, loads - kStages); b < loads; ++b) wait(&sm.done[b % kStages], (uint32_t)(b / kStages));
+        } else if (warp == kMmaWarp && rank == 0) {
             constexpr uint32_t idesc = umma::instr_desc(0, 0, 2 * kRows, kCols);             // e4m3 x e4m3 -> f32
+            const bool elected = umma::elect_one();
             bool ok = true;
-            for (int t = pair; t < tiles && ok; t += pairs) {
-                for (int g = 0; g < G; ++g) {
-                    const int s = issued % kStages, b = issued & 1;
-                    if (!(ok = wait(&sm.full[s], (uint32_t)(issued / kStages)) && wait(&sm.acc_empty[b], (uint32_t)(issued / 2 + 1)) &&
-                               !*timeout))
-                        break;
-                    umma::fence_after_sync();
-                    const uint32_t at = umma::smem_addr(stages + (size_t)s * kStage);
-                    const uint64_t ad = desc_sw128(at), bd = desc_sw128(at + kHalfStage);
+            int s = 0;
+            uint32_t turn = 0;
+            const int blocks = (tiles - pair + pairs - 1) / pairs * G;
+            ok = all(wait(&sm.full[0], 0));
+            for (; issued < blocks && ok; ++issued) {
+                const int b = issued & 1;
+                if (!(ok = all(wait(&sm.acc_empty[b], (uint32_t)(issued / 2 + 1))))) break;
+                umma::fence_after_sync();
+                const uint32_t at = umma::smem_addr(stages + (size_t)s * kStage);
+                const uint64_t ad = desc_sw128(at), bd = desc_sw128(at + kHalfStage);
+                if (elected) {
 #pragma unroll
                     for (int kk = 0; kk < kGroup / 32; ++kk)      // K = 32 bytes per MMA: +2 in the address field
                         umma::mma_e4m3_pair(tmem + b * kCols, ad + 2 * kk, bd + 2 * kk, idesc, kk != 0 ? 1u : 0u);
-                    umma::mma_commit_pair(&sm.empty[s], 3);
-                    umma::mma_commit_pair(&sm.acc_full[b], 3);
-                    ++issued;
+                    umma::mma_commit_pair(&sm.done[s], 3);
                 }
+                __syncwarp();
+                if (++s == kStages) {
+                    s = 0;
+                    ++turn;
+                }
+                if (issued + 1 < blocks) ok = all(wait(&sm.full[s], turn));
             }
         } else if (warp == kScaleWarp) {
             // the blocks' scales, some way ahead of the work (a load from L2 takes as long as two blocks)
@@ -216,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 const int slot = base / kBatch % kBatches;
-                if (!__all_sync(0xffffffffu, wait(&sm.scale_empty[slot], (uint32_t)(base / (kBatch * kBatches) + 1)))) break;
+                if (!all(wait(&sm.scale_empty[slot], (uint32_t)(base / (kBatch * kBatches) + 1)))) break;
 #pragma unroll
                 for (int u = 0; u < kBatch; ++u) {
 #pragma unroll
@@ -250,10 +285,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok = true;
             for (int g = 0; g < G; ++g) {
                 const int b = done & 1, at = done % (kBatch * kBatches), slot = at / kBatch;
-                if (at % kBatch == 0 && !__all_sync(0xffffffffu, wait(&sm.scale_full[slot], (uint32_t)(done / (kBatch * kBatches))))) ok = false;
+                if (at % kBatch == 0 && !all(wait(&sm.scale_full[slot], (uint32_t)(done / (kBatch * kBatches))))) ok = false;
                 const float x = sm.token_scale[at][row];
                 const float s0 = x * sm.weight_scale[at][kGated ? 0 : half], s1 = kGated ? x * sm.weight_scale[at][1] : s0;
-                if (!(ok = ok && __all_sync(0xffffffffu, wait(&sm.acc_full[b], (uint32_t)(done >> 1))))) break;
+                if (!(ok = ok && all(wait(&sm.done[done % kStages], (uint32_t)(done / kStages))))) break;
                 umma::fence_after_sync();
                 // a chunk is on its way while the one before it is added
                 uint32_t d[2][32];
@@ -291,38 +326,43 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                 }
             } else {
-                float amax = 0.0f;
+                // h = g u / (1 + exp(-g)), two quotients from one reciprocal 1 / (a b) where no gate of the warp's is so
+                // low that the product passes fp32: the reciprocals and exponentials bound this part
+                constexpr float kLog2e = 1.4426950408889634f;
+                float low = 0.0f, amax = 0.0f;
 #pragma unroll
                 for (int c = 0; c < 2; ++c)
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const float v0 = f8b::gated(lo32(acc[c][j]), lo32(acc[c + 2][j]));
-                        const float v1 = f8b::gated(hi32(acc[c][j]), hi32(acc[c + 2][j]));
-                        amax = max_abs(amax, v0, v1);
-                        acc[c][j] = f2(v0, v1);
-                    }
+                    for (int j = 0; j < 16; ++j) low = min_of(low, lo32(acc[c][j]), hi32(acc[c][j]));
+                if (all(low >= -43.0f)) {
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            const uint64_t x = mul2(acc[c][j], f2(-kLog2e, -kLog2e));
+                            const uint64_t e = add2(f2(ex2(lo32(x)), ex2(hi32(x))), f2(1.0f, 1.0f));
+                            const float r = rcp_approx(lo32(e) * hi32(e));
+                            const uint64_t v = mul2(mul2(acc[c][j], mul2(f2(hi32(e), lo32(e)), f2(r, r))), acc[c + 2][j]);
+                            amax = max_abs(amax, lo32(v), hi32(v));
+                            acc[c][j] = v;
+                        }
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            const float v0 = f8b::gated(lo32(acc[c][j]), lo32(acc[c + 2][j]));
+                            const float v1 = f8b::gated(hi32(acc[c][j]), hi32(acc[c + 2][j]));
+                            amax = max_abs(amax, v0, v1);
+                            acc[c][j] = f2(v0, v1);
+                        }
+                }
                 sm.top[parity][half][row] = amax;
                 asm volatile("bar.sync 1, %0;" ::"n"(kWork) : "memory");
                 amax = max_abs(amax, sm.top[parity][half ^ 1][row], 0.0f);
                 parity ^= 1;
                 if (in && ok) {
                     const int n = ct * kChannels + half * 64;
-                    if (a.hq != nullptr) {
-                        const f8b::Quant q(amax);
-                        uint4 *out = reinterpret_cast<uint4 *>(a.hq + (size_t)m * a.N + n);
-#pragma unroll
-                        for (int c = 0; c < 2; ++c)
-#pragma unroll
-                            for (int j = 0; j < 16; j += 8) {
-                                uint32_t w[4];
-#pragma unroll
-                                for (int e = 0; e < 4; ++e)
-                                    w[e] = q.four(lo32(acc[c][j + 2 * e]), hi32(acc[c][j + 2 * e]), lo32(acc[c][j + 2 * e + 1]),
-                                                  hi32(acc[c][j + 2 * e + 1]));
-                                out[2 * c + j / 8] = make_uint4(w[0], w[1], w[2], w[3]);
-                            }
-                        if (half == 0) a.sh[(size_t)ct * a.ldh + m] = q.s;
-                    }
                     if (a.y != nullptr) {
                         uint16_t *y = a.y + (size_t)m * a.ldy;
 #pragma unroll
@@ -333,6 +373,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                     lo32(acc[c][j + 2]), hi32(acc[c][j + 2]), lo32(acc[c][j + 3]), hi32(acc[c][j + 3])};
                                 store8(y, n + c * 32 + 2 * j, a.N, wide != 0, v);
                             }
+                    }
+                    if (a.hq != nullptr) {
+                        const f8b::Quant q(amax);
+                        const uint64_t by = f2(q.inv, q.inv);
+                        if (q.up != 1.0f) {                              // (h in bf16 was stored before; no code of -0 for a scale of 0)
+#pragma unroll
+                            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                                for (int j = 0; j < 16; ++j) acc[c][j] = q.s == 0.0f ? 0 : mul2(acc[c][j], f2(q.up, q.up));
+                        }
+                        uint4 *out = reinterpret_cast<uint4 *>(a.hq + (size_t)m * a.N + n);
+#pragma unroll
+                        for (int c = 0; c < 2; ++c)
+#pragma unroll
+                            for (int j = 0; j < 16; j += 8) {
+                                uint32_t w[4];
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    const uint64_t v0 = mul2(acc[c][j + 2 * e], by), v1 = mul2(acc[c][j + 2 * e + 1], by);
+                                    w[e] = f8b::codes4(lo32(v0), hi32(v0), lo32(v1), hi32(v1));
+                                }
+                                out[2 * c + j / 8] = make_uint4(w[0], w[1], w[2], w[3]);
+                            }
+                        if (half == 0) a.sh[(size_t)ct * a.ldh + m] = q.s;
                     }
                     if (half == 0 && !(amax < (a.y != nullptr ? 3.3961775292304601e38f : INFINITY))) flag(a.st, QSPEC_ERR_NONFINITE);
                 }
@@ -346,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // time (a copy takes microseconds), as a barrier that lacks one CTA's copies never completes.
     __syncthreads();
     if (*timeout) {
-        if (rank == 0 && warp == kMmaWarp && lane == 0 && issued > 0) {
+        if (rank == 0 && warp == kMmaWarp && umma::elect_one() && issued > 0) {
             umma::mma_commit_pair(&sm.drain, 1);
             umma::mbar_wait(&sm.drain, 0, kWaitLimit);
         }
