@@ -6,12 +6,13 @@
 //   gated: h = silu(gate) up, out as E4M3 with a scale per token and 128 and / or bf16
 //
 // The weights are read once, so HBM bounds it: 128 output channels are the lanes
-// of the accumulator, BN tokens its columns.  TMA fills a ring of stages, one
-// block of K to a stage (128 x 128 bytes of weights, twice for the gated one, and
-// BN x 128 of the tokens); one lane issues the four products of a block into an
-// accumulator of its own, and eight warps (thread = channel, half the tokens each)
-// add it to their registers in fp32, times the block's two scales, while the next
-// block's products run.
+// of the accumulator, up to 256 tokens its columns (gated: up to 128, for each of the
+// two parts).  TMA fills a ring of stages, one block of K to a stage (128 x 128 bytes of
+// weights, twice for the gated one, and the tokens' 128 bytes each); one warp issues the
+// products of a block into an accumulator of its own, and eight warps (thread = channel,
+// half the tokens each) add it to their registers in fp32, times the block's scales, while
+// the next blocks' products run.  The scales' products (token times weight) are made by
+// a warp of its own, some blocks ahead.
 // K is split over the CTAs of a cluster where the channels alone would leave
 // multiprocessors idle; the parts meet in shared memory, in the order of K: a warp
 // takes a token, its lanes four channels each, so that the maximum of 128 channels
@@ -30,23 +31,31 @@ namespace f8s {
 using f8b::Args;
 
 constexpr int kTile = 128;                       // channels per CTA, and K per stage
-constexpr int kWorkWarps = 8, kLoadWarp = 8, kMmaWarp = 9, kThreads = 320;
+constexpr int kWorkWarps = 8, kWork = 32 * kWorkWarps, kLoadWarp = 8, kMmaWarp = 9, kScaleWarp = 10, kThreads = kWork + 128;
+constexpr int kBatch = 4, kBatches = 2;          // scales: blocks per hand-over, hand-overs in flight
+constexpr int kMaxSplit = 8;
 
+// BN: most tokens of a CTA
 template <int BN, bool kGated>
 struct Cfg {
-    static constexpr int kParts = kGated ? 2 : 1;
+    static constexpr int kParts = kGated ? 2 : 1, kHalf = BN / 2;
     static constexpr int kCols = BN * kParts;                    // accumulator columns of one block
     static constexpr int kStage = kTile * kTile * kParts + BN * kTile;
-    static constexpr int kOcc = BN / 2 * kParts <= 64 ? 2 : 1;   // CTAs per SM: as the sums leave registers for
-    static constexpr int kTmem = kOcc == 2 ? 256 : 512;
-    static constexpr int kBufs = kTmem / kCols < 4 ? kTmem / kCols : 4;
-    static constexpr uint32_t kAlloc = kBufs * kCols < 32 ? 32 : kBufs * kCols;
-    static constexpr int kBudget = kOcc == 2 ? 110 * 1024 : 220 * 1024;
-    static constexpr int kCtl = 1024 + 2 * kWorkWarps * (BN / 2) * 4 * kParts;        // barriers; scales of the warps
-    static constexpr int kStages = (kBudget - 1024 - kCtl) / kStage < 8 ? (kBudget - 1024 - kCtl) / kStage : 8;
+    static constexpr int kOcc = kCols <= 64 && kStage <= 36 * 1024 - 1024 ? 2 : 1;    // CTAs per SM, as stages and sums allow
+    static constexpr int kFit = 512 / kOcc / kCols < 4 ? 512 / kOcc / kCols : 4;      // accumulators in tensor memory
+    static constexpr int kCtl = 512, kScales = kBatch * kBatches * kCols * 4;        // barriers; scales of blocks to come
+    static constexpr int kBudget = (kOcc == 2 ? 112 : 224) * 1024 - 1024 - kCtl - kScales;
+    static constexpr int kStages = kBudget / kStage < 8 ? kBudget / kStage : 8;
+    // A stage's barrier also tells the work of its sums: it must not complete twice while a warp has yet to look at it, so
+    // the products of the block that next uses the stage wait for all warps to have read this one's
+    static constexpr int kBufs = kFit < kStages ? kFit : kStages;
+    static constexpr uint32_t kAlloc = kBufs * kCols <= 32 ? 32 : kBufs * kCols <= 64 ? 64 : kBufs * kCols <= 128 ? 128 : kBufs * kCols <= 256 ? 256 : 512;
     static constexpr int kJoin = kCols * kTile * 4;              // a CTA's sums, over the stages
-    static_assert(kStages >= 2 && kJoin <= kStages * kStage, "shared memory");
-    static constexpr size_t kSmem = 1024 + (size_t)kStages * kStage + kCtl;
+    static_assert(kStages >= 3 && kJoin <= kStages * kStage, "shared memory");
+    static constexpr size_t kSmem = 1024 + (size_t)kStages * kStage + kCtl + kScales;
+    // registers per thread at launch and after the warps have shared them out
+    static constexpr int kRegs = kOcc == 2 ? 80 : 168, kRegsWork = kOcc == 2 ? 96 : 200, kRegsRest = kOcc == 2 ? 48 : 96;
+    static_assert(kOcc * kThreads * kRegs <= 65536 && kWork * kRegsWork + 128 * kRegsRest <= kThreads * kRegs, "register shares");
 };
 
 __device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr) {       // K-major, rows of 128 bytes, 128-byte swizzle
@@ -54,193 +63,241 @@ __device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr) {       // K-majo
            (uint64_t)2 << 61;
 }
 
+__device__ __forceinline__ uint64_t f2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float lo32(uint64_t v) { return __uint_as_float((uint32_t)v); }
+__device__ __forceinline__ float hi32(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+
 template <int BN, bool kGated>
 __global__ void __launch_bounds__(kThreads, (Cfg<BN, kGated>::kOcc))
     stream_kernel(const __grid_constant__ CUtensorMap t0, const __grid_constant__ CUtensorMap t1,
-                  const __grid_constant__ CUtensorMap tx, const __grid_constant__ Args a, int split, uint32_t wait_limit) {
+                  const __grid_constant__ CUtensorMap tx, const __grid_constant__ Args a, int bn, int split, uint32_t wait_limit) {
     using C = Cfg<BN, kGated>;
-    constexpr int S = C::kStages, kParts = C::kParts, kHalf = BN / 2, kLd = kHalf < 16 ? kHalf : 16;   // (32 at a time spill)
+    constexpr int S = C::kStages, kParts = C::kParts, kHalf = C::kHalf, kLd = kHalf < 16 ? kHalf : 16;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *stages = smem_raw + ((1024u - (umma::smem_addr(smem_raw) & 1023u)) & 1023u);
     uint64_t *full = reinterpret_cast<uint64_t *>(stages + (size_t)S * C::kStage);
-    uint64_t *empty = full + S, *acc_full = empty + S, *acc_empty = acc_full + C::kBufs, *drain = acc_empty + C::kBufs;
+    uint64_t *done = full + S, *acc_empty = done + S, *scale_full = acc_empty + C::kBufs, *scale_empty = scale_full + kBatches,
+             *drain = scale_empty + kBatches;
     uint32_t *tslot = reinterpret_cast<uint32_t *>(drain + 1);
     volatile int *timeout = reinterpret_cast<volatile int *>(tslot + 1);
-    float *scales = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(full) + 1024);
+    float *scales = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(full) + C::kCtl);     // [slot][part][token]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = (int)(blockIdx.x % (unsigned)split), tile = (int)(blockIdx.x / (unsigned)split);
-    const int n0 = tile * kTile, m0 = blockIdx.y * BN;
+    const int n0 = tile * kTile, m0 = blockIdx.y * bn;
     const int G = a.K / kGroup;
-    const int k0 = (int)((long long)G * rank / split), k1 = (int)((long long)G * (rank + 1) / split), nk = k1 - k0;
+    const int k0 = (int)((long long)G * rank / split), nk = (int)((long long)G * (rank + 1) / split) - k0;
     auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
+        if (umma::mbar_try_wait(bar, parity & 1)) return true;
         if (*timeout) return false;
         if (umma::mbar_wait(bar, parity & 1, wait_limit)) return true;
         *timeout = 1;
         return false;
     };
+    auto all = [](bool mine) { return __all_sync(0xffffffffu, mine) != 0; };
+    const uint32_t bytes = (uint32_t)(kParts * kTile * kTile + bn * kTile);
+    auto load_weights = [&](int i) {
+        uint8_t *stg = stages + (size_t)(i % S) * C::kStage;
+        umma::mbar_arrive_expect_tx(&full[i % S], bytes);
+        umma::tma_load_2d(stg, &t0, (k0 + i) * kGroup, n0, &full[i % S]);
+        if (kGated) umma::tma_load_2d(stg + kTile * kTile, &t1, (k0 + i) * kGroup, n0, &full[i % S]);
+    };
+    auto load_tokens = [&](int i) {
+        umma::tma_load_2d(stages + (size_t)(i % S) * C::kStage + kParts * kTile * kTile, &tx, (k0 + i) * kGroup, m0, &full[i % S]);
+    };
 
-    if (threadIdx.x == 0) {
+    const bool elected = umma::elect_one();
+    const int pre = min(S, nk);
+    if (warp == kLoadWarp && elected) {
         *timeout = 0;
         for (int i = 0; i < S; ++i) {
             umma::mbar_init(&full[i], 1);
-            umma::mbar_init(&empty[i], 1);
+            umma::mbar_init(&done[i], 1);
         }
-        for (int i = 0; i < C::kBufs; ++i) {
-            umma::mbar_init(&acc_full[i], 1);
-            umma::mbar_init(&acc_empty[i], kWorkWarps);
+        for (int i = 0; i < C::kBufs; ++i) umma::mbar_init(&acc_empty[i], kWorkWarps);
+        for (int i = 0; i < kBatches; ++i) {
+            umma::mbar_init(&scale_full[i], 1);
+            umma::mbar_init(&scale_empty[i], kWorkWarps);
         }
         umma::mbar_init(drain, 1);
         umma::mbar_fence_init();
+        umma::fence_proxy_async();
+        // the first stages' weights at once, before the dependency wait too (they are immutable)
+        for (int i = 0; i < pre; ++i) load_weights(i);
     }
     if (warp == kMmaWarp) umma::tmem_alloc(tslot, C::kAlloc);
-    if (warp == kLoadWarp && lane == 0) {
-        umma::prefetch_tmap(&t0);
-        if (kGated) umma::prefetch_tmap(&t1);
-        umma::prefetch_tmap(&tx);
-    }
     umma::fence_before_sync();
     __syncthreads();
     umma::fence_after_sync();
     pdl_launch_dependents();
     const uint32_t tmem = *tslot;
     int loads = 0, issued = 0;
-    float acc[kParts][kHalf];
+    // all warps' way to the end: the CTA's, then (behind a timeout's drain) the cluster's barrier
+    auto meet = [&]() {
+        if (split > 1)
+            umma::cluster_sync();
+        else
+            __syncthreads();
+    };
 
-    if (warp == kLoadWarp) {
-        if (lane == 0) {
-            auto weights = [&](int i) {
-                uint8_t *stg = stages + (size_t)(i % S) * C::kStage;
-                umma::mbar_arrive_expect_tx(&full[i % S], C::kStage);
-                umma::tma_load_2d(stg, &t0, (k0 + i) * kGroup, n0, &full[i % S]);
-                if (kGated) umma::tma_load_2d(stg + kTile * kTile, &t1, (k0 + i) * kGroup, n0, &full[i % S]);
-            };
-            auto tokens = [&](int i) {
-                umma::tma_load_2d(stages + (size_t)(i % S) * C::kStage + kParts * kTile * kTile, &tx, (k0 + i) * kGroup, m0,
-                                  &full[i % S]);
-            };
-            // the first stages' weights before the dependency wait (they are immutable)
-            const int pre = min(S, nk);
-            for (int i = 0; i < pre; ++i) weights(i);
+    if (warp >= kWorkWarps) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsRest));
+        if (warp == kLoadWarp) {
             pdl_wait();
-            for (int i = 0; i < pre; ++i) tokens(i);
+            if (elected)
+                for (int i = 0; i < pre; ++i) load_tokens(i);
+            __syncwarp();
             loads = pre;
             for (int i = pre; i < nk; ++i) {
-                if (!wait(&empty[i % S], (uint32_t)(i / S + 1))) break;
-                weights(i);
-                tokens(i);
+                if (!all(wait(&done[i % S], (uint32_t)(i / S + 1)))) break;
+                if (elected) {
+                    load_weights(i);
+                    load_tokens(i);
+                }
+                __syncwarp();
                 loads = i + 1;
             }
-        }
-    } else if (warp == kMmaWarp) {
-        if (lane == 0) {
-            constexpr uint32_t idesc = umma::instr_desc(0, 0, kTile, BN);        // e4m3 x e4m3 -> f32
+        } else if (warp == kMmaWarp) {
+            const uint32_t idesc = umma::instr_desc(0, 0, kTile, bn);            // e4m3 x e4m3 -> f32
             for (int i = 0; i < nk; ++i) {
                 const int s = i % S, b = i % C::kBufs;
-                if (!wait(&full[s], (uint32_t)(i / S)) || !wait(&acc_empty[b], (uint32_t)(i / C::kBufs + 1))) break;
+                if (!all(wait(&full[s], (uint32_t)(i / S))) || !all(wait(&acc_empty[b], (uint32_t)(i / C::kBufs + 1)))) break;
                 umma::fence_after_sync();
                 const uint32_t at = umma::smem_addr(stages + (size_t)s * C::kStage);
                 const uint64_t bd = desc_sw128(at + kParts * kTile * kTile);
+                if (elected) {
 #pragma unroll
-                for (int p = 0; p < kParts; ++p) {
-                    const uint64_t ad = desc_sw128(at + p * kTile * kTile);
+                    for (int p = 0; p < kParts; ++p) {
+                        const uint64_t ad = desc_sw128(at + p * kTile * kTile);
 #pragma unroll
-                    for (int kk = 0; kk < kGroup / 32; ++kk)                     // K = 32 bytes per MMA: +2 in the address field
-                        umma::mma_e4m3(tmem + b * C::kCols + p * BN, ad + 2 * kk, bd + 2 * kk, idesc, kk != 0 ? 1u : 0u);
+                        for (int kk = 0; kk < kGroup / 32; ++kk)                 // K = 32 bytes per MMA: +2 in the address field
+                            umma::mma_e4m3(tmem + b * C::kCols + p * BN, ad + 2 * kk, bd + 2 * kk, idesc, kk != 0 ? 1u : 0u);
+                    }
+                    umma::mma_commit(&done[s]);                                  // the stage is free, the sums are there
                 }
-                umma::mma_commit(&empty[s]);
-                umma::mma_commit(&acc_full[b]);
+                __syncwarp();
                 issued = i + 1;
             }
+        } else if (warp == kScaleWarp) {
+            constexpr int kEach = (BN + 31) / 32;
+            const float *w0 = a.s0 + (size_t)tile * G + k0, *w1 = kGated ? a.s1 + (size_t)tile * G + k0 : nullptr;
+            pdl_wait();
+            for (int base = 0; base < nk; base += kBatch) {
+                float x[kBatch][kEach], s0[kBatch], s1[kBatch];
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u) {
+                    const bool some = base + u < nk;
+                    s0[u] = some ? __ldg(w0 + base + u) : 0.0f;
+                    s1[u] = some && kGated ? __ldg(w1 + base + u) : 0.0f;
+#pragma unroll
+                    for (int e = 0; e < kEach; ++e) {
+                        const int j = lane + 32 * e, m = m0 + j;
+                        x[u][e] = some && j < bn && m < a.M ? __ldg(a.sa + (size_t)(k0 + base + u) * a.lds + m) : 0.0f;
+                    }
+                }
+                const int slot = base / kBatch % kBatches;
+                if (!all(wait(&scale_empty[slot], (uint32_t)(base / (kBatch * kBatches) + 1)))) break;
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u)
+#pragma unroll
+                    for (int e = 0; e < kEach; ++e)
+                        if (BN >= 32 || lane < BN) {
+                            float *at = scales + (slot * kBatch + u) * C::kCols + lane + 32 * e;
+                            at[0] = x[u][e] * s0[u];
+                            if (kGated) at[BN] = x[u][e] * s1[u];
+                        }
+                __syncwarp();
+                if (lane == 0) umma::mbar_arrive(&scale_full[slot]);
+            }
         }
+        // after a timeout: the copies and products in flight finish (bounded) before the memory they use is used
+        // again; both issuers stopped at the timeout, so at most S copies are outstanding
+        __syncthreads();
+        if (*timeout) {
+            if (warp == kLoadWarp && elected)
+                for (int b = max(0, loads - S); b < loads; ++b) umma::mbar_wait(&full[b % S], (uint32_t)((b / S) & 1), kWaitLimit);
+            if (warp == kMmaWarp && elected && issued > 0) {
+                umma::mma_commit(drain);
+                umma::mbar_wait(drain, 0, kWaitLimit);
+            }
+            if (warp == kScaleWarp && lane == 0) flag(a.st, QSPEC_ERR_TIMEOUT);
+            __syncwarp();
+        }
+        meet();
+        if (warp == kMmaWarp) umma::tmem_free(tmem, C::kAlloc);
     } else {
-        // ---- thread = channel, kHalf tokens: sum over the blocks ----
-        const int c0 = (warp >> 2) * kHalf;                      // first of its tokens
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegsWork));
+        // ---- thread = channel, half the tokens: sum over the blocks ----
+        const int half = bn / 2, c0 = (warp >> 2) * half;        // its tokens: c0 .. c0 + half - 1
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-        float *mine = scales + warp * (2 * kHalf * kParts);      // its scales, two blocks' in turn
+        uint64_t acc[kParts][kHalf / 2];
 #pragma unroll
         for (int p = 0; p < kParts; ++p)
 #pragma unroll
-            for (int j = 0; j < kHalf; ++j) acc[p][j] = 0.0f;
-        const float *w0 = a.s0 + (size_t)tile * G + k0, *w1 = kGated ? a.s1 + (size_t)tile * G + k0 : nullptr;
-        constexpr int kEach = (kHalf + 31) / 32;
-        float next[kEach], n0s = 0.0f, n1s = 0.0f;
-        auto ask = [&](int i) {                                   // scales of block i
-            n0s = __ldg(w0 + i);
-            if (kGated) n1s = __ldg(w1 + i);
-#pragma unroll
-            for (int e = 0; e < kEach; ++e) {
-                const int j = lane + 32 * e, m = m0 + c0 + j;
-                next[e] = j < kHalf && m < a.M ? __ldg(a.sa + (size_t)(k0 + i) * a.lds + m) : 0.0f;
-            }
-        };
-        pdl_wait();
-        if (nk > 0) ask(0);
+            for (int j = 0; j < kHalf / 2; ++j) acc[p][j] = 0;
+        bool ok = true;
         for (int i = 0; i < nk; ++i) {
-            const int b = i % C::kBufs;
-            float *at = mine + (i & 1) * kHalf * kParts;
-#pragma unroll
-            for (int e = 0; e < kEach; ++e)
-                if (lane + 32 * e < kHalf) {
-                    at[lane + 32 * e] = next[e] * n0s;
-                    if (kGated) at[kHalf + lane + 32 * e] = next[e] * n1s;
-                }
-            if (i + 1 < nk) ask(i + 1);
-            __syncwarp();
-            if (!__all_sync(0xffffffffu, wait(&acc_full[b], (uint32_t)(i / C::kBufs)))) break;
+            const int b = i % C::kBufs, at = i % (kBatch * kBatches), slot = at / kBatch;
+            if (at % kBatch == 0 && !(ok = all(wait(&scale_full[slot], (uint32_t)(i / (kBatch * kBatches)))))) break;
+            if (!(ok = all(wait(&done[i % S], (uint32_t)(i / S))))) break;
             umma::fence_after_sync();
+            const float *sc = scales + at * C::kCols + c0;
+            const uint32_t from = tmem + lanes + b * C::kCols + c0;
+            // a chunk is on its way while the one before it is added (the last ones may reach past the half's tokens:
+            // into columns of the accumulator whose sums nobody looks at)
+            constexpr int kChunks = kHalf / kLd, kAll = kParts * kChunks;
+            uint32_t d[2][kLd];
+            umma::tmem_ld_cols<kLd>(from, d[0]);
+#pragma unroll
+            for (int c = 0; c < kAll; ++c) {
+                const int p = c / kChunks, j0 = c % kChunks * kLd;
+                umma::tmem_ld_wait();
+                if (c + 1 < kAll) {
+                    const int p1 = (c + 1) / kChunks, j1 = (c + 1) % kChunks * kLd;
+                    if (j1 < half) umma::tmem_ld_cols<kLd>(from + p1 * BN + j1, d[(c + 1) & 1]);
+                } else {
+                    umma::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) umma::mbar_arrive(&acc_empty[b]);
+                }
+                if (j0 < half) {
+#pragma unroll
+                    for (int j = 0; j < kLd; j += 4) {
+                        const ulonglong2 f = *reinterpret_cast<const ulonglong2 *>(sc + p * BN + j0 + j);
+                        acc[p][(j0 + j) / 2] = fma2(f2(__uint_as_float(d[c & 1][j]), __uint_as_float(d[c & 1][j + 1])), f.x, acc[p][(j0 + j) / 2]);
+                        acc[p][(j0 + j) / 2 + 1] =
+                            fma2(f2(__uint_as_float(d[c & 1][j + 2]), __uint_as_float(d[c & 1][j + 3])), f.y, acc[p][(j0 + j) / 2 + 1]);
+                    }
+                }
+            }
+            if (at % kBatch == kBatch - 1) {
+                __syncwarp();
+                if (lane == 0) umma::mbar_arrive(&scale_empty[slot]);
+            }
+        }
+        // ---- the parts of K meet: [part][token][channel] over the stages, whose last products are done ----
+        const int tokens = min(bn, a.M - m0);
+        float *sums = reinterpret_cast<float *>(stages);
+        if (ok) {
+            const int ch = 32 * (warp & 3) + lane;
 #pragma unroll
             for (int p = 0; p < kParts; ++p)
 #pragma unroll
-                for (int j0 = 0; j0 < kHalf; j0 += kLd) {
-                    uint32_t d[kLd];
-                    umma::tmem_ld_cols<kLd>(tmem + lanes + b * C::kCols + p * BN + c0 + j0, d);
-                    umma::tmem_ld_wait();
-#pragma unroll
-                    for (int j = 0; j < kLd; j += 4) {
-                        const float4 s = *reinterpret_cast<const float4 *>(at + p * kHalf + j0 + j);
-                        acc[p][j0 + j] = fmaf(__uint_as_float(d[j]), s.x, acc[p][j0 + j]);
-                        acc[p][j0 + j + 1] = fmaf(__uint_as_float(d[j + 1]), s.y, acc[p][j0 + j + 1]);
-                        acc[p][j0 + j + 2] = fmaf(__uint_as_float(d[j + 2]), s.z, acc[p][j0 + j + 2]);
-                        acc[p][j0 + j + 3] = fmaf(__uint_as_float(d[j + 3]), s.w, acc[p][j0 + j + 3]);
-                    }
+                for (int j = 0; j < kHalf; j += 2) {
+                    if (j < half && c0 + j < tokens) sums[(p * BN + c0 + j) * kTile + ch] = lo32(acc[p][j / 2]);
+                    if (j + 1 < half && c0 + j + 1 < tokens) sums[(p * BN + c0 + j + 1) * kTile + ch] = hi32(acc[p][j / 2]);
                 }
-            umma::fence_before_sync();
-            __syncwarp();
-            if (lane == 0) umma::mbar_arrive(&acc_empty[b]);
         }
-    }
-
-    // after a timeout: the copies and products in flight finish (bounded) before the memory they use is used
-    // again; both issuers stopped at the timeout, so at most S copies are outstanding
-    __syncthreads();
-    if (*timeout) {
-        if (warp == kLoadWarp && lane == 0)
-            for (int b = max(0, loads - S); b < loads; ++b) umma::mbar_wait(&full[b % S], (uint32_t)((b / S) & 1), kWaitLimit);
-        if (warp == kMmaWarp && lane == 0 && issued > 0) {
-            umma::mma_commit(drain);
-            umma::mbar_wait(drain, 0, kWaitLimit);
-        }
-        if (threadIdx.x == 0) flag(a.st, QSPEC_ERR_TIMEOUT);
-    }
-    umma::fence_before_sync();
-    __syncthreads();
-    if (warp == kMmaWarp) umma::tmem_free(tmem, C::kAlloc);
-
-    // ---- the parts of K meet: [part][token][channel] over the stages ----
-    float *sums = reinterpret_cast<float *>(stages);
-    if (warp < kWorkWarps) {
-        const int c0 = (warp >> 2) * kHalf, ch = 32 * (warp & 3) + lane;
-#pragma unroll
-        for (int p = 0; p < kParts; ++p)
-#pragma unroll
-            for (int j = 0; j < kHalf; ++j) sums[(p * BN + c0 + j) * kTile + ch] = acc[p][j];
-    }
-    if (split > 1)
-        umma::cluster_sync();
-    else
         __syncthreads();
-    const int tokens = min(BN, a.M - m0);
-    if (warp < kWorkWarps) {
+        meet();
         const int n = n0 + 4 * lane;
         for (int c = warp * split + rank; c < tokens; c += kWorkWarps * split) {
             const int m = m0 + c;
@@ -248,20 +305,23 @@ __global__ void __launch_bounds__(kThreads, (Cfg<BN, kGated>::kOcc))
 #pragma unroll
             for (int p = 0; p < kParts; ++p) {
                 const float *at = sums + (p * BN + c) * kTile + 4 * lane;
+                if (split == 1) {
+                    const float4 f = *reinterpret_cast<const float4 *>(at);
+                    v[p][0] = f.x, v[p][1] = f.y, v[p][2] = f.z, v[p][3] = f.w;
+                } else {
+                    uint4 w[kMaxSplit];                          // (all asked for before the first is added)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) v[p][e] = 0.0f;
-                for (int r = 0; r < split; ++r) {
-                    float4 f;
-                    if (split > 1) {
-                        const uint4 w = umma::ld_peer_v4(at, (uint32_t)r);
-                        f = make_float4(__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w));
-                    } else {
-                        f = *reinterpret_cast<const float4 *>(at);
+                    for (int r = 0; r < kMaxSplit; ++r)
+                        w[r] = r < split ? umma::ld_peer_v4(at, (uint32_t)r) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[p][e] = 0.0f;
+#pragma unroll
+                    for (int r = 0; r < kMaxSplit; ++r) {
+                        v[p][0] += __uint_as_float(w[r].x);
+                        v[p][1] += __uint_as_float(w[r].y);
+                        v[p][2] += __uint_as_float(w[r].z);
+                        v[p][3] += __uint_as_float(w[r].w);
                     }
-                    v[p][0] += f.x;
-                    v[p][1] += f.y;
-                    v[p][2] += f.z;
-                    v[p][3] += f.w;
                 }
             }
             if constexpr (kGated) {
@@ -302,34 +362,48 @@ __global__ void __launch_bounds__(kThreads, (Cfg<BN, kGated>::kOcc))
 }
 
 template <int BN, bool kGated>
-int launch(const char *where, const uint8_t *xq, const uint8_t *w0, const uint8_t *w1, const Args &a, cudaStream_t stream,
-           uint32_t wait_limit) {
+int launch(const char *where, const uint8_t *xq, const uint8_t *w0, const uint8_t *w1, const Args &a, int bn, int split,
+           cudaStream_t stream, uint32_t wait_limit) {
     using C = Cfg<BN, kGated>;
     CUtensorMap t0, t1, tx;
     if (byte_tmap_sw128(&t0, w0, a.N, a.K, (size_t)a.K, kTile) ||
         (kGated && byte_tmap_sw128(&t1, w1, a.N, a.K, (size_t)a.K, kTile)) ||
-        byte_tmap_sw128(&tx, xq, a.M, a.K, (size_t)a.K, BN))
+        byte_tmap_sw128(&tx, xq, a.M, a.K, (size_t)a.K, bn))
         return QSPEC_ERR_UNSUPPORTED;
     if (!kGated) t1 = t0;
     auto kern = stream_kernel<BN, kGated>;
     int rc = smem_limit_once(reinterpret_cast<const void *>(kern), (int)C::kSmem, true);
     if (rc) return rc;
-    const int tiles = (a.N + kTile - 1) / kTile, rows = (a.M + BN - 1) / BN, G = a.K / kGroup;
-    int split = 1;
-    while (split < 8 && (long long)tiles * rows * split * 2 <= (long long)sm_count() * C::kOcc && G / (split * 2) >= 2) split *= 2;
-    const dim3 grid((unsigned)(tiles * split), (unsigned)rows);
+    const int tiles = (a.N + kTile - 1) / kTile;
+    const dim3 grid((unsigned)(tiles * split), (unsigned)((a.M + bn - 1) / bn));
     if (split == 1)
-        return launch_pdl(where, kern, grid, dim3(kThreads), C::kSmem, stream, t0, t1, tx, a, split, wait_limit);
-    return launch_pdl_cluster(where, kern, grid, dim3(kThreads), C::kSmem, stream, split, t0, t1, tx, a, split, wait_limit);
+        return launch_pdl(where, kern, grid, dim3(kThreads), C::kSmem, stream, t0, t1, tx, a, bn, split, wait_limit);
+    return launch_pdl_cluster(where, kern, grid, dim3(kThreads), C::kSmem, stream, split, t0, t1, tx, a, bn, split, wait_limit);
 }
 
 template <bool kGated>
 int launch_any(const char *where, const uint8_t *xq, const uint8_t *w0, const uint8_t *w1, const Args &a, cudaStream_t st) {
-    if (a.M <= 16) return launch<16, kGated>(where, xq, w0, w1, a, st, kWaitLimit);
-    if (a.M <= 32) return launch<32, kGated>(where, xq, w0, w1, a, st, kWaitLimit);
-    if (a.M <= 64) return launch<64, kGated>(where, xq, w0, w1, a, st, kWaitLimit);
-    if (a.M <= 128) return launch<128, kGated>(where, xq, w0, w1, a, st, kWaitLimit);
-    return f8b::launch_tile(where, xq, w0, w1, a, st, kWaitLimit);
+    constexpr int kMost = kGated ? 128 : 256;
+    const int rows = (a.M + kMost - 1) / kMost;                  // CTAs that share the tokens
+    int bn = ((a.M + rows - 1) / rows + 15) / 16 * 16;
+    int split = 1;
+    const long long ctas = (long long)((a.N + kTile - 1) / kTile) * rows;
+    const int occ = bn <= (kGated ? 16 : 64) ? 2 : 1;
+#ifdef EXP_ENV
+    if (getenv("BN")) bn = atoi(getenv("BN"));
+#endif
+    while (split < kMaxSplit && ctas * split * 2 <= (long long)sm_count() * occ && a.K / kGroup / (split * 2) >= 2) split *= 2;
+#ifdef EXP_ENV
+    if (getenv("SPLIT")) split = atoi(getenv("SPLIT"));
+    if (getenv("TILE")) return f8b::launch_tile(where, xq, w0, w1, a, st, kWaitLimit);
+    if (!getenv("STREAM"))
+#endif
+    if (a.M > 512) return f8b::launch_tile(where, xq, w0, w1, a, st, kWaitLimit);
+    if (bn <= 16) return launch<16, kGated>(where, xq, w0, w1, a, bn, split, st, kWaitLimit);
+    if (bn <= 32) return launch<32, kGated>(where, xq, w0, w1, a, bn, split, st, kWaitLimit);
+    if (bn <= 64) return launch<64, kGated>(where, xq, w0, w1, a, bn, split, st, kWaitLimit);
+    if (kGated || bn <= 128) return launch<128, kGated>(where, xq, w0, w1, a, bn, split, st, kWaitLimit);
+    return launch<kMost, kGated>(where, xq, w0, w1, a, bn, split, st, kWaitLimit);
 }
 
 }  // namespace f8s

@@ -33,6 +33,7 @@ constexpr int kRows = 128, kCols = 256;              // of a CTA's accumulator
 constexpr int kWorkWarps = 8, kWork = 32 * kWorkWarps, kLoadWarp = 8, kMmaWarp = 9, kScaleWarp = 10, kThreads = kWork + 128;
 constexpr int kHalfStage = 128 * 128, kStage = 2 * kHalfStage;
 constexpr int kStages = 6;
+static_assert(kStages >= 2, "a stage's products must not be done twice before all warps have looked: two accumulators");
 constexpr int kBatch = 4, kBatches = 4;              // scales: blocks per hand-over, hand-overs in flight
 constexpr int kGroupTiles = 8;                       // token tiles that go through the channels together
 // registers per thread: all start with 168; 128 sums and their operands need more, the issuing warps less
