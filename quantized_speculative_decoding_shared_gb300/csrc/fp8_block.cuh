@@ -1,10 +1,12 @@
 // fp8_block.cuh -- what the products of E4M3 codes with a scale for each block
-// of 128 share: their arguments, and the epilogue of the gated one.
+// of 128 share: their arguments, the gated one's function, and the ends of sums that
+// lie in shared memory.
 #pragma once
 
 #include <cuda_fp8.h>
 
 #include "qspec_device.cuh"
+#include "umma.cuh"
 
 namespace qspec {
 namespace f8b {
@@ -40,6 +42,62 @@ __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
     const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
     const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
     return lo | hi << 16;
+}
+
+// Four neighbouring channels n .. n + 3 of token m in bf16.
+__device__ __forceinline__ void store_bf16(const Args &a, int m, int n, const float (&v)[4]) {
+    uint16_t *y = a.y + (size_t)m * a.ldy + n;
+    if ((reinterpret_cast<uintptr_t>(y) & 7) == 0 && n + 4 <= a.N) {
+        *reinterpret_cast<uint2 *>(y) =
+            make_uint2((uint32_t)float_to_bf16_bits(v[0]) | (uint32_t)float_to_bf16_bits(v[1]) << 16,
+                       (uint32_t)float_to_bf16_bits(v[2]) | (uint32_t)float_to_bf16_bits(v[3]) << 16);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (n + e < a.N) y[e] = float_to_bf16_bits(v[e]);
+    }
+}
+
+// The gated product's outputs for token m and the 128 channels of block `block` by a warp, four channels to a lane.
+__device__ __forceinline__ void store_gated(const Args &a, int m, int block, int lane, const float (&g)[4], const float (&u)[4]) {
+    float h[4], amax = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        h[e] = gated(g[e], u[e]);
+        asm("max.NaN.f32 %0, %0, %1;" : "+f"(amax) : "f"(fabsf(h[e])));
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) {
+        const float other = __shfl_xor_sync(0xffffffffu, amax, o);
+        asm("max.NaN.f32 %0, %0, %1;" : "+f"(amax) : "f"(other));
+    }
+    if (a.hq != nullptr) {
+        const Quant q(amax);
+        reinterpret_cast<uint32_t *>(a.hq + (size_t)m * a.N + (size_t)block * kGroup)[lane] =
+            q.s == 0.0f ? 0u : codes4(h[0] * q.up * q.inv, h[1] * q.up * q.inv, h[2] * q.up * q.inv, h[3] * q.up * q.inv);
+        if (lane == 0) a.sh[(size_t)block * a.ldh + m] = q.s;
+    }
+    if (lane == 0 && !(amax < (a.y != nullptr ? 3.3961775292304601e38f : INFINITY))) flag(a.st, QSPEC_ERR_NONFINITE);
+    if (a.y != nullptr) store_bf16(a, m, block * kGroup + 4 * lane, h);
+}
+
+// The sum over a cluster's parts of K of the four floats at `at` in the shared memory of the CTAs first, first + 1, ...,
+// in that order; all are asked for before the first is added.
+constexpr int kMaxSplit = 8;
+__device__ __forceinline__ void sum_parts(const float *at, int split, int first, float (&v)[4]) {
+    uint4 w[kMaxSplit];
+#pragma unroll
+    for (int r = 0; r < kMaxSplit; ++r)
+        w[r] = r < split ? umma::ld_peer_v4(at, (uint32_t)(first + r)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = 0.0f;
+#pragma unroll
+    for (int r = 0; r < kMaxSplit; ++r) {
+        v[0] += __uint_as_float(w[r].x);
+        v[1] += __uint_as_float(w[r].y);
+        v[2] += __uint_as_float(w[r].z);
+        v[3] += __uint_as_float(w[r].w);
+    }
 }
 
 }  // namespace f8b

@@ -33,7 +33,7 @@ using f8b::Args;
 constexpr int kTile = 128;                       // channels per CTA, and K per stage
 constexpr int kWorkWarps = 8, kWork = 32 * kWorkWarps, kLoadWarp = 8, kMmaWarp = 9, kScaleWarp = 10, kThreads = kWork + 128;
 constexpr int kBatch = 4, kBatches = 2;          // scales: blocks per hand-over, hand-overs in flight
-constexpr int kMaxSplit = 8;
+using f8b::kMaxSplit;
 
 // BN: most tokens of a CTA
 template <int BN, bool kGated>
@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<BN, kGated>::kOcc))
     float *scales = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(full) + C::kCtl);     // [slot][part][token]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = (int)(blockIdx.x % (unsigned)split), tile = (int)(blockIdx.x / (unsigned)split);
-    const int n0 = tile * kTile, m0 = blockIdx.y * bn;
+    const int n0 = tile * kTile, m0 = 0;
     const int G = a.K / kGroup;
     const int k0 = (int)((long long)G * rank / split), nk = (int)((long long)G * (rank + 1) / split) - k0;
     auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
@@ -305,64 +305,24 @@ __global__ void __launch_bounds__(kThreads, (Cfg<BN, kGated>::kOcc))
 #pragma unroll
             for (int p = 0; p < kParts; ++p) {
                 const float *at = sums + (p * BN + c) * kTile + 4 * lane;
-                if (split == 1) {
+                if (split > 1) {
+                    f8b::sum_parts(at, split, 0, v[p]);
+                } else {
                     const float4 f = *reinterpret_cast<const float4 *>(at);
                     v[p][0] = f.x, v[p][1] = f.y, v[p][2] = f.z, v[p][3] = f.w;
-                } else {
-                    uint4 w[kMaxSplit];                          // (all asked for before the first is added)
-#pragma unroll
-                    for (int r = 0; r < kMaxSplit; ++r)
-                        w[r] = r < split ? umma::ld_peer_v4(at, (uint32_t)r) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) v[p][e] = 0.0f;
-#pragma unroll
-                    for (int r = 0; r < kMaxSplit; ++r) {
-                        v[p][0] += __uint_as_float(w[r].x);
-                        v[p][1] += __uint_as_float(w[r].y);
-                        v[p][2] += __uint_as_float(w[r].z);
-                        v[p][3] += __uint_as_float(w[r].w);
-                    }
                 }
             }
-            if constexpr (kGated) {
-                float amax = 0.0f;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    v[0][e] = f8b::gated(v[0][e], v[kParts - 1][e]);
-                    asm("max.NaN.f32 %0, %0, %1;" : "+f"(amax) : "f"(fabsf(v[0][e])));
-                }
-#pragma unroll
-                for (int o = 16; o >= 1; o >>= 1) {
-                    const float other = __shfl_xor_sync(0xffffffffu, amax, o);
-                    asm("max.NaN.f32 %0, %0, %1;" : "+f"(amax) : "f"(other));
-                }
-                if (a.hq != nullptr) {
-                    const f8b::Quant q(amax);
-                    reinterpret_cast<uint32_t *>(a.hq + (size_t)m * a.N + n0)[lane] =
-                        q.s == 0.0f ? 0u : f8b::codes4(v[0][0] * q.up * q.inv, v[0][1] * q.up * q.inv, v[0][2] * q.up * q.inv, v[0][3] * q.up * q.inv);
-                    if (lane == 0) a.sh[(size_t)tile * a.ldh + m] = q.s;
-                }
-                if (lane == 0 && !(amax < (a.y != nullptr ? 3.3961775292304601e38f : INFINITY))) flag(a.st, QSPEC_ERR_NONFINITE);
-            }
-            if (!kGated || a.y != nullptr) {
-                uint16_t *y = a.y + (size_t)m * a.ldy + n;
-                if ((reinterpret_cast<uintptr_t>(y) & 7) == 0 && n + 4 <= a.N) {
-                    *reinterpret_cast<uint2 *>(y) =
-                        make_uint2((uint32_t)float_to_bf16_bits(v[0][0]) | (uint32_t)float_to_bf16_bits(v[0][1]) << 16,
-                                   (uint32_t)float_to_bf16_bits(v[0][2]) | (uint32_t)float_to_bf16_bits(v[0][3]) << 16);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (n + e < a.N) y[e] = float_to_bf16_bits(v[0][e]);
-                }
-            }
+            if constexpr (kGated)
+                f8b::store_gated(a, m, tile, lane, v[0], v[1]);
+            else
+                f8b::store_bf16(a, m, n, v[0]);
         }
     }
     if (split > 1) umma::cluster_sync();         // (a peer may still read this CTA's sums)
 }
 
 template <int BN, bool kGated>
-int launch(const char *where, const uint8_t *xq, const uint8_t *w0, const uint8_t *w1, const Args &a, int bn, int split,
+int launch(const char *where, const uint8_t *xq, const uint8_t *w0, const uint8_t *w1, const Args &a, int bn,
            cudaStream_t stream, uint32_t wait_limit) {
     using C = Cfg<BN, kGated>;
     CUtensorMap t0, t1, tx;
@@ -375,35 +335,28 @@ int launch(const char *where, const uint8_t *xq, const uint8_t *w0, const uint8_
     int rc = smem_limit_once(reinterpret_cast<const void *>(kern), (int)C::kSmem, true);
     if (rc) return rc;
     const int tiles = (a.N + kTile - 1) / kTile;
-    const dim3 grid((unsigned)(tiles * split), (unsigned)((a.M + bn - 1) / bn));
+    int split = 1;                               // parts of K: as many as there is room for, two blocks to each
+    while (split < kMaxSplit && (long long)tiles * split * 2 <= (long long)sm_count() * C::kOcc && a.K / kGroup / (split * 2) >= 2) split *= 2;
+    const dim3 grid((unsigned)(tiles * split));
     if (split == 1)
         return launch_pdl(where, kern, grid, dim3(kThreads), C::kSmem, stream, t0, t1, tx, a, bn, split, wait_limit);
     return launch_pdl_cluster(where, kern, grid, dim3(kThreads), C::kSmem, stream, split, t0, t1, tx, a, bn, split, wait_limit);
 }
 
+// Few tokens here, many in tiles of 128 (fp8_block_tile.cu): 128 channels by M tokens against 128 tokens by 256 channels.
+// Measured here / there, us: linear 80 x 4096 x 14336 15.8 / 18.0, 128 18.1 / 19.5, 192 (in two parts) 25.4 / 21.5; gated
+// 32 x 14336 x 4096 22.5 / 24.4, 64 25.0 / 24.6, 80 32.3 / 24.7.
 template <bool kGated>
 int launch_any(const char *where, const uint8_t *xq, const uint8_t *w0, const uint8_t *w1, const Args &a, cudaStream_t st) {
-    constexpr int kMost = kGated ? 128 : 256;
-    const int rows = (a.M + kMost - 1) / kMost;                  // CTAs that share the tokens
-    int bn = ((a.M + rows - 1) / rows + 15) / 16 * 16;
-    int split = 1;
-    const long long ctas = (long long)((a.N + kTile - 1) / kTile) * rows;
-    const int occ = bn <= (kGated ? 16 : 64) ? 2 : 1;
-#ifdef EXP_ENV
-    if (getenv("BN")) bn = atoi(getenv("BN"));
-#endif
-    while (split < kMaxSplit && ctas * split * 2 <= (long long)sm_count() * occ && a.K / kGroup / (split * 2) >= 2) split *= 2;
-#ifdef EXP_ENV
-    if (getenv("SPLIT")) split = atoi(getenv("SPLIT"));
-    if (getenv("TILE")) return f8b::launch_tile(where, xq, w0, w1, a, st, kWaitLimit);
-    if (!getenv("STREAM"))
-#endif
-    if (a.M > 512) return f8b::launch_tile(where, xq, w0, w1, a, st, kWaitLimit);
-    if (bn <= 16) return launch<16, kGated>(where, xq, w0, w1, a, bn, split, st, kWaitLimit);
-    if (bn <= 32) return launch<32, kGated>(where, xq, w0, w1, a, bn, split, st, kWaitLimit);
-    if (bn <= 64) return launch<64, kGated>(where, xq, w0, w1, a, bn, split, st, kWaitLimit);
-    if (kGated || bn <= 128) return launch<128, kGated>(where, xq, w0, w1, a, bn, split, st, kWaitLimit);
-    return launch<kMost, kGated>(where, xq, w0, w1, a, bn, split, st, kWaitLimit);
+    constexpr int kMost = kGated ? 32 : 128;
+    const int bn = (a.M + 15) / 16 * 16;
+    if (bn <= 16) return launch<16, kGated>(where, xq, w0, w1, a, bn, st, kWaitLimit);
+    if (bn <= 32) return launch<32, kGated>(where, xq, w0, w1, a, bn, st, kWaitLimit);
+    if constexpr (!kGated) {
+        if (bn <= 64) return launch<64, kGated>(where, xq, w0, w1, a, bn, st, kWaitLimit);
+        if (bn <= kMost) return launch<kMost, kGated>(where, xq, w0, w1, a, bn, st, kWaitLimit);
+    }
+    return f8b::launch_tile(where, xq, w0, w1, a, st, kWaitLimit);
 }
 
 }  // namespace f8s

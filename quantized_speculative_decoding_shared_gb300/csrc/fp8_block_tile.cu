@@ -2,21 +2,21 @@
 // for many tokens (prompts, verify passes of large batches): the linear, and the gated
 // product.  Definitions: fp8_block_stream.cu.
 //
-// A pair of CTAs takes 256 tokens (the accumulator's lanes, 128 in each CTA) x
-// 256 channels (its columns; gated: 128 of the gate, 128 of the up projection), so that each
-// reads half of either operand: 64 bytes per clock for 128 x 256 x 128 products in 512.
-// Persistent: a pair goes through tiles in groups of 8 token tiles, whose operands
-// stay in L2 while the channels go by.
+// A CTA takes 128 tokens (the accumulator's lanes) x 256 channels (its columns; gated: 128
+// of the gate, 128 of the up projection).  Persistent: it goes through tiles in groups of
+// 8 token tiles, whose operands stay in L2 while the channels go by.
 // The tensor cores cannot scale a block's sums, so the products of a block (K = 128)
 // go into an accumulator of their own, two of them in turn (all of tensor memory), and
 // eight warps (thread = token, half the channels) add it to 128 sums in registers, times
 // the token's scale and the channels', while the next block's products run: 256 clocks of
 // reads and of packed products against 512 of the tensor cores.  The sums' way out (SiLU,
 // product, maxima, codes) has two blocks' products of the next tile beside it.
-// One lane of each CTA issues its copies, one of the even CTA the products; barriers of
-// filled stages and freed accumulators live in the even CTA, those of finished products
-// (a stage free, an accumulator full) in both.
+// One warp issues the copies, one the products, one fetches the scales some blocks ahead.
+// The tiles behind the last full round of CTAs are split along K over the CTAs of a
+// cluster, whose parts meet in shared memory, in the order of K.
 #include <algorithm>
+#include <atomic>
+#include <climits>
 
 #include "fp8_block_host.h"
 #include "umma.cuh"
@@ -28,16 +28,18 @@ namespace {
 namespace f8t {
 
 using f8b::Args;
+using f8b::kMaxSplit;
 
-constexpr int kRows = 128, kCols = 256;              // of a CTA's accumulator
+constexpr int kRows = 128, kCols = 256;              // of the accumulator
 constexpr int kWorkWarps = 8, kWork = 32 * kWorkWarps, kLoadWarp = 8, kMmaWarp = 9, kScaleWarp = 10, kThreads = kWork + 128;
-constexpr int kHalfStage = 128 * 128, kStage = 2 * kHalfStage;
-constexpr int kStages = 6;
+constexpr int kPiece = 128 * 128;                    // 128 rows of an operand's block
+constexpr int kStage = 3 * kPiece, kStages = 4;
 static_assert(kStages >= 2, "a stage's products must not be done twice before all warps have looked: two accumulators");
+static_assert(kRows * kCols * 4 <= kStages * kStage, "a CTA's sums lie over the stages");
 constexpr int kBatch = 4, kBatches = 4;              // scales: blocks per hand-over, hand-overs in flight
 constexpr int kGroupTiles = 8;                       // token tiles that go through the channels together
 // registers per thread: all start with 168; 128 sums and their operands need more, the issuing warps less
-constexpr int kRegsWork = 200, kRegsRest = 96;
+constexpr int kRegsWork = 208, kRegsRest = 88;
 static_assert(kThreads * 168 <= 65536 && kWork * kRegsWork + 128 * kRegsRest <= kThreads * 168, "register shares");
 
 struct Ctl {
@@ -51,6 +53,12 @@ struct Ctl {
     float top[2][2][kRows];                          // gated: maxima of the two halves of the channels, two tiles' in turn
 };
 constexpr size_t kSmem = 1024 + (size_t)kStages * kStage + sizeof(Ctl);
+
+// What a launch goes through: the tiles 0 .. full - 1 one by one, each CTA every gridDim.x-th, then the others in parts
+// of K, `split` CTAs of a cluster to a tile.
+struct Plan {
+    int row_tiles, col_tiles, full, split;
+};
 
 __device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr) {       // K-major, rows of 128 bytes, 128-byte swizzle
     return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)1 << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 |
@@ -114,16 +122,30 @@ __device__ __forceinline__ void store8(uint16_t *row, int n, int N, bool wide, c
 template <bool kGated>
 __global__ void __launch_bounds__(kThreads, 1)
     tile_kernel(const __grid_constant__ CUtensorMap t0, const __grid_constant__ CUtensorMap t1,
-                const __grid_constant__ CUtensorMap tx, const __grid_constant__ Args a, int row_tiles, int col_tiles, int wide,
+                const __grid_constant__ CUtensorMap tx, const __grid_constant__ Args a, const Plan plan, int wide,
                 uint32_t wait_limit) {
     constexpr int kChannels = kGated ? 128 : 256;                // channels of a tile
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *stages = smem_raw + ((1024u - (umma::smem_addr(smem_raw) & 1023u)) & 1023u);
     Ctl &sm = *reinterpret_cast<Ctl *>(stages + (size_t)kStages * kStage);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rank = (int)umma::cluster_rank();
-    const int pair = (int)(blockIdx.x >> 1), pairs = (int)(gridDim.x >> 1);
-    const int G = a.K / kGroup, tiles = row_tiles * col_tiles;
+    const int G = a.K / kGroup, cta = (int)blockIdx.x, ctas = (int)gridDim.x;
+    const int fulls = cta < plan.full ? (plan.full - cta + ctas - 1) / ctas : 0;      // whole tiles of this CTA
+    const int part = cta % plan.split;                            // of K, of its last tile
+    const int last = plan.full + cta / plan.split;
+    const int items = fulls + (last < plan.row_tiles * plan.col_tiles ? 1 : 0);
+    const bool shared = items > fulls;
+    const int shared_k0 = (int)((long long)G * part / plan.split), shared_nk = (int)((long long)G * (part + 1) / plan.split) - shared_k0;
+    // item i: its tile's place (token tile, channel tile) and blocks of K
+    auto item = [&](int i, int &rt, int &ct, int &k0) -> int {
+        const int t = i < fulls ? cta + i * ctas : last;
+        const int in = kGroupTiles * plan.col_tiles, g = t / in, r = t - g * in;
+        const int rows = min(kGroupTiles, plan.row_tiles - g * kGroupTiles);
+        ct = rows == kGroupTiles ? r / kGroupTiles : r / rows;
+        rt = g * kGroupTiles + (r - ct * rows);
+        k0 = i < fulls ? 0 : shared_k0;
+        return i < fulls ? G : shared_nk;
+    };
     volatile int *timeout = &sm.timeout;
     auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
         if (umma::mbar_try_wait(bar, parity & 1)) return true;
@@ -133,21 +155,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         return false;
     };
     auto all = [](bool mine) { return __all_sync(0xffffffffu, mine) != 0; };
-    // tile t -> (token tile, channel tile)
-    auto place = [&](int t, int &rt, int &ct) {
-        const int in = kGroupTiles * col_tiles, g = t / in, r = t - g * in;
-        const int rows = min(kGroupTiles, row_tiles - g * kGroupTiles);
-        ct = rows == kGroupTiles ? r / kGroupTiles : r / rows;
-        rt = g * kGroupTiles + (r - ct * rows);
-    };
-
+    // where four neighbouring sums of a token lie while the parts of K meet
+    auto piece = [&](int row, int p) { return reinterpret_cast<float4 *>(stages) + row * (kCols / 4) + (p ^ (row & 7)); };
     if (threadIdx.x == 0) {
         sm.timeout = 0;
         for (int i = 0; i < kStages; ++i) {
             umma::mbar_init(&sm.full[i], 1);
             umma::mbar_init(&sm.done[i], 1);
         }
-        for (int i = 0; i < 2; ++i) umma::mbar_init(&sm.acc_empty[i], 2 * kWorkWarps);
+        for (int i = 0; i < 2; ++i) umma::mbar_init(&sm.acc_empty[i], kWorkWarps);
         for (int i = 0; i < kBatches; ++i) {
             umma::mbar_init(&sm.scale_full[i], 1);
             umma::mbar_init(&sm.scale_empty[i], kWorkWarps);
@@ -155,41 +171,46 @@ __global__ void __launch_bounds__(kThreads, 1)
         umma::mbar_init(&sm.drain, 1);
         umma::mbar_fence_init();
     }
-    if (warp == kMmaWarp) umma::tmem_alloc_pair(&sm.tmem, 2 * kCols);
+    if (warp == kMmaWarp) umma::tmem_alloc(&sm.tmem, 2 * kCols);
     if (warp == kLoadWarp && lane == 0) {
         umma::prefetch_tmap(&t0);
         if (kGated) umma::prefetch_tmap(&t1);
         umma::prefetch_tmap(&tx);
     }
     umma::fence_before_sync();
-    umma::cluster_sync();
+    __syncthreads();
     umma::fence_after_sync();
     pdl_launch_dependents();
     const uint32_t tmem = sm.tmem;
     int loads = 0, issued = 0;                                    // blocks whose copies, whose products were issued
+    auto meet = [&]() {                                           // (behind the CTA's own barrier and a timeout's drain)
+        if (plan.split > 1)
+            umma::cluster_sync();
+        else
+            __syncthreads();
+    };
 
     if (warp >= kWorkWarps) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
         // (the issuing warps go through their loops whole and elect a lane where it counts: a lane's own loop is
         // slower by the divergence that the compiler allows for at every step)
         if (warp == kLoadWarp) {
-            const CUtensorMap *tw = kGated && rank == 1 ? &t1 : &t0;
+            const CUtensorMap *tw = kGated ? &t1 : &t0;
             const bool elected = umma::elect_one();
             pdl_wait();
             bool ok = true;
             int s = 0, turn = 0;                                  // the stage, and how often it was filled before
-            for (int t = pair; t < tiles && ok; t += pairs) {
-                int rt, ct;
-                place(t, rt, ct);
-                const int m0 = rt * 2 * kRows + rank * kRows, n0 = ct * kChannels + (kGated ? 0 : rank * 128);
-                for (int g = 0; g < G; ++g) {
+            for (int i = 0; i < items && ok; ++i) {
+                int rt, ct, k0;
+                const int nk = item(i, rt, ct, k0), m0 = rt * kRows, n0 = ct * kChannels;
+                for (int g = k0; g < k0 + nk; ++g) {
                     if (!(ok = turn == 0 || all(wait(&sm.done[s], (uint32_t)(turn + 1))))) break;
                     if (elected) {
                         uint8_t *at = stages + (size_t)s * kStage;
-                        if (rank == 0) umma::mbar_arrive_expect_tx(&sm.full[s], 2 * kStage);      // both CTAs' bytes
-                        const uint32_t bar = umma::peer_addr(&sm.full[s], 0);
-                        umma::tma_load_2d_pair(at, &tx, g * kGroup, m0, bar);
-                        umma::tma_load_2d_pair(at + kHalfStage, tw, g * kGroup, n0, bar);
+                        umma::mbar_arrive_expect_tx(&sm.full[s], kStage);
+                        umma::tma_load_2d(at, &tx, g * kGroup, m0, &sm.full[s]);
+                        umma::tma_load_2d(at + kPiece, &t0, g * kGroup, n0, &sm.full[s]);
+                        umma::tma_load_2d(at + 2 * kPiece, tw, g * kGroup, n0 + (kGated ? 0 : 128), &sm.full[s]);
                     }
                     __syncwarp();
                     ++loads;
@@ -199,56 +220,51 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            // (the last arrivals of the even CTA's products on this CTA's barriers come before it ends)
-            for (int b = max(0, loads - kStages); b < loads; ++b) wait(&sm.done[b % kStages], (uint32_t)(b / kStages));
-        } else if (warp == kMmaWarp && rank == 0) {
-            constexpr uint32_t idesc = umma::instr_desc(0, 0, 2 * kRows, kCols);             // e4m3 x e4m3 -> f32
+        } else if (warp == kMmaWarp) {
+            constexpr uint32_t idesc = umma::instr_desc(0, 0, kRows, kCols);                 // e4m3 x e4m3 -> f32
             const bool elected = umma::elect_one();
-            bool ok = true;
+            const int blocks = fulls * G + (shared ? shared_nk : 0);
             int s = 0;
             uint32_t turn = 0;
-            const int blocks = (tiles - pair + pairs - 1) / pairs * G;
-            ok = all(wait(&sm.full[0], 0));
-            for (; issued < blocks && ok; ++issued) {
+            for (; issued < blocks; ++issued) {
                 const int b = issued & 1;
-                if (!(ok = all(wait(&sm.acc_empty[b], (uint32_t)(issued / 2 + 1))))) break;
+                if (!all(wait(&sm.full[s], turn)) || !all(wait(&sm.acc_empty[b], (uint32_t)(issued / 2 + 1)))) break;
                 umma::fence_after_sync();
                 const uint32_t at = umma::smem_addr(stages + (size_t)s * kStage);
-                const uint64_t ad = desc_sw128(at), bd = desc_sw128(at + kHalfStage);
+                const uint64_t ad = desc_sw128(at), bd = desc_sw128(at + kPiece);
                 if (elected) {
 #pragma unroll
                     for (int kk = 0; kk < kGroup / 32; ++kk)      // K = 32 bytes per MMA: +2 in the address field
-                        umma::mma_e4m3_pair(tmem + b * kCols, ad + 2 * kk, bd + 2 * kk, idesc, kk != 0 ? 1u : 0u);
-                    umma::mma_commit_pair(&sm.done[s], 3);
+                        umma::mma_e4m3(tmem + b * kCols, ad + 2 * kk, bd + 2 * kk, idesc, kk != 0 ? 1u : 0u);
+                    umma::mma_commit(&sm.done[s]);
                 }
                 __syncwarp();
                 if (++s == kStages) {
                     s = 0;
                     ++turn;
                 }
-                if (issued + 1 < blocks) ok = all(wait(&sm.full[s], turn));
             }
         } else if (warp == kScaleWarp) {
             // the blocks' scales, some way ahead of the work (a load from L2 takes as long as two blocks)
             const int blocks_n = (a.N + kGroup - 1) / kGroup;
-            int t = pair, g = 0, rt, ct;
-            place(t, rt, ct);
+            int i = 0, g = 0, rt, ct, k0, nk = 0;
+            if (items > 0) nk = item(0, rt, ct, k0);
             pdl_wait();
-            for (int base = 0; t < tiles; base += kBatch) {
+            for (int base = 0; i < items; base += kBatch) {
                 float x[kBatch][kRows / 32], w[kBatch];
 #pragma unroll
                 for (int u = 0; u < kBatch; ++u) {
-                    const bool some = t < tiles;
-                    const int m0 = rt * 2 * kRows + rank * kRows + lane;
+                    const bool some = i < items;
+                    const int m0 = rt * kRows + lane;
 #pragma unroll
-                    for (int i = 0; i < kRows / 32; ++i)
-                        x[u][i] = some && m0 + 32 * i < a.M ? __ldg(a.sa + (size_t)g * a.lds + m0 + 32 * i) : 0.0f;
+                    for (int e = 0; e < kRows / 32; ++e)
+                        x[u][e] = some && m0 + 32 * e < a.M ? __ldg(a.sa + (size_t)(k0 + g) * a.lds + m0 + 32 * e) : 0.0f;
                     // lane 0: of the lower half of the channels, or the gate; lane 1: of the upper half, or up
                     const float *from = kGated && lane == 1 ? a.s1 : a.s0;
-                    w[u] = some && lane < 2 ? __ldg(from + (size_t)(kGated ? ct : min(2 * ct + lane, blocks_n - 1)) * G + g) : 0.0f;
-                    if (++g == G) {
+                    w[u] = some && lane < 2 ? __ldg(from + (size_t)(kGated ? ct : min(2 * ct + lane, blocks_n - 1)) * G + k0 + g) : 0.0f;
+                    if (some && ++g == nk) {
                         g = 0;
-                        if ((t += pairs) < tiles) place(t, rt, ct);
+                        if (++i < items) nk = item(i, rt, ct, k0);
                     }
                 }
                 const int slot = base / kBatch % kBatches;
@@ -256,13 +272,30 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int u = 0; u < kBatch; ++u) {
 #pragma unroll
-                    for (int i = 0; i < kRows / 32; ++i) sm.token_scale[slot * kBatch + u][lane + 32 * i] = x[u][i];
+                    for (int e = 0; e < kRows / 32; ++e) sm.token_scale[slot * kBatch + u][lane + 32 * e] = x[u][e];
                     if (lane < 2) sm.weight_scale[slot * kBatch + u][lane] = w[u];
                 }
                 __syncwarp();
                 if (lane == 0) umma::mbar_arrive(&sm.scale_full[slot]);
             }
         }
+        // after a timeout: the copies and products in flight finish (bounded) before the memory they use is used
+        // again; both issuers stopped at the timeout, so at most kStages copies are outstanding
+        __syncthreads();
+        if (*timeout) {
+            if (warp == kLoadWarp && umma::elect_one())
+                for (int b = max(0, loads - kStages); b < loads; ++b)
+                    umma::mbar_wait(&sm.full[b % kStages], (uint32_t)((b / kStages) & 1), kWaitLimit);
+            if (warp == kMmaWarp && umma::elect_one() && issued > 0) {
+                umma::mma_commit(&sm.drain);
+                umma::mbar_wait(&sm.drain, 0, kWaitLimit);
+            }
+            if (warp == kScaleWarp && lane == 0) flag(a.st, QSPEC_ERR_TIMEOUT);
+            __syncwarp();
+        }
+        meet();
+        if (warp == kMmaWarp) umma::tmem_free(tmem, 2 * kCols);
+        if (plan.split > 1) umma::cluster_sync();
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsWork));
         // ---- thread = token; warps 0 .. 3 the lower half of the channels (gated: of both parts), 4 .. 7 the upper ----
@@ -270,13 +303,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         // columns of its four chunks of 32
         auto column = [&](int c) { return kGated ? (c >> 1) * 128 + half * 64 + (c & 1) * 32 : half * 128 + c * 32; };
-        const uint32_t freed[2] = {umma::peer_addr(&sm.acc_empty[0], 0), umma::peer_addr(&sm.acc_empty[1], 0)};
         int done = 0, parity = 0;
         pdl_wait();
-        for (int t = pair; t < tiles; t += pairs) {
-            int rt, ct;
-            place(t, rt, ct);
-            const int m = rt * 2 * kRows + rank * kRows + row;
+        for (int i = 0; i < items; ++i) {
+            int rt, ct, k0;
+            const int nk = item(i, rt, ct, k0), m = rt * kRows + row;
             const bool in = m < a.M;
             uint64_t acc[4][16];
 #pragma unroll
@@ -284,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int j = 0; j < 16; ++j) acc[c][j] = 0;
             bool ok = true;
-            for (int g = 0; g < G; ++g) {
+            for (int g = 0; g < nk; ++g) {
                 const int b = done & 1, at = done % (kBatch * kBatches), slot = at / kBatch;
                 if (at % kBatch == 0 && !all(wait(&sm.scale_full[slot], (uint32_t)(done / (kBatch * kBatches))))) ok = false;
                 const float x = sm.token_scale[at][row];
@@ -302,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         umma::fence_before_sync();
                         __syncwarp();
                         if (lane == 0) {
-                            umma::mbar_arrive_relaxed_at(freed[b]);
+                            umma::mbar_arrive(&sm.acc_empty[b]);
                             if (at % kBatch == kBatch - 1) umma::mbar_arrive(&sm.scale_empty[slot]);
                         }
                     }
@@ -314,7 +345,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++done;
             }
             // ---- the sums' way out (after a timeout too, without stores: the warps meet in it) ----
-            if constexpr (!kGated) {
+            if (i == fulls) {
+                // [token][256 columns] over the stages, whose products are done; 16-byte pieces exchanged within 128 bytes
+                // by the token, for the banks
+                if (ok) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int j = 0; j < 16; j += 2)
+                            *piece(row, column(c) / 4 + j / 2) =
+                                make_float4(lo32(acc[c][j]), hi32(acc[c][j]), lo32(acc[c][j + 1]), hi32(acc[c][j + 1]));
+                }
+            } else if constexpr (!kGated) {
                 if (in && ok) {
                     uint16_t *y = a.y + (size_t)m * a.ldy;
 #pragma unroll
@@ -403,29 +445,60 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         }
+        __syncthreads();
+        meet();
+        if (shared) {
+            // ---- the parts of K meet: a warp takes a token, its lanes four channels of either half ----
+            int rt, ct, k0;
+            item(fulls, rt, ct, k0);
+            const int m0 = rt * kRows, first = (int)umma::cluster_rank() - part;
+            for (int r = warp * plan.split + part; r < min(kRows, a.M - m0); r += kWorkWarps * plan.split) {
+                float v[2][4];
+#pragma unroll
+                for (int p = 0; p < 2; ++p) f8b::sum_parts(reinterpret_cast<const float *>(piece(r, 32 * p + lane)), plan.split, first, v[p]);
+                if constexpr (kGated) {
+                    f8b::store_gated(a, m0 + r, ct, lane, v[0], v[1]);
+                } else {
+#pragma unroll
+                    for (int p = 0; p < 2; ++p) f8b::store_bf16(a, m0 + r, ct * kChannels + 128 * p + 4 * lane, v[p]);
+                }
+            }
+        }
+        if (plan.split > 1) umma::cluster_sync();                // (a peer may still read this CTA's sums)
     }
+}
 
-    // The pair ends together: a CTA's barriers and operands are used by its neighbour's copies and products.  After a
-    // timeout (of either CTA: what it does not do runs out in the other) the issuers have stopped; the products in
-    // flight are waited for, and the copies: by their barriers in the even CTA, whose bytes are both CTAs', then by
-    // time (a copy takes microseconds), as a barrier that lacks one CTA's copies never completes.
-    __syncthreads();
-    if (*timeout) {
-        if (rank == 0 && warp == kMmaWarp && umma::elect_one() && issued > 0) {
-            umma::mma_commit_pair(&sm.drain, 1);
-            umma::mbar_wait(&sm.drain, 0, kWaitLimit);
+// CTAs of a cluster of `c` that the device runs at once, a whole number of clusters (0: none).  Asked once for each device.
+template <bool kGated>
+int resident(int c) {
+    constexpr int kDevices = 64;
+    static std::atomic<int> known[kDevices][kMaxSplit + 1];       // 0: not asked yet, else the number + 1
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev < 0 || dev >= kDevices) return c == 1 ? sm_count() : 0;
+    int n = known[dev][c].load(std::memory_order_relaxed);
+    if (n == 0) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)(sm_count() / c * c));
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = kSmem;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = (unsigned)c;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int clusters = 0;
+        if (c == 1)
+            clusters = sm_count();
+        else if (cudaOccupancyMaxActiveClusters(&clusters, tile_kernel<kGated>, &cfg) != cudaSuccess) {
+            cudaGetLastError();
+            clusters = 0;
         }
-        if (warp == kLoadWarp && lane == 0) {
-            if (rank == 0)
-                for (int b = max(0, loads - kStages); b < loads; ++b)
-                    umma::mbar_wait(&sm.full[b % kStages], (uint32_t)((b / kStages) & 1), 1u << 12);
-            for (int i = 0; i < 64; ++i) __nanosleep(10000);
-        }
-        if (threadIdx.x == 0) flag(a.st, QSPEC_ERR_TIMEOUT);
+        n = std::min(clusters * c, sm_count() / c * c) + 1;
+        known[dev][c].store(n, std::memory_order_relaxed);
     }
-    umma::fence_before_sync();
-    umma::cluster_sync();
-    if (warp == kMmaWarp) umma::tmem_free_pair(tmem, 2 * kCols);
+    return n - 1;
 }
 
 template <bool kGated>
@@ -440,12 +513,33 @@ int launch(const char *where, const uint8_t *xq, const uint8_t *w0, const uint8_
     int rc = smem_limit_once(reinterpret_cast<const void *>(kern), (int)kSmem);
     if (rc) return rc;
     constexpr int kChannels = kGated ? 128 : 256;
-    const int row_tiles = (a.M + 2 * kRows - 1) / (2 * kRows), col_tiles = (a.N + kChannels - 1) / kChannels;
-    const long long tiles = (long long)row_tiles * col_tiles;
-    const int pairs = (int)std::min<long long>(tiles, sm_count() / 2);
+    Plan plan = {(a.M + kRows - 1) / kRows, (a.N + kChannels - 1) / kChannels, 0, 1};
+    const long long all = (long long)plan.row_tiles * plan.col_tiles;
+    if (all > INT_MAX / 16) return QSPEC_ERR_SHAPE;
+    const int tiles = (int)all, G = a.K / kGroup;
+    // The cluster's size by what a call would take, in blocks of K of one CTA: full rounds of tiles, then the rest in as
+    // many parts as there are CTAs for; parts cost kMeet blocks to meet.
+    constexpr double kMeet = 6;
+    double least = 1e30;
+    int c = 1, grid = 0;
+    for (int s = 1; s <= kMaxSplit && s <= G; ++s) {
+        const int ctas = resident<kGated>(s);
+        if (ctas < s) continue;
+        const int rounds = tiles / ctas, rest = tiles - rounds * ctas;
+        if (s > 1 && (rest == 0 || rest * s > ctas)) continue;
+        const double takes = (double)rounds * G + (rest == 0 ? 0.0 : s == 1 ? (double)G : (double)((G + s - 1) / s) + kMeet);
+        if (takes < least) {
+            least = takes;
+            c = s;
+            plan.full = s == 1 ? tiles : rounds * ctas;
+            grid = s == 1 ? std::min(tiles, ctas) : rounds > 0 ? ctas : rest * s;
+        }
+    }
+    plan.split = c;
     const int wide = a.y != nullptr && aligned(a.y, 16) && a.ldy % 8 == 0;
-    return launch_pdl_cluster(where, kern, dim3((unsigned)(2 * pairs)), dim3(kThreads), kSmem, stream, 2, t0, t1, tx, a, row_tiles,
-                              col_tiles, wide, wait_limit);
+    if (c == 1)
+        return launch_pdl(where, kern, dim3((unsigned)grid), dim3(kThreads), kSmem, stream, t0, t1, tx, a, plan, wide, wait_limit);
+    return launch_pdl_cluster(where, kern, dim3((unsigned)grid), dim3(kThreads), kSmem, stream, c, t0, t1, tx, a, plan, wide, wait_limit);
 }
 
 }  // namespace f8t

@@ -274,51 +274,5 @@ __device__ __forceinline__ float ld_peer_f32(const void *local_smem, uint32_t ra
     return v;
 }
 
-// ---- pairs of CTAs (a cluster of two, or two neighbours of a larger one): products of 256 rows, 128 of them and half
-// of the columns' operand in each CTA's shared memory, 128 rows of the accumulator in each CTA's tensor memory ----
-__device__ __forceinline__ void tmem_alloc_pair(uint32_t *dst_smem, uint32_t ncols) {        // one warp of each CTA
-    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(smem_addr(dst_smem)),
-                 "r"(ncols));
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;\n");
-}
-__device__ __forceinline__ void tmem_free_pair(uint32_t taddr, uint32_t ncols) {             // one warp of each CTA
-    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;\n" ::"r"(taddr), "r"(ncols));
-}
-// issued by the even CTA alone
-__device__ __forceinline__ void mma_e4m3_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                              uint32_t accumulate) {
-    asm volatile(
-        "{.reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;}\n" ::"r"(
-            d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate));
-}
-// arrive on the barrier at `bar`'s place in every CTA of `mask` once the products issued so far have completed
-__device__ __forceinline__ void mma_commit_pair(uint64_t *bar, uint16_t mask) {
-    asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n" ::"r"(
-            smem_addr(bar)),
-        "h"(mask)
-        : "memory");
-}
-// the address of a peer CTA's copy of a shared variable
-__device__ __forceinline__ uint32_t peer_addr(const void *local_smem, uint32_t rank) {
-    uint32_t remote;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(remote) : "r"(smem_addr(local_smem)), "r"(rank));
-    return remote;
-}
-// Tells of tensor memory that has been read (tcgen05.wait, fence_before_sync), not of writes to memory: a release for
-// the cluster waits for every load in flight (1400 clocks in the work loop of fp8_block_tile.cu).
-__device__ __forceinline__ void mbar_arrive_relaxed_at(uint32_t cluster_addr) {
-    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(cluster_addr) : "memory");
-}
-// TMA load into this CTA's shared memory that completes on a barrier of either CTA of the pair
-__device__ __forceinline__ void tma_load_2d_pair(void *dst, const void *tmap, int x, int y, uint32_t bar_cluster_addr) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
-        "[%4];\n" ::"r"(smem_addr(dst)),
-        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(bar_cluster_addr)
-        : "memory");
-}
-
 }  // namespace umma
 }  // namespace qspec
