@@ -505,6 +505,8 @@ int qspec_attn_prompt(const uint16_t *q_bf16, int ldq, const uint16_t *k_bf16, i
  *   w8 uint8 [N][K]                      E4M3 codes of weights
  *   sw float [ceil(N / 128)][K / 128]    their scales
  * K is a multiple of 128.  E4M3 and its rounding are those of the Q8 variant.
+ * Weights are read ahead of the call's turn in the stream: in front of a product on
+ * the same stream, of the calls here only qspec_quant_weights_fp8_block may write them.
  * ------------------------------------------------------------------------ */
 
 /*

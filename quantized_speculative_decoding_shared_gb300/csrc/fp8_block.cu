@@ -161,7 +161,6 @@ __global__ void __launch_bounds__(kThreads, 3)
     __shared__ float red[kThreads / 32];
     const int half = threadIdx.x >> 4, lane = threadIdx.x & 15, warp = threadIdx.x >> 5;
     const int G = K / kGroup, g = (int)(blockIdx.x % (unsigned)G), nb = (int)(blockIdx.x / (unsigned)G), n0 = nb * kGroup;
-    pdl_launch_dependents();
     pdl_wait();
     uint4 v[kPer];
 #pragma unroll
@@ -191,6 +190,11 @@ __global__ void __launch_bounds__(kThreads, 3)
         sw[(size_t)nb * G + g] = s;
         if (!(amax < INFINITY)) flag(st, QSPEC_ERR_NONFINITE);
     }
+    // Only now may the next kernel begin: a product behind this one reads its weights ahead of its dependency wait.  (A
+    // CTA's first thread to come here speaks for all of them.)
+    __threadfence();
+    __syncthreads();
+    pdl_launch_dependents();
 }
 
 template <int NI>

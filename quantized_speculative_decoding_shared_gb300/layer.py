@@ -1,5 +1,6 @@
-"""The attention half of a decoder layer, from library calls only.
+"""The two halves of a decoder layer, from library calls only.
 
+Attention (AttentionLayer):
     h = x + residual                                   rmsnorm_fp8 (sum, norm and E4M3 codes in one pass)
     [q k v] = norm(h) W_qkv                            linear_fp8
     cache[b][:, base[b] + i] = 4 bits of (k, v)        kv4_append
@@ -12,8 +13,15 @@ the cache's entries, read back by kv4_load.  A draft step is one row per
 sequence, a verify pass gamma + 1 rows whose entries overwrite the draft's
 (both from position `base`).  The class holds no rotary positions and no biases: a
 model that has them makes the same calls, with its own step between the projection
-and kv4_append.  ``python -m quantized_speculative_decoding_shared_gb300.layer``
-runs prompts, draft steps and a verify pass on seeded inputs.
+and kv4_append.
+
+Feed-forward (FeedForward), E4M3 with a scale for each block of 128:
+    h = x + residual                                   rmsnorm_fp8_block
+    u = silu(norm(h) W_gate) * (norm(h) W_up)          gated_fp8_block (one kernel, its codes ready for the next call)
+    y = u W_down                                       linear_fp8_block
+
+``python -m quantized_speculative_decoding_shared_gb300.layer`` runs prompts, draft
+steps and a verify pass through both on seeded inputs.
 """
 from __future__ import annotations
 
@@ -85,24 +93,55 @@ class AttentionLayer:
             return self._out(o), h
 
 
+class FeedForward:
+    """Weights of the gated half of a layer: w_gate, w_up fp16 [N][K], w_down fp16 [K][N] (parents of the E4M3 weights),
+    w_norm bf16 [K]; N and K multiples of 128.
+
+    The weights are quantised on torch's current stream; run works on `stream` (None: the current one), and all that it
+    makes belongs to it, its results included.  It keeps nothing between calls: calls on different streams may overlap."""
+
+    def __init__(self, w_norm, w_gate, w_up, w_down, eps=1e-5):
+        self.w_norm, self.eps = w_norm, eps
+        self.status = torch.zeros(1, dtype=torch.int32, device=w_norm.device)
+        self.gate = q.quant_weights_fp8_block(w_gate, dev_status=self.status)
+        self.up = q.quant_weights_fp8_block(w_up, dev_status=self.status)
+        self.down = q.quant_weights_fp8_block(w_down, dev_status=self.status)
+
+    def run(self, x, residual=None, stream=None):
+        """Rows x bf16 [rows][K] of prompts, draft steps or a verify pass.  Returns (y, h): the block's output and the
+        residual stream (None without residual)."""
+        with q.on_stream(stream):
+            if x.shape[0] == 0:                          # (the calls take one row at least)
+                return torch.empty_like(x), None if residual is None else torch.empty_like(x)
+            xq, sa, h, _ = q.rmsnorm_fp8_block(x, self.w_norm, self.eps, residual=residual, dev_status=self.status)
+            hq, sh, _ = q.gated_fp8_block(xq, sa, *self.gate, *self.up, dev_status=self.status)
+            return q.linear_fp8_block(hq, sh, *self.down, dev_status=self.status), h
+
+
 def main():
     from . import synthetic as syn
     dev = torch.device("cuda")
-    K, Hq, H, D, B, T, gamma = 2048, 16, 4, 128, 4, 512, 4
+    K, N, Hq, H, D, B, T, gamma = 2048, 5632, 16, 4, 128, 4, 512, 4
     fp16 = lambda n, k, seed: (syn.activations(n, k, seed, device=dev).float() * 0.02).to(torch.float16)   # noqa: E731
-    layer = AttentionLayer(torch.ones(K, dtype=torch.bfloat16, device=dev), fp16((Hq + 2 * H) * D, K, 1),
-                           fp16(K, Hq * D, 2), Hq, H, D, B, T)
+    ones = torch.ones(K, dtype=torch.bfloat16, device=dev)
+    layer = AttentionLayer(ones, fp16((Hq + 2 * H) * D, K, 1), fp16(K, Hq * D, 2), Hq, H, D, B, T)
+    ffn = FeedForward(ones, fp16(N, K, 5), fp16(N, K, 6), fp16(K, N, 7))
     lens = [200, 1, 77, 130]
     start = torch.tensor([0, 200, 201, 278, 408], dtype=torch.int32, device=dev)
     x = syn.activations(sum(lens), K, 3, device=dev)
     y, h = layer.prompt(x, start, residual=syn.activations(sum(lens), K, 4, device=dev))
+    y, h = ffn.run(y, residual=h)
     base = torch.tensor(lens, dtype=torch.int32, device=dev)
     for i in range(gamma):
-        layer.step(syn.activations(B, K, 10 + i, device=dev), base + i)
-    y, _ = layer.step(syn.activations(B * (gamma + 1), K, 20, device=dev), base)
+        x = syn.activations(B, K, 10 + i, device=dev)
+        y, h = layer.step(x, base + i, residual=x)
+        ffn.run(y, residual=h)
+    x = syn.activations(B * (gamma + 1), K, 20, device=dev)
+    y, h = layer.step(x, base, residual=x)
+    y, _ = ffn.run(y, residual=h)
     torch.cuda.synchronize()
     print("prompts of %s rows, %d draft steps, a verify pass of %d rows: status %d, |y| mean %.4f"
-          % (lens, gamma, y.shape[0], int(layer.status.item()), float(y.float().abs().mean())))
+          % (lens, gamma, y.shape[0], int((layer.status + ffn.status).item()), float(y.float().abs().mean())))
 
 
 if __name__ == "__main__":
