@@ -5,18 +5,23 @@
 //   quotient, round to nearest even, saturated at 448); a block of zeros has
 //   s = 0 and codes 0.
 //
-// The quotient takes two fused steps from the correctly rounded reciprocal y of
-// s: q = v y, t = q + y (v - q s), the remainder exact.  That is the IEEE quotient
-// wherever nothing under- or overflows on the way (Markstein, "Computation of
-// elementary functions on the IBM RISC System/6000 processor", IBM J. Res.
-// Dev. 34, 1990).  Scales outside (2^-80, 2^80) take the division; inside, a value
-// with a code that is not 0 is at least 2^-90, and its remainder's last place, 47
-// below its first, is a number.
+// The quotient takes two fused steps from the reciprocal y of s: q = v y, t = q + y (v - q s),
+// the remainder exact.  With y correctly rounded that is the IEEE quotient wherever nothing
+// under- or overflows on the way (Markstein, "Computation of elementary functions on the IBM
+// RISC System/6000 processor", IBM J. Res. Dev. 34, 1990); y here is one Newton step from the
+// approximate reciprocal, in the last place the correctly rounded one or its neighbour, and
+// the codes are the division's for all values of either type over the scales of all maxima
+// (tests/test_gpu_fp8_block.py goes through them).  Scales outside (2^-80, 2^80) take
+// the division; inside, a value with a code that is not 0 is at least 2^-90, and its
+// remainder's last place, 47 below its first, is a number.
 //
-// Bound: HBM (2 bytes in, 1 out per value).  Half a warp has one token's 128
-// values, 16 bytes to a lane; a CTA takes 4 neighbouring blocks of up to 32
-// tokens, so that reads are 1 KB at a time and the scales, which lie token by
-// token, go out 128 bytes at a time through shared memory.
+// Bound: HBM (2 bytes in, 1 out per value).  8 lanes have one token's 128 values, 32 bytes
+// to a lane (16 lanes and 16 bytes where addresses are no multiples of 32: 4099 x 14336 in
+// 30.7 us for 28.8, 6.1 TB/s); a CTA takes 4 neighbouring blocks of some tokens, so that reads are
+// 1 KB at a time and the scales, which lie token by token, go out in runs through
+// shared memory.  With the divisions of s and y, 16 lanes and half the CTAs resident
+// it took 34.7 us.
+#include <algorithm>
 #include <climits>
 
 #include <cuda_fp16.h>
@@ -32,7 +37,6 @@ namespace {
 namespace f8b {
 
 constexpr int kThreads = 256;
-constexpr int kHalves = kThreads / 16;          // half warps
 constexpr int kBlocksX = 4;                     // neighbouring blocks per CTA
 
 // max(a, |b|, |c|) and max(a, b) that keep a NaN (a >= 0)
@@ -75,133 +79,180 @@ __device__ __forceinline__ uint64_t both(uint32_t w) {
     }
     return f2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
 }
-template <bool kHalf>
-__device__ __forceinline__ float max_of(uint4 v, float amax) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+// W words of a row; 8 of them, 32 bytes, in one load
+template <int W>
+struct Words {
+    uint32_t w[W];
+};
+template <int W>
+__device__ __forceinline__ Words<W> load(const uint16_t *p, bool in) {
+    Words<W> v;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const uint64_t f = both<kHalf>(w[e]);
+    for (int e = 0; e < W; ++e) v.w[e] = 0;
+    if (in) {
+        if constexpr (W == 8) {
+            asm volatile("ld.global.cs.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
+                         : "=r"(v.w[0]), "=r"(v.w[1]), "=r"(v.w[2]), "=r"(v.w[3]), "=r"(v.w[4]), "=r"(v.w[5]), "=r"(v.w[6]), "=r"(v.w[7])
+                         : "l"(p));
+        } else {
+            const uint4 u = __ldcs(reinterpret_cast<const uint4 *>(p));
+            v.w[0] = u.x, v.w[1] = u.y, v.w[2] = u.z, v.w[3] = u.w;
+        }
+    }
+    return v;
+}
+template <bool kHalf, int W>
+__device__ __forceinline__ float max_of(const Words<W> &v, float amax) {
+#pragma unroll
+    for (int e = 0; e < W; ++e) {
+        const uint64_t f = both<kHalf>(v.w[e]);
         amax = max_abs(amax, lo32(f), hi32(f));
     }
     return amax;
+}
+
+// amax / 448 (the quotient's two steps, 1 / 448 rounded; the division at fp32's ends)
+__device__ __forceinline__ float scale_of(float amax) {
+    constexpr float kY = 1.0f / 448.0f;
+    if (!(amax > 1.0e-30f && amax < 1.0e38f)) return __fdiv_rn(amax, 448.0f);
+    const float q = __fmul_rn(amax, kY);
+    return __fmaf_rn(__fmaf_rn(-q, 448.0f, amax), kY, q);
+}
+__device__ __forceinline__ float reciprocal(float s) {
+    const float y = rcp_approx(s);
+    return __fmaf_rn(__fmaf_rn(-s, y, 1.0f), y, y);
 }
 
 __device__ __forceinline__ uint32_t pack_e4m3(float a, float b) {          // the first in the low byte
     return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
 }
 
-// the codes of 8 values over the scale s; one of 0 stands for a block of zeros
-template <bool kHalf>
-__device__ __forceinline__ uint2 codes_of(uint4 v, float s, float y) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    uint32_t c[4];
+// the codes of 2 W values over the scale s, stored; s = 0 stands for a block of zeros
+template <bool kHalf, int W>
+__device__ __forceinline__ void store_codes(uint8_t *out, const Words<W> &v, float s, float y, bool in) {
+    uint32_t c[W / 2];
     if (s > 8.271806125530277e-25f && s < 1.2089258196146292e24f) {        // 2^-80, 2^80
         const uint64_t yy = f2(y, y), ss = f2(-s, -s);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const uint64_t f = both<kHalf>(w[e]), q = mul2(f, yy), t = fma2(fma2(q, ss, f), yy, q);
-            c[e] = pack_e4m3(copysignf(lo32(t), lo32(f)), copysignf(hi32(t), hi32(f)));      // (-0 stays -0)
+        for (int e = 0; e < W; ++e) {
+            const uint64_t f = both<kHalf>(v.w[e]), q = mul2(f, yy), t = fma2(fma2(q, ss, f), yy, q);
+            const uint32_t h = pack_e4m3(copysignf(lo32(t), lo32(f)), copysignf(hi32(t), hi32(f)));      // (-0 stays -0)
+            c[e / 2] = e % 2 == 0 ? h : c[e / 2] | h << 16;
         }
     } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const uint64_t f = both<kHalf>(w[e]);
-            c[e] = s == 0.0f ? 0u : pack_e4m3(__fdiv_rn(lo32(f), s), __fdiv_rn(hi32(f), s));
+        for (int e = 0; e < W; ++e) {
+            const uint64_t f = both<kHalf>(v.w[e]);
+            const uint32_t h = s == 0.0f ? 0u : pack_e4m3(__fdiv_rn(lo32(f), s), __fdiv_rn(hi32(f), s));
+            c[e / 2] = e % 2 == 0 ? h : c[e / 2] | h << 16;
         }
     }
-    return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+    if (!in) return;
+    if constexpr (W == 8)
+        *reinterpret_cast<uint4 *>(out) = make_uint4(c[0], c[1], c[2], c[3]);
+    else
+        *reinterpret_cast<uint2 *>(out) = make_uint2(c[0], c[1]);
 }
 
-// NI items (token, block) per half warp: NI * kHalves / kBlocksX tokens per CTA
-template <int NI>
-__global__ void __launch_bounds__(kThreads)
+// teams of 64 / W lanes, each with NI items (token, block)
+template <int W>
+struct Act {
+    static constexpr int kTeam = 64 / W, kTeams = kThreads / kTeam, kItems = W == 8 ? 2 : 4, kRows = kItems * kTeams / kBlocksX;
+};
+
+template <int W>
+__global__ void __launch_bounds__(kThreads, (W == 8 ? 6 : 7))
     quant_act_kernel(const uint16_t *__restrict__ x, int M, int K, int ldx, uint8_t *__restrict__ xq,
                      float *__restrict__ sa, int lds, int32_t *st) {
-    constexpr int kRows = NI * kHalves / kBlocksX;
-    __shared__ float scales[kBlocksX][kRows];
-    const int half = threadIdx.x >> 4, lane = threadIdx.x & 15;
+    using A = Act<W>;
+    __shared__ float scales[kBlocksX][A::kRows];
+    const int team = threadIdx.x / A::kTeam, lane = threadIdx.x % A::kTeam;
     const int G = K / kGroup, across = (G + kBlocksX - 1) / kBlocksX;
-    const int g0 = (int)(blockIdx.x % (unsigned)across) * kBlocksX, r0 = (int)(blockIdx.x / (unsigned)across) * kRows;
-    const int g = g0 + half % kBlocksX;
+    const int g0 = (int)(blockIdx.x % (unsigned)across) * kBlocksX, r0 = (int)(blockIdx.x / (unsigned)across) * A::kRows;
+    const int g = g0 + team % kBlocksX;
+    const size_t col = (size_t)g * kGroup + lane * 2 * W;
     pdl_launch_dependents();
     pdl_wait();
-    uint4 v[NI];
+    Words<W> v[A::kItems];
 #pragma unroll
-    for (int i = 0; i < NI; ++i) {
-        const int m = r0 + half / kBlocksX + i * (kHalves / kBlocksX);
-        v[i] = m < M && g < G ? __ldcs(reinterpret_cast<const uint4 *>(x + (size_t)m * ldx + (size_t)g * kGroup) + lane)
-                              : make_uint4(0, 0, 0, 0);
+    for (int i = 0; i < A::kItems; ++i) {
+        const int m = r0 + team / kBlocksX + i * (A::kTeams / kBlocksX);
+        v[i] = load<W>(x + (size_t)m * ldx + col, m < M && g < G);
     }
     bool bad = false;
 #pragma unroll
-    for (int i = 0; i < NI; ++i) {
-        const int r = half / kBlocksX + i * (kHalves / kBlocksX), m = r0 + r;
-        float amax = max_of<false>(v[i], 0.0f);
+    for (int i = 0; i < A::kItems; ++i) {
+        const int r = team / kBlocksX + i * (A::kTeams / kBlocksX), m = r0 + r;
+        float amax = max_of<false, W>(v[i], 0.0f);
 #pragma unroll
-        for (int o = 8; o >= 1; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        const float s = __fdiv_rn(amax, 448.0f);
+        for (int o = A::kTeam / 2; o >= 1; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        const float s = scale_of(amax);
         bad |= !(amax < INFINITY);
-        const uint2 c = codes_of<false>(v[i], s, __frcp_rn(s));
-        if (m < M && g < G) reinterpret_cast<uint2 *>(xq + (size_t)m * K + (size_t)g * kGroup)[lane] = c;
-        if (lane == 0) scales[half % kBlocksX][r] = s;
+        store_codes<false, W>(xq + (size_t)m * K + col, v[i], s, reciprocal(s), m < M && g < G);
+        if (lane == 0) scales[team % kBlocksX][r] = s;
     }
     const int bad_any = __syncthreads_or(bad ? 1 : 0);
-    for (int i = threadIdx.x; i < kBlocksX * kRows; i += kThreads) {
-        const int gg = g0 + i / kRows, m = r0 + i % kRows;
-        if (gg < G && m < M) sa[(size_t)gg * lds + m] = scales[i / kRows][i % kRows];
+    for (int i = threadIdx.x; i < kBlocksX * A::kRows; i += kThreads) {
+        const int gg = g0 + i / A::kRows, m = r0 + i % A::kRows;
+        if (gg < G && m < M) sa[(size_t)gg * lds + m] = scales[i / A::kRows][i % A::kRows];
     }
     if (threadIdx.x == 0 && bad_any) flag(st, QSPEC_ERR_NONFINITE);
 }
 
-// one 128 x 128 block per CTA, kept in registers between its load and its codes
+// One 128 x 128 block at a time, kept in registers between its load and its codes.
+template <int W>
 __global__ void __launch_bounds__(kThreads, 3)
-    quant_weights_kernel(const uint16_t *__restrict__ w, int N, int K, uint8_t *__restrict__ w8, float *__restrict__ sw,
-                         int32_t *st) {
-    constexpr int kPer = kGroup / kHalves;       // rows per half warp
-    __shared__ float red[kThreads / 32];
-    const int half = threadIdx.x >> 4, lane = threadIdx.x & 15, warp = threadIdx.x >> 5;
-    const int G = K / kGroup, g = (int)(blockIdx.x % (unsigned)G), nb = (int)(blockIdx.x / (unsigned)G), n0 = nb * kGroup;
+    quant_weights_kernel(const uint16_t *__restrict__ w, int N, int K, int blocks, uint8_t *__restrict__ w8,
+                         float *__restrict__ sw, int32_t *st) {
+    constexpr int kTeam = 64 / W, kTeams = kThreads / kTeam, kPer = kGroup / kTeams;       // rows per team
+    __shared__ float red[2][kThreads / 32];
+    const int team = threadIdx.x / kTeam, lane = threadIdx.x % kTeam, warp = threadIdx.x >> 5;
+    const int G = K / kGroup;
     pdl_wait();
-    uint4 v[kPer];
+    int turn = 0;
+    for (long long b = blockIdx.x; b < blocks; b += gridDim.x, turn ^= 1) {
+        const int g = (int)(b % G), nb = (int)(b / G), n0 = nb * kGroup + team;
+        const size_t col = (size_t)g * kGroup + lane * 2 * W;
+        Words<W> v[kPer];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const int n = n0 + half + i * kHalves;
-        v[i] = n < N ? __ldcs(reinterpret_cast<const uint4 *>(w + (size_t)n * K + (size_t)g * kGroup) + lane)
-                     : make_uint4(0, 0, 0, 0);
-    }
-    float amax = 0.0f;
+        for (int i = 0; i < kPer; ++i) v[i] = load<W>(w + (size_t)(n0 + i * kTeams) * K + col, n0 + i * kTeams < N);
+        float amax = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) amax = max_of<true>(v[i], amax);
+        for (int i = 0; i < kPer; ++i) amax = max_of<true, W>(v[i], amax);
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    if ((threadIdx.x & 31) == 0) red[warp] = amax;
-    __syncthreads();
-    amax = red[0];
+        for (int o = 16; o >= 1; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        if ((threadIdx.x & 31) == 0) red[turn][warp] = amax;
+        __syncthreads();
+        amax = red[turn][0];
 #pragma unroll
-    for (int i = 1; i < kThreads / 32; ++i) amax = max_nan(amax, red[i]);
-    const float s = __fdiv_rn(amax, 448.0f), y = __frcp_rn(s);
+        for (int i = 1; i < kThreads / 32; ++i) amax = max_nan(amax, red[turn][i]);
+        const float s = scale_of(amax), y = reciprocal(s);
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const int n = n0 + half + i * kHalves;
-        const uint2 c = codes_of<true>(v[i], s, y);
-        if (n < N) reinterpret_cast<uint2 *>(w8 + (size_t)n * K + (size_t)g * kGroup)[lane] = c;
-    }
-    if (threadIdx.x == 0) {
-        sw[(size_t)nb * G + g] = s;
-        if (!(amax < INFINITY)) flag(st, QSPEC_ERR_NONFINITE);
+        for (int i = 0; i < kPer; ++i)
+            store_codes<true, W>(w8 + (size_t)(n0 + i * kTeams) * K + col, v[i], s, y, n0 + i * kTeams < N);
+        if (threadIdx.x == 0) {
+            sw[(size_t)nb * G + g] = s;
+            if (!(amax < INFINITY)) flag(st, QSPEC_ERR_NONFINITE);
+        }
     }
     // Only now may the next kernel begin: a product behind this one reads its weights ahead of its dependency wait.  (A
-    // CTA's first thread to come here speaks for all of them.)
+    // CTA's first thread to come here speaks for all of them.  A fence behind every block took 3 of 34 us at 4099 x
+    // 14336, so a CTA goes through several.)
     __threadfence();
     __syncthreads();
     pdl_launch_dependents();
 }
 
-template <int NI>
+template <int W>
 int launch_act(const uint16_t *x, int M, int K, int ldx, uint8_t *xq, float *sa, int lds, int32_t *st, cudaStream_t s) {
-    constexpr int kRows = NI * kHalves / kBlocksX;
-    const long long ctas = (long long)((K / kGroup + kBlocksX - 1) / kBlocksX) * (((long long)M + kRows - 1) / kRows);
-    return launch_pdl("qspec_quant_act_fp8_block", quant_act_kernel<NI>, dim3((unsigned)ctas), dim3(kThreads), 0, s, x, M, K, ldx, xq, sa, lds, st);
+    const long long ctas = (long long)((K / kGroup + kBlocksX - 1) / kBlocksX) * (((long long)M + Act<W>::kRows - 1) / Act<W>::kRows);
+    return launch_pdl("qspec_quant_act_fp8_block", quant_act_kernel<W>, dim3((unsigned)ctas), dim3(kThreads), 0, s, x, M, K, ldx, xq, sa, lds, st);
+}
+
+template <int W>
+int launch_weights(const uint16_t *w, int N, int K, int blocks, uint8_t *w8, float *sw, int32_t *st, cudaStream_t s) {
+    return launch_pdl("qspec_quant_weights_fp8_block", quant_weights_kernel<W>, dim3((unsigned)std::min(blocks, 3 * sm_count())),
+                      dim3(kThreads), 0, s, w, N, K, blocks, w8, sw, st);
 }
 
 }  // namespace f8b
@@ -221,8 +272,10 @@ extern "C" int qspec_quant_weights_fp8_block(const uint16_t *w_fp16, int N, int 
     if (blocks > INT_MAX) return QSPEC_ERR_SHAPE;
     int rc = check_device();
     if (rc) return rc;
-    return launch_pdl("qspec_quant_weights_fp8_block", f8b::quant_weights_kernel, dim3((unsigned)blocks), dim3(f8b::kThreads), 0,
-                      as_cuda(stream), w_fp16, N, K, w8, sw, dev_status);
+    cudaStream_t s = as_cuda(stream);
+    // 32 bytes to a lane where the addresses allow it
+    if (aligned(w_fp16, 32) && aligned(w8, 16)) return f8b::launch_weights<8>(w_fp16, N, K, (int)blocks, w8, sw, dev_status, s);
+    return f8b::launch_weights<4>(w_fp16, N, K, (int)blocks, w8, sw, dev_status, s);
 }
 
 extern "C" int qspec_quant_act_fp8_block(const uint16_t *x_bf16, int M, int K, int ldx, uint8_t *xq, float *sa, int lds,
@@ -233,6 +286,7 @@ extern "C" int qspec_quant_act_fp8_block(const uint16_t *x_bf16, int M, int K, i
     int rc = check_device();
     if (rc) return rc;
     cudaStream_t s = as_cuda(stream);
-    if ((long long)M * K < 1 << 22) return f8b::launch_act<2>(x_bf16, M, K, ldx, xq, sa, lds, dev_status, s);
-    return f8b::launch_act<8>(x_bf16, M, K, ldx, xq, sa, lds, dev_status, s);
+    if (aligned(x_bf16, 32) && ldx % 16 == 0 && aligned(xq, 16))
+        return f8b::launch_act<8>(x_bf16, M, K, ldx, xq, sa, lds, dev_status, s);
+    return f8b::launch_act<4>(x_bf16, M, K, ldx, xq, sa, lds, dev_status, s);
 }

@@ -63,22 +63,68 @@ def test_activation_codes_of_extreme_magnitudes(scale):
     assert same(sa, want[1]) and same(xq, want[0])
 
 
-def test_every_bf16_value_over_several_scales():
-    """All finite bf16 values not above a block's maximum: code and quotient agree with the division."""
+def over_all_maxima(bits, top_bits, dtype, dev):
+    """Blocks of 128 that pair every value of `bits` with every maximum of `top_bits` that is not below it."""
+    v = torch.tensor(bits, dtype=torch.int32).to(torch.int16).view(dtype).to(dev)
+    blocks = []
+    for t in top_bits:
+        top = torch.tensor([t], dtype=torch.int32).to(torch.int16).view(dtype).to(dev)
+        x = v[v.abs() <= top]
+        n = -(-len(x) // 127)
+        pad = torch.zeros(n * 127, dtype=dtype, device=dev)
+        pad[:len(x)] = x
+        blocks.append(torch.cat([top.expand(n, 1), pad.view(n, 127)], dim=1))
+    return torch.cat(blocks)
+
+
+def test_every_bf16_value_over_every_scale():
+    """All 128 significands of a maximum with all values of 26 binades below it, of either sign, zeros and subnormal codes among
+    them: code and quotient are the division's."""
     dev = need_gpu()
-    for top in (448.0, 1.0, 3.140625, 0.0087890625, 1.5e30, 2.0 ** -70):
-        top = torch.tensor(top).to(torch.bfloat16)
-        v = torch.arange(0, 1 << 16, dtype=torch.int32).to(torch.int16).view(torch.bfloat16)
-        v = v[torch.isfinite(v) & (v.abs() <= top)]
-        n = -(-len(v) // 127)
-        rows = torch.zeros((n, 128), dtype=torch.bfloat16)
-        rows[:, 0] = top
-        pad = torch.zeros(n * 127, dtype=torch.bfloat16)
-        pad[: len(v)] = v
-        rows[:, 1:] = pad.view(n, 127)
-        xq, sa = q.quant_act_fp8_block(rows.to(dev))
-        want = act_codes(rows)
-        assert same(xq, want[0]) and same(sa, want[1])
+    bits = [sign | (e << 7) | f for sign in (0, 0x8000) for e in range(102, 129) for f in range(128)] + [0, 0x8000, 1, 0x8001]
+    x = over_all_maxima(bits, [(127 << 7) | f for f in range(128)] + [(128 << 7)], torch.bfloat16, dev)
+    xq, sa = q.quant_act_fp8_block(x)
+    v = x.float()
+    s = v.abs().amax(-1) / torch.tensor(448.0, device=dev)      # (by a number it would be times 1 / 448)
+    want = (v / s[:, None]).clamp(-448.0, 448.0).to(torch.float8_e4m3fn)
+    assert torch.equal(sa[0], s) and torch.equal(xq, want.view(torch.uint8))
+
+
+def test_every_fp16_value_over_every_scale():
+    """All 1024 significands of a maximum with all values of 20 binades, as weights (a block's values in its 128 rows)."""
+    dev = need_gpu()
+    bits = [sign | (e << 10) | f for sign in (0, 0x8000) for e in range(0, 17) for f in range(0, 1024)]
+    for part in range(0, 1024, 64):
+        x = over_all_maxima(bits, [(15 << 10) | f for f in range(part, part + 64)], torch.float16, dev)
+        n = x.shape[0]
+        w = torch.zeros((128, n * 128), dtype=torch.float16, device=dev)
+        w[5] = x.reshape(-1)
+        w8, sw = q.quant_weights_fp8_block(w)
+        v = x.float()
+        s = v.abs().amax(-1) / torch.tensor(448.0, device=dev)      # (by a number it would be times 1 / 448)
+        want = (v / s[:, None]).clamp(-448.0, 448.0).to(torch.float8_e4m3fn)
+        assert torch.equal(sw[0], s) and torch.equal(w8[5].view(n, 128), want.view(torch.uint8))
+        assert int(w8.count_nonzero()) == int(w8[5].count_nonzero())
+
+
+@pytest.mark.parametrize("off", [0, 8])
+def test_addresses_on_16_bytes(off):
+    """Rows that begin between multiples of 32 bytes take their own way."""
+    dev = need_gpu()
+    M, K = 37, 640
+    wide = torch.zeros((M, K + 24), dtype=torch.bfloat16, device=dev)
+    wide[:, off:off + K] = acts(M, K, 2, dev)
+    x = wide[:, off:off + K]
+    st = status(dev)
+    xq, sa = q.quant_act_fp8_block(x, dev_status=st)
+    want = act_codes(x)
+    assert read_status(st) == 0 and same(xq, want[0]) and same(sa, want[1])
+    flat = torch.zeros(M * K + 16, dtype=torch.float16, device=dev)
+    flat[off:off + M * K] = parent(M, K, 3, dev).reshape(-1)
+    w = flat[off:off + M * K].view(M, K)
+    w8, sw = q.quant_weights_fp8_block(w, dev_status=st)
+    want = weight_codes(w)
+    assert read_status(st) == 0 and same(w8, want[0]) and same(sw, want[1])
 
 
 def test_rows_and_scales_apart():
