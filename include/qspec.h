@@ -619,6 +619,16 @@ int qspec_debug_attn_prompt_bounded(const uint16_t *q_bf16, int ldq, const uint1
                                     float scale, uint16_t *o_bf16, int ldo, uint32_t wait_limit, int stall,
                                     int32_t *dev_status, qspec_stream_t stream);
 
+/*
+ * The same for the products with block scales: the arguments of
+ * qspec_gated_fp8_block, or with w1 NULL those of qspec_linear_fp8_block (s1, hq, sh
+ * and ldh unused), on the kernel that the regular call would take.
+ */
+int qspec_debug_fp8_block_bounded(const uint8_t *xq, const float *sa, int lds, const uint8_t *w0, const float *s0,
+                                  const uint8_t *w1, const float *s1, int M, int N, int K, uint8_t *hq, float *sh,
+                                  int ldh, uint16_t *y_bf16, int ldy, uint32_t wait_limit, int stall,
+                                  int32_t *dev_status, qspec_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -41,7 +41,7 @@ EXPORTED = ["qspec_version", "qspec_status_string", "qspec_last_cuda_error", "qs
             "qspec_rmsnorm_fp8", "qspec_kv4_append", "qspec_kv4_load", "qspec_attn_kv4_workspace_bytes",
             "qspec_attn_kv4", "qspec_attn_prompt", "qspec_debug_attn_kv4_bounded",
             "qspec_debug_attn_prompt_bounded", "qspec_quant_weights_fp8_block", "qspec_quant_act_fp8_block",
-            "qspec_rmsnorm_fp8_block", "qspec_linear_fp8_block", "qspec_gated_fp8_block"]
+            "qspec_rmsnorm_fp8_block", "qspec_linear_fp8_block", "qspec_gated_fp8_block", "qspec_debug_fp8_block_bounded"]
 KERNEL_W4A16_TC, KERNEL_W4A4_GEMV_TC, KERNEL_W4A4_TC = 0, 1, 2
 NOALLOC_SCRATCH_BYTES = 1 << 20
 
@@ -121,6 +121,8 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
                                         i32),
             "qspec_linear_fp8_block": ([vp, vp, i32, vp, vp, i32, i32, i32, vp, i32, vp, vp], i32),
             "qspec_gated_fp8_block": ([vp, vp, i32, vp, vp, vp, vp, i32, i32, i32, vp, vp, i32, vp, i32, vp, vp], i32),
+            "qspec_debug_fp8_block_bounded": ([vp, vp, i32, vp, vp, vp, vp, i32, i32, i32, vp, vp, i32, vp, i32,
+                                               ctypes.c_uint32, i32, vp, vp], i32),
         }
         for name, (args, res) in proto.items():
             f = getattr(lib, name)
@@ -382,6 +384,13 @@ def qspec_gated_fp8_block(xq, sa, lds, w_gate, s_gate, w_up, s_up, M, N, K, hq, 
     return load_library().qspec_gated_fp8_block(_ptr(xq), _ptr(sa), lds, _ptr(w_gate), _ptr(s_gate), _ptr(w_up),
                                                 _ptr(s_up), M, N, K, _ptr(hq), _ptr(sh), ldh, _ptr(h), ldy,
                                                 _ptr(dev_status), _stream(stream))
+
+
+def qspec_debug_fp8_block_bounded(xq, sa, lds, w0, s0, w1, s1, M, N, K, hq, sh, ldh, y, ldy, wait_limit, stall,
+                                  dev_status=None, stream=None):
+    return load_library().qspec_debug_fp8_block_bounded(
+        _ptr(xq), _ptr(sa), lds, _ptr(w0), _ptr(s0), _ptr(w1), _ptr(s1), M, N, K, _ptr(hq), _ptr(sh), ldh, _ptr(y), ldy,
+        wait_limit, stall, _ptr(dev_status), _stream(stream))
 
 
 # ---------------------------------------------------------------------------

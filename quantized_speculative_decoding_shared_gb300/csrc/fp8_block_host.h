@@ -7,9 +7,10 @@
 namespace qspec {
 namespace f8b {
 
+// wait_limit, stall: as in qspec_host.h's launches of the other tensor-core kernels.
 // Many tokens (fp8_block_tile.cu); w1: the up projection's weights of the gated product, else null.
 int launch_tile(const char *where, const uint8_t *xq, const uint8_t *w0, const uint8_t *w1, const Args &a, cudaStream_t stream,
-                uint32_t wait_limit);
+                uint32_t wait_limit, int stall);
 
 }  // namespace f8b
 }  // namespace qspec

@@ -79,7 +79,8 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
 template <int BN, bool kGated>
 __global__ void __launch_bounds__(kThreads, (Cfg<BN, kGated>::kOcc))
     stream_kernel(const __grid_constant__ CUtensorMap t0, const __grid_constant__ CUtensorMap t1,
-                  const __grid_constant__ CUtensorMap tx, const __grid_constant__ Args a, int bn, int split, uint32_t wait_limit) {
+                  const __grid_constant__ CUtensorMap tx, const __grid_constant__ Args a, int bn, int split, uint32_t wait_limit,
+                  int stall) {
     using C = Cfg<BN, kGated>;
     constexpr int S = C::kStages, kParts = C::kParts, kHalf = C::kHalf, kLd = kHalf < 16 ? kHalf : 16;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -167,7 +168,9 @@ __global__ void __launch_bounds__(kThreads, (Cfg<BN, kGated>::kOcc))
             }
         } else if (warp == kMmaWarp) {
             const uint32_t idesc = umma::instr_desc(0, 0, kTile, bn);            // e4m3 x e4m3 -> f32
-            for (int i = 0; i < nk; ++i) {
+            pdl_wait();
+            const bool go = !stall || all(wait(drain, 0));       // (tests: nothing arrives there before the end)
+            for (int i = 0; go && i < nk; ++i) {
                 const int s = i % S, b = i % C::kBufs;
                 if (!all(wait(&full[s], (uint32_t)(i / S))) || !all(wait(&acc_empty[b], (uint32_t)(i / C::kBufs + 1)))) break;
                 umma::fence_after_sync();
@@ -244,6 +247,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<BN, kGated>::kOcc))
 #pragma unroll
             for (int j = 0; j < kHalf / 2; ++j) acc[p][j] = 0;
         bool ok = true;
+        pdl_wait();
         for (int i = 0; i < nk; ++i) {
             const int b = i % C::kBufs, at = i % (kBatch * kBatches), slot = at / kBatch;
             if (at % kBatch == 0 && !(ok = all(wait(&scale_full[slot], (uint32_t)(i / (kBatch * kBatches)))))) break;
@@ -323,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<BN, kGated>::kOcc))
 
 template <int BN, bool kGated>
 int launch(const char *where, const uint8_t *xq, const uint8_t *w0, const uint8_t *w1, const Args &a, int bn,
-           cudaStream_t stream, uint32_t wait_limit) {
+           cudaStream_t stream, uint32_t wait_limit, int stall) {
     using C = Cfg<BN, kGated>;
     CUtensorMap t0, t1, tx;
     if (byte_tmap_sw128(&t0, w0, a.N, a.K, (size_t)a.K, kTile) ||
@@ -339,24 +343,25 @@ int launch(const char *where, const uint8_t *xq, const uint8_t *w0, const uint8_
     while (split < kMaxSplit && (long long)tiles * split * 2 <= (long long)sm_count() * C::kOcc && a.K / kGroup / (split * 2) >= 2) split *= 2;
     const dim3 grid((unsigned)(tiles * split));
     if (split == 1)
-        return launch_pdl(where, kern, grid, dim3(kThreads), C::kSmem, stream, t0, t1, tx, a, bn, split, wait_limit);
-    return launch_pdl_cluster(where, kern, grid, dim3(kThreads), C::kSmem, stream, split, t0, t1, tx, a, bn, split, wait_limit);
+        return launch_pdl(where, kern, grid, dim3(kThreads), C::kSmem, stream, t0, t1, tx, a, bn, split, wait_limit, stall);
+    return launch_pdl_cluster(where, kern, grid, dim3(kThreads), C::kSmem, stream, split, t0, t1, tx, a, bn, split, wait_limit, stall);
 }
 
 // Few tokens here, many in tiles of 128 (fp8_block_tile.cu): 128 channels by M tokens against 128 tokens by 256 channels.
 // Measured here / there, us: linear 80 x 4096 x 14336 15.8 / 18.0, 128 18.1 / 19.5, 192 (in two parts) 25.4 / 21.5; gated
 // 32 x 14336 x 4096 22.5 / 24.4, 64 25.0 / 24.6, 80 32.3 / 24.7.
 template <bool kGated>
-int launch_any(const char *where, const uint8_t *xq, const uint8_t *w0, const uint8_t *w1, const Args &a, cudaStream_t st) {
+int launch_any(const char *where, const uint8_t *xq, const uint8_t *w0, const uint8_t *w1, const Args &a, cudaStream_t st,
+               uint32_t wait_limit = kWaitLimit, int stall = 0) {
     constexpr int kMost = kGated ? 32 : 128;
     const int bn = (a.M + 15) / 16 * 16;
-    if (bn <= 16) return launch<16, kGated>(where, xq, w0, w1, a, bn, st, kWaitLimit);
-    if (bn <= 32) return launch<32, kGated>(where, xq, w0, w1, a, bn, st, kWaitLimit);
+    if (bn <= 16) return launch<16, kGated>(where, xq, w0, w1, a, bn, st, wait_limit, stall);
+    if (bn <= 32) return launch<32, kGated>(where, xq, w0, w1, a, bn, st, wait_limit, stall);
     if constexpr (!kGated) {
-        if (bn <= 64) return launch<64, kGated>(where, xq, w0, w1, a, bn, st, kWaitLimit);
-        if (bn <= kMost) return launch<kMost, kGated>(where, xq, w0, w1, a, bn, st, kWaitLimit);
+        if (bn <= 64) return launch<64, kGated>(where, xq, w0, w1, a, bn, st, wait_limit, stall);
+        if (bn <= kMost) return launch<kMost, kGated>(where, xq, w0, w1, a, bn, st, wait_limit, stall);
     }
-    return f8b::launch_tile(where, xq, w0, w1, a, st, kWaitLimit);
+    return f8b::launch_tile(where, xq, w0, w1, a, st, wait_limit, stall);
 }
 
 }  // namespace f8s
@@ -367,13 +372,37 @@ int launch_any(const char *where, const uint8_t *xq, const uint8_t *w0, const ui
 
 using namespace qspec;
 
-extern "C" int qspec_linear_fp8_block(const uint8_t *xq, const float *sa, int lds, const uint8_t *w8, const float *sw, int M,
-                                      int N, int K, uint16_t *y_bf16, int ldy, int32_t *dev_status, qspec_stream_t stream) {
+namespace {
+
+int check_linear(const uint8_t *xq, const float *sa, int lds, const uint8_t *w8, const float *sw, int M, int N, int K,
+                 const uint16_t *y_bf16, int ldy) {
     if (!xq || !sa || !w8 || !sw || !y_bf16) return QSPEC_ERR_NULL;
-    if (M < 1 || M > f8b::kMaxM || N < 1 || N > f8b::kMaxN || K < kGroup || K % kGroup || ldy < N || lds < M) return QSPEC_ERR_SHAPE;
+    if (M < 1 || M > f8b::kMaxM || N < 1 || N > f8b::kMaxN || K < kGroup || K % kGroup || ldy < N || lds < M)
+        return QSPEC_ERR_SHAPE;
     if (!aligned(xq, 16) || !aligned(w8, 16) || !aligned(sa, 4) || !aligned(sw, 4) || !aligned(y_bf16, 2))
         return QSPEC_ERR_ALIGN;
-    int rc = check_device();
+    return check_device();
+}
+
+int check_gated(const uint8_t *xq, const float *sa, int lds, const uint8_t *w_gate, const float *s_gate, const uint8_t *w_up,
+                const float *s_up, int M, int N, int K, const uint8_t *hq, const float *sh, int ldh, const uint16_t *h_bf16,
+                int ldy) {
+    if (!xq || !sa || !w_gate || !s_gate || !w_up || !s_up || (hq != nullptr) != (sh != nullptr) || (!hq && !h_bf16))
+        return QSPEC_ERR_NULL;
+    if (M < 1 || M > f8b::kMaxM || N < kGroup || N > f8b::kMaxN || N % kGroup || K < kGroup || K % kGroup || lds < M ||
+        (hq && ldh < M) || (h_bf16 && ldy < N))
+        return QSPEC_ERR_SHAPE;
+    if (!aligned(xq, 16) || !aligned(w_gate, 16) || !aligned(w_up, 16) || !aligned(sa, 4) || !aligned(s_gate, 4) ||
+        !aligned(s_up, 4) || (hq && (!aligned(hq, 16) || !aligned(sh, 4))) || (h_bf16 && !aligned(h_bf16, 2)))
+        return QSPEC_ERR_ALIGN;
+    return check_device();
+}
+
+}  // namespace
+
+extern "C" int qspec_linear_fp8_block(const uint8_t *xq, const float *sa, int lds, const uint8_t *w8, const float *sw, int M,
+                                      int N, int K, uint16_t *y_bf16, int ldy, int32_t *dev_status, qspec_stream_t stream) {
+    const int rc = check_linear(xq, sa, lds, w8, sw, M, N, K, y_bf16, ldy);
     if (rc) return rc;
     const f8b::Args a = {sa, sw, nullptr, y_bf16, nullptr, nullptr, dev_status, lds, M, N, K, ldy, 0};
     return f8s::launch_any<false>("qspec_linear_fp8_block", xq, w8, nullptr, a, as_cuda(stream));
@@ -382,15 +411,22 @@ extern "C" int qspec_linear_fp8_block(const uint8_t *xq, const float *sa, int ld
 extern "C" int qspec_gated_fp8_block(const uint8_t *xq, const float *sa, int lds, const uint8_t *w_gate, const float *s_gate,
                                      const uint8_t *w_up, const float *s_up, int M, int N, int K, uint8_t *hq, float *sh,
                                      int ldh, uint16_t *h_bf16, int ldy, int32_t *dev_status, qspec_stream_t stream) {
-    if (!xq || !sa || !w_gate || !s_gate || !w_up || !s_up || (hq != nullptr) != (sh != nullptr) || (!hq && !h_bf16))
-        return QSPEC_ERR_NULL;
-    if (M < 1 || M > f8b::kMaxM || N < kGroup || N > f8b::kMaxN || N % kGroup || K < kGroup || K % kGroup || lds < M || (hq && ldh < M) || (h_bf16 && ldy < N))
-        return QSPEC_ERR_SHAPE;
-    if (!aligned(xq, 16) || !aligned(w_gate, 16) || !aligned(w_up, 16) || !aligned(sa, 4) || !aligned(s_gate, 4) ||
-        !aligned(s_up, 4) || (hq && (!aligned(hq, 16) || !aligned(sh, 4))) || (h_bf16 && !aligned(h_bf16, 2)))
-        return QSPEC_ERR_ALIGN;
-    int rc = check_device();
+    const int rc = check_gated(xq, sa, lds, w_gate, s_gate, w_up, s_up, M, N, K, hq, sh, ldh, h_bf16, ldy);
     if (rc) return rc;
     const f8b::Args a = {sa, s_gate, s_up, h_bf16, hq, sh, dev_status, lds, M, N, K, ldy, ldh};
     return f8s::launch_any<true>("qspec_gated_fp8_block", xq, w_gate, w_up, a, as_cuda(stream));
+}
+
+extern "C" int qspec_debug_fp8_block_bounded(const uint8_t *xq, const float *sa, int lds, const uint8_t *w0, const float *s0,
+                                             const uint8_t *w1, const float *s1, int M, int N, int K, uint8_t *hq, float *sh,
+                                             int ldh, uint16_t *y_bf16, int ldy, uint32_t wait_limit, int stall,
+                                             int32_t *dev_status, qspec_stream_t stream) {
+    if (wait_limit < 1) return QSPEC_ERR_SHAPE;
+    const bool gated = w1 != nullptr;
+    const int rc = gated ? check_gated(xq, sa, lds, w0, s0, w1, s1, M, N, K, hq, sh, ldh, y_bf16, ldy)
+                         : check_linear(xq, sa, lds, w0, s0, M, N, K, y_bf16, ldy);
+    if (rc) return rc;
+    const f8b::Args a = {sa, s0, s1, y_bf16, hq, sh, dev_status, lds, M, N, K, ldy, ldh};
+    return gated ? f8s::launch_any<true>("qspec_debug_fp8_block_bounded", xq, w0, w1, a, as_cuda(stream), wait_limit, stall)
+                 : f8s::launch_any<false>("qspec_debug_fp8_block_bounded", xq, w0, nullptr, a, as_cuda(stream), wait_limit, stall);
 }

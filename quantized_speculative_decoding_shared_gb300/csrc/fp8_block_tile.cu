@@ -123,7 +123,7 @@ template <bool kGated>
 __global__ void __launch_bounds__(kThreads, 1)
     tile_kernel(const __grid_constant__ CUtensorMap t0, const __grid_constant__ CUtensorMap t1,
                 const __grid_constant__ CUtensorMap tx, const __grid_constant__ Args a, const Plan plan, int wide,
-                uint32_t wait_limit) {
+                uint32_t wait_limit, int stall) {
     constexpr int kChannels = kGated ? 128 : 256;                // channels of a tile
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *stages = smem_raw + ((1024u - (umma::smem_addr(smem_raw) & 1023u)) & 1023u);
@@ -226,7 +226,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int blocks = fulls * G + (shared ? shared_nk : 0);
             int s = 0;
             uint32_t turn = 0;
-            for (; issued < blocks; ++issued) {
+            pdl_wait();
+            const bool go = !stall || all(wait(&sm.drain, 0));   // (tests: nothing arrives there before the end)
+            for (; go && issued < blocks; ++issued) {
                 const int b = issued & 1;
                 if (!all(wait(&sm.full[s], turn)) || !all(wait(&sm.acc_empty[b], (uint32_t)(issued / 2 + 1)))) break;
                 umma::fence_after_sync();
@@ -503,7 +505,7 @@ int resident(int c) {
 
 template <bool kGated>
 int launch(const char *where, const uint8_t *xq, const uint8_t *w0, const uint8_t *w1, const Args &a, cudaStream_t stream,
-           uint32_t wait_limit) {
+           uint32_t wait_limit, int stall) {
     CUtensorMap t0, t1, tx;
     if (byte_tmap_sw128(&t0, w0, a.N, a.K, (size_t)a.K, 128) || (kGated && byte_tmap_sw128(&t1, w1, a.N, a.K, (size_t)a.K, 128)) ||
         byte_tmap_sw128(&tx, xq, a.M, a.K, (size_t)a.K, 128))
@@ -538,8 +540,10 @@ int launch(const char *where, const uint8_t *xq, const uint8_t *w0, const uint8_
     plan.split = c;
     const int wide = a.y != nullptr && aligned(a.y, 16) && a.ldy % 8 == 0;
     if (c == 1)
-        return launch_pdl(where, kern, dim3((unsigned)grid), dim3(kThreads), kSmem, stream, t0, t1, tx, a, plan, wide, wait_limit);
-    return launch_pdl_cluster(where, kern, dim3((unsigned)grid), dim3(kThreads), kSmem, stream, c, t0, t1, tx, a, plan, wide, wait_limit);
+        return launch_pdl(where, kern, dim3((unsigned)grid), dim3(kThreads), kSmem, stream, t0, t1, tx, a, plan, wide, wait_limit,
+                          stall);
+    return launch_pdl_cluster(where, kern, dim3((unsigned)grid), dim3(kThreads), kSmem, stream, c, t0, t1, tx, a, plan, wide, wait_limit,
+                              stall);
 }
 
 }  // namespace f8t
@@ -549,9 +553,9 @@ int launch(const char *where, const uint8_t *xq, const uint8_t *w0, const uint8_
 namespace f8b {
 
 int launch_tile(const char *where, const uint8_t *xq, const uint8_t *w0, const uint8_t *w1, const Args &a, cudaStream_t stream,
-                uint32_t wait_limit) {
-    return w1 != nullptr ? f8t::launch<true>(where, xq, w0, w1, a, stream, wait_limit)
-                         : f8t::launch<false>(where, xq, w0, w1, a, stream, wait_limit);
+                uint32_t wait_limit, int stall) {
+    return w1 != nullptr ? f8t::launch<true>(where, xq, w0, w1, a, stream, wait_limit, stall)
+                         : f8t::launch<false>(where, xq, w0, w1, a, stream, wait_limit, stall);
 }
 
 }  // namespace f8b

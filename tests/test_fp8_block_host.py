@@ -83,3 +83,13 @@ def test_conveniences_refuse_what_they_cannot_pass_on():
                  lambda: binding.gated_fp8_block(u8, s, u8, s, u8, s)):
         with pytest.raises(ValueError):
             call()
+
+
+def test_the_diagnostic_entry(lib):
+    linear = dict(xq=at(), sa=at(), lds=5, w=at(), sw=at(), w1=None, s1=None, M=5, N=100, K=256, hq=None, sh=None, ldh=0, y=at(), ldy=100,
+                  limit=1000, stall=1, st=None, s=None)
+    refuse(lib.qspec_debug_fp8_block_bounded, linear, [
+        (SHAPE, dict(limit=0)), (NULL, dict(y=None)), (SHAPE, dict(K=130)), (SHAPE, dict(lds=4)), (ALIGN, dict(w=at(0x1008)))])
+    gated = dict(linear, w1=at(), s1=at(), N=128, hq=at(), sh=at(), ldh=5, ldy=128)
+    refuse(lib.qspec_debug_fp8_block_bounded, gated, [
+        (SHAPE, dict(limit=0)), (NULL, dict(s1=None)), (NULL, dict(sh=None)), (SHAPE, dict(N=100)), (ALIGN, dict(w1=at(0x1008)))])
