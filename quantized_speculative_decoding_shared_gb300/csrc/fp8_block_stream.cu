@@ -306,13 +306,15 @@ __global__ void __launch_bounds__(kThreads, (Cfg<BN, kGated>::kOcc))
         for (int c = warp * split + rank; c < tokens; c += kWorkWarps * split) {
             const int m = m0 + c;
             float v[kParts][4];
+            const float *at[kParts];
 #pragma unroll
-            for (int p = 0; p < kParts; ++p) {
-                const float *at = sums + (p * BN + c) * kTile + 4 * lane;
-                if (split > 1) {
-                    f8b::sum_parts(at, split, 0, v[p]);
-                } else {
-                    const float4 f = *reinterpret_cast<const float4 *>(at);
+            for (int p = 0; p < kParts; ++p) at[p] = sums + (p * BN + c) * kTile + 4 * lane;
+            if (split > 1) {
+                f8b::sum_parts(at, split, 0, v);
+            } else {
+#pragma unroll
+                for (int p = 0; p < kParts; ++p) {
+                    const float4 f = *reinterpret_cast<const float4 *>(at[p]);
                     v[p][0] = f.x, v[p][1] = f.y, v[p][2] = f.z, v[p][3] = f.w;
                 }
             }

@@ -15,8 +15,8 @@
 // The tiles behind the last full round of CTAs are split along K over the CTAs of a
 // cluster, whose parts meet in shared memory, in the order of K.
 #include <algorithm>
-#include <atomic>
 #include <climits>
+#include <mutex>
 
 #include "fp8_block_host.h"
 #include "umma.cuh"
@@ -157,26 +157,42 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto all = [](bool mine) { return __all_sync(0xffffffffu, mine) != 0; };
     // where four neighbouring sums of a token lie while the parts of K meet
     auto piece = [&](int row, int p) { return reinterpret_cast<float4 *>(stages) + row * (kCols / 4) + (p ^ (row & 7)); };
-    if (threadIdx.x == 0) {
-        sm.timeout = 0;
-        for (int i = 0; i < kStages; ++i) {
-            umma::mbar_init(&sm.full[i], 1);
-            umma::mbar_init(&sm.done[i], 1);
+    auto load_weights = [&](int s, int g, int n0) {               // block g of K, channels n0 ..., into stage s
+        uint8_t *at = stages + (size_t)s * kStage;
+        umma::mbar_arrive_expect_tx(&sm.full[s], kStage);
+        umma::tma_load_2d(at + kPiece, &t0, g * kGroup, n0, &sm.full[s]);
+        umma::tma_load_2d(at + 2 * kPiece, kGated ? &t1 : &t0, g * kGroup, n0 + (kGated ? 0 : 128), &sm.full[s]);
+    };
+    auto load_tokens = [&](int s, int g, int m0) {
+        umma::tma_load_2d(stages + (size_t)s * kStage, &tx, g * kGroup, m0, &sm.full[s]);
+    };
+
+    const bool elected = umma::elect_one();
+    int early = 0;                                                // blocks of the first tile whose weights are under way
+    if (warp == kLoadWarp) {
+        int rt, ct, k0;
+        const int nk = items > 0 ? item(0, rt, ct, k0) : 0;
+        early = min(kStages, nk);
+        if (elected) {
+            sm.timeout = 0;
+            for (int i = 0; i < kStages; ++i) {
+                umma::mbar_init(&sm.full[i], 1);
+                umma::mbar_init(&sm.done[i], 1);
+            }
+            for (int i = 0; i < 2; ++i) umma::mbar_init(&sm.acc_empty[i], kWorkWarps);
+            for (int i = 0; i < kBatches; ++i) {
+                umma::mbar_init(&sm.scale_full[i], 1);
+                umma::mbar_init(&sm.scale_empty[i], kWorkWarps);
+            }
+            umma::mbar_init(&sm.drain, 1);
+            umma::mbar_fence_init();
+            umma::fence_proxy_async();
+            // the first stages' weights at once, before the dependency wait too (they are immutable)
+            for (int i = 0; i < early; ++i) load_weights(i, k0 + i, ct * kChannels);
         }
-        for (int i = 0; i < 2; ++i) umma::mbar_init(&sm.acc_empty[i], kWorkWarps);
-        for (int i = 0; i < kBatches; ++i) {
-            umma::mbar_init(&sm.scale_full[i], 1);
-            umma::mbar_init(&sm.scale_empty[i], kWorkWarps);
-        }
-        umma::mbar_init(&sm.drain, 1);
-        umma::mbar_fence_init();
+        __syncwarp();
     }
     if (warp == kMmaWarp) umma::tmem_alloc(&sm.tmem, 2 * kCols);
-    if (warp == kLoadWarp && lane == 0) {
-        umma::prefetch_tmap(&t0);
-        if (kGated) umma::prefetch_tmap(&t1);
-        umma::prefetch_tmap(&tx);
-    }
     umma::fence_before_sync();
     __syncthreads();
     umma::fence_after_sync();
@@ -195,22 +211,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         // (the issuing warps go through their loops whole and elect a lane where it counts: a lane's own loop is
         // slower by the divergence that the compiler allows for at every step)
         if (warp == kLoadWarp) {
-            const CUtensorMap *tw = kGated ? &t1 : &t0;
-            const bool elected = umma::elect_one();
             pdl_wait();
             bool ok = true;
             int s = 0, turn = 0;                                  // the stage, and how often it was filled before
             for (int i = 0; i < items && ok; ++i) {
                 int rt, ct, k0;
-                const int nk = item(i, rt, ct, k0), m0 = rt * kRows, n0 = ct * kChannels;
+                const int nk = item(i, rt, ct, k0);
                 for (int g = k0; g < k0 + nk; ++g) {
                     if (!(ok = turn == 0 || all(wait(&sm.done[s], (uint32_t)(turn + 1))))) break;
                     if (elected) {
-                        uint8_t *at = stages + (size_t)s * kStage;
-                        umma::mbar_arrive_expect_tx(&sm.full[s], kStage);
-                        umma::tma_load_2d(at, &tx, g * kGroup, m0, &sm.full[s]);
-                        umma::tma_load_2d(at + kPiece, &t0, g * kGroup, n0, &sm.full[s]);
-                        umma::tma_load_2d(at + 2 * kPiece, tw, g * kGroup, n0 + (kGated ? 0 : 128), &sm.full[s]);
+                        if (loads >= early) load_weights(s, g, ct * kChannels);
+                        load_tokens(s, g, rt * kRows);
                     }
                     __syncwarp();
                     ++loads;
@@ -222,7 +233,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         } else if (warp == kMmaWarp) {
             constexpr uint32_t idesc = umma::instr_desc(0, 0, kRows, kCols);                 // e4m3 x e4m3 -> f32
-            const bool elected = umma::elect_one();
             const int blocks = fulls * G + (shared ? shared_nk : 0);
             int s = 0;
             uint32_t turn = 0;
@@ -285,10 +295,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         // again; both issuers stopped at the timeout, so at most kStages copies are outstanding
         __syncthreads();
         if (*timeout) {
-            if (warp == kLoadWarp && umma::elect_one())
+            if (warp == kLoadWarp && elected)
                 for (int b = max(0, loads - kStages); b < loads; ++b)
                     umma::mbar_wait(&sm.full[b % kStages], (uint32_t)((b / kStages) & 1), kWaitLimit);
-            if (warp == kMmaWarp && umma::elect_one() && issued > 0) {
+            if (warp == kMmaWarp && elected && issued > 0) {
                 umma::mma_commit(&sm.drain);
                 umma::mbar_wait(&sm.drain, 0, kWaitLimit);
             }
@@ -453,16 +463,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             // ---- the parts of K meet: a warp takes a token, its lanes four channels of either half ----
             int rt, ct, k0;
             item(fulls, rt, ct, k0);
-            const int m0 = rt * kRows, first = (int)umma::cluster_rank() - part;
-            for (int r = warp * plan.split + part; r < min(kRows, a.M - m0); r += kWorkWarps * plan.split) {
+            const int m0 = rt * kRows, rows = min(kRows, a.M - m0), first = (int)umma::cluster_rank() - part;
+            for (int r = warp * plan.split + part; r < rows; r += kWorkWarps * plan.split) {
+                const float *at[2] = {reinterpret_cast<const float *>(piece(r, lane)), reinterpret_cast<const float *>(piece(r, 32 + lane))};
                 float v[2][4];
-#pragma unroll
-                for (int p = 0; p < 2; ++p) f8b::sum_parts(reinterpret_cast<const float *>(piece(r, 32 * p + lane)), plan.split, first, v[p]);
+                f8b::sum_parts(at, plan.split, first, v);
                 if constexpr (kGated) {
                     f8b::store_gated(a, m0 + r, ct, lane, v[0], v[1]);
                 } else {
-#pragma unroll
-                    for (int p = 0; p < 2; ++p) f8b::store_bf16(a, m0 + r, ct * kChannels + 128 * p + 4 * lane, v[p]);
+                    f8b::store_bf16(a, m0 + r, ct * kChannels + 4 * lane, v[0]);
+                    f8b::store_bf16(a, m0 + r, ct * kChannels + 128 + 4 * lane, v[1]);
                 }
             }
         }
@@ -470,18 +480,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-// CTAs of a cluster of `c` that the device runs at once, a whole number of clusters (0: none).  Asked once for each device.
+// CTAs that the device runs at once in clusters of each size, a whole number of clusters (0: none).  Asked once for each
+// device (the questions take some microseconds).
+struct Resident {
+    int ctas[kMaxSplit + 1];
+};
 template <bool kGated>
-int resident(int c) {
-    constexpr int kDevices = 64;
-    static std::atomic<int> known[kDevices][kMaxSplit + 1];       // 0: not asked yet, else the number + 1
-    int dev = 0;
-    cudaGetDevice(&dev);
-    if (dev < 0 || dev >= kDevices) return c == 1 ? sm_count() : 0;
-    int n = known[dev][c].load(std::memory_order_relaxed);
-    if (n == 0) {
+Resident ask_resident() {
+    Resident r = {};
+    const int sms = sm_count();
+    r.ctas[1] = sms;
+    for (int c = 2; c <= kMaxSplit; ++c) {
         cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((unsigned)(sm_count() / c * c));
+        cfg.gridDim = dim3((unsigned)(sms / c * c));
         cfg.blockDim = dim3(kThreads);
         cfg.dynamicSmemBytes = kSmem;
         cudaLaunchAttribute attr[1];
@@ -491,16 +502,24 @@ int resident(int c) {
         cfg.attrs = attr;
         cfg.numAttrs = 1;
         int clusters = 0;
-        if (c == 1)
-            clusters = sm_count();
-        else if (cudaOccupancyMaxActiveClusters(&clusters, tile_kernel<kGated>, &cfg) != cudaSuccess) {
+        if (cudaOccupancyMaxActiveClusters(&clusters, tile_kernel<kGated>, &cfg) != cudaSuccess) {
             cudaGetLastError();
             clusters = 0;
         }
-        n = std::min(clusters * c, sm_count() / c * c) + 1;
-        known[dev][c].store(n, std::memory_order_relaxed);
+        r.ctas[c] = std::min(clusters * c, sms / c * c);
     }
-    return n - 1;
+    return r;
+}
+template <bool kGated>
+Resident resident() {
+    constexpr int kDevices = 64;
+    static Resident known[kDevices];
+    static std::once_flag once[kDevices];
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev < 0 || dev >= kDevices) return ask_resident<kGated>();
+    std::call_once(once[dev], [&] { known[dev] = ask_resident<kGated>(); });
+    return known[dev];
 }
 
 template <bool kGated>
@@ -522,10 +541,11 @@ int launch(const char *where, const uint8_t *xq, const uint8_t *w0, const uint8_
     // The cluster's size by what a call would take, in blocks of K of one CTA: full rounds of tiles, then the rest in as
     // many parts as there are CTAs for; parts cost kMeet blocks to meet.
     constexpr double kMeet = 6;
+    const Resident there = resident<kGated>();
     double least = 1e30;
     int c = 1, grid = 0;
     for (int s = 1; s <= kMaxSplit && s <= G; ++s) {
-        const int ctas = resident<kGated>(s);
+        const int ctas = there.ctas[s];
         if (ctas < s) continue;
         const int rounds = tiles / ctas, rest = tiles - rounds * ctas;
         if (s > 1 && (rest == 0 || rest * s > ctas)) continue;
