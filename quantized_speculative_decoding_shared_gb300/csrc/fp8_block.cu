@@ -27,14 +27,14 @@
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
-#include "qspec_device.cuh"
+#include "fp8_block.cuh"
 #include "qspec_host.h"
 
 namespace qspec {
 
 namespace {
 
-namespace f8b {
+namespace f8q {
 
 constexpr int kThreads = 256;
 constexpr int kBlocksX = 4;                     // neighbouring blocks per CTA
@@ -111,18 +111,6 @@ __device__ __forceinline__ float max_of(const Words<W> &v, float amax) {
     return amax;
 }
 
-// amax / 448 (the quotient's two steps, 1 / 448 rounded; the division at fp32's ends)
-__device__ __forceinline__ float scale_of(float amax) {
-    constexpr float kY = 1.0f / 448.0f;
-    if (!(amax > 1.0e-30f && amax < 1.0e38f)) return __fdiv_rn(amax, 448.0f);
-    const float q = __fmul_rn(amax, kY);
-    return __fmaf_rn(__fmaf_rn(-q, 448.0f, amax), kY, q);
-}
-__device__ __forceinline__ float reciprocal(float s) {
-    const float y = rcp_approx(s);
-    return __fmaf_rn(__fmaf_rn(-s, y, 1.0f), y, y);
-}
-
 __device__ __forceinline__ uint32_t pack_e4m3(float a, float b) {          // the first in the low byte
     return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
 }
@@ -186,9 +174,9 @@ __global__ void __launch_bounds__(kThreads, (W == 8 ? 6 : 7))
         float amax = max_of<false, W>(v[i], 0.0f);
 #pragma unroll
         for (int o = A::kTeam / 2; o >= 1; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        const float s = scale_of(amax);
+        const float s = f8b::scale_of(amax);
         bad |= !(amax < INFINITY);
-        store_codes<false, W>(xq + (size_t)m * K + col, v[i], s, reciprocal(s), m < M && g < G);
+        store_codes<false, W>(xq + (size_t)m * K + col, v[i], s, f8b::reciprocal(s), m < M && g < G);
         if (lane == 0) scales[team % kBlocksX][r] = s;
     }
     const int bad_any = __syncthreads_or(bad ? 1 : 0);
@@ -226,7 +214,7 @@ __global__ void __launch_bounds__(kThreads, 3)
         amax = red[turn][0];
 #pragma unroll
         for (int i = 1; i < kThreads / 32; ++i) amax = max_nan(amax, red[turn][i]);
-        const float s = scale_of(amax), y = reciprocal(s);
+        const float s = f8b::scale_of(amax), y = f8b::reciprocal(s);
 #pragma unroll
         for (int i = 0; i < kPer; ++i)
             store_codes<true, W>(w8 + (size_t)(n0 + i * kTeams) * K + col, v[i], s, y, n0 + i * kTeams < N);
@@ -255,7 +243,7 @@ int launch_weights(const uint16_t *w, int N, int K, int blocks, uint8_t *w8, flo
                       dim3(kThreads), 0, s, w, N, K, blocks, w8, sw, st);
 }
 
-}  // namespace f8b
+}  // namespace f8q
 
 }  // namespace
 
@@ -274,8 +262,8 @@ extern "C" int qspec_quant_weights_fp8_block(const uint16_t *w_fp16, int N, int 
     if (rc) return rc;
     cudaStream_t s = as_cuda(stream);
     // 32 bytes to a lane where the addresses allow it
-    if (aligned(w_fp16, 32) && aligned(w8, 16)) return f8b::launch_weights<8>(w_fp16, N, K, (int)blocks, w8, sw, dev_status, s);
-    return f8b::launch_weights<4>(w_fp16, N, K, (int)blocks, w8, sw, dev_status, s);
+    if (aligned(w_fp16, 32) && aligned(w8, 16)) return f8q::launch_weights<8>(w_fp16, N, K, (int)blocks, w8, sw, dev_status, s);
+    return f8q::launch_weights<4>(w_fp16, N, K, (int)blocks, w8, sw, dev_status, s);
 }
 
 extern "C" int qspec_quant_act_fp8_block(const uint16_t *x_bf16, int M, int K, int ldx, uint8_t *xq, float *sa, int lds,
@@ -287,6 +275,6 @@ extern "C" int qspec_quant_act_fp8_block(const uint16_t *x_bf16, int M, int K, i
     if (rc) return rc;
     cudaStream_t s = as_cuda(stream);
     if (aligned(x_bf16, 32) && ldx % 16 == 0 && aligned(xq, 16))
-        return f8b::launch_act<8>(x_bf16, M, K, ldx, xq, sa, lds, dev_status, s);
-    return f8b::launch_act<4>(x_bf16, M, K, ldx, xq, sa, lds, dev_status, s);
+        return f8q::launch_act<8>(x_bf16, M, K, ldx, xq, sa, lds, dev_status, s);
+    return f8q::launch_act<4>(x_bf16, M, K, ldx, xq, sa, lds, dev_status, s);
 }

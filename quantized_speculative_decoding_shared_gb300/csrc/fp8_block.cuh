@@ -26,16 +26,41 @@ struct Args {
 // h = silu(g) u = g u / (1 + exp(-g)).  exp(-g) passes fp32 below -88.7: 1 / inf is the limit 0; a NaN stays one.
 __device__ __forceinline__ float gated(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
 
-// A block's scale and what its codes are taken with: E4M3(v up inv), inv = 448 / (up max |v|), up = 2^96 where 448 / max
-// |v| would pass fp32.  Within 2 x 2^-24 of v / s in the quotient.  A scale of 0 has the codes 0.
+// amax / 448: the quotient's two steps (fp8_block.cu) with 1 / 448 rounded; the division at fp32's ends.
+__device__ __forceinline__ float scale_of(float amax) {
+    constexpr float kY = 1.0f / 448.0f;
+    if (!(amax > 1.0e-30f && amax < 1.0e38f)) return __fdiv_rn(amax, 448.0f);
+    const float q = __fmul_rn(amax, kY);
+    return __fmaf_rn(__fmaf_rn(-q, 448.0f, amax), kY, q);
+}
+// 1 / s by one Newton step, for s within 2^-126 .. 2^126.
+__device__ __forceinline__ float reciprocal(float s) {
+    const float y = rcp_approx(s);
+    return __fmaf_rn(__fmaf_rn(-s, y, 1.0f), y, y);
+}
+
+// A block's scale and what its codes are taken with: E4M3(v up inv), inv = 448 / (up max |v|), up a power of two that
+// keeps the reciprocal inside fp32.  Within 3 x 2^-24 of v / s in the quotient.  A scale of 0 has the codes 0.
 struct Quant {
     float s, inv, up;
     __device__ __forceinline__ explicit Quant(float amax) {
-        up = amax < 1.0e-30f ? 7.9228162514264338e28f : 1.0f;
-        s = __fdiv_rn(amax, 448.0f);
-        inv = s > 0.0f ? __fdiv_rn(448.0f, amax * up) : 0.0f;
+        up = amax < 1.0e-30f ? 7.9228162514264338e28f : amax > 1.0e30f ? 1.262177448353619e-29f : 1.0f;      // 2^96, 2^-96
+        s = scale_of(amax);
+        inv = s > 0.0f ? 448.0f * reciprocal(amax * up) : 0.0f;
     }
 };
+
+// 32 neighbouring bytes (`wide`: on a multiple of 32, else of 16)
+__device__ __forceinline__ void store32(void *p, const uint32_t (&w)[8], bool wide) {
+    if (wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+                     "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+    } else {
+        reinterpret_cast<uint4 *>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        reinterpret_cast<uint4 *>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+}
 
 // four codes, the first in the low byte
 __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {

@@ -38,9 +38,13 @@ static_assert(kStages >= 2, "a stage's products must not be done twice before al
 static_assert(kRows * kCols * 4 <= kStages * kStage, "a CTA's sums lie over the stages");
 constexpr int kBatch = 4, kBatches = 4;              // scales: blocks per hand-over, hand-overs in flight
 constexpr int kGroupTiles = 8;                       // token tiles that go through the channels together
-// registers per thread: all start with 168; 128 sums and their operands need more, the issuing warps less
-constexpr int kRegsWork = 208, kRegsRest = 88;
-static_assert(kThreads * 168 <= 65536 && kWork * kRegsWork + 128 * kRegsRest <= kThreads * 168, "register shares");
+// registers per thread: all start with 168; 128 sums and their operands need more, the issuing warps less (shares at
+// which either kernel compiles without spills: 200 / 104 cost the gated one 10 %)
+template <bool kGated>
+struct Regs {
+    static constexpr int kWork = kGated ? 216 : 208, kRest = kGated ? 72 : 88;
+    static_assert(kThreads * 168 <= 65536 && f8t::kWork * kWork + 128 * kRest <= kThreads * 168, "register shares");
+};
 
 struct Ctl {
     uint64_t full[kStages], done[kStages];           // a stage's copies landed; its products done: stage free, sums there
@@ -107,23 +111,26 @@ __device__ __forceinline__ float max_abs(float a, float b, float c) {          /
     return d;
 }
 
-// 8 neighbouring values of a row to bf16, channels n .. n + 7 of N
-__device__ __forceinline__ void store8(uint16_t *row, int n, int N, bool wide, const float (&v)[8]) {
-    if (wide && n + 8 <= N) {
-        *reinterpret_cast<uint4 *>(row + n) =
-            make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+// 16 neighbouring sums of a row to bf16, channels n .. n + 15 of N.  How: 0 value by value, 1 in 16, 2 in 32 bytes (half
+// the way through the store unit, which 32 rows of a warp's take one by one).
+__device__ __forceinline__ void store16(uint16_t *row, int n, int N, int how, const uint64_t *v) {
+    if (how != 0 && n + 16 <= N) {
+        uint32_t w[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = pack_bf16(lo32(v[e]), hi32(v[e]));
+        f8b::store32(row + n, w, how == 2);
     } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (n + e < N) row[n + e] = float_to_bf16_bits(v[e]);
+        for (int e = 0; e < 16; ++e)
+            if (n + e < N) row[n + e] = float_to_bf16_bits(e % 2 == 0 ? lo32(v[e / 2]) : hi32(v[e / 2]));
     }
 }
 
 template <bool kGated>
 __global__ void __launch_bounds__(kThreads, 1)
     tile_kernel(const __grid_constant__ CUtensorMap t0, const __grid_constant__ CUtensorMap t1,
-                const __grid_constant__ CUtensorMap tx, const __grid_constant__ Args a, const Plan plan, int wide,
-                uint32_t wait_limit, int stall) {
+                const __grid_constant__ CUtensorMap tx, const __grid_constant__ Args a, const Plan plan, int how_y,
+                int how_h, uint32_t wait_limit, int stall) {
     constexpr int kChannels = kGated ? 128 : 256;                // channels of a tile
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *stages = smem_raw + ((1024u - (umma::smem_addr(smem_raw) & 1023u)) & 1023u);
@@ -207,7 +214,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
 
     if (warp >= kWorkWarps) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<kGated>::kRest));
         // (the issuing warps go through their loops whole and elect a lane where it counts: a lane's own loop is
         // slower by the divergence that the compiler allows for at every step)
         if (warp == kLoadWarp) {
@@ -309,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (warp == kMmaWarp) umma::tmem_free(tmem, 2 * kCols);
         if (plan.split > 1) umma::cluster_sync();
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsWork));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Regs<kGated>::kWork));
         // ---- thread = token; warps 0 .. 3 the lower half of the channels (gated: of both parts), 4 .. 7 the upper ----
         const int half = warp >> 2, row = 32 * (warp & 3) + lane;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
@@ -374,11 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
 #pragma unroll
-                        for (int j = 0; j < 16; j += 4) {
-                            const float v[8] = {lo32(acc[c][j]), hi32(acc[c][j]), lo32(acc[c][j + 1]), hi32(acc[c][j + 1]),
-                                                lo32(acc[c][j + 2]), hi32(acc[c][j + 2]), lo32(acc[c][j + 3]), hi32(acc[c][j + 3])};
-                            store8(y, ct * kChannels + column(c) + 2 * j, a.N, wide != 0, v);
-                        }
+                        for (int j = 0; j < 16; j += 8) store16(y, ct * kChannels + column(c) + 2 * j, a.N, how_y, &acc[c][j]);
                 }
             } else {
                 // h = g u / (1 + exp(-g)), two quotients from one reciprocal 1 / (a b) where no gate of the warp's is so
@@ -423,11 +426,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int c = 0; c < 2; ++c)
 #pragma unroll
-                            for (int j = 0; j < 16; j += 4) {
-                                const float v[8] = {lo32(acc[c][j]), hi32(acc[c][j]), lo32(acc[c][j + 1]), hi32(acc[c][j + 1]),
-                                                    lo32(acc[c][j + 2]), hi32(acc[c][j + 2]), lo32(acc[c][j + 3]), hi32(acc[c][j + 3])};
-                                store8(y, n + c * 32 + 2 * j, a.N, wide != 0, v);
-                            }
+                            for (int j = 0; j < 16; j += 8) store16(y, n + c * 32 + 2 * j, a.N, how_y, &acc[c][j]);
                     }
                     if (a.hq != nullptr) {
                         const f8b::Quant q(amax);
@@ -438,19 +437,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                                 for (int j = 0; j < 16; ++j) acc[c][j] = q.s == 0.0f ? 0 : mul2(acc[c][j], f2(q.up, q.up));
                         }
-                        uint4 *out = reinterpret_cast<uint4 *>(a.hq + (size_t)m * a.N + n);
+                        uint8_t *out = a.hq + (size_t)m * a.N + n;
 #pragma unroll
-                        for (int c = 0; c < 2; ++c)
+                        for (int c = 0; c < 2; ++c) {
+                            uint32_t w[8];
 #pragma unroll
-                            for (int j = 0; j < 16; j += 8) {
-                                uint32_t w[4];
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    const uint64_t v0 = mul2(acc[c][j + 2 * e], by), v1 = mul2(acc[c][j + 2 * e + 1], by);
-                                    w[e] = f8b::codes4(lo32(v0), hi32(v0), lo32(v1), hi32(v1));
-                                }
-                                out[2 * c + j / 8] = make_uint4(w[0], w[1], w[2], w[3]);
+                            for (int e = 0; e < 8; ++e) {
+                                const uint64_t v0 = mul2(acc[c][2 * e], by), v1 = mul2(acc[c][2 * e + 1], by);
+                                w[e] = f8b::codes4(lo32(v0), hi32(v0), lo32(v1), hi32(v1));
                             }
+                            f8b::store32(out + 32 * c, w, how_h == 2);
+                        }
                         if (half == 0) a.sh[(size_t)ct * a.ldh + m] = q.s;
                     }
                     if (half == 0 && !(amax < (a.y != nullptr ? 3.3961775292304601e38f : INFINITY))) flag(a.st, QSPEC_ERR_NONFINITE);
@@ -558,11 +555,12 @@ int launch(const char *where, const uint8_t *xq, const uint8_t *w0, const uint8_
         }
     }
     plan.split = c;
-    const int wide = a.y != nullptr && aligned(a.y, 16) && a.ldy % 8 == 0;
+    const int how_y = a.y == nullptr || !aligned(a.y, 16) || a.ldy % 8 ? 0 : aligned(a.y, 32) && a.ldy % 16 == 0 ? 2 : 1;
+    const int how_h = aligned(a.hq, 32) ? 2 : 1;
     if (c == 1)
-        return launch_pdl(where, kern, dim3((unsigned)grid), dim3(kThreads), kSmem, stream, t0, t1, tx, a, plan, wide, wait_limit,
+        return launch_pdl(where, kern, dim3((unsigned)grid), dim3(kThreads), kSmem, stream, t0, t1, tx, a, plan, how_y, how_h, wait_limit,
                           stall);
-    return launch_pdl_cluster(where, kern, dim3((unsigned)grid), dim3(kThreads), kSmem, stream, c, t0, t1, tx, a, plan, wide, wait_limit,
+    return launch_pdl_cluster(where, kern, dim3((unsigned)grid), dim3(kThreads), kSmem, stream, c, t0, t1, tx, a, plan, how_y, how_h, wait_limit,
                               stall);
 }
 
