@@ -416,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                 }
                 sm.top[parity][half][row] = amax;
-                asm volatile("bar.sync 1, %0;" ::"n"(kWork) : "memory");
+                asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp & 3)) : "memory");      // (the two warps of the same tokens)
                 amax = max_abs(amax, sm.top[parity][half ^ 1][row], 0.0f);
                 parity ^= 1;
                 if (in && ok) {
