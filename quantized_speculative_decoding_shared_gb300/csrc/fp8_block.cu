@@ -187,9 +187,10 @@ __global__ void __launch_bounds__(kThreads, (W == 8 ? 6 : 7))
     if (threadIdx.x == 0 && bad_any) flag(st, QSPEC_ERR_NONFINITE);
 }
 
-// One 128 x 128 block at a time, kept in registers between its load and its codes.
+// One 128 x 128 block after another, kept in registers between its load and its codes, the next one's loads under way
+// meanwhile: 3584 x 18944 in 32.9 us, 6.2 TB/s (35.7 with three CTAs to an SM and no loads ahead).
 template <int W>
-__global__ void __launch_bounds__(kThreads, 3)
+__global__ void __launch_bounds__(kThreads, 2)
     quant_weights_kernel(const uint16_t *__restrict__ w, int N, int K, int blocks, uint8_t *__restrict__ w8,
                          float *__restrict__ sw, int32_t *st) {
     constexpr int kTeam = 64 / W, kTeams = kThreads / kTeam, kPer = kGroup / kTeams;       // rows per team
@@ -197,16 +198,20 @@ __global__ void __launch_bounds__(kThreads, 3)
     const int team = threadIdx.x / kTeam, lane = threadIdx.x % kTeam, warp = threadIdx.x >> 5;
     const int G = K / kGroup;
     pdl_wait();
-    int turn = 0;
-    for (long long b = blockIdx.x; b < blocks; b += gridDim.x, turn ^= 1) {
-        const int g = (int)(b % G), nb = (int)(b / G), n0 = nb * kGroup + team;
-        const size_t col = (size_t)g * kGroup + lane * 2 * W;
-        Words<W> v[kPer];
+    Words<W> v[2][kPer];
+    auto fetch = [&](int b, Words<W> (&d)[kPer]) {
+        const int nb = b / G, g = b - nb * G, n0 = nb * kGroup + team;
+        const uint16_t *p = w + (size_t)n0 * K + (size_t)g * kGroup + lane * 2 * W;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) v[i] = load<W>(w + (size_t)(n0 + i * kTeams) * K + col, n0 + i * kTeams < N);
+        for (int i = 0; i < kPer; ++i) d[i] = load<W>(p + (size_t)(i * kTeams) * K, b < blocks && n0 + i * kTeams < N);
+    };
+    // a block's maximum, scale and codes
+    auto code = [&](int b, const Words<W> (&d)[kPer], int turn) {
+        const int nb = b / G, g = b - nb * G, n0 = nb * kGroup + team;
+        uint8_t *p = w8 + (size_t)n0 * K + (size_t)g * kGroup + lane * 2 * W;
         float amax = 0.0f;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) amax = max_of<true, W>(v[i], amax);
+        for (int i = 0; i < kPer; ++i) amax = max_of<true, W>(d[i], amax);
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
         if ((threadIdx.x & 31) == 0) red[turn][warp] = amax;
@@ -216,16 +221,23 @@ __global__ void __launch_bounds__(kThreads, 3)
         for (int i = 1; i < kThreads / 32; ++i) amax = max_nan(amax, red[turn][i]);
         const float s = f8b::scale_of(amax), y = f8b::reciprocal(s);
 #pragma unroll
-        for (int i = 0; i < kPer; ++i)
-            store_codes<true, W>(w8 + (size_t)(n0 + i * kTeams) * K + col, v[i], s, y, n0 + i * kTeams < N);
+        for (int i = 0; i < kPer; ++i) store_codes<true, W>(p + (size_t)(i * kTeams) * K, d[i], s, y, n0 + i * kTeams < N);
         if (threadIdx.x == 0) {
             sw[(size_t)nb * G + g] = s;
             if (!(amax < INFINITY)) flag(st, QSPEC_ERR_NONFINITE);
         }
+    };
+    int b = blockIdx.x;
+    fetch(b, v[0]);
+    for (; b < blocks; b += 2 * gridDim.x) {
+        fetch(b + gridDim.x, v[1]);
+        code(b, v[0], 0);
+        if (b + (int)gridDim.x >= blocks) break;
+        fetch(b + 2 * gridDim.x, v[0]);
+        code(b + gridDim.x, v[1], 1);
     }
     // Only now may the next kernel begin: a product behind this one reads its weights ahead of its dependency wait.  (A
-    // CTA's first thread to come here speaks for all of them.  A fence behind every block took 3 of 34 us at 4099 x
-    // 14336, so a CTA goes through several.)
+    // CTA's first thread to come here speaks for all of them.  A fence behind every block took 3 us at 4099 x 14336.)
     __threadfence();
     __syncthreads();
     pdl_launch_dependents();
@@ -239,7 +251,7 @@ int launch_act(const uint16_t *x, int M, int K, int ldx, uint8_t *xq, float *sa,
 
 template <int W>
 int launch_weights(const uint16_t *w, int N, int K, int blocks, uint8_t *w8, float *sw, int32_t *st, cudaStream_t s) {
-    return launch_pdl("qspec_quant_weights_fp8_block", quant_weights_kernel<W>, dim3((unsigned)std::min(blocks, 3 * sm_count())),
+    return launch_pdl("qspec_quant_weights_fp8_block", quant_weights_kernel<W>, dim3((unsigned)std::min(blocks, 2 * sm_count())),
                       dim3(kThreads), 0, s, w, N, K, blocks, w8, sw, st);
 }
 
@@ -257,7 +269,7 @@ extern "C" int qspec_quant_weights_fp8_block(const uint16_t *w_fp16, int N, int 
     if (N < 1 || K < kGroup || K % kGroup) return QSPEC_ERR_SHAPE;
     if (!aligned(w_fp16, 16) || !aligned(w8, 8) || !aligned(sw, 4)) return QSPEC_ERR_ALIGN;
     const long long blocks = (long long)(K / kGroup) * (((long long)N + kGroup - 1) / kGroup);
-    if (blocks > INT_MAX) return QSPEC_ERR_SHAPE;
+    if (blocks > INT_MAX / 2) return QSPEC_ERR_SHAPE;
     int rc = check_device();
     if (rc) return rc;
     cudaStream_t s = as_cuda(stream);
