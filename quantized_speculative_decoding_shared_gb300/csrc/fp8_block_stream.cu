@@ -234,8 +234,11 @@ __global__ void __launch_bounds__(kThreads, (Cfg<BN, kGated>::kOcc))
             if (warp == kScaleWarp && lane == 0) flag(a.st, QSPEC_ERR_TIMEOUT);
             __syncwarp();
         }
-        meet();
+        // (freed before the cluster's barrier: a CTA that waits for its peers holds no tensor memory that one of them may
+        // be waiting for, behind another stream's kernel)
+        umma::fence_after_sync();
         if (warp == kMmaWarp) umma::tmem_free(tmem, C::kAlloc);
+        meet();
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegsWork));
         // ---- thread = channel, half the tokens: sum over the blocks ----

@@ -312,8 +312,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (warp == kScaleWarp && lane == 0) flag(a.st, QSPEC_ERR_TIMEOUT);
             __syncwarp();
         }
-        meet();
+        // (freed before the cluster's barrier: a CTA that waits for its peers holds no tensor memory that one of them may
+        // be waiting for, behind another stream's kernel)
+        umma::fence_after_sync();
         if (warp == kMmaWarp) umma::tmem_free(tmem, 2 * kCols);
+        meet();
         if (plan.split > 1) umma::cluster_sync();
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Regs<kGated>::kWork));
