@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(kQThreads)
     __shared__ float red[kQThreads / 32];
     const int r = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint4 *row = reinterpret_cast<const uint4 *>(in + (size_t)r * ld);
-    pdl_launch_dependents();
+    if (!kHalf) pdl_launch_dependents();
     pdl_wait();
     auto val = [&](uint32_t bits) {
         return kHalf ? __half2float(__ushort_as_half((uint16_t)bits)) : bf16_bits_to_float(bits);
@@ -98,6 +98,13 @@ __global__ void __launch_bounds__(kQThreads)
     if (threadIdx.x == 0) {
         scale[r] = s;
         if (bad_any) flag(st, QSPEC_ERR_NONFINITE);
+    }
+    if (kHalf) {
+        // Weights: only now may the next kernel begin, as a linear behind this one reads them ahead of its dependency
+        // wait.  (A CTA's first thread to come here speaks for all of them.)
+        __threadfence();
+        __syncthreads();
+        pdl_launch_dependents();
     }
 }
 
