@@ -8,12 +8,22 @@
 // The tensor cores cannot scale a block's sums, so the products of a block (K = 128)
 // go into an accumulator of their own, two of them in turn (all of tensor memory), and
 // eight warps (thread = token, half the channels) add it to 128 sums in registers, times
-// the token's scale and the channels', while the next block's products run: 256 clocks of
-// reads and of packed products against 512 of the tensor cores.  The sums' way out (SiLU,
-// product, maxima, codes) has two blocks' products of the next tile beside it.
+// the token's scale and the channels', while the next block's products run.  The sums' way out
+// (SiLU, product, maxima, codes) has two blocks' products of the next tile beside it.
 // One warp issues the copies, one the products, one fetches the scales some blocks ahead.
 // The tiles behind the last full round of CTAs are split along K over the CTAs of a
 // cluster, whose parts meet in shared memory, in the order of K.
+//
+// Bound: shared memory.  A block is written (48 KB) and read by the products (48 KB), 768
+// clocks at 128 bytes; the products take 512, the packed additions 256.  Measured: some 830
+// clocks a block (0.43 us), 8192 x 4096 x 14336 in 352 us (2730 TFLOP/s), gated 8192 x 14336 x
+// 4096 in 725 us (2650) as long as the clock holds, 398 and 800 us under the power cap (1.6 GHz).
+// The same pipeline without the additions, one accumulator handed over for 16 blocks: 317 and 630.
+// Pairs of CTAs (256 tokens, half of either operand in each) need 512 clocks of shared memory,
+// but with barriers in the other CTA an accumulator's way round took 900: 363 us, with sixteen
+// warps of 64 sums 374, and at 80 to 512 tokens a half-empty tile more often (gated 128 x
+// 14336 x 4096 36 us for 25).  Halves of 128 columns with two accumulators each read the tokens
+// twice: 477 us.
 #include <algorithm>
 #include <climits>
 #include <mutex>
@@ -539,7 +549,9 @@ int launch(const char *where, const uint8_t *xq, const uint8_t *w0, const uint8_
     if (all > INT_MAX / 16) return QSPEC_ERR_SHAPE;
     const int tiles = (int)all, G = a.K / kGroup;
     // The cluster's size by what a call would take, in blocks of K of one CTA: full rounds of tiles, then the rest in as
-    // many parts as there are CTAs for; parts cost kMeet blocks to meet.
+    // many parts as there are CTAs for; parts cost kMeet blocks to meet.  (One part / two, us: linear 512 x 4096 x 4096, 64
+    // tiles, 19.4 / 16.8; gated 192 x 14336 x 4096, 224 tiles, 35.6 / 34.7; gated 1024 x 14336 x 4096, 896 tiles, with the rest
+    // in four 95.1 / 102.7.)
     constexpr double kMeet = 6;
     const Resident there = resident<kGated>();
     double least = 1e30;
