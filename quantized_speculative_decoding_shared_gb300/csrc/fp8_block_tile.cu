@@ -66,7 +66,7 @@ struct Ctl {
     float token_scale[kBatches * kBatch][kRows], weight_scale[kBatches * kBatch][2];
     float top[2][2][kRows];                          // gated: maxima of the two halves of the channels, two tiles' in turn
 };
-constexpr size_t kSmem = 1024 + (size_t)kStages * kStage + sizeof(Ctl);
+constexpr size_t kSmem = 1024 + (size_t)kStages * kStage + sizeof(Ctl), kSmemApart = kSmem + kWorkWarps * 32 * 17 * 4;
 
 // What a launch goes through: the tiles 0 .. full - 1 one by one, each CTA every gridDim.x-th, then the others in parts
 // of K, `split` CTAs of a cluster to a tile.
@@ -121,30 +121,55 @@ __device__ __forceinline__ float max_abs(float a, float b, float c) {          /
     return d;
 }
 
-// 16 neighbouring sums of a row to bf16, channels n .. n + 15 of N.  How: 0 value by value, 1 in 16, 2 in 32 bytes (half
-// the way through the store unit, which 32 rows of a warp's take one by one).
-__device__ __forceinline__ void store16(uint16_t *row, int n, int N, int how, const uint64_t *v) {
-    if (how != 0 && n + 16 <= N) {
-        uint32_t w[8];
+// A warp's part of shared memory for results whose rows begin anywhere (17: the rows of it begin in different banks).
+struct Rows {
+    uint32_t w[32][17];
+};
+
+// 32 neighbouring channels n .. n + 31 of a row m to bf16, thread = row.  In 16-byte stores, or 32-byte ones where y allows
+// (`wide`; half the way through the store unit, which a warp's 32 rows take one by one); kApart: through shared
+// memory, row after row, lane = channel (8192 x 4097 x 256 in 43 us; value by value from where they are 278).
+template <bool kApart>
+__device__ __forceinline__ void store_row(const Args &a, int m, int n, bool wide, const uint64_t *v, Rows *buf) {
+    if constexpr (kApart) {
+        const int lane = threadIdx.x & 31, m0 = m - lane;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) w[e] = pack_bf16(lo32(v[e]), hi32(v[e]));
-        f8b::store32(row + n, w, how == 2);
-    } else {
+        for (int j = 0; j < 16; ++j) buf->w[lane][j] = pack_bf16(lo32(v[j]), hi32(v[j]));
+        __syncwarp();
+        if (n + lane < a.N)
+#pragma unroll 8
+            for (int r = 0; r < 32; ++r)
+                if (m0 + r < a.M) a.y[(size_t)(m0 + r) * a.ldy + n + lane] = reinterpret_cast<const uint16_t *>(buf->w[r])[lane];
+        __syncwarp();
+    } else if (m < a.M) {
+        uint16_t *row = a.y + (size_t)m * a.ldy;
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-            if (n + e < N) row[n + e] = float_to_bf16_bits(e % 2 == 0 ? lo32(v[e / 2]) : hi32(v[e / 2]));
+        for (int j = 0; j < 16; j += 8) {
+            const int at = n + 2 * j;
+            if (at + 16 <= a.N) {
+                uint32_t w[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) w[e] = pack_bf16(lo32(v[j + e]), hi32(v[j + e]));
+                f8b::store32(row + at, w, wide);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    if (at + e < a.N) row[at + e] = float_to_bf16_bits(e % 2 == 0 ? lo32(v[j + e / 2]) : hi32(v[j + e / 2]));
+            }
+        }
     }
 }
 
-template <bool kGated>
+template <bool kGated, bool kApart>
 __global__ void __launch_bounds__(kThreads, 1)
     tile_kernel(const __grid_constant__ CUtensorMap t0, const __grid_constant__ CUtensorMap t1,
-                const __grid_constant__ CUtensorMap tx, const __grid_constant__ Args a, const Plan plan, int how_y,
-                int how_h, uint32_t wait_limit, int stall) {
+                const __grid_constant__ CUtensorMap tx, const __grid_constant__ Args a, const Plan plan, bool wide_y,
+                bool wide_h, uint32_t wait_limit, int stall) {
     constexpr int kChannels = kGated ? 128 : 256;                // channels of a tile
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *stages = smem_raw + ((1024u - (umma::smem_addr(smem_raw) & 1023u)) & 1023u);
     Ctl &sm = *reinterpret_cast<Ctl *>(stages + (size_t)kStages * kStage);
+    Rows *rows = reinterpret_cast<Rows *>(&sm + 1);              // (kApart)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int G = a.K / kGroup, cta = (int)blockIdx.x, ctas = (int)gridDim.x;
     const int fulls = cta < plan.full ? (plan.full - cta + ctas - 1) / ctas : 0;      // whole tiles of this CTA
@@ -389,12 +414,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 make_float4(lo32(acc[c][j]), hi32(acc[c][j]), lo32(acc[c][j + 1]), hi32(acc[c][j + 1]));
                 }
             } else if constexpr (!kGated) {
-                if (in && ok) {
-                    uint16_t *y = a.y + (size_t)m * a.ldy;
+                if (ok) {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
-#pragma unroll
-                        for (int j = 0; j < 16; j += 8) store16(y, ct * kChannels + column(c) + 2 * j, a.N, how_y, &acc[c][j]);
+                    for (int c = 0; c < 4; ++c) store_row<kApart>(a, m, ct * kChannels + column(c), wide_y, acc[c], rows + warp);
                 }
             } else {
                 // h = g u / (1 + exp(-g)), two quotients from one reciprocal 1 / (a b) where no gate of the warp's is so
@@ -432,15 +454,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp & 3)) : "memory");      // (the two warps of the same tokens)
                 amax = max_abs(amax, sm.top[parity][half ^ 1][row], 0.0f);
                 parity ^= 1;
+                const int n = ct * kChannels + half * 64;
+                if (ok && a.y != nullptr) {
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) store_row<kApart>(a, m, n + c * 32, wide_y, acc[c], rows + warp);
+                }
                 if (in && ok) {
-                    const int n = ct * kChannels + half * 64;
-                    if (a.y != nullptr) {
-                        uint16_t *y = a.y + (size_t)m * a.ldy;
-#pragma unroll
-                        for (int c = 0; c < 2; ++c)
-#pragma unroll
-                            for (int j = 0; j < 16; j += 8) store16(y, n + c * 32 + 2 * j, a.N, how_y, &acc[c][j]);
-                    }
                     if (a.hq != nullptr) {
                         const f8b::Quant q(amax);
                         const uint64_t by = f2(q.inv, q.inv);
@@ -459,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 const uint64_t v0 = mul2(acc[c][2 * e], by), v1 = mul2(acc[c][2 * e + 1], by);
                                 w[e] = f8b::codes4(lo32(v0), hi32(v0), lo32(v1), hi32(v1));
                             }
-                            f8b::store32(out + 32 * c, w, how_h == 2);
+                            f8b::store32(out + 32 * c, w, wide_h);
                         }
                         if (half == 0) a.sh[(size_t)ct * a.ldh + m] = q.s;
                     }
@@ -512,7 +531,7 @@ Resident ask_resident() {
         cfg.attrs = attr;
         cfg.numAttrs = 1;
         int clusters = 0;
-        if (cudaOccupancyMaxActiveClusters(&clusters, tile_kernel<kGated>, &cfg) != cudaSuccess) {
+        if (cudaOccupancyMaxActiveClusters(&clusters, tile_kernel<kGated, false>, &cfg) != cudaSuccess) {
             cudaGetLastError();
             clusters = 0;
         }
@@ -532,7 +551,7 @@ Resident resident() {
     return known[dev];
 }
 
-template <bool kGated>
+template <bool kGated, bool kApart>
 int launch(const char *where, const uint8_t *xq, const uint8_t *w0, const uint8_t *w1, const Args &a, cudaStream_t stream,
            uint32_t wait_limit, int stall) {
     CUtensorMap t0, t1, tx;
@@ -540,8 +559,10 @@ int launch(const char *where, const uint8_t *xq, const uint8_t *w0, const uint8_
         byte_tmap_sw128(&tx, xq, a.M, a.K, (size_t)a.K, 128))
         return QSPEC_ERR_UNSUPPORTED;
     if (!kGated) t1 = t0;
-    auto kern = tile_kernel<kGated>;
-    int rc = smem_limit_once(reinterpret_cast<const void *>(kern), (int)kSmem);
+    auto kern = tile_kernel<kGated, kApart>;
+    constexpr size_t smem = kApart ? kSmemApart : kSmem;
+    int rc = smem_limit_once(reinterpret_cast<const void *>(kern), (int)smem);
+    if (!rc && kApart) rc = smem_limit_once(reinterpret_cast<const void *>(tile_kernel<kGated, false>), (int)kSmem);     // (asked about below)
     if (rc) return rc;
     constexpr int kChannels = kGated ? 128 : 256;
     Plan plan = {(a.M + kRows - 1) / kRows, (a.N + kChannels - 1) / kChannels, 0, 1};
@@ -570,12 +591,11 @@ int launch(const char *where, const uint8_t *xq, const uint8_t *w0, const uint8_
         }
     }
     plan.split = c;
-    const int how_y = a.y == nullptr || !aligned(a.y, 16) || a.ldy % 8 ? 0 : aligned(a.y, 32) && a.ldy % 16 == 0 ? 2 : 1;
-    const int how_h = aligned(a.hq, 32) ? 2 : 1;
+    const bool wide_y = aligned(a.y, 32) && a.ldy % 16 == 0, wide_h = aligned(a.hq, 32);
     if (c == 1)
-        return launch_pdl(where, kern, dim3((unsigned)grid), dim3(kThreads), kSmem, stream, t0, t1, tx, a, plan, how_y, how_h, wait_limit,
+        return launch_pdl(where, kern, dim3((unsigned)grid), dim3(kThreads), smem, stream, t0, t1, tx, a, plan, wide_y, wide_h, wait_limit,
                           stall);
-    return launch_pdl_cluster(where, kern, dim3((unsigned)grid), dim3(kThreads), kSmem, stream, c, t0, t1, tx, a, plan, how_y, how_h, wait_limit,
+    return launch_pdl_cluster(where, kern, dim3((unsigned)grid), dim3(kThreads), smem, stream, c, t0, t1, tx, a, plan, wide_y, wide_h, wait_limit,
                               stall);
 }
 
@@ -587,8 +607,12 @@ namespace f8b {
 
 int launch_tile(const char *where, const uint8_t *xq, const uint8_t *w0, const uint8_t *w1, const Args &a, cudaStream_t stream,
                 uint32_t wait_limit, int stall) {
-    return w1 != nullptr ? f8t::launch<true>(where, xq, w0, w1, a, stream, wait_limit, stall)
-                         : f8t::launch<false>(where, xq, w0, w1, a, stream, wait_limit, stall);
+    const bool apart = a.y != nullptr && (!aligned(a.y, 16) || a.ldy % 8 != 0);           // rows on no 16-byte boundary
+    if (w1 != nullptr)
+        return apart ? f8t::launch<true, true>(where, xq, w0, w1, a, stream, wait_limit, stall)
+                     : f8t::launch<true, false>(where, xq, w0, w1, a, stream, wait_limit, stall);
+    return apart ? f8t::launch<false, true>(where, xq, w0, w1, a, stream, wait_limit, stall)
+                 : f8t::launch<false, false>(where, xq, w0, w1, a, stream, wait_limit, stall);
 }
 
 }  // namespace f8b
