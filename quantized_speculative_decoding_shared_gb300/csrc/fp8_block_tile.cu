@@ -419,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int c = 0; c < 4; ++c) store_row<kApart>(a, m, ct * kChannels + column(c), wide_y, acc[c], rows + warp);
                 }
             } else {
-                // h = g u / (1 + exp(-g)), two quotients from one reciprocal 1 / (a b) where no gate of the warp's is so
+                // h = g u / (1 + exp(-g)), two quotients from one reciprocal 1 / (a b) where no gate of the thread's is so
                 // low that the product passes fp32: the reciprocals and exponentials bound this part
                 constexpr float kLog2e = 1.4426950408889634f;
                 float low = 0.0f, amax = 0.0f;
@@ -427,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int c = 0; c < 2; ++c)
 #pragma unroll
                     for (int j = 0; j < 16; ++j) low = min_of(low, lo32(acc[c][j]), hi32(acc[c][j]));
-                if (all(low >= -43.0f)) {
+                if (low >= -43.0f) {                             // (no NaN)
 #pragma unroll
                     for (int c = 0; c < 2; ++c)
 #pragma unroll

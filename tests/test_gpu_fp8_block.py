@@ -228,11 +228,12 @@ def test_blocks_of_zeros(M):
 
 
 @pytest.mark.parametrize("M", [7, 64, 130, 513])
-def test_outputs_apart(M):
-    """Leading dimensions wider than the rows, odd ones among them, scales further apart than tokens: nothing else is
-    written, and what stands past the last token is not read."""
+@pytest.mark.parametrize("ldy", [391, 392, 400])
+def test_outputs_apart(M, ldy):
+    """Leading dimensions wider than the rows, odd ones and such on 16 bytes among them, codes on 16 bytes, scales further
+    apart than tokens: nothing else is written, and what stands past the last token is not read."""
     dev = need_gpu()
-    N, K, lds, ldh, ldy = 384, 640, M + 3, M + 5, 391
+    N, K, lds, ldh = 384, 640, M + 3, M + 5
     xq, sa0 = codes(M, K, 4, dev)
     sa = torch.full((K // 128, lds), float("nan"), device=dev)
     sa[:, :M] = sa0
@@ -242,11 +243,12 @@ def test_outputs_apart(M):
     assert q.qspec_linear_fp8_block(xq, sa, lds, *wg, M, N - 1, K, y, ldy, st) == 0 and read_status(st) == 0
     assert torch.all(y[:, N - 1:] == 7.0)
     check_linear(y[:, :N - 1], act_values(xq, sa0), weight_values(*wg)[:N - 1])
-    hq = torch.full((M + 1, N), 9, dtype=torch.uint8, device=dev)
+    flat = torch.full((16 + (M + 1) * N,), 9, dtype=torch.uint8, device=dev)
+    hq = flat[16:].view(M + 1, N)
     sh = torch.full((N // 128, ldh), -7.0, device=dev)
     h = torch.full((M, ldy), 7.0, dtype=torch.bfloat16, device=dev)
     assert q.qspec_gated_fp8_block(xq, sa, lds, *wg, *wu, M, N, K, hq, sh, ldh, h, ldy, st) == 0 and read_status(st) == 0
-    assert torch.all(hq[M] == 9) and torch.all(sh[:, M:] == -7.0) and torch.all(h[:, N:] == 7.0)
+    assert torch.all(hq[M] == 9) and torch.all(flat[:16] == 9) and torch.all(sh[:, M:] == -7.0) and torch.all(h[:, N:] == 7.0)
     ref, d = gated(act_values(xq, sa0), weight_values(*wg), weight_values(*wu))
     check_codes(hq[:M], sh[:, :M], ref, d)
     check_bf16(h[:, :N], ref, d)
@@ -277,3 +279,88 @@ def test_the_models_shapes_in_sampled_channels(M, N, K):
     y = q.linear_fp8_block(xq, sa, w8, sw)
     for n in (0, 128 * (N // 256), N - 128):
         check_linear(y[:, n:n + 128], act_values(xq, sa), weight_values(w8[n:n + 128], sw[n // 128:n // 128 + 1]))
+
+
+def test_a_token_does_not_depend_on_the_others():
+    """Gates far below zero, or not finite, in one token of a tile: the other tokens keep their bits."""
+    dev = need_gpu()
+    M, N, K = 300, 256, 512
+    x = acts(M, K, 8, dev)
+    wg, wu = (q.quant_weights_fp8_block(parent(N, K, i, dev)) for i in (1, 2))
+    want = q.gated_fp8_block(*q.quant_act_fp8_block(x), *wg, *wu, want_bf16=True)
+    x[17] *= 4000.0
+    x[200, 3] = float("nan")
+    got = q.gated_fp8_block(*q.quant_act_fp8_block(x), *wg, *wu, want_bf16=True)
+    keep = [m for m in range(M) if m not in (17, 200)]
+    assert torch.equal(got[0][keep], want[0][keep]) and torch.equal(got[1][:, keep], want[1][:, keep]) and torch.equal(got[2][keep], want[2][keep])
+    assert torch.isnan(got[1][:, 200]).all()
+
+
+def test_offsets_past_32_bits():
+    """Tensors of more than 2^32 values: their last rows against the definitions."""
+    dev = need_gpu()
+    M, K = 263000, 16384
+    x = torch.zeros((M, K), dtype=torch.bfloat16, device=dev)
+    x[-5:] = acts(5, K, 1, dev)
+    xq, sa = q.quant_act_fp8_block(x)
+    want = act_codes(x[-5:])
+    assert same(xq[-5:], want[0]) and same(sa[:, -5:].contiguous(), want[1])
+    w = x.view(torch.int16).zero_().view(torch.float16)                       # (the same memory as weights)
+    w[-200:] = parent(200, K, 2, dev)
+    w8, sw = q.quant_weights_fp8_block(w)
+    n0 = (M - 200) // 128 * 128
+    want = weight_codes(w[n0:])
+    assert same(w8[n0:], want[0]) and same(sw[n0 // 128:], want[1])
+    del x, w, xq, sa
+    a = codes(3, K, 3, dev)
+    y = q.linear_fp8_block(*a, w8, sw)
+    check_linear(y[:, n0:], act_values(*a), weight_values(w8[n0:], sw[n0 // 128:]))
+    del w8, sw, y
+    M, N, K = 66000, 66048, 128
+    xq, sa = codes(M, K, 4, dev)
+    wg, wu = (q.quant_weights_fp8_block(parent(N, K, i, dev)) for i in (5, 6))
+    y = q.linear_fp8_block(xq, sa, *wg)
+    xs, gs, us = act_values(xq[-200:], sa[:, -200:]), weight_values(wg[0][-256:], wg[1][-2:]), weight_values(wu[0][-256:], wu[1][-2:])
+    check_linear(y[-200:, -256:], xs, gs)
+    hq, sh, h = q.gated_fp8_block(xq, sa, *wg, *wu, want_bf16=True)
+    ref, d = gated(xs, gs, us)
+    check_codes(hq[-200:, -256:], sh[-2:, -200:], ref, d)
+    check_bf16(h[-200:, -256:], ref, d)
+
+
+FIRST = """
+import sys; sys.path[:0] = [%r, %r]
+import torch
+from quantized_speculative_decoding_shared_gb300 import binding as q
+dev = torch.device('cuda')
+g = torch.Generator(device=dev).manual_seed(1)
+make = lambda r, c: torch.randint(0, 100, (r, c), generator=g, device=dev, dtype=torch.uint8)
+K, N = 512, 384
+rows = (3, 40, 100, 300)
+xs = [(make(m, K), torch.rand((K // 128, m), generator=g, device=dev)) for m in rows]
+w = [(make(N, K), torch.rand((N // 128, K // 128), generator=g, device=dev)) for _ in range(2)]
+def program():
+    out = []
+    for x in xs:
+        out += [q.linear_fp8_block(*x, *w[0]), *q.gated_fp8_block(*x, *w[0], *w[1])[:2]]
+    return out
+torch.cuda.synchronize()
+s, gr = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+with torch.cuda.graph(gr, stream=s):
+    got = program()
+gr.replay()
+torch.cuda.synchronize()
+want = program()
+torch.cuda.synchronize()
+print('same', all(torch.equal(a, b) for a, b in zip(got, want)))
+"""
+
+
+def test_the_first_calls_of_a_process_are_captured():
+    import os
+    import subprocess
+    import sys
+    need_gpu()
+    here = os.path.dirname(os.path.abspath(__file__))
+    r = subprocess.run([sys.executable, "-c", FIRST % (os.path.dirname(here), here)], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "same True" in r.stdout, r.stdout + r.stderr
