@@ -36,39 +36,16 @@ namespace {
 
 namespace f8q {
 
+using f8b::f2;
+using f8b::fma2;
+using f8b::hi32;
+using f8b::lo32;
+using f8b::max_abs;
+using f8b::max_nan;
+using f8b::mul2;
+
 constexpr int kThreads = 256;
 constexpr int kBlocksX = 4;                     // neighbouring blocks per CTA
-
-// max(a, |b|, |c|) and max(a, b) that keep a NaN (a >= 0)
-__device__ __forceinline__ float max_abs(float a, float b, float c) {
-    float d;
-    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-    return d;
-}
-__device__ __forceinline__ float max_nan(float a, float b) {
-    float d;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
-    return d;
-}
-
-// two fp32 values in a register pair, and packed operations on them
-__device__ __forceinline__ uint64_t f2(float a, float b) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ float lo32(uint64_t v) { return __uint_as_float((uint32_t)v); }
-__device__ __forceinline__ float hi32(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-    uint64_t d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
 
 // a word of two fp16 or bf16 values
 template <bool kHalf>

@@ -23,6 +23,47 @@ struct Args {
     int lds, M, N, K, ldy, ldh;
 };
 
+// two fp32 values in a register pair, and packed operations on them
+__device__ __forceinline__ uint64_t f2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float lo32(uint64_t v) { return __uint_as_float((uint32_t)v); }
+__device__ __forceinline__ float hi32(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+// max(a, |b|, |c|) and max(a, b) that keep a NaN (a >= 0)
+__device__ __forceinline__ float max_abs(float a, float b, float c) {
+    float d;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+
+// shared-memory descriptor of a K-major operand with rows of 128 bytes in the 128-byte swizzle (fp8.cu)
+__device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr) {
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)1 << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 |
+           (uint64_t)2 << 61;
+}
+
 // h = silu(g) u = g u / (1 + exp(-g)).  exp(-g) passes fp32 below -88.7: 1 / inf is the limit 0; a NaN stays one.
 __device__ __forceinline__ float gated(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
 
@@ -89,13 +130,10 @@ __device__ __forceinline__ void store_gated(const Args &a, int m, int block, int
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         h[e] = gated(g[e], u[e]);
-        asm("max.NaN.f32 %0, %0, %1;" : "+f"(amax) : "f"(fabsf(h[e])));
+        amax = max_nan(amax, fabsf(h[e]));
     }
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) {
-        const float other = __shfl_xor_sync(0xffffffffu, amax, o);
-        asm("max.NaN.f32 %0, %0, %1;" : "+f"(amax) : "f"(other));
-    }
+    for (int o = 16; o >= 1; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
     if (a.hq != nullptr) {
         const Quant q(amax);
         reinterpret_cast<uint32_t *>(a.hq + (size_t)m * a.N + (size_t)block * kGroup)[lane] =

@@ -32,6 +32,11 @@ namespace {
 namespace f8s {
 
 using f8b::Args;
+using f8b::desc_sw128;
+using f8b::f2;
+using f8b::fma2;
+using f8b::hi32;
+using f8b::lo32;
 
 constexpr int kTile = 128;                       // channels per CTA, and K per stage
 constexpr int kWorkWarps = 8, kWork = 32 * kWorkWarps, kLoadWarp = 8, kMmaWarp = 9, kScaleWarp = 10, kThreads = kWork + 128;
@@ -60,24 +65,6 @@ struct Cfg {
     static constexpr int kRegs = kOcc == 2 ? 80 : 168, kRegsWork = kOcc == 2 ? 96 : 200, kRegsRest = kOcc == 2 ? 48 : 96;
     static_assert(kOcc * kThreads * kRegs <= 65536 && kWork * kRegsWork + 128 * kRegsRest <= kThreads * kRegs, "register shares");
 };
-
-__device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr) {       // K-major, rows of 128 bytes, 128-byte swizzle
-    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)1 << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 |
-           (uint64_t)2 << 61;
-}
-
-__device__ __forceinline__ uint64_t f2(float a, float b) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ float lo32(uint64_t v) { return __uint_as_float((uint32_t)v); }
-__device__ __forceinline__ float hi32(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
 
 template <int BN, bool kGated>
 __global__ void __launch_bounds__(kThreads, (Cfg<BN, kGated>::kOcc))

@@ -37,8 +37,16 @@ namespace {
 
 namespace f8t {
 
+using f8b::add2;
 using f8b::Args;
+using f8b::desc_sw128;
+using f8b::f2;
+using f8b::fma2;
+using f8b::hi32;
 using f8b::kMaxSplit;
+using f8b::lo32;
+using f8b::max_abs;
+using f8b::mul2;
 
 constexpr int kRows = 128, kCols = 256;              // of the accumulator
 constexpr int kWorkWarps = 8, kWork = 32 * kWorkWarps, kLoadWarp = 8, kMmaWarp = 9, kScaleWarp = 10, kThreads = kWork + 128;
@@ -74,32 +82,6 @@ struct Plan {
     int row_tiles, col_tiles, full, split;
 };
 
-__device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr) {       // K-major, rows of 128 bytes, 128-byte swizzle
-    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)1 << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 |
-           (uint64_t)2 << 61;
-}
-__device__ __forceinline__ uint64_t f2(float a, float b) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ float lo32(uint64_t v) { return __uint_as_float((uint32_t)v); }
-__device__ __forceinline__ float hi32(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-    uint64_t d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -114,11 +96,6 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
-}
-__device__ __forceinline__ float max_abs(float a, float b, float c) {          // keeps a NaN (a >= 0)
-    float d;
-    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-    return d;
 }
 
 // A warp's part of shared memory for results whose rows begin anywhere (17: the rows of it begin in different banks).
@@ -313,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int e = 0; e < kRows / 32; ++e)
                         x[u][e] = some && m0 + 32 * e < a.M ? __ldg(a.sa + (size_t)(k0 + g) * a.lds + m0 + 32 * e) : 0.0f;
-                    // lane 0: of the lower half of the channels, or the gate; lane 1: of the upper half, or up
+                    // lane 0: of the lower 128 channels, or the gate; lane 1: of the upper 128, or up
                     const float *from = kGated && lane == 1 ? a.s1 : a.s0;
                     w[u] = some && lane < 2 ? __ldg(from + (size_t)(kGated ? ct : min(2 * ct + lane, blocks_n - 1)) * G + k0 + g) : 0.0f;
                     if (some && ++g == nk) {
@@ -492,8 +469,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             // ---- the parts of K meet: a warp takes a token, its lanes four channels of either half ----
             int rt, ct, k0;
             item(fulls, rt, ct, k0);
-            const int m0 = rt * kRows, rows = min(kRows, a.M - m0), first = (int)umma::cluster_rank() - part;
-            for (int r = warp * plan.split + part; r < rows; r += kWorkWarps * plan.split) {
+            const int m0 = rt * kRows, tokens = min(kRows, a.M - m0), first = (int)umma::cluster_rank() - part;
+            for (int r = warp * plan.split + part; r < tokens; r += kWorkWarps * plan.split) {
                 const float *at[2] = {reinterpret_cast<const float *>(piece(r, lane)), reinterpret_cast<const float *>(piece(r, 32 + lane))};
                 float v[2][4];
                 f8b::sum_parts(at, plan.split, first, v);
