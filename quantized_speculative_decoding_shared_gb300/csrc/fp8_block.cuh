@@ -145,24 +145,23 @@ __device__ __forceinline__ void store_gated(const Args &a, int m, int block, int
 }
 
 // Sums over a cluster's parts of K, in their order: four floats at each of `at` in the shared memory of the CTAs first,
-// first + 1, ..., first + split - 1.  All are asked for before the first is added: an answer takes about a microsecond.
-// (Several tokens of a tile at once took 1 us off two parts of 512 x 4096 x 4096, but with that much inlined behind it
-// the many-token kernel's loop was compiled to run 3 % longer.)
+// first + 1, ..., first + split - 1 (R of them at most).  All are asked for before the first is added: an answer takes about a
+// microsecond.
 constexpr int kMaxSplit = 8;
-template <int T>
+template <int R = kMaxSplit, int T>
 __device__ __forceinline__ void sum_parts(const float *const (&at)[T], int split, int first, float (&v)[T][4]) {
-    uint4 w[T][kMaxSplit];
+    uint4 w[T][R];
 #pragma unroll
     for (int t = 0; t < T; ++t)
 #pragma unroll
-        for (int r = 0; r < kMaxSplit; ++r)
+        for (int r = 0; r < R; ++r)
             w[t][r] = r < split ? umma::ld_peer_v4(at[t], (uint32_t)(first + r)) : make_uint4(0, 0, 0, 0);
 #pragma unroll
     for (int t = 0; t < T; ++t) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[t][e] = 0.0f;
 #pragma unroll
-        for (int r = 0; r < kMaxSplit; ++r) {
+        for (int r = 0; r < R; ++r) {
             v[t][0] += __uint_as_float(w[t][r].x);
             v[t][1] += __uint_as_float(w[t][r].y);
             v[t][2] += __uint_as_float(w[t][r].z);

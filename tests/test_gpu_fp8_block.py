@@ -281,6 +281,25 @@ def test_the_models_shapes_in_sampled_channels(M, N, K):
         check_linear(y[:, n:n + 128], act_values(xq, sa), weight_values(w8[n:n + 128], sw[n // 128:n // 128 + 1]))
 
 
+@pytest.mark.parametrize("M", [513, 531, 546, 640])
+@pytest.mark.parametrize("N", [3840, 2304, 1792, 768])
+def test_parts_of_k_that_meet(M, N):
+    """Tiles in two, three, four and more parts of K, the last tile of 1, 19, 34 and 128 tokens."""
+    dev = need_gpu()
+    K = 2048
+    xq, sa = codes(M, K, M + N, dev)
+    w8, sw = q.quant_weights_fp8_block(parent(N, K, N, dev))
+    st = status(dev)
+    y = torch.full((M + 3, N), -7.0, dtype=torch.bfloat16, device=dev)
+    q.linear_fp8_block(xq, sa, w8, sw, out=y[:M], dev_status=st)
+    assert read_status(st) == 0
+    check_linear(y[:M], act_values(xq, sa), weight_values(w8, sw))
+    assert torch.all(y[M:] == -7.0)                                   # rows behind the last are left as they were
+    z = torch.full((M + 1, N + 1), -7.0, dtype=torch.bfloat16, device=dev)
+    assert q.qspec_linear_fp8_block(xq, sa, M, w8, sw, M, N, K, z, N + 1, st) == 0 and read_status(st) == 0
+    assert torch.equal(z[:M, :N], y[:M]) and torch.all(z[M:] == -7.0) and torch.all(z[:, N:] == -7.0)
+
+
 def test_a_token_does_not_depend_on_the_others():
     """Gates far below zero, or not finite, in one token of a tile: the other tokens keep their bits."""
     dev = need_gpu()
