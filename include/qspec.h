@@ -554,7 +554,7 @@ int qspec_linear_fp8_block(const uint8_t *xq, const float *sa, int lds, const ui
  * The gated product: gate and up projection, SiLU, product and quantisation in
  * one kernel.  g and u are the sums of qspec_linear_fp8_block with the two sets
  * of weights, not rounded:
- *   h = g / (1 + exp(-g)) u                               (fp32)
+ *   h = g / (1 + exp(-g)) u                               (fp32; 0 where 1 + exp(-g) passes 2^126, from g = -87.3 down)
  *   sh[j ldh + m] = max |h| / 448 over channels 128 j .. 128 j + 127 of token m
  *   hq = E4M3(h / sh)                                     (a block of zeros: 0)
  * so that hq and sh are the xq and sa of the next qspec_linear_fp8_block (the down

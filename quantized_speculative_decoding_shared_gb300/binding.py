@@ -695,17 +695,21 @@ def _rows_of(t, name):
     """A bf16 CUDA tensor [M][K] with contiguous rows: (M, K, leading dimension)."""
     if t.device.type != "cuda" or t.dtype != torch.bfloat16 or t.dim() != 2 or (t.numel() and t.stride(1) != 1):
         raise ValueError("%s must be a bf16 CUDA tensor [M][K] with contiguous rows" % name)
-    return t.shape[0], t.shape[1], (t.stride(0) if t.shape[0] > 1 else t.shape[1])
+    ld = t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    if ld >= 2 ** 31:
+        raise ValueError("%s: its rows must be less than 2^31 values apart" % name)
+    return t.shape[0], t.shape[1], ld
 
 
 def _block_codes(xq, sa):
-    """Codes uint8 [M][K] with scales fp32 [K / 128][M] (rows of scales may be strided): (M, K, lds)."""
+    """Codes uint8 [M][K] with scales fp32 [K / 128][M] (rows of scales at least M apart): (M, K, lds)."""
     _need(xq, torch.uint8, "xq")
     M, K = xq.shape
+    lds = sa.stride(0) if K > GROUP and sa.dim() == 2 else M
     if (sa.device.type != "cuda" or sa.dtype != torch.float32 or sa.shape != (K // GROUP, M)
-            or (M > 1 and sa.stride(1) != 1)):
-        raise ValueError("sa must be a fp32 CUDA tensor [%d][%d] with contiguous rows" % (K // GROUP, M))
-    return M, K, max(M, sa.stride(0))
+            or (M > 1 and sa.stride(1) != 1) or not M <= lds < 2 ** 31):
+        raise ValueError("sa must be a fp32 CUDA tensor [%d][%d] with contiguous rows, %d or more apart" % (K // GROUP, M, M))
+    return M, K, lds
 
 
 def _block_weights(w8, sw, K, name):

@@ -85,6 +85,36 @@ def test_conveniences_refuse_what_they_cannot_pass_on():
             call()
 
 
+class OnDevice:
+    """A tensor that says it lies on a GPU."""
+
+    def __init__(self, t):
+        self.t, self.device = t, torch.device("cuda")
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+
+def test_rows_of_scales_that_overlap_are_refused():
+    xq = OnDevice(torch.zeros((3, 256), dtype=torch.uint8))
+    wide = torch.zeros((2, 8))
+    assert binding._block_codes(xq, OnDevice(wide[:, :3])) == (3, 256, 8)
+    assert binding._block_codes(xq, OnDevice(wide[0, :6].view(2, 3))) == (3, 256, 3)
+    one = OnDevice(torch.zeros((1, 256), dtype=torch.uint8))
+    assert binding._block_codes(one, OnDevice(wide[:, :1])) == (1, 256, 8)
+    block = OnDevice(torch.zeros((3, 128), dtype=torch.uint8))
+    assert binding._block_codes(block, OnDevice(wide[:1, :3])) == (3, 128, 3)      # (one row: its distance is nobody's)
+    assert binding._block_codes(block, OnDevice(torch.zeros(3).expand(1, 3))) == (3, 128, 3)
+    for codes, sa in ((xq, torch.zeros(3).expand(2, 3)), (xq, torch.zeros(6).as_strided((2, 3), (2, 1))),
+                      (xq, torch.zeros((3, 2)).t()), (xq, torch.zeros((2, 1)).expand(2, 3)), (one, torch.zeros(1).expand(2, 1)),
+                      (xq, torch.zeros(6)), (xq, torch.zeros((2, 4))), (one, torch.empty((2, 1), device="meta").as_strided((2, 1), (2 ** 31, 1)))):
+        with pytest.raises(ValueError):
+            binding._block_codes(codes, OnDevice(sa))
+    far = torch.empty((2, 128), dtype=torch.bfloat16, device="meta").as_strided((2, 128), (2 ** 31 + 128, 1))
+    with pytest.raises(ValueError):
+        binding._rows_of(OnDevice(far), "x")
+
+
 def test_the_diagnostic_entry(lib):
     linear = dict(xq=at(), sa=at(), lds=5, w=at(), sw=at(), w1=None, s1=None, M=5, N=100, K=256, hq=None, sh=None, ldh=0, y=at(), ldy=100,
                   limit=1000, stall=1, st=None, s=None)
