@@ -222,14 +222,44 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR)
 // four shuffles and the row's reduction only the sum of squares.  Where the squares pass fp32 the sum is taken again
 // times 2^-160; a block whose products with the weights pass it is taken again times 2^-80, the other blocks stand.
 // Scales lie token by token, [K / 128][lds]: 4 bytes a block, next to those of the neighbouring rows' CTAs.
+//
+// Many rows take half the threads and twice the words to each (NV = 4, 1024 threads to an SM): more rows at once, each with
+// twice the loads in flight.  A thread's odd words are summed apart, as the thread does that has them in the wide form, so
+// that a row's bits do not depend on the number of rows.
 template <int TPR, int NV>
-__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR)
+constexpr bool kNarrow = NV == 4 && TPR >= 128 && TPR < 1024;
+template <int TPR, int NV>                     // CTAs to an SM
+constexpr int kOcc = kNarrow<TPR, NV> ? 1024 / TPR : NV == 2 && TPR == 256 ? 5 : NV == 2 && TPR == 512 ? 3 : 1;
+
+template <int TPR, int S>
+__device__ __forceinline__ float row_sum(float (&part)[S], float *red) {
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < S; ++i) part[i] += __shfl_xor_sync(0xffffffffu, part[i], o);
+    float sum = S == 2 ? part[0] + part[S - 1] : part[0];
+    if constexpr (TPR > 32) {
+        constexpr int kW = TPR / 32;
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        __syncthreads();                       // red free again (a second pass over the row)
+        if (lane == 0) red[warp] = sum;
+        __syncthreads();
+        sum = red[lane % kW];                  // every warp folds the kW partials in the same order
+#pragma unroll
+        for (int o = kW / 2; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    }
+    return sum;
+}
+
+template <int TPR, int NV>
+__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, (kOcc<TPR, NV>))
     rmsnorm_fp8_block_kernel(const uint16_t *x, int ldx, const uint16_t *res, int ldr, const uint16_t *__restrict__ w,
                              float eps, int M, int K, uint16_t *h, int ldh, uint8_t *__restrict__ xq,
                              float *__restrict__ sa, int lds, uint16_t *__restrict__ y, int ldy, int32_t *st) {
     constexpr int kRows = TPR < 128 ? 128 / TPR : 1;
     constexpr float kDown = 8.271806125530277e-25f, kUp = 1.2089258196146292e24f;      // 2^-80, 2^80
-    __shared__ float2 red[32];
+    constexpr int S = kNarrow<TPR, NV> ? 2 : 1;
+    __shared__ float red[32];
     const int t = threadIdx.x % TPR;
     const int m = blockIdx.x * kRows + (TPR < 128 ? threadIdx.x / TPR : 0);
     const int n8 = K / 8;
@@ -260,7 +290,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR)
             if (row_ok && i < n8) reinterpret_cast<uint4 *>(h + (size_t)m * ldh)[i] = hv[j];
         }
     }
-    uint64_t a[NV][4], sq = 0;
+    uint64_t a[NV][4], sq[S] = {};
     float top[NV];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -269,28 +299,31 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const uint64_t v = both(hw[e]);
-            sq = fma2(v, v, sq);
+            sq[j % S] = fma2(v, v, sq[j % S]);
             a[j][e] = mul2(v, both(ww[e]));
             top[j] = max_abs(top[j], lo32(a[j][e]), hi32(a[j][e]));
         }
 #pragma unroll
         for (int o = 8; o >= 1; o >>= 1) top[j] = max_nan(top[j], __shfl_xor_sync(0xffffffffu, top[j], o));
     }
-    float ss = lo32(sq) + hi32(sq), none = 0.0f;
-    row_reduce<TPR>(ss, none, red);
+    float part[S];
+#pragma unroll
+    for (int i = 0; i < S; ++i) part[i] = lo32(sq[i]) + hi32(sq[i]);
+    float ss = row_sum<TPR>(part, red);
     const uint16_t *row = res != nullptr ? h + (size_t)m * ldh : x + (size_t)m * ldx;
     const bool stands = ss < INFINITY;                    // (the same for a row's threads, and for TPR = 32 for a warp's)
     if (!stands) {
-        ss = 0.0f;
+#pragma unroll
+        for (int i = 0; i < S; ++i) part[i] = 0.0f;
 #pragma unroll
         for (int j = 0; j < NV; ++j)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int i = 4 * (t + j * TPR) + e;
                 const uint64_t v = mul2(both(row_ok && i < 4 * n8 ? reinterpret_cast<const uint32_t *>(row)[i] : 0u), f2(kDown, kDown));
-                ss = fmaf(lo32(v), lo32(v), fmaf(hi32(v), hi32(v), ss));
+                part[j % S] = fmaf(lo32(v), lo32(v), fmaf(hi32(v), hi32(v), part[j % S]));
             }
-        row_reduce<TPR>(ss, none, red);
+        ss = row_sum<TPR>(part, red);
     }
     if (!row_ok) return;                                  // (whole warps: a row has at least one)
     const float near = rsqrtf(fmaf(ss, 1.0f / (float)K, stands ? eps : eps * kDown * kDown));
@@ -422,8 +455,15 @@ extern "C" int qspec_rmsnorm_fp8_block(const uint16_t *x_bf16, int ldx, const ui
         return launcher(x_bf16, ldx, res_bf16, ldr, w_bf16, eps, M, K, h_bf16, ldh, xq, sa, lds, y_bf16, ldy, dev_status,
                         s);
     };
-    const int n8 = K / 8;                        // (widths as in qspec_rmsnorm_fp8)
+    // Widths as in qspec_rmsnorm_fp8, halved where the rows fill the device even so.  (us, wide / halved, with residual and y:
+    // 2047 x 3584 10.6 / 10.1, 8192 x 2048 29.5 / 25.2, 2047 x 5120 17.4 / 15.1, 8192 x 14336 201 / 157, but 912 x 4096 6.7 /
+    // 6.9, 456 x 8192 6.7 / 7.1, 64 x 14336 3.5 / 4.0.)
+    const int n8 = K / 8;
+    const auto many = [&](int threads) { return (long long)M * threads >= 1024LL * sm_count(); };
     if (n8 <= 128) return go(nrm::launch_block<32, 4>);
+    if (n8 <= 512 && many(128)) return go(nrm::launch_block<128, 4>);
+    if (n8 > 512 && n8 <= 1024 && many(256)) return go(nrm::launch_block<256, 4>);
+    if (n8 > 1024 && n8 <= 2048 && many(512)) return go(nrm::launch_block<512, 4>);
     if (n8 <= 512) return go(nrm::launch_block<256, 2>);
     if (n8 <= 1024) return go(nrm::launch_block<512, 2>);
     if (n8 <= 2048) return go(nrm::launch_block<1024, 2>);

@@ -59,6 +59,32 @@ def test_against_64_bits(M, K, residual):
     assert again[3] is None and torch.equal(again[0], got[0]) and torch.equal(again[1], got[1])
 
 
+@pytest.mark.parametrize("K", [1152, 2048, 4096, 4224, 8192, 8320, 14336, 16384])
+@pytest.mark.parametrize("residual", [False, True])
+def test_many_rows_have_the_bits_of_few(K, residual):
+    """Above some number of rows a row is spread over half the threads: against 64 bits, and bit by bit against the same
+    rows in calls of 40, rows among them whose squares, or whose products with the weights, pass fp32."""
+    dev = need_gpu()
+    M = 1321
+    x = syn.activations(M, K, K, device=dev).float()
+    x[1::7] *= 2.0 ** 66
+    x[2::7, :128] *= 2.0 ** 100
+    x[3] = 0.0
+    x = x.to(torch.bfloat16)
+    r = syn.activations(M, K, K + 1, device=dev) if residual else None
+    w = syn.activations(1, K, 9, device=dev).float().view(K)
+    w[128:256] *= 2.0 ** 60
+    w = w.to(torch.bfloat16)
+    st = status(dev)
+    got = q.rmsnorm_fp8_block(x, w, EPS, residual=r, want_bf16=True, dev_status=st)
+    assert read_status(st) == 0
+    check(x, w, EPS, r, got)
+    for m in range(0, M, 40):
+        few = q.rmsnorm_fp8_block(x[m:m + 40], w, EPS, residual=None if r is None else r[m:m + 40], want_bf16=True)
+        assert torch.equal(few[0], got[0][m:m + 40]) and torch.equal(few[1], got[1][:, m:m + 40])
+        assert torch.equal(few[3], got[3][m:m + 40]) and (r is None or torch.equal(few[2], got[2][m:m + 40]))
+
+
 def test_strided_rows_scales_apart_and_the_residual_in_place():
     dev = need_gpu()
     M, K, lds = 9, 512, 13
