@@ -15,7 +15,7 @@
 #include <cmath>
 #include <cuda_fp8.h>
 
-#include "qspec_device.cuh"
+#include "fp8_block.cuh"
 #include "qspec_host.h"
 
 namespace qspec {
@@ -329,19 +329,19 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, (kOcc<TPR, NV>))
     const float near = rsqrtf(fmaf(ss, 1.0f / (float)K, stands ? eps : eps * kDown * kDown));
     // 1 / rms, for products as they are and for those times 2^-80
     const float rstd = stands ? near : near * kDown, rstd_up = stands ? near * kUp : near;
-    bool bad = !(ss < INFINITY);
+    bool bad = !(ss < INFINITY), any = false;
+    uint32_t again = 0;                                   // bit j: block j was taken again
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const int i = t + j * TPR;
-        float by = rstd;
-        const bool again = !(top[j] < INFINITY);
-        if (__any_sync(0xffffffffu, again)) {
-            if (again) {
-                by = rstd_up;
+    for (int j = 0; j < NV; ++j) any |= !(top[j] < INFINITY);
+    if (__any_sync(0xffffffffu, any)) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            if (!(top[j] < INFINITY)) {
+                again |= 1u << j;
                 top[j] = 0.0f;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const int at = 4 * i + e;
+                    const int at = 4 * (t + j * TPR) + e;
                     const bool in = at < 4 * n8;
                     a[j][e] = mul2(mul2(both(in ? reinterpret_cast<const uint32_t *>(row)[at] : 0u), f2(kDown, kDown)),
                                    both(in ? reinterpret_cast<const uint32_t *>(w)[at] : 0u));
@@ -352,6 +352,11 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, (kOcc<TPR, NV>))
             for (int o = 8; o >= 1; o >>= 1) top[j] = max_nan(top[j], __shfl_xor_sync(0xffffffffu, top[j], o));
             if (!(top[j] < INFINITY)) top[j] = INFINITY;          // (NaN too)
         }
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int i = t + j * TPR;
+        const float by = again >> j & 1 ? rstd_up : rstd;
         if (i >= n8) continue;
         if (y != nullptr) {
             uint32_t o[4];
@@ -362,9 +367,9 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, (kOcc<TPR, NV>))
             }
             reinterpret_cast<uint4 *>(y + (size_t)m * ldy)[i] = make_uint4(o[0], o[1], o[2], o[3]);
         }
-        // codes a (448 / top), where 448 / top would pass fp32 with a brought up first
-        const float up = top[j] < 1.0e-30f ? 7.9228162514264338e28f : 1.0f;   // 2^96
-        const float inv = top[j] > 0.0f ? __fdiv_rn(448.0f, top[j] * up) : 0.0f;
+        // codes a (448 / top), within 3 x 2^-24; a power of two beside them where the reciprocal would leave fp32
+        const float up = top[j] < 1.0e-30f ? 7.9228162514264338e28f : top[j] > 1.0e30f ? 1.262177448353619e-29f : 1.0f;   // 2^96, 2^-96
+        const float inv = 448.0f * f8b::reciprocal(top[j] * up);
         uint32_t code[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -376,7 +381,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, (kOcc<TPR, NV>))
                           : make_uint2(0u, 0u);       // no code of -0 in a block of zeros
         const float most = top[j] * by;                // max |y|, in the bf16 output inf from the midpoint behind the
         bad |= !(most < (y != nullptr ? 3.3961775292304601e38f : INFINITY));   // largest bf16 value
-        if ((threadIdx.x & 15) == 0) sa[(size_t)(i / 16) * lds + m] = __fdiv_rn(most, 448.0f);
+        if ((threadIdx.x & 15) == 0) sa[(size_t)(i / 16) * lds + m] = f8b::scale_of(most);
     }
     if (bad) flag(st, QSPEC_ERR_NONFINITE);
 }
@@ -457,7 +462,7 @@ extern "C" int qspec_rmsnorm_fp8_block(const uint16_t *x_bf16, int ldx, const ui
     };
     // Widths as in qspec_rmsnorm_fp8, halved where the rows fill the device even so.  (us, wide / halved, with residual and y:
     // 2047 x 3584 10.6 / 10.1, 8192 x 2048 29.5 / 25.2, 2047 x 5120 17.4 / 15.1, 8192 x 14336 201 / 157, but 912 x 4096 6.7 /
-    // 6.9, 456 x 8192 6.7 / 7.1, 64 x 14336 3.5 / 4.0.)
+    // 6.9, 456 x 8192 6.7 / 7.1, 64 x 14336 3.5 / 4.0; since then a twentieth less by scales without divisions.)
     const int n8 = K / 8;
     const auto many = [&](int threads) { return (long long)M * threads >= 1024LL * sm_count(); };
     if (n8 <= 128) return go(nrm::launch_block<32, 4>);
