@@ -383,7 +383,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, (kOcc<TPR, NV>))
         bad |= !(most < (y != nullptr ? 3.3961775292304601e38f : INFINITY));   // largest bf16 value
         if ((threadIdx.x & 15) == 0) sa[(size_t)(i / 16) * lds + m] = f8b::scale_of(most);
     }
-    if (bad) flag(st, QSPEC_ERR_NONFINITE);
+    if (__any_sync(0xffffffffu, bad) && (threadIdx.x & 31) == 0) flag(st, QSPEC_ERR_NONFINITE);
 }
 
 template <int TPR, int NV>
