@@ -563,10 +563,11 @@ int launch(const char *where, const uint8_t *xq, const uint8_t *w0, const uint8_
     if (all > INT_MAX / 16) return QSPEC_ERR_SHAPE;
     const int tiles = (int)all, G = a.K / kGroup;
     // The cluster's size by what a call would take, in blocks of K of one CTA: full rounds of tiles, then the rest in as
-    // many parts as there are CTAs for; parts cost kMeet blocks to meet.  (One part / two, us: linear 512 x 4096 x 4096, 64
-    // tiles, 19.4 / 14.8; gated 192 x 14336 x 4096, 224 tiles, 35.6 / 34.7; gated 1024 x 14336 x 4096, 896 tiles, with the rest
-    // in four 95.1 / 102.7.)
-    constexpr double kMeet = 6;
+    // many parts as there are CTAs for; the parts' meeting costs some blocks too, more behind the gate, and in two parts
+    // with no round before them more again (the whole tiles have the machine's memory for fewer CTAs).  One part / several, us:
+    // linear 512 x 4096 (64 tiles) with K = 2048 11.1 / 11.3, 2560 12.7 / 12.1, 4096 17.6 / 14.6; 256 x 4096 (in four) 1536
+    // 8.9 / 9.8, 2048 10.6 / 10.4; gated 128 x 8192 (64 tiles) 2048 11.7 / 15.1, 4096 18.9 / 20.2; 192 x 14336 (224 tiles, the last
+    // 72 in two) 2048 19.5 / 22.0, 4096 33.5 / 32.7; 128 x 4096 (in four) 1536 8.8 / 10.4.
     const Resident there = resident<kGated>();
     double least = 1e30;
     int c = 1, grid = 0;
@@ -575,7 +576,8 @@ int launch(const char *where, const uint8_t *xq, const uint8_t *w0, const uint8_
         if (ctas < s) continue;
         const int rounds = tiles / ctas, rest = tiles - rounds * ctas;
         if (s > 1 && (rest == 0 || rest * s > ctas)) continue;
-        const double takes = (double)rounds * G + (rest == 0 ? 0.0 : s == 1 ? (double)G : (double)((G + s - 1) / s) + kMeet);
+        const double meet = kGated ? (s == 2 && rounds == 0 ? 18.0 : 13.0) : s == 2 ? 8.5 : 11.0;
+        const double takes = (double)rounds * G + (rest == 0 ? 0.0 : s == 1 ? (double)G : (double)((G + s - 1) / s) + meet);
         if (takes < least) {
             least = takes;
             c = s;

@@ -283,10 +283,10 @@ def test_the_models_shapes_in_sampled_channels(M, N, K):
 
 @pytest.mark.parametrize("M", [513, 531, 546, 640])
 @pytest.mark.parametrize("N", [3840, 2304, 1792, 768])
-def test_parts_of_k_that_meet(M, N):
+@pytest.mark.parametrize("K", [2048, 4096])
+def test_parts_of_k_that_meet(M, N, K):
     """Tiles in two, three, four and more parts of K, the last tile of 1, 19, 34 and 128 tokens."""
     dev = need_gpu()
-    K = 2048
     xq, sa = codes(M, K, M + N, dev)
     w8, sw = q.quant_weights_fp8_block(parent(N, K, N, dev))
     st = status(dev)
@@ -298,6 +298,25 @@ def test_parts_of_k_that_meet(M, N):
     z = torch.full((M + 1, N + 1), -7.0, dtype=torch.bfloat16, device=dev)
     assert q.qspec_linear_fp8_block(xq, sa, M, w8, sw, M, N, K, z, N + 1, st) == 0 and read_status(st) == 0
     assert torch.equal(z[:M, :N], y[:M]) and torch.all(z[M:] == -7.0) and torch.all(z[:, N:] == -7.0)
+
+
+@pytest.mark.parametrize("M,N,K", [(640, 1920, 5120), (520, 1152, 4096), (513, 896, 4096), (200, 512, 4096), (130, 14336, 4096), (300, 8192, 4096)])
+def test_gated_parts_of_k_that_meet(M, N, K):
+    """Tiles in two, three, four and eight parts of K, and tiles behind a full round in two and three."""
+    dev = need_gpu()
+    xq, sa = codes(M, K, M + N, dev)
+    wg, wu = (q.quant_weights_fp8_block(parent(N, K, N + i, dev)) for i in (1, 2))
+    st = status(dev)
+    flat = torch.full((M + 1, N), 9, dtype=torch.uint8, device=dev)
+    sh = torch.full((N // 128, M + 2), -7.0, device=dev)
+    h = torch.full((M + 1, N + 1), -7.0, dtype=torch.bfloat16, device=dev)
+    assert q.qspec_gated_fp8_block(xq, sa, M, *wg, *wu, M, N, K, flat, sh, M + 2, h, N + 1, st) == 0 and read_status(st) == 0
+    ref, d = gated(act_values(xq, sa), weight_values(*wg), weight_values(*wu))
+    check_codes(flat[:M], sh[:, :M], ref, d)
+    check_bf16(h[:M, :N], ref, d)
+    assert torch.all(flat[M] == 9) and torch.all(sh[:, M:] == -7.0) and torch.all(h[M] == -7.0) and torch.all(h[:, N:] == -7.0)
+    again = q.gated_fp8_block(xq, sa, *wg, *wu, want_bf16=True)
+    assert torch.equal(again[0], flat[:M]) and torch.equal(again[1], sh[:, :M]) and torch.equal(again[2], h[:M, :N])
 
 
 def test_a_token_does_not_depend_on_the_others():
