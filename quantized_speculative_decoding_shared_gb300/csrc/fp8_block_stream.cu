@@ -320,6 +320,24 @@ __global__ void __launch_bounds__(kThreads, (Cfg<BN, kGated>::kOcc))
 }
 
 template <int BN, bool kGated>
+int slots() { return sm_count() * Cfg<BN, kGated>::kOcc; }       // CTAs that run at once
+
+// Parts of K: doubled as long as there is room and two blocks for each; then three, five or six where they shorten the
+// longest part by a fifth and leave a tenth of the machine free, which the clusters of such sizes cannot all fill (us, with
+// powers of two / best: 1 x 5120 x 13824, 40 tiles, four 14.5 / six 13.7, seven do not fit 18.9; 128 x 5120 x 13824 two 27.6 /
+// three 21.2; 1 x 10240 x 8192 two 16.6 / three 15.5; but 1 x 6144 x 4096 four 6.6 / five 7.1, 80 x 3584 x 3584, 28 tiles, four 7.6 /
+// five 9.2.)
+template <int BN, bool kGated>
+int parts(int tiles, int G) {
+    const long long room = slots<BN, kGated>();
+    int split = 1;
+    while (split < kMaxSplit && (long long)tiles * split * 2 <= room && G / (split * 2) >= 2) split *= 2;
+    for (int s : {3, 5, 6})
+        if (s > split && (long long)tiles * s * 10 <= room * 9 && G / s >= 2 && (G + s - 1) / s * 5 <= (G + split - 1) / split * 4) split = s;
+    return split;
+}
+
+template <int BN, bool kGated>
 int launch(const char *where, const uint8_t *xq, const uint8_t *w0, const uint8_t *w1, const Args &a, int bn,
            cudaStream_t stream, uint32_t wait_limit, int stall) {
     using C = Cfg<BN, kGated>;
@@ -333,26 +351,30 @@ int launch(const char *where, const uint8_t *xq, const uint8_t *w0, const uint8_
     int rc = smem_limit_once(reinterpret_cast<const void *>(kern), (int)C::kSmem, true);
     if (rc) return rc;
     const int tiles = (a.N + kTile - 1) / kTile;
-    int split = 1;                               // parts of K: as many as there is room for, two blocks to each
-    while (split < kMaxSplit && (long long)tiles * split * 2 <= (long long)sm_count() * C::kOcc && a.K / kGroup / (split * 2) >= 2) split *= 2;
+    const int split = parts<BN, kGated>(tiles, a.K / kGroup);
     if (split == 1)
         return launch_pdl(where, kern, dim3((unsigned)tiles), dim3(kThreads), C::kSmem, stream, t0, t1, tx, a, bn, split, wait_limit, stall);
     return launch_pdl_cluster(where, kern, dim3((unsigned)(tiles * split)), dim3(kThreads), C::kSmem, stream, split, t0, t1, tx, a, bn, split, wait_limit, stall);
 }
 
 // Few tokens here, many in tiles of 128 (fp8_block_tile.cu): 128 channels by M tokens against 128 tokens by 256 channels.
-// Measured here / there, us: linear 80 x 4096 x 14336 15.8 / 18.0, 128 18.1 / 19.5, 192 (in two parts) 25.4 / 21.5; gated
-// 32 x 14336 x 4096 22.5 / 24.4, 64 25.0 / 24.6, 80 32.3 / 24.7.
+// Up to 16 tokens here.  Up to 32 (gated), 64 and 128 here too while the channels' tiles fit the machine at once, since a CTA
+// goes through one tile; above 64 tokens not where a CTA has 48 blocks of K or more, above 96 not from 32, which take longer
+// than the many-token kernel's.  Measured here / there, us: 72 x 28672 x 8192 52.9 / 41.4, 48 x 128256 x 4096 91.9 / 85.1, 64 x 28672 x 4096 22.9 / 23.4, 80
+// x 4096 x 4096 8.4 / 10.4, 96 x 14336 x 4096 15.8 / 16.2, 96 x 10240 x 8192 (64 blocks) 25.8 / 20.8, 128 x 14336 x 4096 (32) 18.1 / 16.8, 128 x 4096 x 14336 (28) 17.5 /
+// 19.0; gated 32 x 14336 x 4096 21.6 / 22.8, 32 x 24576 x 4096 41.3 / 37.4, 16 x 28672 x 8192 70.9 / 74.7.
 template <bool kGated>
 int launch_any(const char *where, const uint8_t *xq, const uint8_t *w0, const uint8_t *w1, const Args &a, cudaStream_t st,
                uint32_t wait_limit = kWaitLimit, int stall = 0) {
-    constexpr int kMost = kGated ? 32 : 128;
-    const int bn = (a.M + 15) / 16 * 16;
+    const int bn = (a.M + 15) / 16 * 16, tiles = (a.N + kTile - 1) / kTile, G = a.K / kGroup;
     if (bn <= 16) return launch<16, kGated>(where, xq, w0, w1, a, bn, st, wait_limit, stall);
-    if (bn <= 32) return launch<32, kGated>(where, xq, w0, w1, a, bn, st, wait_limit, stall);
+    if (bn <= 32 && (!kGated || tiles <= slots<32, kGated>())) return launch<32, kGated>(where, xq, w0, w1, a, bn, st, wait_limit, stall);
     if constexpr (!kGated) {
-        if (bn <= 64) return launch<64, kGated>(where, xq, w0, w1, a, bn, st, wait_limit, stall);
-        if (bn <= kMost) return launch<kMost, kGated>(where, xq, w0, w1, a, bn, st, wait_limit, stall);
+        if (bn <= 64 && tiles <= slots<64, kGated>()) return launch<64, kGated>(where, xq, w0, w1, a, bn, st, wait_limit, stall);
+        if (bn > 64 && bn <= 128 && tiles <= slots<128, kGated>()) {
+            const int p = parts<128, kGated>(tiles, G);
+            if ((G + p - 1) / p < (bn <= 96 ? 48 : 32)) return launch<128, kGated>(where, xq, w0, w1, a, bn, st, wait_limit, stall);
+        }
     }
     return f8b::launch_tile(where, xq, w0, w1, a, st, wait_limit, stall);
 }

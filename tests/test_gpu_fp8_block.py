@@ -300,6 +300,28 @@ def test_parts_of_k_that_meet(M, N, K):
     assert torch.equal(z[:M, :N], y[:M]) and torch.all(z[M:] == -7.0) and torch.all(z[:, N:] == -7.0)
 
 
+# few tokens with K in three, five and six parts, one CTA and two to an SM; more channels than fit the machine at once; long K
+PARTS = [(1, 10240, 1536), (7, 6144, 2560), (16, 5120, 2048), (64, 5120, 2048), (100, 5120, 1280), (90, 2560, 2560), (100, 20480, 256), (40, 39424, 128),
+         (128, 14336, 4096), (30, 5120, 1280), (20, 19584, 256)]
+
+
+@pytest.mark.parametrize("M,N,K", PARTS)
+@pytest.mark.parametrize("is_gated", [False, True])
+def test_few_tokens_in_odd_parts_and_wide(M, N, K, is_gated):
+    dev = need_gpu()
+    xq, sa = codes(M, K, M + 1, dev)
+    w, v = (q.quant_weights_fp8_block(parent(N, K, N + i, dev)) for i in (1, 2))
+    st = status(dev)
+    if is_gated:
+        hq, sh, h = q.gated_fp8_block(xq, sa, *w, *v, want_bf16=True, dev_status=st)
+        ref, d = gated(act_values(xq, sa), weight_values(*w), weight_values(*v))
+        check_codes(hq, sh, ref, d)
+        check_bf16(h, ref, d)
+    else:
+        check_linear(q.linear_fp8_block(xq, sa, *w, dev_status=st), act_values(xq, sa), weight_values(*w))
+    assert read_status(st) == 0
+
+
 @pytest.mark.parametrize("M,N,K", [(640, 1920, 5120), (520, 1152, 4096), (513, 896, 4096), (200, 512, 4096), (130, 14336, 4096), (300, 8192, 4096)])
 def test_gated_parts_of_k_that_meet(M, N, K):
     """Tiles in two, three, four and eight parts of K, and tiles behind a full round in two and three."""
