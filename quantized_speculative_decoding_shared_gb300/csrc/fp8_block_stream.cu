@@ -6,7 +6,7 @@
 //   gated: h = silu(gate) up, out as E4M3 with a scale per token and 128 and / or bf16
 //
 // The weights are read once, so HBM bounds it: 128 output channels are the lanes
-// of the accumulator, up to 128 tokens its columns (gated: up to 32, for each of the
+// of the accumulator, up to 128 tokens its columns (gated: up to 64, for each of the
 // two parts).  TMA fills a ring of stages, one block of K to a stage (128 x 128 bytes of
 // weights, twice for the gated one, and the tokens' 128 bytes each); one warp issues the
 // products of a block into an accumulator of its own, and eight warps (thread = channel,
@@ -320,7 +320,18 @@ __global__ void __launch_bounds__(kThreads, (Cfg<BN, kGated>::kOcc))
 }
 
 template <int BN, bool kGated>
+struct Kernel {
+    static const void *address() { return reinterpret_cast<const void *>(stream_kernel<BN, kGated>); }
+    static constexpr int threads = kThreads, per = Cfg<BN, kGated>::kOcc;
+    static constexpr size_t smem = Cfg<BN, kGated>::kSmem;
+    static constexpr bool carveout = true;
+};
+template <int BN, bool kGated>
 int slots() { return sm_count() * Cfg<BN, kGated>::kOcc; }       // CTAs that run at once
+// The same in clusters of s.  (Where two CTAs share an SM the runtime's count takes one for what fits: 256 of them in
+// clusters of eight, and 240 in clusters of six, run at once.)
+template <int BN, bool kGated>
+int room(int s) { return Cfg<BN, kGated>::kOcc == 1 ? f8b::resident<Kernel<BN, kGated>>().ctas[s] : slots<BN, kGated>(); }
 
 // Parts of K: doubled as long as there is room and two blocks for each; then three, five or six where they shorten the
 // longest part by a fifth and leave a tenth of the machine free, which the clusters of such sizes cannot all fill (us, with
@@ -329,11 +340,11 @@ int slots() { return sm_count() * Cfg<BN, kGated>::kOcc; }       // CTAs that ru
 // five 9.2.)
 template <int BN, bool kGated>
 int parts(int tiles, int G) {
-    const long long room = slots<BN, kGated>();
+    const long long all = slots<BN, kGated>();
     int split = 1;
-    while (split < kMaxSplit && (long long)tiles * split * 2 <= room && G / (split * 2) >= 2) split *= 2;
+    while (split < kMaxSplit && (long long)tiles * split * 2 <= room<BN, kGated>(split * 2) && G / (split * 2) >= 2) split *= 2;
     for (int s : {3, 5, 6})
-        if (s > split && (long long)tiles * s * 10 <= room * 9 && G / s >= 2 && (G + s - 1) / s * 5 <= (G + split - 1) / split * 4) split = s;
+        if (s > split && (long long)tiles * s * 10 <= all * 9 && tiles * s <= room<BN, kGated>(s) && G / s >= 2 && (G + s - 1) / s * 5 <= (G + split - 1) / split * 4) split = s;
     return split;
 }
 
@@ -359,17 +370,20 @@ int launch(const char *where, const uint8_t *xq, const uint8_t *w0, const uint8_
 
 // Few tokens here, many in tiles of 128 (fp8_block_tile.cu): 128 channels by M tokens against 128 tokens by 256 channels.
 // Up to 16 tokens here.  Up to 32 (gated), 64 and 128 here too while the channels' tiles fit the machine at once, since a CTA
-// goes through one tile; above 64 tokens not where a CTA has 48 blocks of K or more, above 96 not from 32, which take longer
+// goes through one tile, and up to 64 behind the gate while they fit it twice; above 64 tokens not where a CTA has 48 blocks of K or more, above 96 not from 32, which take longer
 // than the many-token kernel's.  Measured here / there, us: 72 x 28672 x 8192 52.9 / 41.4, 48 x 128256 x 4096 91.9 / 85.1, 64 x 28672 x 4096 22.9 / 23.4, 80
 // x 4096 x 4096 8.4 / 10.4, 96 x 14336 x 4096 15.8 / 16.2, 96 x 10240 x 8192 (64 blocks) 25.8 / 20.8, 128 x 14336 x 4096 (32) 18.1 / 16.8, 128 x 4096 x 14336 (28) 17.5 /
-// 19.0; gated 32 x 14336 x 4096 21.6 / 22.8, 32 x 24576 x 4096 41.3 / 37.4, 16 x 28672 x 8192 70.9 / 74.7.
+// 19.0; gated 32 x 14336 x 4096 21.6 / 22.8, 32 x 24576 x 4096 41.3 / 37.4, 16 x 28672 x 8192 70.9 / 74.7, 48 x 4096 x 4096 10.7 / 11.9, 48 x 9216 x
+// 4096 17.1 / 18.3, 48 x 11008 x 4096 20.9 / 20.5.
 template <bool kGated>
 int launch_any(const char *where, const uint8_t *xq, const uint8_t *w0, const uint8_t *w1, const Args &a, cudaStream_t st,
                uint32_t wait_limit = kWaitLimit, int stall = 0) {
     const int bn = (a.M + 15) / 16 * 16, tiles = (a.N + kTile - 1) / kTile, G = a.K / kGroup;
     if (bn <= 16) return launch<16, kGated>(where, xq, w0, w1, a, bn, st, wait_limit, stall);
     if (bn <= 32 && (!kGated || tiles <= slots<32, kGated>())) return launch<32, kGated>(where, xq, w0, w1, a, bn, st, wait_limit, stall);
-    if constexpr (!kGated) {
+    if constexpr (kGated) {
+        if (bn > 32 && bn <= 64 && tiles * 2LL <= slots<64, kGated>()) return launch<64, kGated>(where, xq, w0, w1, a, bn, st, wait_limit, stall);
+    } else {
         if (bn <= 64 && tiles <= slots<64, kGated>()) return launch<64, kGated>(where, xq, w0, w1, a, bn, st, wait_limit, stall);
         if (bn > 64 && bn <= 128 && tiles <= slots<128, kGated>()) {
             const int p = parts<128, kGated>(tiles, G);

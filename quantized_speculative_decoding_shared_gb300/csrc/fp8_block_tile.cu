@@ -26,7 +26,6 @@
 // twice: 477 us.
 #include <algorithm>
 #include <climits>
-#include <mutex>
 
 #include "fp8_block_host.h"
 #include "umma.cuh"
@@ -502,47 +501,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-// CTAs that the device runs at once in clusters of each size, a whole number of clusters (0: none).  Asked once for each
-// device (the questions take some microseconds).
-struct Resident {
-    int ctas[kMaxSplit + 1];
+template <bool kGated>
+struct Kernel {
+    static const void *address() { return reinterpret_cast<const void *>(tile_kernel<kGated, false>); }
+    static constexpr int threads = kThreads, per = 1;
+    static constexpr size_t smem = kSmem;
+    static constexpr bool carveout = false;
 };
-template <bool kGated>
-Resident ask_resident() {
-    Resident r = {};
-    const int sms = sm_count();
-    r.ctas[1] = sms;
-    for (int c = 2; c <= kMaxSplit; ++c) {
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((unsigned)(sms / c * c));
-        cfg.blockDim = dim3(kThreads);
-        cfg.dynamicSmemBytes = kSmem;
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = (unsigned)c;
-        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        int clusters = 0;
-        if (cudaOccupancyMaxActiveClusters(&clusters, tile_kernel<kGated, false>, &cfg) != cudaSuccess) {
-            cudaGetLastError();
-            clusters = 0;
-        }
-        r.ctas[c] = std::min(clusters * c, sms / c * c);
-    }
-    return r;
-}
-template <bool kGated>
-Resident resident() {
-    constexpr int kDevices = 64;
-    static Resident known[kDevices];
-    static std::once_flag once[kDevices];
-    int dev = 0;
-    cudaGetDevice(&dev);
-    if (dev < 0 || dev >= kDevices) return ask_resident<kGated>();
-    std::call_once(once[dev], [&] { known[dev] = ask_resident<kGated>(); });
-    return known[dev];
-}
 
 template <bool kGated, bool kApart>
 int launch(const char *where, const uint8_t *xq, const uint8_t *w0, const uint8_t *w1, const Args &a, cudaStream_t stream,
@@ -555,7 +520,6 @@ int launch(const char *where, const uint8_t *xq, const uint8_t *w0, const uint8_
     auto kern = tile_kernel<kGated, kApart>;
     constexpr size_t smem = kApart ? kSmemApart : kSmem;
     int rc = smem_limit_once(reinterpret_cast<const void *>(kern), (int)smem);
-    if (!rc && kApart) rc = smem_limit_once(reinterpret_cast<const void *>(tile_kernel<kGated, false>), (int)kSmem);     // (asked about below)
     if (rc) return rc;
     constexpr int kChannels = kGated ? 128 : 256;
     Plan plan = {(a.M + kRows - 1) / kRows, (a.N + kChannels - 1) / kChannels, 0, 1};
@@ -568,7 +532,7 @@ int launch(const char *where, const uint8_t *xq, const uint8_t *w0, const uint8_
     // linear 512 x 4096 (64 tiles) with K = 2048 11.1 / 11.3, 2560 12.7 / 12.1, 4096 17.6 / 14.6; 256 x 4096 (in four) 1536
     // 8.9 / 9.8, 2048 10.6 / 10.4; gated 128 x 8192 (64 tiles) 2048 11.7 / 15.1, 4096 18.9 / 20.2; 192 x 14336 (224 tiles, the last
     // 72 in two) 2048 19.5 / 22.0, 4096 33.5 / 32.7; 128 x 4096 (in four) 1536 8.8 / 10.4.
-    const Resident there = resident<kGated>();
+    const f8b::Resident there = f8b::resident<Kernel<kGated>>();
     double least = 1e30;
     int c = 1, grid = 0;
     for (int s = 1; s <= kMaxSplit && s <= G; ++s) {

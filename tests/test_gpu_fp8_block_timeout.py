@@ -19,7 +19,7 @@ SHORT = 2000                # a bound the stalled wait runs through
 # several, all of them in parts, and the last ones in parts
 @pytest.mark.parametrize("M,N,K", [(1, 128, 128), (3, 640, 4096), (16, 40960, 512), (30, 256, 2048), (64, 512, 1024), (100, 384, 4096),
                                    (140, 256, 384), (200, 512, 4096), (300, 20480, 256), (130, 39424, 512), (130, 39424, 2048),
-                                   (1, 10240, 1536), (7, 6144, 2560), (16, 5120, 2048), (100, 5120, 1280)])
+                                   (1, 10240, 1536), (7, 6144, 2560), (16, 5120, 2048), (100, 5120, 1280), (50, 4096, 2048)])
 @pytest.mark.parametrize("is_gated", [False, True])
 def test_then_a_regular_call(M, N, K, is_gated):
     dev = need_gpu()
