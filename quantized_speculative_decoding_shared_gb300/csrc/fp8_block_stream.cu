@@ -328,10 +328,14 @@ struct Kernel {
 };
 template <int BN, bool kGated>
 int slots() { return sm_count() * Cfg<BN, kGated>::kOcc; }       // CTAs that run at once
-// The same in clusters of s.  (Where two CTAs share an SM the runtime's count takes one for what fits: 256 of them in
-// clusters of eight, and 240 in clusters of six, run at once.)
+// The same in clusters of s.  Where two CTAs share an SM the runtime's count takes one for what fits (256 of them in clusters of
+// eight, and 240 in clusters of six, run at once): there a twentieth is left free for what clusters of four or more cannot
+// fill (us, 1 x 4736 x 4096, 37 tiles, in eight parts 9.7, in six 6.3; 1 x 9600 x 4096, 75 tiles, in four 12.3, in three 8.8).
 template <int BN, bool kGated>
-int room(int s) { return Cfg<BN, kGated>::kOcc == 1 ? f8b::resident<Kernel<BN, kGated>>().ctas[s] : slots<BN, kGated>(); }
+int room(int s) {
+    if (Cfg<BN, kGated>::kOcc == 1) return f8b::resident<Kernel<BN, kGated>>().ctas[s];
+    return s >= 4 ? slots<BN, kGated>() * 19 / 20 : slots<BN, kGated>();
+}
 
 // Parts of K: doubled as long as there is room and two blocks for each; then three, five or six where they shorten the
 // longest part by a fifth and leave a tenth of the machine free, which the clusters of such sizes cannot all fill (us, with

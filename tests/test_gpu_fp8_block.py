@@ -302,7 +302,8 @@ def test_parts_of_k_that_meet(M, N, K):
 
 # few tokens with K in three, five and six parts, one CTA and two to an SM; more channels than fit the machine at once; long K
 PARTS = [(1, 10240, 1536), (7, 6144, 2560), (16, 5120, 2048), (64, 5120, 2048), (100, 5120, 1280), (90, 2560, 2560), (100, 20480, 256), (40, 39424, 128),
-         (128, 14336, 4096), (30, 5120, 1280), (20, 19584, 256), (80, 2048, 4096), (33, 1024, 2048), (49, 9216, 512), (64, 4096, 1152), (51, 9856, 256)]
+         (128, 14336, 4096), (30, 5120, 1280), (20, 19584, 256), (80, 2048, 4096), (33, 1024, 2048), (49, 9216, 512), (64, 4096, 1152), (51, 9856, 256),
+         (1, 4736, 4096), (9, 9600, 2048)]
 
 
 @pytest.mark.parametrize("M,N,K", PARTS)
