@@ -182,18 +182,20 @@ __global__ void __launch_bounds__(kThreads, (Cfg<BN, kGated>::kOcc))
         } else if (warp == kScaleWarp) {
             constexpr int kEach = (BN + 31) / 32;
             const float *w0 = a.s0 + (size_t)tile * G + k0, *w1 = kGated ? a.s1 + (size_t)tile * G + k0 : nullptr;
+            // (coherent loads, past L1: the kernel in front may write either kind of scales while this one is resident, and
+            // a product before it may have left their old values in this multiprocessor's L1)
             pdl_wait();
             for (int base = 0; base < nk; base += kBatch) {
                 float x[kBatch][kEach], s0[kBatch], s1[kBatch];
 #pragma unroll
                 for (int u = 0; u < kBatch; ++u) {
                     const bool some = base + u < nk;
-                    s0[u] = some ? __ldg(w0 + base + u) : 0.0f;
-                    s1[u] = some && kGated ? __ldg(w1 + base + u) : 0.0f;
+                    s0[u] = some ? __ldcg(w0 + base + u) : 0.0f;
+                    s1[u] = some && kGated ? __ldcg(w1 + base + u) : 0.0f;
 #pragma unroll
                     for (int e = 0; e < kEach; ++e) {
                         const int m = lane + 32 * e;
-                        x[u][e] = some && m < a.M ? __ldg(a.sa + (size_t)(k0 + base + u) * a.lds + m) : 0.0f;
+                        x[u][e] = some && m < a.M ? __ldcg(a.sa + (size_t)(k0 + base + u) * a.lds + m) : 0.0f;
                     }
                 }
                 const int slot = base / kBatch % kBatches;

@@ -275,7 +275,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         } else if (warp == kScaleWarp) {
-            // the blocks' scales, some way ahead of the work (a load from L2 takes as long as two blocks)
+            // the blocks' scales, some way ahead of the work (a load from L2 takes as long as two blocks); coherent loads,
+            // past L1, as the kernel in front may write them while this one is resident
             const int blocks_n = (a.N + kGroup - 1) / kGroup;
             int i = 0, g = 0, rt, ct, k0, nk = 0;
             if (items > 0) nk = item(0, rt, ct, k0);
@@ -288,10 +289,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int m0 = rt * kRows + lane;
 #pragma unroll
                     for (int e = 0; e < kRows / 32; ++e)
-                        x[u][e] = some && m0 + 32 * e < a.M ? __ldg(a.sa + (size_t)(k0 + g) * a.lds + m0 + 32 * e) : 0.0f;
+                        x[u][e] = some && m0 + 32 * e < a.M ? __ldcg(a.sa + (size_t)(k0 + g) * a.lds + m0 + 32 * e) : 0.0f;
                     // lane 0: of the lower 128 channels, or the gate; lane 1: of the upper 128, or up
                     const float *from = kGated && lane == 1 ? a.s1 : a.s0;
-                    w[u] = some && lane < 2 ? __ldg(from + (size_t)(kGated ? ct : min(2 * ct + lane, blocks_n - 1)) * G + k0 + g) : 0.0f;
+                    w[u] = some && lane < 2 ? __ldcg(from + (size_t)(kGated ? ct : min(2 * ct + lane, blocks_n - 1)) * G + k0 + g) : 0.0f;
                     if (some && ++g == nk) {
                         g = 0;
                         if (++i < items) nk = item(i, rt, ct, k0);

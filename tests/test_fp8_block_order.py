@@ -1,0 +1,38 @@
+"""What the products with block scales read of the kernel in front of them, from the sources: these orders hold by the
+memory model or not at all, and a run that keeps them by chance looks like one that must."""
+import os
+import re
+
+import pytest
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                    "quantized_speculative_decoding_shared_gb300", "csrc")
+
+
+def source(name):
+    """A file of csrc without its comments."""
+    with open(os.path.join(CSRC, name)) as f:
+        return re.sub(r"//[^\n]*|/\*.*?\*/", "", f.read(), flags=re.S)
+
+
+def body(text, name):
+    """The body of the function `name`, braces included."""
+    start = text.index("{", re.search(r"\b%s\([^;{]*\)\s*\{" % name, text).start())
+    depth = 0
+    for i in range(start, len(text)):
+        depth += {"{": 1, "}": -1}.get(text[i], 0)
+        if depth == 0:
+            return text[start:i + 1]
+    raise AssertionError(name)
+
+
+@pytest.mark.parametrize("file,kernel", [("fp8_block_stream.cu", "stream_kernel"), ("fp8_block_tile.cu", "tile_kernel")])
+def test_scales_are_read_coherently(file, kernel):
+    """The kernel in front may still write them while this one is resident: nothing that is read-only by declaration
+    only (ld.global.nc) reads them, and what does is behind the dependency wait."""
+    text = body(source(file), kernel)
+    assert "__ldg(" not in text and ".nc" not in text
+    reads = [m.start() for m in re.finditer(r"__ldcg\(", text)]
+    warp = text.index("warp == kScaleWarp")
+    wait = text.index("pdl_wait()", warp)
+    assert len(reads) >= 2 and all(r > wait for r in reads)
