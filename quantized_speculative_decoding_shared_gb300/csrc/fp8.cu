@@ -100,11 +100,11 @@ __global__ void __launch_bounds__(kQThreads)
         if (bad_any) flag(st, QSPEC_ERR_NONFINITE);
     }
     if (kHalf) {
-        // Weights: only now may the next kernel begin, as a linear behind this one reads them ahead of its dependency
-        // wait.  (A CTA's first thread to come here speaks for all of them.)
+        // Weights: a linear behind this kernel reads them ahead of its dependency wait, by asynchronous copies.  So the
+        // next kernel begins only when this grid is complete (it never lets it begin earlier), each thread's codes
+        // performed for the device and ordered before such copies.
         __threadfence();
-        __syncthreads();
-        pdl_launch_dependents();
+        umma::fence_proxy_async_global();
     }
 }
 
@@ -184,6 +184,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             // the first stages' weight boxes before the dependency wait, then
             // their activation boxes; one barrier per stage counts both
             const int pre = min(S, nk);
+            umma::fence_proxy_async_global();           // (the weights may be the kernel's in front, which is complete)
             for (int i = 0; i < pre; ++i) {
                 uint8_t *stg = smem + (size_t)i * kStage;
                 umma::mbar_arrive_expect_tx(&full[i], kStage);

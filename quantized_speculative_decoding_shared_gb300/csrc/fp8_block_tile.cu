@@ -205,7 +205,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             umma::mbar_init(&sm.drain, 1);
             umma::mbar_fence_init();
             umma::fence_proxy_async();
-            // the first stages' weights at once, before the dependency wait too (they are immutable)
+            umma::fence_proxy_async_global();           // (the weights may be the kernel's in front, which is complete)
+            // the first stages' weights at once, before the dependency wait too
             for (int i = 0; i < early; ++i) load_weights(i, k0 + i, ct * kChannels);
         }
         __syncwarp();

@@ -21,6 +21,8 @@ constexpr int kGroup = QSPEC_GROUP;
 // only reads immutable data (packed weights, scale/zero words); every read
 // of another kernel's output and every write comes after pdl_wait(), which
 // returns once the previous grid has completed and its writes are visible.
+// A kernel that makes such data (the quantisers of weights) never calls
+// pdl_launch_dependents(): what follows it begins when it is complete.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
 // Lets the next PDL-launched kernel be scheduled as this grid's CTAs retire.
 __device__ __forceinline__ void pdl_launch_dependents() {

@@ -59,6 +59,10 @@ __device__ __forceinline__ void fence_before_sync() { asm volatile("tcgen05.fenc
 // generic-proxy shared-memory writes -> visible to the tensor core (async proxy)
 __device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory"); }
 
+// the same for global memory that copies read: behind what this thread has written and fenced for the device, and in
+// front of the first copy of what other kernels' threads wrote so
+__device__ __forceinline__ void fence_proxy_async_global() { asm volatile("fence.proxy.async.global;\n" ::: "memory"); }
+
 // ---- mbarriers ----
 __device__ __forceinline__ void mbar_init(uint64_t *bar, uint32_t count) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;\n" ::"r"(smem_addr(bar)), "r"(count));

@@ -36,3 +36,23 @@ def test_scales_are_read_coherently(file, kernel):
     warp = text.index("warp == kScaleWarp")
     wait = text.index("pdl_wait()", warp)
     assert len(reads) >= 2 and all(r > wait for r in reads)
+
+
+@pytest.mark.parametrize("file,kernel", [("fp8_block.cu", "quant_weights_kernel"), ("fp8.cu", "quant_rows_kernel")])
+def test_quantisers_of_weights_end_before_the_next_kernel_begins(file, kernel):
+    """Linears read their weights ahead of the dependency wait: their maker never lets them begin early, and ends with
+    its codes performed for the device and ordered before asynchronous copies."""
+    text = body(source(file), kernel)
+    early = [line.strip() for line in text.splitlines() if "pdl_launch_dependents" in line]
+    assert early == ([] if kernel == "quant_weights_kernel" else ["if (!kHalf) pdl_launch_dependents();"])
+    stored, fence, proxy = (text.rindex(s) for s in ("store_codes" if early == [] else "make_uint2(lo, hi)", "__threadfence();",
+                                                     "umma::fence_proxy_async_global();"))
+    assert stored < fence < proxy
+
+
+@pytest.mark.parametrize("file,kernel,first", [("fp8_block_stream.cu", "stream_kernel", "i < pre; ++i) load_weights("),
+                                               ("fp8_block_tile.cu", "tile_kernel", "i < early; ++i) load_weights("),
+                                               ("fp8.cu", "fp8_umma_kernel", "umma::tma_load_2d(")])
+def test_early_weights_are_read_behind_a_fence_of_the_proxies(file, kernel, first):
+    text = body(source(file), kernel)
+    assert 0 <= text.find("umma::fence_proxy_async_global();") < text.index(first)
