@@ -505,6 +505,11 @@ int qspec_attn_prompt(const uint16_t *q_bf16, int ldq, const uint16_t *k_bf16, i
  *   w8 uint8 [N][K]                      E4M3 codes of weights
  *   sw float [ceil(N / 128)][K / 128]    their scales
  * K is a multiple of 128.  E4M3 and its rounding are those of the Q8 variant.
+ * In the products a block's two scales are multiplied first, s = sa sw, rounded to fp32.
+ * Where s is below 2^-126 it is off by up to 2^-150, a block's term by as much times the sum
+ * of its codes' products; with scales of the quantisers that begins where a block's largest
+ * activation times its largest weight is below 2^-108.  An s that passes fp32 gives an inf
+ * or NaN; scales of the quantisers never do.
  * Weights are read ahead of the call's turn in the stream: in front of a product on
  * the same stream, of the calls here only qspec_quant_weights_fp8_block may write them.
  * ------------------------------------------------------------------------ */
