@@ -377,7 +377,7 @@ int qspec_linear_fp8(const uint8_t *xq, const float *sa, const uint8_t *w8, cons
  * one pass: what stands in front of qspec_linear_fp8.  Per row m:
  *   h = bf16(x + res)  (h = x when res is NULL), stored to h_out
  *   y = h w / sqrt(mean_k h^2 + eps)
- *   sa = max_k |y| / 448, xq = E4M3(y / sa)   (a row of zeros: sa = 0, codes 0)
+ *   sa = max_k |y| / 448, xq = E4M3(y / sa)   (sa = 0, of a row of zeros: codes 0)
  * Sums, norm and quotient in fp32; y is rounded once, to E4M3 (and to bf16
  * where y_bf16 is asked for, for a W4A16 linear on the same rows).
  *
@@ -534,7 +534,7 @@ int qspec_quant_act_fp8_block(const uint16_t *x_bf16, int M, int K, int ldx, uin
  * qspec_rmsnorm_fp8 with a scale for each block: h, y and every argument but sa
  * and lds as there; per token m and block g of K
  *   sa[g lds + m] = max |y| / 448 over the block, xq = E4M3(y / sa)
- * (a block of zeros: sa = 0, codes 0), in fp32, y rounded once.  Device errors:
+ * (sa = 0, of a block of zeros or of a y that small: codes 0), in fp32, y rounded once.  Device errors:
  * QSPEC_ERR_NONFINITE as there.
  */
 int qspec_rmsnorm_fp8_block(const uint16_t *x_bf16, int ldx, const uint16_t *res_bf16, int ldr,

@@ -80,11 +80,14 @@ __device__ __forceinline__ float reciprocal(float s) {
     return __fmaf_rn(__fmaf_rn(-s, y, 1.0f), y, y);
 }
 
+constexpr float kSubnormal = 0x1.cp-118f, kNothing = 0x1.cp-142f;       // 448 x 2^-126, 2^-150: maxima below the one have a subnormal scale, up to the other one of 0
+
 // A block's scale and what its codes are taken with: E4M3(v up inv), inv = 448 / (up max |v|), up a power of two that
 // keeps the reciprocal inside fp32.  Within 3 x 2^-24 of v / s in the quotient.  A scale of 0 has the codes 0.
 struct Quant {
     float s, inv, up;
     __device__ __forceinline__ explicit Quant(float amax) {
+        if (amax < kSubnormal) amax = 448.0f * scale_of(amax);                      // (the scale as it is stored)
         up = amax < 1.0e-30f ? 7.9228162514264338e28f : amax > 1.0e30f ? 1.262177448353619e-29f : 1.0f;      // 2^96, 2^-96
         s = scale_of(amax);
         inv = s > 0.0f ? 448.0f * reciprocal(amax * up) : 0.0f;
