@@ -82,13 +82,18 @@ __device__ __forceinline__ float reciprocal(float s) {
 
 constexpr float kSubnormal = 0x1.cp-118f, kNothing = 0x1.cp-142f;       // 448 x 2^-126, 2^-150: maxima below the one have a subnormal scale, up to the other one of 0
 
+// A power of two that brings a maximum to where its reciprocal is a normal number: 2^96, 2^-96 or 1.
+__device__ __forceinline__ float lift(float top) {
+    return top < 1.0e-30f ? 7.9228162514264338e28f : top > 1.0e30f ? 1.262177448353619e-29f : 1.0f;
+}
+
 // A block's scale and what its codes are taken with: E4M3(v up inv), inv = 448 / (up max |v|), up a power of two that
 // keeps the reciprocal inside fp32.  Within 3 x 2^-24 of v / s in the quotient.  A scale of 0 has the codes 0.
 struct Quant {
     float s, inv, up;
     __device__ __forceinline__ explicit Quant(float amax) {
         if (amax < kSubnormal) amax = 448.0f * scale_of(amax);                      // (the scale as it is stored)
-        up = amax < 1.0e-30f ? 7.9228162514264338e28f : amax > 1.0e30f ? 1.262177448353619e-29f : 1.0f;      // 2^96, 2^-96
+        up = lift(amax);
         s = scale_of(amax);
         inv = s > 0.0f ? 448.0f * reciprocal(amax * up) : 0.0f;
     }
@@ -147,8 +152,8 @@ __device__ __forceinline__ void store_gated(const Args &a, int m, int block, int
     if (a.y != nullptr) store_bf16(a, m, block * kGroup + 4 * lane, h);
 }
 
-// Sums over a cluster's parts of K, in their order: four floats at each of `at` in the shared memory of the CTAs first,
-// first + 1, ..., first + split - 1 (R of them at most).  All are asked for before the first is added: an answer takes about a
+// Sums over a cluster's parts of K, in their order: four floats at each of `at` in the shared memory of the CTAs first ..
+// first + split - 1 (R of them at most).  All are asked for before the first is added: an answer takes about a
 // microsecond.
 constexpr int kMaxSplit = 8;
 template <int R = kMaxSplit, int T>

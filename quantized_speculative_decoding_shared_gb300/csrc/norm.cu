@@ -24,6 +24,14 @@ namespace {
 
 namespace nrm {
 
+using f8b::f2;
+using f8b::fma2;
+using f8b::hi32;
+using f8b::lo32;
+using f8b::max_abs;
+using f8b::max_nan;
+using f8b::mul2;
+
 constexpr int kMaxK = 32768;
 
 __device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
@@ -38,36 +46,7 @@ __device__ __forceinline__ uint32_t add_bf16(uint32_t a, uint32_t b) {      // t
     asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
     return d;
 }
-// two fp32 values in a register pair, and packed operations on them
-__device__ __forceinline__ uint64_t f2(float a, float b) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
 __device__ __forceinline__ uint64_t both(uint32_t w) { return f2(lo_f(w), hi_f(w)); }
-__device__ __forceinline__ float lo32(uint64_t v) { return __uint_as_float((uint32_t)v); }
-__device__ __forceinline__ float hi32(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-    uint64_t d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
-// max(a, |b|, |c|) and max(a, b) that keep a NaN (a >= 0)
-__device__ __forceinline__ float max_abs(float a, float b, float c) {
-    float d;
-    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-    return d;
-}
-__device__ __forceinline__ float max_nan(float a, float b) {
-    float d;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
-    return d;
-}
 // two E4M3 codes, the first in the low byte
 __device__ __forceinline__ uint32_t pack_e4m3(uint64_t v) {
     return __nv_cvt_float2_to_fp8x2(make_float2(lo32(v), hi32(v)), __NV_SATFINITE, __NV_E4M3);
@@ -382,7 +361,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, (kOcc<TPR, NV>))
             reinterpret_cast<uint4 *>(y + (size_t)m * ldy)[i] = make_uint4(o[0], o[1], o[2], o[3]);
         }
         // codes a (448 / top), within 3 x 2^-24; a power of two beside them where the reciprocal would leave fp32
-        const float up = top[j] < 1.0e-30f ? 7.9228162514264338e28f : top[j] > 1.0e30f ? 1.262177448353619e-29f : 1.0f;   // 2^96, 2^-96
+        const float up = f8b::lift(top[j]);
         const float inv = 448.0f * f8b::reciprocal(top[j] * up);
         uint32_t code[4];
 #pragma unroll
