@@ -62,7 +62,7 @@ __global__ void __launch_bounds__(kQThreads)
     float amax = 0.0f;
     bool bad = false;
     for (int i = threadIdx.x; i < K / 8; i += kQThreads) {
-        const uint4 v = row[i];
+        const uint4 v = ld_written(row + i);
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(kQThreads)
     for (int i = 1; i < kQThreads / 32; ++i) amax = fmaxf(amax, red[i]);
     const float s = __fdiv_rn(amax, 448.0f);
     for (int i = threadIdx.x; i < K / 8; i += kQThreads) {
-        const uint4 v = row[i];
+        const uint4 v = ld_written(row + i);
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
         uint32_t lo = 0, hi = 0;
 #pragma unroll
@@ -228,11 +228,14 @@ __global__ void __launch_bounds__(kThreads, 2)
             umma::fence_after_sync();
             const int n = n0 + 32 * warp + lane;
             const uint32_t lane_off = (uint32_t)(32 * warp) << 16;
-            const float sn = n < N ? s8[n] : 0.0f;
+            const float sn = n < N ? ld_written(s8 + n) : 0.0f;
 #pragma unroll
             for (int c0 = 0; c0 < BN; c0 += 16) {
                 uint32_t d[16];
                 umma::tmem_ld_cols<16>(tbase + lane_off + c0, d);
+                float sm[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) sm[j] = t0 + c0 + j < M ? ld_written(sa + t0 + c0 + j) : 0.0f;
                 umma::tmem_ld_wait();
                 if (n < N) {
 #pragma unroll
@@ -240,7 +243,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                         const int m = t0 + c0 + j;
                         if (m < M)
                             y[(size_t)m * ldy + n] =
-                                float_to_bf16_bits(__fmul_rn(__fmul_rn(__uint_as_float(d[j]), sa[m]), sn));
+                                float_to_bf16_bits(__fmul_rn(__fmul_rn(__uint_as_float(d[j]), sm[j]), sn));
                     }
                 }
             }

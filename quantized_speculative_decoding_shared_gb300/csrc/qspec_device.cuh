@@ -29,6 +29,19 @@ __device__ __forceinline__ void pdl_launch_dependents() {
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
 }
 
+// Coherent loads, kept behind pdl_wait(): of what a kernel in front may write while this one is resident.  (A load through
+// `const T *__restrict__` may become one that takes memory for read-only as long as the kernel lives.)
+__device__ __forceinline__ float ld_written(const float *p) {
+    float v;
+    asm volatile("ld.global.f32 %0, [%1];\n" : "=f"(v) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint4 ld_written(const uint4 *p) {
+    uint4 v;
+    asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];\n" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+
 // First data error wins: later codes never overwrite an earlier one.
 __device__ __forceinline__ void flag(int32_t *st, int code) {
     if (st != nullptr && code != QSPEC_OK) atomicCAS(st, 0, code);

@@ -56,3 +56,12 @@ def test_quantisers_of_weights_end_before_the_next_kernel_begins(file, kernel):
 def test_early_weights_are_read_behind_a_fence_of_the_proxies(file, kernel, first):
     text = body(source(file), kernel)
     assert 0 <= text.find("umma::fence_proxy_async_global();") < text.index(first)
+
+
+def test_scales_and_rows_of_the_per_token_linear_are_read_coherently():
+    text = source("fp8.cu")
+    quant, linear = body(text, "quant_rows_kernel"), body(text, "fp8_umma_kernel")
+    assert not re.search(r"\brow\[", quant) and quant.count("ld_written(row + i)") == 2
+    assert not re.search(r"\b(sa|s8)\[", linear) and "ld_written(sa +" in linear and "ld_written(s8 +" in linear
+    assert quant.index("pdl_wait()") < quant.index("ld_written(") and linear.rindex("pdl_wait()") < linear.index("ld_written(")
+    assert "asm volatile(\"ld.global.f32" in source("qspec_device.cuh")
