@@ -331,9 +331,11 @@ struct Kernel {
 };
 template <int BN, bool kGated>
 int slots() { return sm_count() * Cfg<BN, kGated>::kOcc; }       // CTAs that run at once
-// The same in clusters of s.  Where two CTAs share an SM the runtime's count takes one for what fits (256 of them in clusters of
-// eight, and 240 in clusters of six, run at once): there a twentieth is left free for what clusters of four or more cannot
-// fill (us, 1 x 4736 x 4096, 37 tiles, in eight parts 9.7, in six 6.3; 1 x 9600 x 4096, 75 tiles, in four 12.3, in three 8.8).
+// The same in clusters of s.  Where two CTAs share an SM the runtime's count takes one for what fits: there a twentieth is left
+// free for what clusters of four or more cannot fill, 288 of 304 CTAs.  (Clusters of eight: 264, 272, 280 and 288 CTAs run at
+// once, 296 do not: 1 x N x 4096 with 33 / 34 / 35 / 36 / 37 tiles 6.0 / 6.1 / 6.3 / 6.7 / 9.8 us in eight parts, 6.0 / 6.1 / 6.2 / 6.3 /
+// 6.3 in six; K = 14336 12.1 / 12.6 / 12.7 / 13.3 / 17.8 and 12.7 / 12.9 / 13.1 / 13.3 / 13.6.  1 x 9600 x 4096, 75 tiles, in four 12.3, in
+// three 8.8.)
 template <int BN, bool kGated>
 int room(int s) {
     if (Cfg<BN, kGated>::kOcc == 1) return f8b::resident<Kernel<BN, kGated>>().ctas[s];

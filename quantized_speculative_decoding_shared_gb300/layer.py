@@ -98,7 +98,9 @@ class FeedForward:
     w_norm bf16 [K]; N and K multiples of 128.
 
     The weights are quantised on torch's current stream; run works on `stream` (None: the current one), and all that it
-    makes belongs to it, its results included.  It keeps nothing between calls: calls on different streams may overlap."""
+    makes belongs to it, its results included.  It keeps nothing between calls: calls on different streams may overlap, but the
+    caller orders a stream's first call after the making.  `status` is one word for the weights and all calls: the first
+    error stays in it."""
 
     def __init__(self, w_norm, w_gate, w_up, w_down, eps=1e-5):
         self.w_norm, self.eps = w_norm, eps
