@@ -510,6 +510,7 @@ int qspec_attn_prompt(const uint16_t *q_bf16, int ldq, const uint16_t *k_bf16, i
  * of its codes' products; with scales of the quantisers that begins where a block's largest
  * activation times its largest weight is below 2^-108.  An s that passes fp32 gives an inf
  * or NaN; scales of the quantisers never do.
+ * Outputs overlap no input of their call (h_bf16 of the norm as it says there).
  * Weights are read ahead of the call's turn in the stream: in front of a product on
  * the same stream, of the calls here only qspec_quant_weights_fp8_block may write them.
  * ------------------------------------------------------------------------ */

@@ -17,7 +17,7 @@
 //
 // Bound: HBM (2 bytes in, 1 out per value).  8 lanes have one token's 128 values, 32 bytes
 // to a lane (16 lanes and 16 bytes where addresses are no multiples of 32: 4099 x 14336 in
-// 30.7 us for 28.8, 6.1 TB/s); a CTA takes 4 neighbouring blocks of some tokens, so that reads are
+// 29.9 us for 28.0, 6.4 TB/s, with seven CTAs to an SM and 36 bytes of spills); a CTA takes 4 neighbouring blocks of some tokens, so that reads are
 // 1 KB at a time and the scales, which lie token by token, go out in runs through
 // shared memory.  With the divisions of s and y, 16 lanes and half the CTAs resident
 // it took 34.7 us.

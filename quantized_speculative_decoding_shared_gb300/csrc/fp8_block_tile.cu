@@ -17,11 +17,13 @@
 // The tiles behind the last full round of CTAs are split along K over the CTAs of a
 // cluster, whose parts meet in shared memory, in the order of K.
 //
-// Bound: shared memory.  A block is written (48 KB) and read by the products (48 KB), 768
+// Bound: shared memory, by count.  A block is written (48 KB) and read by the products (48 KB), 768
 // clocks at 128 bytes; the products take 512, the packed additions 256.  Measured: some 830
-// clocks a block (0.43 us), 8192 x 4096 x 14336 in 352 us (2730 TFLOP/s), gated 8192 x 14336 x
-// 4096 in 725 us (2650) as long as the clock holds, 398 and 800 us under the power cap (1.6 GHz).
+// clocks a block (0.43 us), 8192 x 4096 x 14336 in 354 us (2720 TFLOP/s), gated 8192 x 14336 x
+// 4096 in 715 us (2690) as long as the clock holds, 410 and 811 us under the power cap (1.6 GHz).
 // The same pipeline without the additions, one accumulator handed over for 16 blocks: 317 and 630.
+// The counters of the memory's banks agree with the bytes (13.5 K words read and 13.4 K written a block, of
+// which 12.3 K each are the operands'), but not on the rate: they take 64 words a clock of either kind for the peak.
 // Pairs of CTAs (256 tokens, half of either operand in each) need 512 clocks of shared memory,
 // but with barriers in the other CTA an accumulator's way round took 900: 363 us, with sixteen
 // warps of 64 sums 374, and at 80 to 512 tokens a half-empty tile more often (gated 128 x
