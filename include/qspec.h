@@ -378,6 +378,7 @@ int qspec_linear_fp8(const uint8_t *xq, const float *sa, const uint8_t *w8, cons
  *   h = bf16(x + res)  (h = x when res is NULL), stored to h_out
  *   y = h w / sqrt(mean_k h^2 + eps)
  *   sa = max_k |y| / 448, xq = E4M3(y / sa)   (sa = 0, of a row of zeros: codes 0)
+ * (over an sa below 2^-126 by what sa is before its last rounding).
  * Sums, norm and quotient in fp32; y is rounded once, to E4M3 (and to bf16
  * where y_bf16 is asked for, for a W4A16 linear on the same rows).
  *
